@@ -1,5 +1,5 @@
-"""Python binding of libgmm (include/gmm.h): the fused GMM EM step and top-m
-soft assignment on one GB300.
+"""Python binding of libgmm (include/gmm.h, include/gmm_experts.h): the fused
+GMM EM step, top-m soft assignment, and local experts behind it, on one GB300.
 
 Argument marshalling only.  Every function here has the name of the C entry
 point it calls and forwards device pointers taken from torch tensors (or
@@ -27,7 +27,9 @@ EXPORTS = (
     "gmm_prepare", "gmm_em_step", "gmm_workspace_bytes_host", "gmm_em_step_host",
     "gmm_assign_topm", "gmm_last_device_status", "gmm_profile_enable", "gmm_profile_read",
     "gmm_profile_reset", "gmm_em_step_noalloc", "gmm_debug_tc_gemm", "gmm_ivf_lists_ws_bytes",
-    "gmm_ivf_lists",
+    "gmm_ivf_lists", "gmm_route_ws_bytes", "gmm_route", "gmm_spread", "gmm_collect",
+    "gmm_expert_ws_bytes", "gmm_expert_product", "gmm_expert_product_dx",
+    "gmm_expert_product_dw", "gmm_adamw_step", "gmm_adamw_moments",
 )
 
 
@@ -38,6 +40,21 @@ class gmm_params(ctypes.Structure):
 class gmm_opts(ctypes.Structure):
     _fields_ = [("ridge_rel", ctypes.c_float), ("var_floor", ctypes.c_float),
                 ("min_s0", ctypes.c_float), ("flags", ctypes.c_int)]
+
+
+class gmm_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int)]
+
+
+class gmm_adamw_opts(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("grad_scale", ctypes.c_double), ("step", ctypes.c_int64),
+                ("state_bits", ctypes.c_int), ("skip", ctypes.c_void_p)]
 
 
 class GmmError(RuntimeError):
@@ -82,6 +99,19 @@ def lib():
         L.gmm_ivf_lists_ws_bytes.argtypes = [i64, i32, i32]
         L.gmm_ivf_lists_ws_bytes.restype = sz
         L.gmm_ivf_lists.argtypes = [vp, vp, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, sz, vp]
+        L.gmm_route_ws_bytes.argtypes = [i64, i32, i32]
+        L.gmm_route_ws_bytes.restype = sz
+        L.gmm_route.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.gmm_spread.argtypes = [vp, i32, i64, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.gmm_collect.argtypes = [vp, i32, i64, i32, i32, i64, vp, vp, vp, vp]
+        L.gmm_expert_ws_bytes.argtypes = [i64, i32, i32, i32, i32]
+        L.gmm_expert_ws_bytes.restype = sz
+        for f in ("gmm_expert_product", "gmm_expert_product_dx"):
+            getattr(L, f).argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.gmm_expert_product_dw.argtypes = [vp, vp, i32, i64, i32, i32, i32, vp, vp, i32, vp, sz,
+                                            vp]
+        L.gmm_adamw_step.argtypes = [P(gmm_adamw_tensor), i32, P(gmm_adamw_opts), vp]
+        L.gmm_adamw_moments.argtypes = [P(gmm_adamw_tensor), i32, i32, P(vp), P(vp), vp]
         L.gmm_profile_enable.argtypes = [i32]
         L.gmm_profile_enable.restype = None
         L.gmm_profile_read.argtypes = [P(ctypes.c_char_p), P(ctypes.c_double), P(ctypes.c_long),
@@ -89,7 +119,10 @@ def lib():
         L.gmm_profile_read.restype = i32
         L.gmm_profile_reset.restype = None
         for f in ("gmm_prepare", "gmm_em_step", "gmm_em_step_host", "gmm_assign_topm",
-                  "gmm_last_device_status", "gmm_em_step_noalloc", "gmm_ivf_lists"):
+                  "gmm_last_device_status", "gmm_em_step_noalloc", "gmm_ivf_lists",
+                  "gmm_route", "gmm_spread", "gmm_collect", "gmm_expert_product",
+                  "gmm_expert_product_dx", "gmm_expert_product_dw", "gmm_adamw_step",
+                  "gmm_adamw_moments"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -209,6 +242,68 @@ def gmm_ivf_lists(ids, gamma, N, m, K, gamma_min, offsets, list_pts, list_gamma,
     st = lib().gmm_ivf_lists(_ptr(ids), _ptr(gamma), N, m, K, float(gamma_min), _ptr(offsets),
                              _ptr(list_pts), _ptr(list_gamma), _ptr(ws), ws_bytes, _stream(stream))
     return _check(st, "gmm_ivf_lists", raise_on_error)
+
+
+def gmm_route_ws_bytes(N, m, K) -> int:
+    return int(lib().gmm_route_ws_bytes(N, m, K))
+
+
+def gmm_route(ids, N, m, K, offsets, entry, slot, ws, ws_bytes, stream=None,
+              raise_on_error=True):
+    st = lib().gmm_route(_ptr(ids), N, m, K, _ptr(offsets), _ptr(entry), _ptr(slot), _ptr(ws),
+                         ws_bytes, _stream(stream))
+    return _check(st, "gmm_route", raise_on_error)
+
+
+def gmm_spread(X, xdtype, N, D, m, K, R, slot, offsets, gamma, Z, Y, dgamma, stream=None,
+               raise_on_error=True):
+    st = lib().gmm_spread(_ptr(X), xdtype, N, D, m, K, R, _ptr(slot), _ptr(offsets), _ptr(gamma),
+                          _ptr(Z), _ptr(Y), _ptr(dgamma), _stream(stream))
+    return _check(st, "gmm_spread", raise_on_error)
+
+
+def gmm_collect(Z, xdtype, N, D, m, R, slot, gamma, out, stream=None, raise_on_error=True):
+    st = lib().gmm_collect(_ptr(Z), xdtype, N, D, m, R, _ptr(slot), _ptr(gamma), _ptr(out),
+                           _stream(stream))
+    return _check(st, "gmm_collect", raise_on_error)
+
+
+def gmm_expert_ws_bytes(R, d_in, d_out, K, xdtype) -> int:
+    return int(lib().gmm_expert_ws_bytes(R, d_in, d_out, K, xdtype))
+
+
+def gmm_expert_product(A, xdtype, R, d_in, d_out, K, offsets, W, Y, ws, ws_bytes, stream=None,
+                       raise_on_error=True):
+    st = lib().gmm_expert_product(_ptr(A), xdtype, R, d_in, d_out, K, _ptr(offsets), _ptr(W),
+                                  _ptr(Y), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "gmm_expert_product", raise_on_error)
+
+
+def gmm_expert_product_dx(dY, xdtype, R, d_in, d_out, K, offsets, W, dA, ws, ws_bytes,
+                          stream=None, raise_on_error=True):
+    st = lib().gmm_expert_product_dx(_ptr(dY), xdtype, R, d_in, d_out, K, _ptr(offsets), _ptr(W),
+                                     _ptr(dA), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "gmm_expert_product_dx", raise_on_error)
+
+
+def gmm_expert_product_dw(dY, A, xdtype, R, d_in, d_out, K, offsets, dW, wdtype, ws, ws_bytes,
+                          stream=None, raise_on_error=True):
+    st = lib().gmm_expert_product_dw(_ptr(dY), _ptr(A), xdtype, R, d_in, d_out, K, _ptr(offsets),
+                                     _ptr(dW), wdtype, _ptr(ws), ws_bytes, _stream(stream))
+    return _check(st, "gmm_expert_product_dw", raise_on_error)
+
+
+def gmm_adamw_step(tensors, count, opts, stream=None, raise_on_error=True):
+    """tensors: a ctypes array of gmm_adamw_tensor; opts: gmm_adamw_opts."""
+    st = lib().gmm_adamw_step(tensors, count, ctypes.byref(opts), _stream(stream))
+    return _check(st, "gmm_adamw_step", raise_on_error)
+
+
+def gmm_adamw_moments(tensors, count, state_bits, m_out, v_out, stream=None,
+                      raise_on_error=True):
+    """m_out, v_out: ctypes arrays of device addresses."""
+    st = lib().gmm_adamw_moments(tensors, count, state_bits, m_out, v_out, _stream(stream))
+    return _check(st, "gmm_adamw_moments", raise_on_error)
 
 
 def gmm_last_device_status(ws, stream=None) -> int:

@@ -1,0 +1,117 @@
+"""AdamW over a list of tensors in one launch, moments in 32 or 8 bits.
+
+``AdamW`` holds the parameters' moments as torch tensors and calls
+``gmm_adamw_step`` on the current torch stream.  No arithmetic happens here.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (gmm_adamw_moments, gmm_adamw_opts, gmm_adamw_step, gmm_adamw_tensor)
+from .torch_api import TORCH_XDTYPE
+
+BLOCK = 256  # elements that share one scale of an 8-bit moment
+
+
+def _dense(t, name, n, dtypes, device):
+    if not torch.is_tensor(t) or t.numel() != n or t.dtype not in dtypes or t.device != device:
+        raise ValueError("%s: expected %d elements of %s on %s" % (name, n, dtypes, device))
+    if not t.is_contiguous():
+        raise ValueError("%s is not dense (strides %s)" % (name, t.stride()))
+    return t
+
+
+class AdamW:
+    """Decoupled weight decay Adam on `params`, dense float32 / float16 / bfloat16
+    CUDA tensors, updated in place.
+
+    state_bits: 32 (float moments) or 8 (codes with a scale per 256 elements).
+    master: hold 16-bit parameters in float32 as well (``self.master``).
+    state, step: resume; a dict of lists m, v (and m_scale, v_scale in 8 bits,
+    master with master=True) as ``self.state`` holds them, and the steps taken.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits=32, master=False, state=None, step=0):
+        self.params = list(params)
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits %s: expected 8 or 32" % (state_bits,))
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.state_bits, self.steps = state_bits, int(step)
+        for i, p in enumerate(self.params):
+            if not torch.is_tensor(p) or p.device.type != "cuda":
+                raise ValueError("params[%d] is not a CUDA tensor" % i)
+            _dense(p, "params[%d]" % i, p.numel(), tuple(TORCH_XDTYPE), self.params[0].device)
+        self.state = self._state(state, master)
+        self._table = (gmm_adamw_tensor * max(1, len(self.params)))()
+        for i, p in enumerate(self.params):
+            e = self._table[i]
+            e.param, e.n, e.param_dtype = p.data_ptr(), p.numel(), TORCH_XDTYPE[p.dtype]
+            for k, ts in self.state.items():
+                setattr(e, k, ts[i].data_ptr() if ts[i] is not None else None)
+
+    def _state(self, given, master):
+        bits = self.state_bits
+        types = {"m": torch.float32 if bits == 32 else torch.int8,
+                 "v": torch.float32 if bits == 32 else torch.uint8}
+        if bits == 8:
+            types.update(m_scale=torch.float32, v_scale=torch.float32)
+        out = {}
+        for k, dt in types.items():
+            size = (lambda p: -(-p.numel() // BLOCK)) if k.endswith("scale") else (lambda p: p.numel())
+            if given is None:
+                out[k] = [torch.zeros(size(p), dtype=dt, device=p.device) for p in self.params]
+            else:
+                out[k] = [_dense(t, "state[%s][%d]" % (k, i), size(p), (dt,), p.device)
+                          for i, (t, p) in enumerate(zip(given[k], self.params, strict=True))]
+        if master:
+            low = [p.dtype != torch.float32 for p in self.params]
+            if given is not None and "master" in given:
+                out["master"] = [_dense(t, "state[master][%d]" % i, p.numel(), (torch.float32,),
+                                        p.device) if l else None
+                                 for i, (t, p, l) in enumerate(zip(given["master"], self.params, low,
+                                                                   strict=True))]
+            else:
+                out["master"] = [p.detach().float().reshape(-1) if l else None
+                                 for p, l in zip(self.params, low)]
+        return out
+
+    def step(self, grads, grad_scale=1.0, skip=None, stream=None):
+        """One step with `grads` (one tensor per parameter), each multiplied by
+        grad_scale; skip: an int32 device tensor, nothing changes where it is
+        not 0 (the step still counts)."""
+        if len(grads) != len(self.params):
+            raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
+        table = self._table
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if (g.dtype not in TORCH_XDTYPE or g.numel() != p.numel() or g.device != p.device
+                    or not g.is_contiguous()):
+                _dense(g, "grads[%d]" % i, p.numel(), tuple(TORCH_XDTYPE), p.device)
+            e = table[i]
+            e.grad, e.grad_dtype = g.data_ptr(), TORCH_XDTYPE[g.dtype]
+        if skip is not None:
+            _dense(skip, "skip", 1, (torch.int32,), self.params[0].device)
+        self.steps += 1
+        o = gmm_adamw_opts(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                           grad_scale, self.steps, self.state_bits,
+                           skip.data_ptr() if skip is not None else None)
+        return gmm_adamw_step(table, len(self.params), o, stream=stream)
+
+    def moments(self, m_out=None, v_out=None, stream=None):
+        """The moments in float32: two lists of tensors (given ones are written)."""
+        def outs(ts, name):
+            if ts is None:
+                return [torch.empty(p.shape, dtype=torch.float32, device=p.device)
+                        for p in self.params]
+            if len(ts) != len(self.params):
+                raise ValueError("%s: %d tensors for %d parameters" % (name, len(ts), len(self.params)))
+            for i, (t, p) in enumerate(zip(ts, self.params)):
+                _dense(t, "%s[%d]" % (name, i), p.numel(), (torch.float32,), p.device)
+            return ts
+        m_out, v_out = outs(m_out, "m_out"), outs(v_out, "v_out")
+        n = len(self.params)
+        ptrs = lambda ts: (ctypes.c_void_p * max(1, n))(*[t.data_ptr() for t in ts])  # noqa: E731
+        gmm_adamw_moments(self._table, n, self.state_bits, ptrs(m_out), ptrs(v_out), stream=stream)
+        return m_out, v_out

@@ -1,0 +1,225 @@
+// expert_product.cu - the experts' products: argument checks, the list of row
+// tiles, and the CUDA-core kernel that serves every size and type.
+//
+//   product     Y[r]  = W_k A[r]          rows r of component k
+//   product_dx  dA[r] = W_k^T dY[r]
+//   product_dw  dW_k  = sum_r dY[r] A[r]^T
+//
+// One fp32 kernel computes all three as C[i][j] = sum_l P[i][l] Q[j][l] with
+// the strides of the case: 64 x 64 tiles, 16 steps of l staged in shared
+// memory, 4 x 4 outputs a thread.
+#include "expert_product.cuh"
+
+namespace gmm {
+namespace {
+
+constexpr int kT = 64;        // tile rows and columns of the CUDA-core kernel
+constexpr int kStep = 16;
+constexpr int kListThreads = 1024;
+
+// Row tiles of T rows for every component, in order, then those of the rows
+// past offsets[K] (component -1: zeros).  Offsets are held within [0, R].
+__global__ void __launch_bounds__(kListThreads)
+tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T,
+                 DeviceStatus* __restrict__ st, int32_t* __restrict__ count,
+                 int4* __restrict__ tiles) {
+  __shared__ uint32_t wsum[32];
+  if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
+  const int G = K + 1;
+  const int per = (G + kListThreads - 1) / kListThreads;
+  const int k0 = min(G, (int)threadIdx.x * per), k1 = min(G, k0 + per);
+  uint32_t mine = 0;
+  for (int k = k0; k < k1; ++k) {
+    const int64_t a = clamp_row(offsets[k], R), b = k < K ? clamp_row(offsets[k + 1], R) : R;
+    if (b > a) mine += (uint32_t)((b - a + T - 1) / T);
+  }
+  uint32_t at = block_exclusive_1024(mine, wsum);
+  for (int k = k0; k < k1; ++k) {
+    const int64_t a = clamp_row(offsets[k], R), b = k < K ? clamp_row(offsets[k + 1], R) : R;
+    for (int64_t r = a; r < b; r += T)
+      tiles[at++] = make_int4(k < K ? k : -1, (int)r, (int)min((int64_t)T, b - r), 0);
+  }
+  if (k1 == G && k0 < k1) *count = (int32_t)at;
+}
+
+// P[i][l] at p + i*pi + l*pl, likewise Q; C row-major with stride ldc.
+template <typename T, typename TO>
+__device__ __forceinline__ void tile_product(const T* __restrict__ p, int64_t pi, int64_t pl,
+                                             const T* __restrict__ q, int64_t qj, int64_t ql,
+                                             int rows, int cols, int64_t len, TO* __restrict__ c,
+                                             int64_t ldc) {
+  __shared__ float sp[kStep][kT + 4], sq[kStep][kT + 4];
+  const int tid = threadIdx.x;
+  const int ti = (tid >> 4) * 4, tj = (tid & 15) * 4;
+  float acc[4][4] = {};
+  for (int64_t l0 = 0; l0 < len; l0 += kStep) {
+#pragma unroll
+    for (int x = tid; x < kT * kStep; x += 256) {
+      // neighbouring threads along whichever index is contiguous in memory
+      const int ip = pl == 1 ? x / kStep : x % kT, lp = pl == 1 ? x % kStep : x / kT;
+      sp[lp][ip] = (ip < rows && l0 + lp < len) ? to_f(p[ip * pi + (l0 + lp) * pl]) : 0.f;
+      const int jq = ql == 1 ? x / kStep : x % kT, lq = ql == 1 ? x % kStep : x / kT;
+      sq[lq][jq] = (jq < cols && l0 + lq < len) ? to_f(q[jq * qj + (l0 + lq) * ql]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int l = 0; l < kStep; ++l) {
+      const float4 a = *reinterpret_cast<const float4*>(&sp[l][ti]);
+      const float4 b = *reinterpret_cast<const float4*>(&sq[l][tj]);
+      const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (ti + i < rows && tj + j < cols) c[(ti + i) * ldc + tj + j] = from_f<TO>(acc[i][j]);
+}
+
+// Rows (A or dY, width d_from) through W_k to width d_to.  DX: through W_k^T.
+template <typename T, bool DX>
+__global__ void __launch_bounds__(256)
+rows_simt_kernel(const T* __restrict__ A, const T* __restrict__ W, T* __restrict__ Y, int d_from,
+                 int d_to, const int32_t* __restrict__ count, const int4* __restrict__ tiles) {
+  if ((int)blockIdx.x >= *count) return;
+  const int4 t = tiles[blockIdx.x];
+  const int j0 = blockIdx.y * kT;
+  const int cols = min(kT, d_to - j0);
+  const int64_t r0 = t.y;
+  T* y = Y + r0 * d_to + j0;
+  if (t.x < 0) {
+    for (int x = threadIdx.x; x < t.z * cols; x += 256)
+      y[(int64_t)(x / cols) * d_to + x % cols] = from_f<T>(0.f);
+    return;
+  }
+  const T* w = W + (int64_t)t.x * d_from * d_to + (DX ? (int64_t)j0 : (int64_t)j0 * d_from);
+  tile_product<T, T>(A + r0 * d_from, d_from, 1, w, DX ? 1 : d_from, DX ? d_to : 1, t.z, cols,
+                     d_from, y, d_to);
+}
+
+template <typename T, typename TO>
+__global__ void __launch_bounds__(256)
+weights_simt_kernel(const T* __restrict__ dY, const T* __restrict__ A, TO* __restrict__ dW,
+                    int d_in, int d_out, const int64_t* __restrict__ offsets, int64_t R) {
+  const int k = blockIdx.z;
+  const int64_t a = clamp_row(offsets[k], R), b = clamp_row(offsets[k + 1], R);
+  const int i0 = blockIdx.x * kT, o0 = blockIdx.y * kT;
+  tile_product<T, TO>(dY + a * d_out + o0, 1, d_out, A + a * d_in + i0, 1, d_in,
+                      min(kT, d_out - o0), min(kT, d_in - i0), b > a ? b - a : 0,
+                      dW + ((int64_t)k * d_out + o0) * d_in + i0, d_in);
+}
+
+bool sizes_ok(int xdtype, int64_t R, int d_in, int d_out, int K) {
+  return dtype_ok(xdtype) && R >= 0 && R <= INT32_MAX && K >= 1 && K <= kMaxK && d_in >= 1 &&
+         d_out >= 1 && (int64_t)d_in * d_out <= INT32_MAX;
+}
+
+gmm_status check(int xdtype, int64_t R, int d_in, int d_out, int K, const int64_t* offsets,
+                 const void* rows1, const void* rows2, const void* w, void* ws, size_t ws_bytes) {
+  if (!sizes_ok(xdtype, R, d_in, d_out, K) || !offsets || !w || !ws) return GMM_ERR_INVALID_ARG;
+  if (R > 0 && (!rows1 || !rows2)) return GMM_ERR_INVALID_ARG;
+  if (((uintptr_t)rows1 | (uintptr_t)rows2 | (uintptr_t)w) % dtype_size(xdtype))
+    return GMM_ERR_INVALID_ARG;
+  if ((uintptr_t)ws % kAlign) return GMM_ERR_INVALID_ARG;
+  if (ws_bytes < ProductLayout::make(R, d_in, d_out, K).bytes) return GMM_ERR_WORKSPACE;
+  return GMM_OK;
+}
+
+template <typename T>
+gmm_status rows_simt(const void* A, const void* W, void* Y, int64_t R, int d_from, int d_to, int K,
+                     bool dx, const int64_t* offsets, void* ws, cudaStream_t s) {
+  const ProductLayout L = ProductLayout::make(R, d_from, d_to, K);
+  gmm_status r = list_tiles(offsets, K, R, kT, ws, L, s);
+  if (r != GMM_OK || R == 0) return r;
+  const dim3 grid((unsigned)ProductLayout::most_tiles(R, K, kT), (d_to + kT - 1) / kT);
+  ProfScope p(dx ? "rows_simt_kernel(dx)" : "rows_simt_kernel", s);
+  const int32_t* count = at<int32_t>(ws, L.off_count);
+  const int4* tiles = at<int4>(ws, L.off_tiles);
+  if (dx) rows_simt_kernel<T, true><<<grid, 256, 0, s>>>((const T*)A, (const T*)W, (T*)Y, d_from, d_to, count, tiles);
+  else rows_simt_kernel<T, false><<<grid, 256, 0, s>>>((const T*)A, (const T*)W, (T*)Y, d_from, d_to, count, tiles);
+  return launched();
+}
+
+template <typename T, typename TO>
+gmm_status weights_simt(const void* dY, const void* A, void* dW, int64_t R, int d_in, int d_out,
+                        int K, const int64_t* offsets, cudaStream_t s) {
+  const dim3 grid((d_in + kT - 1) / kT, (d_out + kT - 1) / kT, K);
+  ProfScope p("weights_simt_kernel", s);
+  weights_simt_kernel<T, TO><<<grid, 256, 0, s>>>((const T*)dY, (const T*)A, (TO*)dW, d_in, d_out,
+                                                  offsets, R);
+  return launched();
+}
+
+gmm_status rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
+                        int d_to, int K, bool dx, const int64_t* offsets, void* ws,
+                        cudaStream_t s) {
+  if ((d_to + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
+  switch (xdtype) {
+    case GMM_F32: return rows_simt<float>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
+    case GMM_F16: return rows_simt<__half>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
+    default: return rows_simt<__nv_bfloat16>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
+  }
+}
+
+}  // namespace
+
+gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
+                      const ProductLayout& L, cudaStream_t s) {
+  ProfScope p("tile_list_kernel", s);
+  tile_list_kernel<<<1, kListThreads, 0, s>>>(offsets, K, R, T, at<DeviceStatus>(ws, 0),
+                                              at<int32_t>(ws, L.off_count),
+                                              at<int4>(ws, L.off_tiles));
+  return launched();
+}
+
+}  // namespace gmm
+
+using namespace gmm;
+
+extern "C" {
+
+size_t gmm_expert_ws_bytes(int64_t R, int d_in, int d_out, int K, gmm_dtype xdtype) {
+  if (!sizes_ok(xdtype, R, d_in, d_out, K)) return 0;
+  return ProductLayout::make(R, d_in, d_out, K).bytes;
+}
+
+gmm_status gmm_expert_product(const void* A, gmm_dtype xdtype, int64_t R, int d_in, int d_out,
+                              int K, const int64_t* offsets, const void* W, void* Y, void* ws,
+                              size_t ws_bytes, void* stream) {
+  const gmm_status r = check(xdtype, R, d_in, d_out, K, offsets, A, Y, W, ws, ws_bytes);
+  if (r != GMM_OK) return r;
+  return rows_product(A, xdtype, W, Y, R, d_in, d_out, K, false, offsets, ws, (cudaStream_t)stream);
+}
+
+gmm_status gmm_expert_product_dx(const void* dY, gmm_dtype xdtype, int64_t R, int d_in, int d_out,
+                                 int K, const int64_t* offsets, const void* W, void* dA, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  const gmm_status r = check(xdtype, R, d_in, d_out, K, offsets, dY, dA, W, ws, ws_bytes);
+  if (r != GMM_OK) return r;
+  return rows_product(dY, xdtype, W, dA, R, d_out, d_in, K, true, offsets, ws, (cudaStream_t)stream);
+}
+
+gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype, int64_t R,
+                                 int d_in, int d_out, int K, const int64_t* offsets, void* dW,
+                                 gmm_dtype wdtype, void* ws, size_t ws_bytes, void* stream) {
+  gmm_status r = check(xdtype, R, d_in, d_out, K, offsets, dY, A, dW, ws, ws_bytes);
+  if (r != GMM_OK) return r;
+  if ((wdtype != xdtype && wdtype != GMM_F32) || (uintptr_t)dW % dtype_size(wdtype))
+    return GMM_ERR_INVALID_ARG;
+  if (K > 65535 || (d_out + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (xdtype == GMM_F32) return weights_simt<float, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+  if (xdtype == GMM_F16) {
+    if (wdtype == GMM_F32) return weights_simt<__half, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+    return weights_simt<__half, __half>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+  }
+  if (wdtype == GMM_F32) return weights_simt<__nv_bfloat16, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+  return weights_simt<__nv_bfloat16, __nv_bfloat16>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+}
+
+}  // extern "C"

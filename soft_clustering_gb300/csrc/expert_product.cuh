@@ -1,0 +1,35 @@
+// expert_product.cuh - workspace and row tiles of the experts' products.
+#pragma once
+
+#include "expert_internal.cuh"
+
+namespace gmm {
+
+constexpr int kLeastTile = 64;  // fewest rows of a tile in any kernel's list
+
+__host__ __device__ inline int64_t clamp_row(int64_t v, int64_t R) {
+  return v < 0 ? 0 : v > R ? R : v;
+}
+
+struct ProductLayout {
+  size_t off_count, off_tiles, bytes;  // the DeviceStatus comes first
+  // row tiles of K components and of the rows past them
+  static int64_t most_tiles(int64_t R, int K, int T) { return R / T + K + 1; }
+  static ProductLayout make(int64_t R, int d_in, int d_out, int K) {
+    (void)d_in;
+    (void)d_out;
+    ProductLayout L;
+    size_t o = align_up(sizeof(DeviceStatus));
+    L.off_count = o; o = align_up(o + sizeof(int32_t));
+    L.off_tiles = o; o = align_up(o + sizeof(int4) * (size_t)most_tiles(R, K, kLeastTile));
+    L.bytes = o;
+    return L;
+  }
+};
+
+// Fills the tile list {component or -1, first row, rows, 0} and its length,
+// and clears the workspace's status word.
+gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
+                      const ProductLayout& L, cudaStream_t s);
+
+}  // namespace gmm

@@ -1,0 +1,268 @@
+// expert_route.cu - gmm_route: the entries of a top-m table in the order of
+// their components (a stable counting sort), with the way back.
+//
+// slot[e] = offsets[k] + #{e' < e : ids[e'] = k}, k = ids[e]; entry[slot[e]]
+// = e.  Entries left out form group K: their slot is -1 and their places past
+// offsets[K] hold -1 in `entry`.
+//
+// Up to kTinyE entries one block does it alone (latency is all that counts):
+// each thread ranks one entry against all others in shared memory, and
+// offsets[k] is the number of sorted keys below k.
+// Above that: per block of entries a histogram, a prefix over the blocks for
+// each group, and a scatter whose warps take consecutive segments of the
+// block's entries; __match_any_sync ranks the equal keys of 32 entries.  Only
+// integer counts in fixed places, so the order never varies.
+// Floor: 4 bytes read and 8 written per entry.
+#include "expert_internal.cuh"
+
+namespace gmm {
+namespace {
+
+constexpr int kTinyE = 1024;
+constexpr int kCountThreads = 256;
+constexpr int kSlice = 12288;          // groups per shared-memory histogram pass
+constexpr int kMaxWarps = 8;           // scatter warps per block
+constexpr size_t kScatterSmem = 192 * 1024;
+
+// Group of an id: K for entries left out.
+__device__ __forceinline__ int group_of(int32_t id, int K) {
+  return (id >= 0 && id < K) ? id : K;
+}
+
+__global__ void __launch_bounds__(kTinyE)
+route_tiny_kernel(const int32_t* __restrict__ ids, int E, int K, int64_t* __restrict__ offsets,
+                  int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
+  __shared__ __align__(16) int key[kTinyE];
+  __shared__ int sorted[kTinyE];
+  const int e = threadIdx.x;
+  const int padded = (E + 3) & ~3;
+  const int mine = e < E ? group_of(ids[e], K) : INT32_MAX;
+  if (e < padded) key[e] = mine;
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < padded; i += 4) {
+    const int4 q = *reinterpret_cast<const int4*>(key + i);
+    rank += (q.x < mine) || (q.x == mine && i < e);
+    rank += (q.y < mine) || (q.y == mine && i + 1 < e);
+    rank += (q.z < mine) || (q.z == mine && i + 2 < e);
+    rank += (q.w < mine) || (q.w == mine && i + 3 < e);
+  }
+  if (e < E) {
+    sorted[rank] = mine;
+    slot[e] = mine < K ? rank : -1;
+    entry[rank] = mine < K ? e : -1;
+  }
+  __syncthreads();
+  for (int k = e; k <= K; k += blockDim.x) {  // number of keys below k
+    int lo = 0, hi = E;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < k) lo = mid + 1;
+      else hi = mid;
+    }
+    offsets[k] = lo;
+  }
+}
+
+// counts[b][k]: entries of group k in block b's `tile` entries.
+__global__ void __launch_bounds__(kCountThreads)
+route_count_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int tile,
+                   uint32_t* __restrict__ counts) {
+  __shared__ uint32_t hist[kSlice];
+  const int64_t b = blockIdx.x;
+  const int64_t e0 = b * tile, e1 = min(E, e0 + tile);
+  const int G = K + 1;
+  for (int k0 = 0; k0 < G; k0 += kSlice) {
+    const int ks = min(kSlice, G - k0);
+    for (int i = threadIdx.x; i < ks; i += kCountThreads) hist[i] = 0u;
+    __syncthreads();
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += kCountThreads) {
+      const int k = group_of(ids[e], K) - k0;
+      if (k >= 0 && k < ks) atomicAdd(&hist[k], 1u);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ks; i += kCountThreads) counts[(size_t)b * G + k0 + i] = hist[i];
+    __syncthreads();
+  }
+}
+
+// Block: 32 groups (lanes) x 32 stretches of blocks (warps).  counts[b][k]
+// becomes the entries of k in blocks before b; tot[k] the entries of k.
+__global__ void __launch_bounds__(1024)
+route_scan_blocks_kernel(uint32_t* __restrict__ counts, int64_t nb, int G,
+                         uint32_t* __restrict__ tot) {
+  __shared__ uint32_t part[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int k = blockIdx.x * 32 + lane;
+  const int64_t per = (nb + 31) / 32;
+  const int64_t b0 = min(nb, w * per), b1 = min(nb, b0 + per);
+  uint32_t sum = 0;
+  if (k < G)
+    for (int64_t b = b0; b < b1; ++b) sum += counts[(size_t)b * G + k];
+  part[w][lane] = sum;
+  __syncthreads();
+  if (w == 0) {
+    uint32_t run = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t v = part[i][lane];
+      part[i][lane] = run;
+      run += v;
+    }
+    if (k < G) tot[k] = run;
+  }
+  __syncthreads();
+  if (k < G) {
+    uint32_t run = part[w][lane];
+    for (int64_t b = b0; b < b1; ++b) {
+      const uint32_t v = counts[(size_t)b * G + k];
+      counts[(size_t)b * G + k] = run;
+      run += v;
+    }
+  }
+}
+
+// One block: offsets[k] = entries of the groups before k, k = 0 .. K.
+__global__ void __launch_bounds__(1024)
+route_scan_groups_kernel(const uint32_t* __restrict__ tot, int K, int64_t* __restrict__ offsets) {
+  __shared__ uint32_t wsum[32];
+  const int per = (K + 1 + 1023) / 1024;
+  const int k0 = min(K + 1, (int)threadIdx.x * per), k1 = min(K + 1, k0 + per);
+  uint32_t mine = 0;
+  for (int k = k0; k < k1; ++k) mine += tot[k];
+  uint32_t run = block_exclusive_1024(mine, wsum);
+  for (int k = k0; k < k1; ++k) {
+    offsets[k] = run;
+    run += tot[k];
+  }
+}
+
+// hist[w][k]: entries of group k in the segments before warp w's, then the
+// warp's running count.  A segment holds at most 65535 entries.
+__global__ void __launch_bounds__(kMaxWarps * 32)
+route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg,
+                     const uint32_t* __restrict__ counts, const int64_t* __restrict__ offsets,
+                     int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
+  extern __shared__ uint16_t hist[];
+  const int G = K + 1;
+  const int warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t b = blockIdx.x;
+  const int64_t e0 = (b * warps + w) * (int64_t)seg;
+  const int64_t e1 = min(E, e0 + seg);
+  uint16_t* mine = hist + (size_t)w * G;
+  for (int i = threadIdx.x; i < warps * G; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
+  if (warps > 1) {
+    for (int64_t base = e0; base < e1; base += 32) {
+      const int64_t e = base + lane;
+      const int k = e < e1 ? group_of(ids[e], K) : -1;
+      const unsigned same = __match_any_sync(0xffffffffu, k);
+      if (k >= 0 && lane == __ffs(same) - 1) mine[k] += (uint16_t)__popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < G; k += blockDim.x) {
+      uint32_t run = 0;
+      for (int i = 0; i < warps; ++i) {
+        const uint32_t v = hist[(size_t)i * G + k];
+        hist[(size_t)i * G + k] = (uint16_t)run;
+        run += v;
+      }
+    }
+    __syncthreads();
+  }
+  for (int64_t base = e0; base < e1; base += 32) {
+    const int64_t e = base + lane;
+    const int k = e < e1 ? group_of(ids[e], K) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, k);
+    uint32_t at = 0;
+    if (k >= 0) {
+      at = mine[k];
+      const int64_t pos =
+          offsets[k] + counts[(size_t)b * G + k] + at + __popc(same & ((1u << lane) - 1u));
+      slot[e] = k < K ? (int32_t)pos : -1;
+      entry[pos] = k < K ? (int32_t)e : -1;
+    }
+    __syncwarp();
+    if (k >= 0 && lane == __ffs(same) - 1) mine[k] = (uint16_t)(at + __popc(same));
+    __syncwarp();
+  }
+}
+
+struct RouteLayout {
+  int warps, seg, tile;
+  int64_t nb;
+  size_t off_counts, off_tot, bytes;
+  static RouteLayout make(int64_t E, int K) {
+    RouteLayout L;
+    const size_t per_warp = sizeof(uint16_t) * (size_t)(K + 1);
+    L.warps = kMaxWarps;
+    while (L.warps > 1 && per_warp * L.warps > kScatterSmem) L.warps >>= 1;
+    // enough blocks for two a multiprocessor, up to 4096 entries a warp (a
+    // block's K counters are written, scanned and read once more)
+    int64_t seg = (E + (int64_t)L.warps * 304 - 1) / ((int64_t)L.warps * 304);
+    seg = seg < 256 ? 256 : seg > 4096 ? 4096 : (seg + 31) / 32 * 32;
+    L.seg = (int)seg;
+    L.tile = L.warps * L.seg;
+    L.nb = (E + L.tile - 1) / L.tile;
+    size_t o = 0;
+    L.off_counts = o; o = align_up(o + sizeof(uint32_t) * (size_t)(K + 1) * (size_t)L.nb);
+    L.off_tot = o;    o = align_up(o + sizeof(uint32_t) * (size_t)(K + 1));
+    L.bytes = o;
+    return L;
+  }
+};
+
+bool route_sizes_ok(int64_t N, int m, int K) {
+  return N >= 0 && m >= 1 && m <= 8 && K >= 1 && K <= kMaxK && N <= INT32_MAX / m;
+}
+
+}  // namespace
+}  // namespace gmm
+
+using namespace gmm;
+
+extern "C" {
+
+size_t gmm_route_ws_bytes(int64_t N, int m, int K) {
+  if (!route_sizes_ok(N, m, K)) return 0;
+  return RouteLayout::make(N * m, K).bytes;
+}
+
+gmm_status gmm_route(const int32_t* ids, int64_t N, int m, int K, int64_t* offsets,
+                     int32_t* entry, int32_t* slot, void* ws, size_t ws_bytes, void* stream) {
+  if (!route_sizes_ok(N, m, K) || !offsets || !ws) return GMM_ERR_INVALID_ARG;
+  if (N > 0 && (!ids || !entry || !slot)) return GMM_ERR_INVALID_ARG;
+  const int64_t E = N * m;
+  const RouteLayout L = RouteLayout::make(E, K);
+  if (ws_bytes < L.bytes) return GMM_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (E <= kTinyE) {
+    ProfScope p("route_tiny_kernel", s);
+    // one thread an entry, and enough of them for the K + 1 offsets
+    int threads = (int)((E + 31) / 32 * 32);
+    if (threads < 256) threads = 256;
+    route_tiny_kernel<<<1, threads, 0, s>>>(ids, (int)E, K, offsets, entry, slot);
+    return launched();
+  }
+  uint32_t* counts = at<uint32_t>(ws, L.off_counts);
+  uint32_t* tot = at<uint32_t>(ws, L.off_tot);
+  const size_t smem = sizeof(uint16_t) * (size_t)(K + 1) * L.warps;
+  if (cudaFuncSetAttribute(route_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kScatterSmem) != cudaSuccess)
+    return GMM_ERR_CUDA;
+  ProfScope p("route_kernels", s, 4);
+  gmm_status r;
+  route_count_kernel<<<(unsigned)L.nb, kCountThreads, 0, s>>>(ids, E, K, L.tile, counts);
+  if ((r = launched()) != GMM_OK) return r;
+  route_scan_blocks_kernel<<<(K + 1 + 31) / 32, 1024, 0, s>>>(counts, L.nb, K + 1, tot);
+  if ((r = launched()) != GMM_OK) return r;
+  route_scan_groups_kernel<<<1, 1024, 0, s>>>(tot, K, offsets);
+  if ((r = launched()) != GMM_OK) return r;
+  route_scatter_kernel<<<(unsigned)L.nb, L.warps * 32, smem, s>>>(ids, E, K, L.seg, counts,
+                                                                  offsets, entry, slot);
+  return launched();
+}
+
+}  // extern "C"
