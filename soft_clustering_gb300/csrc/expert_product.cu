@@ -158,6 +158,8 @@ gmm_status weights_simt(const void* dY, const void* A, void* dW, int64_t R, int 
 gmm_status rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
                         int d_to, int K, bool dx, const int64_t* offsets, void* ws,
                         cudaStream_t s) {
+  if (tc_product_ok(xdtype, R, d_from, d_to, A, W, Y))
+    return tc_rows(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
   if ((d_to + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
   switch (xdtype) {
     case GMM_F32: return rows_simt<float>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
@@ -211,8 +213,10 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
   if (r != GMM_OK) return r;
   if ((wdtype != xdtype && wdtype != GMM_F32) || (uintptr_t)dW % dtype_size(wdtype))
     return GMM_ERR_INVALID_ARG;
-  if (K > 65535 || (d_out + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
   cudaStream_t s = (cudaStream_t)stream;
+  if (R > 0 && tc_product_ok(xdtype, R, d_in, d_out, dY, A, dW))
+    return tc_weights(dY, A, xdtype, R, d_in, d_out, K, offsets, dW, wdtype, ws, s);
+  if (K > 65535 || (d_out + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
   if (xdtype == GMM_F32) return weights_simt<float, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
   if (xdtype == GMM_F16) {
     if (wdtype == GMM_F32) return weights_simt<__half, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
