@@ -43,108 +43,137 @@ __device__ __forceinline__ void zero_tail(T* Y, int64_t R, int D, const int64_t*
     store_vec<T, V>(base + i * V, z);
 }
 
-template <typename T, int V, bool DG>
+// Points a thread has in flight: M rows of up to 16 bytes each for every one.
+__host__ __device__ constexpr int points_in_flight(int M) { return M >= 8 ? 1 : M >= 4 ? 2 : 4; }
+
+// The M slots (and weights) of point n; -1 past m, past N and outside [0, R).
+template <int M>
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ slot,
+                                           const float* __restrict__ gamma, int64_t n, int64_t N,
+                                           int m, int64_t R, int32_t (&at)[M], float (&w)[M]) {
+#pragma unroll
+  for (int t = 0; t < M; ++t) {
+    at[t] = -1;
+    w[t] = 1.f;
+    if (t < m && n < N) {
+      const int32_t s = slot[n * m + t];
+      at[t] = (s >= 0 && s < R) ? s : -1;
+      if (gamma) w[t] = gamma[n * m + t];
+    }
+  }
+}
+
+template <typename T, int V, int M, bool DG>
 __global__ void __launch_bounds__(kThreads)
 spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R,
               const int32_t* __restrict__ slot, const int64_t* __restrict__ offsets,
               const float* __restrict__ gamma, const T* __restrict__ Z, T* __restrict__ Y,
               float* __restrict__ dgamma, int tx_log2) {
+  constexpr int P = points_in_flight(M);
   const int TX = 1 << tx_log2;
   const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2;
   const int rows = kThreads >> tx_log2;
   const int nv = D / V;
-  zero_tail<T, V>(Y, R, D, offsets, K);
   // every lane of a warp takes the same number of turns (shuffles below)
-  for (int64_t n0 = (int64_t)blockIdx.x * rows; n0 < N; n0 += (int64_t)gridDim.x * rows) {
-    const int64_t n = n0 + ty;
-    const bool live = n < N;
-    int32_t at[kMaxM];
-    float w[kMaxM], dot[kMaxM];
+  for (int64_t n0 = (int64_t)blockIdx.x * rows * P; n0 < N; n0 += (int64_t)gridDim.x * rows * P) {
+    int32_t at[P][M];
+    float w[P][M], dot[P][M];
 #pragma unroll
-    for (int t = 0; t < kMaxM; ++t) {
-      at[t] = -1;
-      w[t] = 1.f;
-      dot[t] = 0.f;
-      if (t < m && live) {
-        const int32_t s = slot[n * m + t];
-        at[t] = (s >= 0 && s < R) ? s : -1;
-        if (gamma) w[t] = gamma[n * m + t];
-      }
+    for (int u = 0; u < P; ++u) {
+      load_slots<M>(slot, gamma, n0 + u * rows + ty, N, m, R, at[u], w[u]);
+#pragma unroll
+      for (int t = 0; t < M; ++t) dot[u][t] = 0.f;
     }
-    if (live) {
-      for (int c = tx; c < nv; c += TX) {
-        const Vec<T, V> x = load_vec<T, V>(X + n * D + (int64_t)c * V);
+    for (int c = tx; c < nv; c += TX) {
+      Vec<T, V> x[P], z[P][M];
 #pragma unroll
-        for (int t = 0; t < kMaxM; ++t) {
-          if (at[t] < 0) continue;
-          const int64_t o = (int64_t)at[t] * D + (int64_t)c * V;
+      for (int u = 0; u < P; ++u) {
+        const int64_t n = n0 + u * rows + ty;
+        if (n < N) x[u] = load_vec<T, V>(X + n * D + (int64_t)c * V);
+        if (DG) {
+#pragma unroll
+          for (int t = 0; t < M; ++t)
+            if (at[u][t] >= 0) z[u][t] = load_vec<T, V>(Z + (int64_t)at[u][t] * D + (int64_t)c * V);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < P; ++u) {
+#pragma unroll
+        for (int t = 0; t < M; ++t) {
+          if (at[u][t] < 0) continue;
+          T* y = Y + (int64_t)at[u][t] * D + (int64_t)c * V;
           if (DG) {
-            const Vec<T, V> z = load_vec<T, V>(Z + o);
 #pragma unroll
-            for (int i = 0; i < V; ++i) dot[t] = fmaf(to_f(x.v[i]), to_f(z.v[i]), dot[t]);
+            for (int i = 0; i < V; ++i)
+              dot[u][t] = fmaf(to_f(x[u].v[i]), to_f(z[u][t].v[i]), dot[u][t]);
           }
           if (gamma) {
-            Vec<T, V> y;
+            Vec<T, V> o;
 #pragma unroll
-            for (int i = 0; i < V; ++i) y.v[i] = from_f<T>(to_f(x.v[i]) * w[t]);
-            store_vec<T, V>(Y + o, y);
+            for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(to_f(x[u].v[i]) * w[u][t]);
+            store_vec<T, V>(y, o);
           } else {
-            store_vec<T, V>(Y + o, x);
+            store_vec<T, V>(y, x[u]);
           }
         }
       }
     }
     if (DG) {
 #pragma unroll
-      for (int t = 0; t < kMaxM; ++t) {
-        if (t >= m) break;
-        for (int o = TX >> 1; o > 0; o >>= 1) dot[t] += __shfl_xor_sync(0xffffffffu, dot[t], o);
-        if (live && tx == 0) dgamma[n * m + t] = at[t] >= 0 ? dot[t] : 0.f;
+      for (int u = 0; u < P; ++u) {
+        const int64_t n = n0 + u * rows + ty;
+#pragma unroll
+        for (int t = 0; t < M; ++t) {
+          for (int o = TX >> 1; o > 0; o >>= 1)
+            dot[u][t] += __shfl_xor_sync(0xffffffffu, dot[u][t], o);
+          if (t < m && n < N && tx == 0) dgamma[n * m + t] = at[u][t] >= 0 ? dot[u][t] : 0.f;
+        }
       }
     }
   }
+  zero_tail<T, V>(Y, R, D, offsets, K);
 }
 
-template <typename T, int V>
+template <typename T, int V, int M>
 __global__ void __launch_bounds__(kThreads)
 collect_kernel(const T* __restrict__ Z, int64_t N, int D, int m, int64_t R,
                const int32_t* __restrict__ slot, const float* __restrict__ gamma,
                T* __restrict__ out, int tx_log2) {
+  constexpr int P = points_in_flight(M);
   const int TX = 1 << tx_log2;
   const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2;
   const int rows = kThreads >> tx_log2;
   const int nv = D / V;
-  for (int64_t n = (int64_t)blockIdx.x * rows + ty; n < N; n += (int64_t)gridDim.x * rows) {
-    int32_t at[kMaxM];
-    float w[kMaxM];
+  for (int64_t n0 = (int64_t)blockIdx.x * rows * P; n0 < N; n0 += (int64_t)gridDim.x * rows * P) {
+    int32_t at[P][M];
+    float w[P][M];
 #pragma unroll
-    for (int t = 0; t < kMaxM; ++t) {
-      at[t] = -1;
-      w[t] = 1.f;
-      if (t < m) {
-        const int32_t s = slot[n * m + t];
-        at[t] = (s >= 0 && s < R) ? s : -1;
-        if (gamma) w[t] = gamma[n * m + t];
-      }
-    }
+    for (int u = 0; u < P; ++u)
+      load_slots<M>(slot, gamma, n0 + u * rows + ty, N, m, R, at[u], w[u]);
     for (int c = tx; c < nv; c += TX) {
-      float acc[V];
+      Vec<T, V> z[P][M];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = 0.f;
-      Vec<T, V> z[kMaxM];
+      for (int u = 0; u < P; ++u)
 #pragma unroll
-      for (int t = 0; t < kMaxM; ++t)
-        if (at[t] >= 0) z[t] = load_vec<T, V>(Z + (int64_t)at[t] * D + (int64_t)c * V);
+        for (int t = 0; t < M; ++t)
+          if (at[u][t] >= 0) z[u][t] = load_vec<T, V>(Z + (int64_t)at[u][t] * D + (int64_t)c * V);
 #pragma unroll
-      for (int t = 0; t < kMaxM; ++t)
-        if (at[t] >= 0) {
+      for (int u = 0; u < P; ++u) {
+        const int64_t n = n0 + u * rows + ty;
+        float acc[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(w[t], to_f(z[t].v[i]), acc[i]);
-        }
-      Vec<T, V> y;
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) y.v[i] = from_f<T>(acc[i]);
-      store_vec<T, V>(out + n * D + (int64_t)c * V, y);
+        for (int t = 0; t < M; ++t)
+          if (at[u][t] >= 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u][t], to_f(z[u][t].v[i]), acc[i]);
+          }
+        Vec<T, V> y;
+#pragma unroll
+        for (int i = 0; i < V; ++i) y.v[i] = from_f<T>(acc[i]);
+        if (n < N) store_vec<T, V>(out + n * D + (int64_t)c * V, y);
+      }
     }
   }
 }
@@ -163,34 +192,56 @@ int tx_log2_for(int nv, int most) {
   return l;
 }
 
+// Blocks: one for every `rows * P` points, up to eight a multiprocessor's worth
+// of full blocks; with few points fewer of them share a block, so that the
+// points in flight do not take away from the blocks.
+int64_t grid_for(int64_t N, int rows, int P) {
+  const int64_t g = (N + (int64_t)rows * P - 1) / ((int64_t)rows * P);
+  return g > 152 * 32 ? 152 * 32 : g;
+}
+
+template <typename T, int V, int M>
+void spread_launch_m(const void* X, int64_t N, int D, int m, int K, int64_t R, const int32_t* slot,
+                     const int64_t* offsets, const float* gamma, const void* Z, void* Y,
+                     float* dgamma, cudaStream_t s) {
+  const int l = tx_log2_for(D / V, dgamma ? 5 : 8);
+  int64_t grid = grid_for(N, kThreads >> l, points_in_flight(M));
+  const int64_t tail = (R * (D / V) + kThreads * 8 - 1) / (kThreads * 8);  // if every row were zero
+  if (grid < tail) grid = tail > 152 * 8 ? (grid > 152 * 8 ? grid : 152 * 8) : tail;
+  if (grid < 1) grid = 1;
+  if (dgamma)
+    spread_kernel<T, V, M, true><<<(unsigned)grid, kThreads, 0, s>>>(
+        (const T*)X, N, D, m, K, R, slot, offsets, gamma, (const T*)Z, (T*)Y, dgamma, l);
+  else
+    spread_kernel<T, V, M, false><<<(unsigned)grid, kThreads, 0, s>>>(
+        (const T*)X, N, D, m, K, R, slot, offsets, gamma, (const T*)Z, (T*)Y, dgamma, l);
+}
+
+template <typename T, int V, int M>
+void collect_launch_m(const void* Z, int64_t N, int D, int m, int64_t R, const int32_t* slot,
+                      const float* gamma, void* out, cudaStream_t s) {
+  const int l = tx_log2_for(D / V, 8);
+  const int64_t grid = grid_for(N, kThreads >> l, points_in_flight(M));
+  collect_kernel<T, V, M><<<(unsigned)grid, kThreads, 0, s>>>((const T*)Z, N, D, m, R, slot, gamma,
+                                                              (T*)out, l);
+}
+
+#define GMM_BY_M(m, CALL, ...)          \
+  if ((m) == 1) CALL<T, V, 1>(__VA_ARGS__);      \
+  else if ((m) == 2) CALL<T, V, 2>(__VA_ARGS__); \
+  else if ((m) <= 4) CALL<T, V, 4>(__VA_ARGS__); \
+  else CALL<T, V, 8>(__VA_ARGS__);
+
 template <typename T, int V>
 void spread_launch(const void* X, int64_t N, int D, int m, int K, int64_t R, const int32_t* slot,
                    const int64_t* offsets, const float* gamma, const void* Z, void* Y,
                    float* dgamma, cudaStream_t s) {
-  const int l = tx_log2_for(D / V, dgamma ? 5 : 8);
-  const int rows = kThreads >> l;
-  int64_t grid = (N + rows - 1) / rows;
-  const int64_t tail = (R * (D / V) + kThreads * 8 - 1) / (kThreads * 8);  // if every row were zero
-  if (grid < tail) grid = tail;
-  if (grid > 152 * 8 * 8) grid = 152 * 8 * 8;
-  if (grid < 1) grid = 1;
-  if (dgamma)
-    spread_kernel<T, V, true><<<(unsigned)grid, kThreads, 0, s>>>(
-        (const T*)X, N, D, m, K, R, slot, offsets, gamma, (const T*)Z, (T*)Y, dgamma, l);
-  else
-    spread_kernel<T, V, false><<<(unsigned)grid, kThreads, 0, s>>>(
-        (const T*)X, N, D, m, K, R, slot, offsets, gamma, (const T*)Z, (T*)Y, dgamma, l);
+  GMM_BY_M(m, spread_launch_m, X, N, D, m, K, R, slot, offsets, gamma, Z, Y, dgamma, s)
 }
-
 template <typename T, int V>
 void collect_launch(const void* Z, int64_t N, int D, int m, int64_t R, const int32_t* slot,
                     const float* gamma, void* out, cudaStream_t s) {
-  const int l = tx_log2_for(D / V, 8);
-  const int rows = kThreads >> l;
-  int64_t grid = (N + rows - 1) / rows;
-  if (grid > 152 * 8 * 8) grid = 152 * 8 * 8;
-  collect_kernel<T, V><<<(unsigned)grid, kThreads, 0, s>>>((const T*)Z, N, D, m, R, slot, gamma,
-                                                           (T*)out, l);
+  GMM_BY_M(m, collect_launch_m, Z, N, D, m, R, slot, gamma, out, s)
 }
 
 #define GMM_BY_VEC(T, v, CALL)                      \
