@@ -10,8 +10,12 @@
 // offsets[k] is the number of sorted keys below k.
 // Above that: per block of entries a histogram, a prefix over the blocks for
 // each group, and a scatter whose warps take consecutive segments of the
-// block's entries; __match_any_sync ranks the equal keys of 32 entries.  Only
-// integer counts in fixed places, so the order never varies.
+// block's entries.  The scatter counts its segments again (shared-memory
+// atomics, the order does not matter), turns the counts into each segment's
+// first place, and then walks the segments in order, __match_any_sync ranking
+// the equal keys of 32 entries: fixed places, so the result never varies.
+// Ids are fetched kBatch at a time a lane, since the walk waits on memory
+// more than on anything else.
 // Floor: 4 bytes read and 8 written per entry.
 #include "expert_internal.cuh"
 
@@ -20,7 +24,8 @@ namespace {
 
 constexpr int kTinyE = 1024;
 constexpr int kCountThreads = 256;
-constexpr int kSlice = 12288;          // groups per shared-memory histogram pass
+constexpr int kSlice = 24576;          // groups per shared-memory histogram pass
+constexpr int kBatch = 8;              // entries a lane fetches at once
 constexpr int kMaxWarps = 8;           // scatter warps per block
 constexpr size_t kScatterSmem = 192 * 1024;
 
@@ -68,20 +73,25 @@ route_tiny_kernel(const int32_t* __restrict__ ids, int E, int K, int64_t* __rest
 __global__ void __launch_bounds__(kCountThreads)
 route_count_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int tile,
                    uint32_t* __restrict__ counts) {
-  __shared__ uint32_t hist[kSlice];
+  extern __shared__ uint32_t bins[];
   const int64_t b = blockIdx.x;
   const int64_t e0 = b * tile, e1 = min(E, e0 + tile);
   const int G = K + 1;
   for (int k0 = 0; k0 < G; k0 += kSlice) {
     const int ks = min(kSlice, G - k0);
-    for (int i = threadIdx.x; i < ks; i += kCountThreads) hist[i] = 0u;
+    for (int i = threadIdx.x; i < ks; i += kCountThreads) bins[i] = 0u;
     __syncthreads();
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += kCountThreads) {
-      const int k = group_of(ids[e], K) - k0;
-      if (k >= 0 && k < ks) atomicAdd(&hist[k], 1u);
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += kBatch * kCountThreads) {
+      int k[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        k[j] = e + j * kCountThreads < e1 ? group_of(ids[e + j * kCountThreads], K) - k0 : -1;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (k[j] >= 0 && k[j] < ks) atomicAdd(&bins[k[j]], 1u);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < ks; i += kCountThreads) counts[(size_t)b * G + k0 + i] = hist[i];
+    for (int i = threadIdx.x; i < ks; i += kCountThreads) counts[(size_t)b * G + k0 + i] = bins[i];
     __syncthreads();
   }
 }
@@ -98,6 +108,7 @@ route_scan_blocks_kernel(uint32_t* __restrict__ counts, int64_t nb, int G,
   const int64_t b0 = min(nb, w * per), b1 = min(nb, b0 + per);
   uint32_t sum = 0;
   if (k < G)
+#pragma unroll 8
     for (int64_t b = b0; b < b1; ++b) sum += counts[(size_t)b * G + k];
   part[w][lane] = sum;
   __syncthreads();
@@ -114,10 +125,15 @@ route_scan_blocks_kernel(uint32_t* __restrict__ counts, int64_t nb, int G,
   __syncthreads();
   if (k < G) {
     uint32_t run = part[w][lane];
-    for (int64_t b = b0; b < b1; ++b) {
-      const uint32_t v = counts[(size_t)b * G + k];
-      counts[(size_t)b * G + k] = run;
-      run += v;
+    for (int64_t b = b0; b < b1; b += kBatch) {
+      uint32_t v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) v[j] = b + j < b1 ? counts[(size_t)(b + j) * G + k] : 0u;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (b + j < b1) counts[(size_t)(b + j) * G + k] = run;
+        run += v[j];
+      }
     }
   }
 }
@@ -137,72 +153,86 @@ route_scan_groups_kernel(const uint32_t* __restrict__ tot, int K, int64_t* __res
   }
 }
 
-// hist[w][k]: entries of group k in the segments before warp w's, then the
-// warp's running count.  A segment holds at most 65535 entries.
+// hist[w][k]: entries of group k in the segments before warp w's, then with
+// the warp's running count; two counts to a word (a block holds at most 65535
+// entries).  base[k]: the block's first place of group k, in shared memory
+// where it fits (`base_here`).
 __global__ void __launch_bounds__(kMaxWarps * 32)
-route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg,
+route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg, int base_here,
                      const uint32_t* __restrict__ counts, const int64_t* __restrict__ offsets,
                      int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
-  extern __shared__ uint16_t hist[];
-  const int G = K + 1;
+  extern __shared__ uint32_t words[];
+  const int G = K + 1, H = (G + 1) / 2;  // words of one warp's counts
   const int warps = blockDim.x >> 5;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t b = blockIdx.x;
   const int64_t e0 = (b * warps + w) * (int64_t)seg;
   const int64_t e1 = min(E, e0 + seg);
-  uint16_t* mine = hist + (size_t)w * G;
-  for (int i = threadIdx.x; i < warps * G; i += blockDim.x) hist[i] = 0;
+  const uint32_t* before = counts + (size_t)b * G;
+  uint32_t* base = words + (size_t)warps * H;
+  for (int i = threadIdx.x; i < warps * H; i += blockDim.x) words[i] = 0u;
+  if (base_here)
+    for (int k = threadIdx.x; k < G; k += blockDim.x) base[k] = (uint32_t)offsets[k] + before[k];
   __syncthreads();
   if (warps > 1) {
-    for (int64_t base = e0; base < e1; base += 32) {
-      const int64_t e = base + lane;
-      const int k = e < e1 ? group_of(ids[e], K) : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, k);
-      if (k >= 0 && lane == __ffs(same) - 1) mine[k] += (uint16_t)__popc(same);
-      __syncwarp();
+    for (int64_t e = e0 + lane; e < e1; e += kBatch * 32) {
+      int k[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) k[j] = e + j * 32 < e1 ? group_of(ids[e + j * 32], K) : -1;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (k[j] >= 0) atomicAdd(&words[(size_t)w * H + (k[j] >> 1)], (k[j] & 1) ? 0x10000u : 1u);
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < G; k += blockDim.x) {
-      uint32_t run = 0;
-      for (int i = 0; i < warps; ++i) {
-        const uint32_t v = hist[(size_t)i * G + k];
-        hist[(size_t)i * G + k] = (uint16_t)run;
+    for (int i = threadIdx.x; i < H; i += blockDim.x) {
+      uint32_t run = 0;  // both halves at once: neither sum reaches 65536
+      for (int x = 0; x < warps; ++x) {
+        const uint32_t v = words[(size_t)x * H + i];
+        words[(size_t)x * H + i] = run;
         run += v;
       }
     }
     __syncthreads();
   }
-  for (int64_t base = e0; base < e1; base += 32) {
-    const int64_t e = base + lane;
-    const int k = e < e1 ? group_of(ids[e], K) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, k);
-    uint32_t at = 0;
-    if (k >= 0) {
-      at = mine[k];
-      const int64_t pos =
-          offsets[k] + counts[(size_t)b * G + k] + at + __popc(same & ((1u << lane) - 1u));
-      slot[e] = k < K ? (int32_t)pos : -1;
-      entry[pos] = k < K ? (int32_t)e : -1;
+  uint16_t* mine = reinterpret_cast<uint16_t*>(words + (size_t)w * H);
+  for (int64_t e = e0 + lane; e - lane < e1; e += kBatch * 32) {
+    int k[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) k[j] = e + j * 32 < e1 ? group_of(ids[e + j * 32], K) : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const unsigned same = __match_any_sync(0xffffffffu, k[j]);
+      uint32_t at = 0;
+      if (k[j] >= 0) {
+        at = mine[k[j]];
+        const uint32_t first = base_here ? base[k[j]] : (uint32_t)offsets[k[j]] + before[k[j]];
+        const uint32_t pos = first + at + __popc(same & ((1u << lane) - 1u));
+        slot[e + j * 32] = k[j] < K ? (int32_t)pos : -1;
+        entry[pos] = k[j] < K ? (int32_t)(e + j * 32) : -1;
+      }
+      __syncwarp();
+      if (k[j] >= 0 && lane == __ffs(same) - 1) mine[k[j]] = (uint16_t)(at + __popc(same));
+      __syncwarp();
     }
-    __syncwarp();
-    if (k >= 0 && lane == __ffs(same) - 1) mine[k] = (uint16_t)(at + __popc(same));
-    __syncwarp();
   }
 }
 
 struct RouteLayout {
-  int warps, seg, tile;
+  int warps, seg, tile, base_here;
   int64_t nb;
-  size_t off_counts, off_tot, bytes;
+  size_t smem, off_counts, off_tot, bytes;
   static RouteLayout make(int64_t E, int K) {
     RouteLayout L;
-    const size_t per_warp = sizeof(uint16_t) * (size_t)(K + 1);
+    const size_t per_warp = sizeof(uint32_t) * (size_t)((K + 2) / 2);
+    const size_t bases = sizeof(uint32_t) * (size_t)(K + 1);
     L.warps = kMaxWarps;
-    while (L.warps > 1 && per_warp * L.warps > kScatterSmem) L.warps >>= 1;
-    // enough blocks for two a multiprocessor, up to 4096 entries a warp (a
+    while (L.warps > 1 && per_warp * L.warps + bases > kScatterSmem) L.warps >>= 1;
+    L.base_here = per_warp * L.warps + bases <= kScatterSmem;
+    L.smem = per_warp * L.warps + (L.base_here ? bases : 0);
+    // enough blocks for two a multiprocessor, up to 2048 entries a warp (a
     // block's K counters are written, scanned and read once more)
     int64_t seg = (E + (int64_t)L.warps * 304 - 1) / ((int64_t)L.warps * 304);
-    seg = seg < 256 ? 256 : seg > 4096 ? 4096 : (seg + 31) / 32 * 32;
+    seg = seg < 256 ? 256 : seg > 2048 ? 2048 : (seg + 31) / 32 * 32;
     L.seg = (int)seg;
     L.tile = L.warps * L.seg;
     L.nb = (E + L.tile - 1) / L.tile;
@@ -242,26 +272,30 @@ gmm_status gmm_route(const int32_t* ids, int64_t N, int m, int K, int64_t* offse
     ProfScope p("route_tiny_kernel", s);
     // one thread an entry, and enough of them for the K + 1 offsets
     int threads = (int)((E + 31) / 32 * 32);
-    if (threads < 256) threads = 256;
+    const int spread = (K + 1 + 31) / 32 * 32;
+    if (threads < spread) threads = spread < kTinyE ? spread : kTinyE;
     route_tiny_kernel<<<1, threads, 0, s>>>(ids, (int)E, K, offsets, entry, slot);
     return launched();
   }
   uint32_t* counts = at<uint32_t>(ws, L.off_counts);
   uint32_t* tot = at<uint32_t>(ws, L.off_tot);
-  const size_t smem = sizeof(uint16_t) * (size_t)(K + 1) * L.warps;
+  const int G = K + 1;
+  const size_t bins = sizeof(uint32_t) * (size_t)(G < kSlice ? G : kSlice);
   if (cudaFuncSetAttribute(route_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kScatterSmem) != cudaSuccess)
+                           (int)kScatterSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(route_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(sizeof(uint32_t) * kSlice)) != cudaSuccess)
     return GMM_ERR_CUDA;
   ProfScope p("route_kernels", s, 4);
   gmm_status r;
-  route_count_kernel<<<(unsigned)L.nb, kCountThreads, 0, s>>>(ids, E, K, L.tile, counts);
+  route_count_kernel<<<(unsigned)L.nb, kCountThreads, bins, s>>>(ids, E, K, L.tile, counts);
   if ((r = launched()) != GMM_OK) return r;
   route_scan_blocks_kernel<<<(K + 1 + 31) / 32, 1024, 0, s>>>(counts, L.nb, K + 1, tot);
   if ((r = launched()) != GMM_OK) return r;
   route_scan_groups_kernel<<<1, 1024, 0, s>>>(tot, K, offsets);
   if ((r = launched()) != GMM_OK) return r;
-  route_scatter_kernel<<<(unsigned)L.nb, L.warps * 32, smem, s>>>(ids, E, K, L.seg, counts,
-                                                                  offsets, entry, slot);
+  route_scatter_kernel<<<(unsigned)L.nb, L.warps * 32, L.smem, s>>>(
+      ids, E, K, L.seg, L.base_here, counts, offsets, entry, slot);
   return launched();
 }
 
