@@ -23,6 +23,7 @@
 //     relative error of the update below 2^-21, under the rounding of the
 //     parameter.
 #include <cmath>
+#include <type_traits>
 
 #include "expert_internal.cuh"
 
@@ -31,7 +32,7 @@ namespace {
 
 constexpr int kBlockElems = 256;   // elements of one scale, and of one warp's turn
 constexpr int kWarps = 8;
-constexpr int kChunk = kWarps * kBlockElems;  // elements of one block's turn
+constexpr int kMaxTurns = 16;       // consecutive turns of a warp in one tensor
 constexpr float kTiny = 1e-30f;    // blocks below it are held as zeros
 
 struct AdamwEntry {
@@ -43,7 +44,7 @@ struct AdamwEntry {
   float* ms;
   float* vs;
   int64_t n;
-  int32_t first;     // the tensor's first chunk in this launch
+  int32_t first;     // the tensor's first chunk in this launch (kWarps x turns of 256 elements)
   int8_t pt, gt;     // gmm_dtype
   int8_t wide;       // every array aligned for eight-element accesses
   int8_t pad;
@@ -51,7 +52,8 @@ struct AdamwEntry {
 
 struct AdamwConst {
   float gs, b1, c1, b2, c2, root, eps, decay, rate;
-  int count, chunks;
+  int count, chunks, turns;
+  int eps_covers;    // eps is far above the root of a subnormal
   const int32_t* skip;
 };
 
@@ -61,220 +63,35 @@ struct AdamwTable {
   AdamwEntry e[COUNT];
 };
 
-__device__ __forceinline__ void load8(const void* base, int type, int64_t i, float* x) {
-  if (type == GMM_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (type == GMM_F16) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[j]);
-        x[2 * j] = __half2float(__low2half(h));
-        x[2 * j + 1] = __half2float(__high2half(h));
-      } else {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void store8(void* base, int type, int64_t i, const float* x) {
-  if (type == GMM_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (type == GMM_F16) {
-        const __half2 h = __halves2half2(__float2half_rn(x[2 * j]), __float2half_rn(x[2 * j + 1]));
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-__device__ __forceinline__ float load1(const void* base, int type, int64_t i) {
-  if (type == GMM_F32) return static_cast<const float*>(base)[i];
-  if (type == GMM_F16) return __half2float(static_cast<const __half*>(base)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-}
-
-__device__ __forceinline__ void store1(void* base, int type, int64_t i, float x) {
-  if (type == GMM_F32) static_cast<float*>(base)[i] = x;
-  else if (type == GMM_F16) static_cast<__half*>(base)[i] = __float2half_rn(x);
-  else static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(x);
-}
-
-// `cnt` (0..8) elements from i; the rest read as zeros.
-__device__ __forceinline__ void load_n(const void* base, int type, int64_t i, int cnt, bool wide,
-                                       float* x) {
-  if (wide && cnt == 8) return load8(base, type, i, x);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = j < cnt ? load1(base, type, i + j) : 0.f;
-}
-__device__ __forceinline__ void store_n(void* base, int type, int64_t i, int cnt, bool wide,
-                                        const float* x) {
-  if (wide && cnt == 8) return store8(base, type, i, x);
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < cnt) store1(base, type, i + j, x[j]);
-}
-
-// Eight 8-bit codes as two words.
-__device__ __forceinline__ uint2 load_codes(const void* base, int64_t i, int cnt, bool wide) {
-  const uint8_t* p = static_cast<const uint8_t*>(base) + i;
-  if (wide && cnt == 8) return *reinterpret_cast<const uint2*>(p);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < cnt) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-  return make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void store_codes(void* base, int64_t i, int cnt, bool wide, uint2 c) {
-  uint8_t* p = static_cast<uint8_t*>(base) + i;
-  if (wide && cnt == 8) {
-    *reinterpret_cast<uint2*>(p) = c;
-    return;
-  }
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < cnt) p[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
-}
-
-// Byte j of two words as a float (unsigned, or two's complement).
-template <bool SIGNED>
-__device__ __forceinline__ float code_float(uint2 c, int j) {
-  const uint32_t w = (j < 4 ? c.x : c.y) ^ (SIGNED ? 0x80808080u : 0u);
-  // bits 0x4B0000cc are 2^23 + cc
-  const float f = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (j & 3)));
-  return f - (SIGNED ? 8388736.f : 8388608.f);
-}
-
-// c|c| S
-__device__ __forceinline__ void decode_m(uint2 c, float scale, float* x) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = code_float<true>(c, j);
-    x[j] = __fmul_rn(f * fabsf(f), scale);
-  }
-}
-__device__ __forceinline__ void decode_root(uint2 c, float scale, float* x) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = code_float<false>(c, j);
-    x[j] = __fmul_rn(f * f, scale);
-  }
-}
-
-__device__ __forceinline__ float sqrt_near(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_near(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// 255 x (2^-22 for each root and the product between them) is 2e-4 at most.
-constexpr float kNear = 0.5f - 2e-4f;
-constexpr float kMagic = 12582912.f;  // 1.5 2^23: x + kMagic holds rint(x) in its low bits
-
-// Scale of a block whose largest magnitude is `big`, and its inverse.
-template <int TOP>
-__device__ __forceinline__ float2 scale_of(float big) {
-  if (!(big >= kTiny)) return make_float2(0.f, 0.f);
-  return make_float2(__fmul_rn(big, (float)(1.0 / (TOP * TOP))),
-                     __fmul_rn(__fdiv_rn(1.f, big), (float)(TOP * TOP)));
-}
-
-// Codes of eight m.
-__device__ __forceinline__ uint2 encode_m(const float* m, float inv) {
-  float t[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = __fmul_rn(fabsf(m[j]), inv);
-    float s = sqrt_near(x);
-    t[j] = s + kMagic;
-    if (fabsf(s - (t[j] - kMagic)) > kNear) t[j] = __fsqrt_rn(x) + kMagic;
-  }
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t u = __float_as_uint(t[4 * h + j]);
-      b[j] = m[4 * h + j] < 0.f ? 0u - u : u;  // the low byte of -c
-    }
-    w[h] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-  }
-  return make_uint2(w[0], w[1]);
-}
-
-// Codes of eight sqrt(v); root is near, v exact.
-__device__ __forceinline__ uint2 encode_root(const float* v, const float* root, float inv) {
-  float t[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float s = sqrt_near(root[j] * inv);
-    t[j] = s + kMagic;
-    const bool tiny = v[j] < 1e-36f && v[j] > 0.f;  // the near root of a subnormal is 0
-    if (fabsf(s - (t[j] - kMagic)) > kNear || tiny)
-      t[j] = __fsqrt_rn(__fmul_rn(__fsqrt_rn(v[j]), inv)) + kMagic;
-    if (v[j] > 0.f) t[j] = fmaxf(t[j], 1.f + kMagic);
-  }
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w[h] = __byte_perm(__byte_perm(__float_as_uint(t[4 * h]), __float_as_uint(t[4 * h + 1]), 0x0040),
-                       __byte_perm(__float_as_uint(t[4 * h + 2]), __float_as_uint(t[4 * h + 3]), 0x0040),
-                       0x5410);
-  return make_uint2(w[0], w[1]);
-}
-
-// Largest of the warp's non-negative values (their bits order them).
-__device__ __forceinline__ float warp_max_pos(float v) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-}
-
-// The tensor of a chunk: the last entry whose first chunk is not after it.
-template <int COUNT>
-__device__ __forceinline__ int tensor_of(const AdamwTable<COUNT>& t, int chunk) {
-  int lo = 0, hi = t.k.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].first <= chunk) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+// The eight elements a lane has of its warp's 256: consecutive ones where the
+// moments are bytes, two fours where they are floats, so that a warp's
+// accesses are whole lines either way.
+template <int BITS>
+__device__ __forceinline__ int lane_elem(int j) {
+  const int lane = threadIdx.x & 31;
+  return BITS == 8 ? lane * 8 + j : (j >> 2) * 128 + lane * 4 + (j & 3);
 }
 
 // Eight elements as they lie in memory: 4 words of 16-bit ones, 8 of floats.
 template <bool HALF> struct Raw { uint32_t w[HALF ? 4 : 8]; };
 
-template <bool HALF>
-__device__ __forceinline__ void fetch(Raw<HALF>& r, const void* base, int64_t i, int cnt, bool wide) {
-  if (wide && cnt == 8) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + i * (HALF ? 2 : 4));
-    const uint4 a = p[0];
-    r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
-    if constexpr (!HALF) {
-      const uint4 b = p[1];
+// `i`: first element of the warp's 256; `left` of them are the tensor's, and
+// where all are (`full`, which asks for aligned arrays) the accesses are wide.
+template <int BITS, bool HALF>
+__device__ __forceinline__ void fetch(Raw<HALF>& r, const void* base, int64_t i, int left, bool full) {
+  const int lane = threadIdx.x & 31;
+  if (full) {
+    if constexpr (HALF && BITS == 8) {
+      const uint4 a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i)[lane];
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+    } else if constexpr (HALF) {
+      const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+      const uint2 a = p[lane], b = p[lane + 32];
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = b.x; r.w[3] = b.y;
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
+      const uint4 a = p[BITS == 8 ? 2 * lane : lane], b = p[BITS == 8 ? 2 * lane + 1 : lane + 32];
+      r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
       r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
     }
     return;
@@ -282,12 +99,43 @@ __device__ __forceinline__ void fetch(Raw<HALF>& r, const void* base, int64_t i,
 #pragma unroll
   for (int j = 0; j < (HALF ? 4 : 8); ++j) r.w[j] = 0u;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < cnt) {
-      if (HALF) r.w[j / 2] |= (uint32_t)static_cast<const uint16_t*>(base)[i + j] << (16 * (j & 1));
-      else r.w[j] = static_cast<const uint32_t*>(base)[i + j];
+  for (int j = 0; j < 8; ++j) {
+    const int x = lane_elem<BITS>(j);
+    if (x < left) {
+      if (HALF) r.w[j / 2] |= (uint32_t)static_cast<const uint16_t*>(base)[i + x] << (16 * (j & 1));
+      else r.w[j] = static_cast<const uint32_t*>(base)[i + x];
     }
+  }
 }
+
+template <int BITS, bool HALF>
+__device__ __forceinline__ void put(const Raw<HALF>& r, void* base, int64_t i, int left, bool full) {
+  const int lane = threadIdx.x & 31;
+  if (full) {
+    if constexpr (HALF && BITS == 8) {
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i)[lane] =
+          make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else if constexpr (HALF) {
+      uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i);
+      p[lane] = make_uint2(r.w[0], r.w[1]);
+      p[lane + 32] = make_uint2(r.w[2], r.w[3]);
+    } else {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<float*>(base) + i);
+      p[BITS == 8 ? 2 * lane : lane] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+      p[BITS == 8 ? 2 * lane + 1 : lane + 32] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int x = lane_elem<BITS>(j);
+    if (x < left) {
+      if (HALF) static_cast<uint16_t*>(base)[i + x] = (uint16_t)(r.w[j / 2] >> (16 * (j & 1)));
+      else static_cast<uint32_t*>(base)[i + x] = r.w[j];
+    }
+  }
+}
+
 template <bool HALF>
 __device__ __forceinline__ void widen(const Raw<HALF>& r, int type, float* x) {
   if constexpr (!HALF) {
@@ -309,172 +157,547 @@ __device__ __forceinline__ void widen(const Raw<HALF>& r, int type, float* x) {
   }
 }
 
-// Where a warp is in the list: its tensor, and its eight elements there.
-struct Place {
-  int e;
-  int64_t block, i;
-  int cnt;   // 0: nothing for this lane; < 0: nothing for this warp
-};
+template <int BITS>
+__device__ __forceinline__ void put_float(const float* x, float* base, int64_t i, int left, bool full) {
+  Raw<false> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.w[j] = __float_as_uint(x[j]);
+  put<BITS, false>(r, base, i, left, full);
+}
+template <int BITS>
+__device__ __forceinline__ void put_param(const float* x, int type, void* base, int64_t i, int left,
+                                          bool full) {
+  if (type == GMM_F32) return put_float<BITS>(x, static_cast<float*>(base), i, left, full);
+  Raw<true> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (type == GMM_F16) {
+      const __half2 h = __halves2half2(__float2half_rn(x[2 * j]), __float2half_rn(x[2 * j + 1]));
+      r.w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+      r.w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  put<BITS, true>(r, base, i, left, full);
+}
 
+// Eight 8-bit codes as two words.
+__device__ __forceinline__ uint2 fetch_codes(const void* base, int64_t i, int left, bool full) {
+  const uint8_t* p = static_cast<const uint8_t*>(base) + i;
+  const int x = lane_elem<8>(0);
+  if (full) return reinterpret_cast<const uint2*>(p)[threadIdx.x & 31];
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (x + j < left) w[j >> 2] |= (uint32_t)p[x + j] << (8 * (j & 3));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void put_codes(void* base, int64_t i, int left, bool full, uint2 c) {
+  uint8_t* p = static_cast<uint8_t*>(base) + i;
+  const int x = lane_elem<8>(0);
+  if (full) {
+    reinterpret_cast<uint2*>(p)[threadIdx.x & 31] = c;
+    return;
+  }
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (x + j < left) p[x + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// The sum of two products, each rounded by itself: packed products and packed
+// sums end up as one fused operation, scalar sums do not.
+__device__ __forceinline__ float2 sum_rn(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+__device__ __forceinline__ float with_sign(float x, float of) {  // x >= 0
+  return __uint_as_float(__float_as_uint(x) | (__float_as_uint(of) & 0x80000000u));
+}
+
+// Byte J of a word as the float 2^23 + byte.
+template <int J>
+__device__ __forceinline__ float code_bits(uint32_t w) {
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | J));
+}
+// Four codes as floats (unsigned, or two's complement).
+template <bool SIGNED>
+__device__ __forceinline__ void code_floats(uint32_t w, float2* f) {
+  if (SIGNED) w ^= 0x80808080u;
+  const float2 off = both(SIGNED ? -8388736.f : -8388608.f);
+  f[0] = add2(make_float2(code_bits<0>(w), code_bits<1>(w)), off);
+  f[1] = add2(make_float2(code_bits<2>(w), code_bits<3>(w)), off);
+}
+
+// c|c| S
+__device__ __forceinline__ void decode_m(uint2 c, float scale, float2* x) {
+  code_floats<true>(c.x, x);
+  code_floats<true>(c.y, x + 2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    x[j] = mul2(make_float2(x[j].x * fabsf(x[j].x), x[j].y * fabsf(x[j].y)), both(scale));
+}
+// c^2 S
+__device__ __forceinline__ void decode_root(uint2 c, float scale, float2* x) {
+  code_floats<false>(c.x, x);
+  code_floats<false>(c.y, x + 2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], x[j]), both(scale));
+}
+
+__device__ __forceinline__ float sqrt_near(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_near(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A near root of value / S is off by less than 2^-22 of itself (twice 2^-23
+// for the two roots, half of each product's 2^-24): 6.1e-5 at 255.
+constexpr float kNear = 0.5f - 1.5e-4f;
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: x + kMagic holds rint(x) in its low bits
+
+// Scale of a block whose largest magnitude is `big`, and its inverse.
+template <int TOP>
+__device__ __forceinline__ float2 scale_of(float big) {
+  if (!(big >= kTiny)) return make_float2(0.f, 0.f);
+  return make_float2(__fmul_rn(big, (float)(1.0 / (TOP * TOP))),
+                     __fmul_rn(__fdiv_rn(1.f, big), (float)(TOP * TOP)));
+}
+
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+  const uint32_t x = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+  const uint32_t y = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+  return __byte_perm(x, y, 0x5410);
+}
+// Codes to be: t + kMagic of eight values; how far the farthest is from its
+// whole number.
+__device__ __forceinline__ float round_all(float2* t) {
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 s = t[j];
+    t[j] = add2(s, both(kMagic));
+    const float2 d = sub2(s, add2(t[j], both(-kMagic)));
+    far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+  }
+  return far;
+}
+
+// Codes of eight m.
+__device__ __forceinline__ uint2 encode_m(const float2* m, float inv) {
+  float2 t[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = mul2(m[j], both(inv));
+    t[j].x = with_sign(sqrt_near(fabsf(x.x)), m[j].x);
+    t[j].y = with_sign(sqrt_near(fabsf(x.y)), m[j].y);
+  }
+  if (round_all(t) > kNear) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = mul2(m[j], both(inv));
+      t[j].x = with_sign(__fsqrt_rn(fabsf(x.x)), m[j].x) + kMagic;
+      t[j].y = with_sign(__fsqrt_rn(fabsf(x.y)), m[j].y) + kMagic;
+    }
+  }
+  return make_uint2(low_bytes(t[0], t[1]), low_bytes(t[2], t[3]));
+}
+
+// Whether a byte of w is zero.
+__device__ __forceinline__ bool zero_byte(uint32_t w) {
+  return ((w - 0x01010101u) & ~w & 0x80808080u) != 0u;
+}
+// Byte j of w, where it is zero and v is not, becomes 1.
+__device__ __forceinline__ uint32_t above_zero(uint32_t w, float2 a, float2 b) {
+  const float v[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (v[j] > 0.f && !((w >> (8 * j)) & 0xffu)) w |= 1u << (8 * j);
+  return w;
+}
+
+// Codes of eight sqrt(v); root is near, v exact.  The near root of a
+// subnormal is 0, and so is its code unless S is as small; there, and near
+// halfway, the root is taken again.
+__device__ __forceinline__ uint2 encode_root(const float2* v, const float2* root, float inv) {
+  float2 t[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = mul2(root[j], both(inv));
+    t[j].x = sqrt_near(x.x);
+    t[j].y = sqrt_near(x.y);
+  }
+  if (round_all(t) > kNear || inv > 1e18f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      t[j].x = __fsqrt_rn(__fmul_rn(__fsqrt_rn(v[j].x), inv)) + kMagic;
+      t[j].y = __fsqrt_rn(__fmul_rn(__fsqrt_rn(v[j].y), inv)) + kMagic;
+    }
+  }
+  uint32_t a = low_bytes(t[0], t[1]), b = low_bytes(t[2], t[3]);
+  if (zero_byte(a)) a = above_zero(a, v[0], v[1]);
+  if (zero_byte(b)) b = above_zero(b, v[2], v[3]);
+  return make_uint2(a, b);
+}
+
+// Largest of the warp's non-negative values (their bits order them).
+__device__ __forceinline__ float warp_max_pos(float v) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// The tensor of a chunk: the last entry whose first chunk is not after it.
 template <int COUNT>
-__device__ __forceinline__ Place place_of(const AdamwTable<COUNT>& t, int e, int chunk) {
-  while (e + 1 < t.k.count && t.e[e + 1].first <= chunk) ++e;
+__device__ __forceinline__ int tensor_of(const AdamwTable<COUNT>& t, int chunk) {
+  int lo = 0, hi = t.k.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.e[mid].first <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Where a warp is in a tensor: 256 elements, `left` of them the tensor's.
+struct Place {
+  int left;
+  bool full;
+  int64_t block;
+};
+__device__ __forceinline__ Place place_of(const AdamwEntry& e, int64_t block) {
   Place p;
-  p.e = e;
-  p.block = (int64_t)(chunk - t.e[e].first) * kWarps + (threadIdx.x >> 5);
-  p.i = p.block * kBlockElems + (threadIdx.x & 31) * 8;
-  const int64_t n = t.e[e].n;
-  p.cnt = p.block * kBlockElems >= n ? -1 : (int)max((int64_t)0, min((int64_t)8, n - p.i));
+  p.block = block;
+  const int64_t left = e.n - block * kBlockElems;
+  p.left = left > kBlockElems ? kBlockElems : left < 0 ? 0 : (int)left;
+  p.full = e.wide && p.left == kBlockElems;
   return p;
 }
 
 template <int BITS, bool PH, bool GH> struct Operands {
   Raw<PH> p;
   Raw<GH> g;
-  uint32_t m[BITS == 32 ? 8 : 2], v[BITS == 32 ? 8 : 2];
+  Raw<false> m, v;   // 8 bits: two words of codes each
   float ms, vs;
 };
 
 template <int BITS, bool PH, bool GH>
 __device__ __forceinline__ void fetch_all(Operands<BITS, PH, GH>& o, const AdamwEntry& e, const Place& q) {
-  if (q.cnt < 0) return;
-  const bool wide = e.wide;
-  fetch<GH>(o.g, e.g, q.i, q.cnt, wide);
-  fetch<PH>(o.p, e.master ? (const void*)e.master : e.p, q.i, q.cnt, wide);
+  const int64_t i = q.block * kBlockElems;
+  fetch<BITS, GH>(o.g, e.g, i, q.left, q.full);
+  fetch<BITS, PH>(o.p, e.master ? (const void*)e.master : e.p, i, q.left, q.full);
   if constexpr (BITS == 32) {
-    Raw<false> r;
-    fetch<false>(r, e.m, q.i, q.cnt, wide);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o.m[j] = r.w[j];
-    fetch<false>(r, e.v, q.i, q.cnt, wide);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o.v[j] = r.w[j];
+    fetch<BITS, false>(o.m, e.m, i, q.left, q.full);
+    fetch<BITS, false>(o.v, e.v, i, q.left, q.full);
   } else {
-    const uint2 mc = load_codes(e.m, q.i, q.cnt, wide), vc = load_codes(e.v, q.i, q.cnt, wide);
-    o.m[0] = mc.x; o.m[1] = mc.y;
-    o.v[0] = vc.x; o.v[1] = vc.y;
+    const uint2 mc = fetch_codes(e.m, i, q.left, q.full), vc = fetch_codes(e.v, i, q.left, q.full);
+    o.m.w[0] = mc.x; o.m.w[1] = mc.y;
+    o.v.w[0] = vc.x; o.v.w[1] = vc.y;
     o.ms = e.ms[q.block];
     o.vs = e.vs[q.block];
   }
 }
 
-template <int BITS, bool PH, bool GH>
+// fp32 moments: the documented operations, one by one.
+template <bool PH, bool GH>
 __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry& e, const Place& q,
-                                           const Operands<BITS, PH, GH>& o) {
-  const bool wide = e.wide;
-  float g[8], p[8], m[8], v[8], root[8];
+                                           const Operands<32, PH, GH>& o) {
+  float g[8], p[8], m[8], v[8];
   widen<GH>(o.g, e.gt, g);
   widen<PH>(o.p, e.pt, p);
-  if constexpr (BITS == 32) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = __uint_as_float(o.m[j]);
-      v[j] = __uint_as_float(o.v[j]);
-    }
-  } else {
-    decode_m(make_uint2(o.m[0], o.m[1]), o.ms, m);
-    decode_root(make_uint2(o.v[0], o.v[1]), o.vs, root);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(root[j], root[j]);
-  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float gj = __fmul_rn(g[j], k.gs);
-    m[j] = __fadd_rn(__fmul_rn(m[j], k.b1), __fmul_rn(gj, k.c1));
-    v[j] = __fadd_rn(__fmul_rn(v[j], k.b2), __fmul_rn(__fmul_rn(gj, gj), k.c2));
-    if constexpr (BITS == 32) {
-      root[j] = __fsqrt_rn(v[j]);
-      const float den = __fadd_rn(__fmul_rn(root[j], k.root), k.eps);
-      p[j] = __fsub_rn(__fmul_rn(p[j], k.decay), __fdiv_rn(__fmul_rn(m[j], k.rate), den));
-    } else {
-      root[j] = sqrt_near(v[j]);
-      const float den = fmaf(root[j], k.root, k.eps);
-      float r = rcp_near(den);
-      // outside the reciprocal's range, or the near root's: the exact form
-      if (!(den > 1e-18f && den < 1e37f))
-        r = __fdiv_rn(1.f, __fadd_rn(__fmul_rn(__fsqrt_rn(v[j]), k.root), k.eps));
-      p[j] = __fsub_rn(__fmul_rn(p[j], k.decay), __fmul_rn(__fmul_rn(m[j], k.rate), r));
+    m[j] = __fadd_rn(__fmul_rn(__uint_as_float(o.m.w[j]), k.b1), __fmul_rn(gj, k.c1));
+    v[j] = __fadd_rn(__fmul_rn(__uint_as_float(o.v.w[j]), k.b2), __fmul_rn(__fmul_rn(gj, gj), k.c2));
+    const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v[j]), k.root), k.eps);
+    p[j] = __fsub_rn(__fmul_rn(p[j], k.decay), __fdiv_rn(__fmul_rn(m[j], k.rate), den));
+  }
+  const int64_t i = q.block * kBlockElems;
+  if (e.master) put_float<32>(p, e.master, i, q.left, q.full);
+  put_param<32>(p, e.pt, e.p, i, q.left, q.full);
+  put_float<32>(m, static_cast<float*>(e.m), i, q.left, q.full);
+  put_float<32>(v, static_cast<float*>(e.v), i, q.left, q.full);
+}
+
+// 8-bit moments: pairs of elements, each half rounded as one by one.
+template <bool PH, bool GH>
+__device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry& e, const Place& q,
+                                           const Operands<8, PH, GH>& o) {
+  float g[8], p[8];
+  widen<GH>(o.g, e.gt, g);
+  widen<PH>(o.p, e.pt, p);
+  float2 m[4], v[4], root[4];
+  decode_m(make_uint2(o.m.w[0], o.m.w[1]), o.ms, m);
+  decode_root(make_uint2(o.v.w[0], o.v.w[1]), o.vs, root);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 gj = mul2(make_float2(g[2 * j], g[2 * j + 1]), both(k.gs));
+    m[j] = sum_rn(mul2(m[j], both(k.b1)), mul2(gj, both(k.c1)));
+    v[j] = sum_rn(mul2(mul2(root[j], root[j]), both(k.b2)), mul2(mul2(gj, gj), both(k.c2)));
+    root[j] = make_float2(sqrt_near(v[j].x), sqrt_near(v[j].y));
+    const float2 den = fma2(root[j], both(k.root), both(k.eps));
+    float2 r = make_float2(rcp_near(den.x), rcp_near(den.y));
+    if (!k.eps_covers) {  // a subnormal v's root, flushed to 0 above, may count
+      r.x = __fdiv_rn(1.f, fmaf(__fsqrt_rn(v[j].x), k.root, k.eps));
+      r.y = __fdiv_rn(1.f, fmaf(__fsqrt_rn(v[j].y), k.root, k.eps));
+    }
+    const float2 pj = mul2(make_float2(p[2 * j], p[2 * j + 1]), both(k.decay));
+    const float2 up = mul2(mul2(m[j], both(k.rate)), r);
+    p[2 * j] = __fsub_rn(pj.x, up.x);
+    p[2 * j + 1] = __fsub_rn(pj.y, up.y);
+  }
+  const int64_t i = q.block * kBlockElems;
+  if (e.master) put_float<8>(p, e.master, i, q.left, q.full);
+  put_param<8>(p, e.pt, e.p, i, q.left, q.full);
+  if (!q.full) {  // nothing past the end
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (lane_elem<8>(2 * j) >= q.left) m[j].x = v[j].x = root[j].x = 0.f;
+      if (lane_elem<8>(2 * j + 1) >= q.left) m[j].y = v[j].y = root[j].y = 0.f;
     }
   }
-  if (e.master) store_n(e.master, GMM_F32, q.i, q.cnt, wide, p);
-  store_n(e.p, e.pt, q.i, q.cnt, wide, p);
-  if constexpr (BITS == 32) {
-    store_n(e.m, GMM_F32, q.i, q.cnt, wide, m);
-    store_n(e.v, GMM_F32, q.i, q.cnt, wide, v);
-  } else {
-    if (q.cnt < 8) {  // past the end
+  float mb = 0.f, vb = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j >= q.cnt) m[j] = v[j] = root[j] = 0.f;
-    }
-    float mb = 0.f, vb = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mb = fmaxf(mb, fabsf(m[j]));
-      vb = fmaxf(vb, v[j]);
-    }
-    const float2 ms = scale_of<127>(warp_max_pos(mb));
-    const float2 vs = scale_of<255>(__fsqrt_rn(warp_max_pos(vb)));
-    store_codes(e.m, q.i, q.cnt, wide, encode_m(m, ms.y));
-    store_codes(e.v, q.i, q.cnt, wide, encode_root(v, root, vs.y));
-    if ((threadIdx.x & 31) == 0) {
-      e.ms[q.block] = ms.x;
-      e.vs[q.block] = vs.x;
-    }
+  for (int j = 0; j < 4; ++j) {
+    mb = fmaxf(mb, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
+    vb = fmaxf(vb, fmaxf(v[j].x, v[j].y));
   }
+  const float2 ms = scale_of<127>(warp_max_pos(mb));
+  const float2 vs = scale_of<255>(__fsqrt_rn(warp_max_pos(vb)));
+  put_codes(e.m, i, q.left, q.full, encode_m(m, ms.y));
+  put_codes(e.v, i, q.left, q.full, encode_root(v, root, vs.y));
+  if ((threadIdx.x & 31) == 0) {
+    e.ms[q.block] = ms.x;
+    e.vs[q.block] = vs.x;
+  }
+}
+
+// The odd blocks: a tensor's end, or arrays that are not aligned.
+template <int BITS, bool PH, bool GH>
+__device__ __noinline__ void odd_block(const AdamwConst& k, const AdamwEntry& e, int64_t block) {
+  const Place q = place_of(e, block);
+  if (q.left == 0) return;
+  Operands<BITS, PH, GH> o;
+  fetch_all(o, e, q);
+  step_block(k, e, q, o);
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A lane's operands of a full block in 8 bits, on their way through shared
+// memory: kAhead turns are in flight without holding registers.  A lane reads
+// back only what it copied, so no barrier is needed.
+constexpr int kAhead = 3;
+template <bool PH, bool GH>
+__host__ __device__ constexpr int stage_bytes() { return (GH ? 512 : 1024) + (PH ? 512 : 1024) + 512; }
+template <bool PH, bool GH>
+constexpr size_t ring_bytes() { return (size_t)kWarps * (kAhead + 1) * stage_bytes<PH, GH>(); }
+
+template <bool PH, bool GH>
+__device__ __forceinline__ void stage_copy(uint8_t* st, const AdamwEntry& e, int64_t i) {
+  const int lane = threadIdx.x & 31;
+  const char* g = static_cast<const char*>(e.g) + i * (GH ? 2 : 4);
+  const char* p = (e.master ? reinterpret_cast<const char*>(e.master) : static_cast<const char*>(e.p)) + i * (PH ? 2 : 4);
+#pragma unroll
+  for (int x = 0; x < (GH ? 1 : 2); ++x)
+    copy_async16(st + x * 512 + lane * 16, g + (GH ? lane * 16 : lane * 32 + x * 16));
+  st += GH ? 512 : 1024;
+#pragma unroll
+  for (int x = 0; x < (PH ? 1 : 2); ++x)
+    copy_async16(st + x * 512 + lane * 16, p + (PH ? lane * 16 : lane * 32 + x * 16));
+  st += PH ? 512 : 1024;
+  copy_async8(st + lane * 8, static_cast<const uint8_t*>(e.m) + i + lane * 8);
+  copy_async8(st + 256 + lane * 8, static_cast<const uint8_t*>(e.v) + i + lane * 8);
+}
+
+template <bool PH, bool GH>
+__device__ __forceinline__ void stage_read(Operands<8, PH, GH>& o, const uint8_t* st) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = 0; x < (GH ? 1 : 2); ++x) {
+    const uint4 a = *reinterpret_cast<const uint4*>(st + x * 512 + lane * 16);
+    o.g.w[4 * x] = a.x; o.g.w[4 * x + 1] = a.y; o.g.w[4 * x + 2] = a.z; o.g.w[4 * x + 3] = a.w;
+  }
+  st += GH ? 512 : 1024;
+#pragma unroll
+  for (int x = 0; x < (PH ? 1 : 2); ++x) {
+    const uint4 a = *reinterpret_cast<const uint4*>(st + x * 512 + lane * 16);
+    o.p.w[4 * x] = a.x; o.p.w[4 * x + 1] = a.y; o.p.w[4 * x + 2] = a.z; o.p.w[4 * x + 3] = a.w;
+  }
+  st += PH ? 512 : 1024;
+  const uint2 m = *reinterpret_cast<const uint2*>(st + lane * 8);
+  const uint2 v = *reinterpret_cast<const uint2*>(st + 256 + lane * 8);
+  o.m.w[0] = m.x; o.m.w[1] = m.y;
+  o.v.w[0] = v.x; o.v.w[1] = v.y;
+}
+
+// The full blocks of a warp's turns in one chunk; returns how many it did.
+template <bool PH, bool GH>
+__device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry& e, int64_t block,
+                                          uint8_t* ring, std::integral_constant<int, 8>) {
+  constexpr int B = stage_bytes<PH, GH>();
+  const int64_t fulls = e.wide ? e.n / kBlockElems : 0;  // full blocks of the tensor
+  const int64_t room = (fulls - block + kWarps - 1) / kWarps;
+  const int turns = room < 0 ? 0 : (int)min((int64_t)k.turns, room);
+  if (turns == 0) return 0;
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x) {
+    if (x < turns) stage_copy<PH, GH>(ring + x * B, e, (block + x * kWarps) * kBlockElems);
+    copy_commit();
+  }
+  float ms = e.ms[block], vs = e.vs[block];
+  int slot = 0, ahead = kAhead;
+  for (int turn = 0; turn < turns; ++turn, block += kWarps) {
+    if (turn + kAhead < turns)
+      stage_copy<PH, GH>(ring + ahead * B, e, (block + kAhead * kWarps) * kBlockElems);
+    copy_commit();
+    Operands<8, PH, GH> o;
+    o.ms = ms;
+    o.vs = vs;
+    if (turn + 1 < turns) {
+      ms = e.ms[block + kWarps];
+      vs = e.vs[block + kWarps];
+    }
+    copy_wait<kAhead>();
+    stage_read(o, ring + slot * B);
+    step_block(k, e, Place{kBlockElems, true, block}, o);
+    slot = slot == kAhead ? 0 : slot + 1;
+    ahead = ahead == kAhead ? 0 : ahead + 1;
+  }
+  return turns;
+}
+
+// fp32 moments: a turn's operands are fetched into registers a turn ahead.
+template <bool PH, bool GH>
+__device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry& e, int64_t block,
+                                          uint8_t*, std::integral_constant<int, 32>) {
+  const int64_t fulls = e.wide ? e.n / kBlockElems : 0;
+  const int64_t room = (fulls - block + kWarps - 1) / kWarps;
+  const int turns = room < 0 ? 0 : (int)min((int64_t)k.turns, room);
+  if (turns == 0) return 0;
+  Operands<32, PH, GH> o;
+  fetch_all(o, e, Place{kBlockElems, true, block});
+  for (int turn = 0; turn < turns; ++turn, block += kWarps) {
+    Operands<32, PH, GH> next;
+    if (turn + 1 < turns) fetch_all(next, e, Place{kBlockElems, true, block + kWarps});
+    step_block(k, e, Place{kBlockElems, true, block}, o);
+    o = next;
+  }
+  return turns;
 }
 
 // PH, GH: 16-bit parameters (no master) and gradients.
 template <int BITS, bool PH, bool GH, int COUNT>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, BITS == 8 ? 4 : 2)
 adamw_kernel(const __grid_constant__ AdamwTable<COUNT> t) {
+  extern __shared__ __align__(16) uint8_t rings[];
   const AdamwConst& k = t.k;
   if (k.skip && *k.skip != 0) return;
+  const int warp = threadIdx.x >> 5;
+  uint8_t* ring = rings + warp * (kAhead + 1) * stage_bytes<PH, GH>();
   const int c0 = (int)((int64_t)k.chunks * blockIdx.x / gridDim.x);
   const int c1 = (int)((int64_t)k.chunks * (blockIdx.x + 1) / gridDim.x);
   if (c0 >= c1) return;
-  Place here = place_of(t, tensor_of(t, c0), c0);
-  Operands<BITS, PH, GH> o;
-  fetch_all(o, t.e[here.e], here);
+  int at = tensor_of(t, c0);
   for (int c = c0; c < c1; ++c) {
-    Operands<BITS, PH, GH> next;
-    Place there = here;
-    if (c + 1 < c1) {
-      there = place_of(t, here.e, c + 1);
-      fetch_all(next, t.e[there.e], there);
-    }
-    if (here.cnt >= 0) step_block<BITS, PH, GH>(k, t.e[here.e], here, o);
-    o = next;
-    here = there;
+    while (at + 1 < k.count && t.e[at + 1].first <= c) ++at;
+    const AdamwEntry e = t.e[at];
+    const int64_t block = (int64_t)(c - e.first) * kWarps * k.turns + warp;
+    for (int turn = full_turns<PH, GH>(k, e, block, ring, std::integral_constant<int, BITS>());
+         turn < k.turns; ++turn)
+      odd_block<BITS, PH, GH>(k, t.e[at], block + turn * kWarps);
   }
 }
 
-// Moments in fp32: entry.p and entry.master are the outputs here.
+// Moments in fp32: entry.p and entry.master are the outputs here.  Bytes are
+// read a word at a time, so that the floats are written as whole lines.
+template <int BITS>
+__device__ __forceinline__ void moments_block(const AdamwEntry& e, const Place& q) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = q.block * kBlockElems;
+  float x[8], y[8];
+  if (BITS == 32) {
+    Raw<false> r;
+    fetch<32, false>(r, e.m, i, q.left, q.full);
+    widen<false>(r, GMM_F32, x);
+    fetch<32, false>(r, e.v, i, q.left, q.full);
+    widen<false>(r, GMM_F32, y);
+  } else {
+    uint2 mc, vc;
+    if (q.full) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.m) + i);
+      mc = make_uint2(p[lane], p[lane + 32]);
+      p = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.v) + i);
+      vc = make_uint2(p[lane], p[lane + 32]);
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int z = lane_elem<32>(j);
+        if (z < q.left) {
+          w[j >> 2] |= (uint32_t)static_cast<const uint8_t*>(e.m)[i + z] << (8 * (j & 3));
+          w[2 + (j >> 2)] |= (uint32_t)static_cast<const uint8_t*>(e.v)[i + z] << (8 * (j & 3));
+        }
+      }
+      mc = make_uint2(w[0], w[1]);
+      vc = make_uint2(w[2], w[3]);
+    }
+    float2 m[4], v[4];
+    decode_m(mc, e.ms[q.block], m);
+    decode_root(vc, e.vs[q.block], v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 s = mul2(v[j], v[j]);
+      x[2 * j] = m[j].x; x[2 * j + 1] = m[j].y;
+      y[2 * j] = s.x; y[2 * j + 1] = s.y;
+    }
+  }
+  put_float<32>(x, static_cast<float*>(e.p), i, q.left, q.full);
+  put_float<32>(y, e.master, i, q.left, q.full);
+}
+
 template <int BITS, int COUNT>
 __global__ void __launch_bounds__(kWarps * 32)
 adamw_moments_kernel(const __grid_constant__ AdamwTable<COUNT> t) {
-  const int c0 = (int)((int64_t)t.k.chunks * blockIdx.x / gridDim.x);
-  const int c1 = (int)((int64_t)t.k.chunks * (blockIdx.x + 1) / gridDim.x);
+  const AdamwConst& k = t.k;
+  const int c0 = (int)((int64_t)k.chunks * blockIdx.x / gridDim.x);
+  const int c1 = (int)((int64_t)k.chunks * (blockIdx.x + 1) / gridDim.x);
   if (c0 >= c1) return;
   int at = tensor_of(t, c0);
   for (int c = c0; c < c1; ++c) {
-    const Place q = place_of(t, at, c);
-    at = q.e;
-    if (q.cnt < 0) continue;
-    const AdamwEntry& e = t.e[q.e];
-    const bool wide = e.wide;
-    float m[8], v[8];
-    if (BITS == 32) {
-      load_n(e.m, GMM_F32, q.i, q.cnt, wide, m);
-      load_n(e.v, GMM_F32, q.i, q.cnt, wide, v);
+    while (at + 1 < k.count && t.e[at + 1].first <= c) ++at;
+    const AdamwEntry e = t.e[at];
+    const int64_t block = (int64_t)(c - e.first) * kWarps * k.turns + (threadIdx.x >> 5);
+    const Place last = place_of(e, block + (k.turns - 1) * kWarps);
+    if (last.full) {
+#pragma unroll 4
+      for (int turn = 0; turn < k.turns; ++turn) {
+        Place q{kBlockElems, true, block + turn * kWarps};
+        moments_block<BITS>(e, q);
+      }
     } else {
-      decode_m(load_codes(e.m, q.i, q.cnt, wide), e.ms[q.block], m);
-      decode_root(load_codes(e.v, q.i, q.cnt, wide), e.vs[q.block], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+      for (int turn = 0; turn < k.turns; ++turn) {
+        const Place q = place_of(e, block + turn * kWarps);
+        if (q.left > 0) moments_block<BITS>(e, q);
+      }
     }
-    store_n(e.p, GMM_F32, q.i, q.cnt, wide, m);
-    store_n(e.master, GMM_F32, q.i, q.cnt, wide, v);
   }
 }
 
@@ -499,7 +722,14 @@ bool tensors_ok(const gmm_adamw_tensor* ts, int count, int bits, bool step) {
   return true;
 }
 
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+// Turns of a warp in one chunk: enough chunks for every warp of two blocks a
+// multiprocessor, then up to kMaxTurns (the table is read once a chunk).
+int turns_for(const gmm_adamw_tensor* ts, int count) {
+  int64_t n = 0;
+  for (int i = 0; i < count; ++i) n += ts[i].n;
+  const int64_t t = n / ((int64_t)kBlockElems * kWarps * 304);
+  return t < 1 ? 1 : t > kMaxTurns ? kMaxTurns : (int)t;
+}
 
 // Launches over the non-empty tensors that `take` wants, as many at a time as
 // a table holds (and as 2^30 chunks).
@@ -508,11 +738,13 @@ gmm_status over_tables(const gmm_adamw_tensor* ts, int count, const AdamwConst& 
                        Fill fill, Go go) {
   AdamwTable<COUNT> t;
   t.k = k;
+  t.k.turns = turns_for(ts, count);
   t.k.count = 0;
   int64_t chunks = 0;
   for (int i = 0; i <= count; ++i) {
     const bool end = i == count;
-    const int64_t c = end || !take(i) ? 0 : chunks_of(ts[i].n);
+    const int64_t chunk = (int64_t)kBlockElems * kWarps * t.k.turns;
+    const int64_t c = end || !take(i) ? 0 : (ts[i].n + chunk - 1) / chunk;
     if (t.k.count > 0 && (end || t.k.count == COUNT || chunks + c > (1 << 30))) {
       t.k.chunks = (int)chunks;
       go(t);
@@ -533,7 +765,18 @@ gmm_status over_tables(const gmm_adamw_tensor* ts, int count, const AdamwConst& 
 }
 
 constexpr int kSmallTable = 16, kTable = 400;
-unsigned grid_for(int chunks) { return (unsigned)(chunks < 152 * 8 ? chunks : 152 * 8); }
+// Blocks: one a chunk, up to a few waves of resident ones, so that the last
+// blocks of long lists do not run alone.
+unsigned grid_for(int chunks) { return (unsigned)(chunks < 152 * 12 ? chunks : 152 * 12); }
+
+template <int BITS, bool PH, bool GH, int COUNT>
+void launch_step(const AdamwTable<COUNT>& t, cudaStream_t s) {
+  const size_t smem = BITS == 8 ? ring_bytes<PH, GH>() : 0;
+  if (smem > 48 * 1024)
+    cudaFuncSetAttribute(adamw_kernel<BITS, PH, GH, COUNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)smem);
+  adamw_kernel<BITS, PH, GH, COUNT><<<grid_for(t.k.chunks), kWarps * 32, smem, s>>>(t);
+}
 
 }  // namespace
 }  // namespace gmm
@@ -562,6 +805,7 @@ gmm_status gmm_adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw
   k.decay = (float)(1.0 - o->lr * o->weight_decay);
   k.rate = (float)(o->lr / (1.0 - std::pow(o->beta1, (double)o->step)));
   k.skip = o->skip;
+  k.eps_covers = o->eps >= 1e-10;
   const int bits = o->state_bits;
   auto fill = [&](int i, AdamwEntry& e) {
     const gmm_adamw_tensor& t = ts[i];
@@ -581,13 +825,11 @@ gmm_status gmm_adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw
       return (ts[i].param_dtype != GMM_F32 && !ts[i].master) == ph && (ts[i].grad_dtype != GMM_F32) == gh;
     };
     auto go = [&](const auto& t) {
-      constexpr int C = sizeof(t.e) / sizeof(t.e[0]);
-      const unsigned grid = grid_for(t.k.chunks);
-#define GMM_GO(B)                                                                        \
-  if (ph && gh) adamw_kernel<B, true, true, C><<<grid, kWarps * 32, 0, s>>>(t);           \
-  else if (ph) adamw_kernel<B, true, false, C><<<grid, kWarps * 32, 0, s>>>(t);           \
-  else if (gh) adamw_kernel<B, false, true, C><<<grid, kWarps * 32, 0, s>>>(t);           \
-  else adamw_kernel<B, false, false, C><<<grid, kWarps * 32, 0, s>>>(t);
+#define GMM_GO(B)                                  \
+  if (ph && gh) launch_step<B, true, true>(t, s);   \
+  else if (ph) launch_step<B, true, false>(t, s);   \
+  else if (gh) launch_step<B, false, true>(t, s);   \
+  else launch_step<B, false, false>(t, s);
       if (bits == 32) { GMM_GO(32) } else { GMM_GO(8) }
 #undef GMM_GO
     };

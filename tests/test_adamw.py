@@ -258,3 +258,40 @@ def test_python_refusals(cuda):
     with pytest.raises(G.GmmError):
         opt.lr = float("nan")
         opt.step([torch.zeros(4, device="cuda")])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [256 * 40, 300_001])
+def test_codes_are_those_of_exact_roots(cuda, n):
+    """8-bit codes and scales equal the documented fp32 operations, each
+    rounded once (numpy's float32 operations are), over several steps."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    f = np.float32
+    rng = np.random.default_rng(n)
+    p = torch.zeros(n, device="cuda")
+    opt = AdamW([p], lr=1e-3, betas=(B1, B2), eps=EPS, weight_decay=0.0, state_bits=8)
+    blocks = -(-n // 256)
+    pad = lambda x: np.concatenate([x, np.zeros(blocks * 256 - n, f)]).reshape(blocks, 256)  # noqa: E731
+    m, r = np.zeros((blocks, 256), f), np.zeros((blocks, 256), f)
+    for step in range(4):
+        g = (rng.standard_normal(n) * np.exp(2 * rng.standard_normal(n))).astype(f)
+        opt.step([torch.from_numpy(g).cuda()])
+        g = pad(g)
+        m = m * f(B1) + g * f(1 - B1)
+        v = (r * r) * f(B2) + (g * g) * f(1 - B2)
+        root = np.sqrt(v)
+        for x, top, name in ((m, 127, "m"), (root, 255, "v")):
+            big = np.abs(x).max(1)
+            scale = big * f(1.0 / (top * top))
+            inv = np.where(big > 0, (f(1) / np.where(big > 0, big, f(1))) * f(top * top), f(0)).astype(f)
+            c = np.rint(np.sqrt(np.abs(x) * inv[:, None]))
+            c = np.where((x > 0) & (c < 1), f(1), c) if name == "v" else c * np.sign(x)
+            assert np.array_equal(opt.state[name + "_scale"][0].cpu().numpy(), scale), (step, name)
+            got = opt.state[name][0].cpu().numpy().astype(f)
+            assert np.array_equal(got, c.reshape(-1)[:n]), (step, name, (got != c.reshape(-1)[:n]).sum())
+            val = c * np.abs(c) * scale[:, None]
+            if name == "m":
+                m = val
+            else:
+                r = val
