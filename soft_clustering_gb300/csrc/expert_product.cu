@@ -19,12 +19,16 @@ constexpr int kListThreads = 1024;
 
 // Row tiles of T rows for every component, in order, then those of the rows
 // past offsets[K] (component -1: zeros).  Offsets are held within [0, R].
+// `tiles` NULL: the status word alone.  The kernel after it may start at once
+// (its set-up overlaps this one) and waits for this one's end itself.
 __global__ void __launch_bounds__(kListThreads)
 tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T,
                  DeviceStatus* __restrict__ st, int32_t* __restrict__ count,
                  int4* __restrict__ tiles) {
   __shared__ uint32_t wsum[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
+  if (!tiles) return;
   const int G = K + 1;
   const int per = (G + kListThreads - 1) / kListThreads;
   const int k0 = min(G, (int)threadIdx.x * per), k1 = min(G, k0 + per);
@@ -158,7 +162,10 @@ gmm_status weights_simt(const void* dY, const void* A, void* dW, int64_t R, int 
 gmm_status rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
                         int d_to, int K, bool dx, const int64_t* offsets, void* ws,
                         cudaStream_t s) {
-  if (tc_product_ok(xdtype, R, d_from, d_to, A, W, Y))
+  const bool tc = tc_product_ok(xdtype, R, d_from, d_to, A, W, Y);
+  if (tc && !dx && R > 0 && R <= kFewRows)
+    return few_rows_product(A, xdtype, W, Y, R, d_from, d_to, K, offsets, ws, s);
+  if (tc)
     return tc_rows(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
   if ((d_to + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
   switch (xdtype) {
@@ -176,6 +183,12 @@ gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
   tile_list_kernel<<<1, kListThreads, 0, s>>>(offsets, K, R, T, at<DeviceStatus>(ws, 0),
                                               at<int32_t>(ws, L.off_count),
                                               at<int4>(ws, L.off_tiles));
+  return launched();
+}
+
+gmm_status clear_status(void* ws, cudaStream_t s) {
+  ProfScope p("tile_list_kernel(status)", s);
+  tile_list_kernel<<<1, 64, 0, s>>>(nullptr, 0, 0, 1, at<DeviceStatus>(ws, 0), nullptr, nullptr);
   return launched();
 }
 

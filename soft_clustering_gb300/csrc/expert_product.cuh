@@ -32,10 +32,16 @@ struct ProductLayout {
 gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
                       const ProductLayout& L, cudaStream_t s);
 
+gmm_status clear_status(void* ws, cudaStream_t s);
+
 // The tensor-core forms (expert_product_tc.cu) and what they take.
 bool tc_product_ok(int xdtype, int64_t R, int d_in, int d_out, const void* a, const void* b, const void* c);
 gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
                    int d_to, int K, bool dx, const int64_t* offsets, void* ws, cudaStream_t s);
+// ... and the one for few rows, 16-bit types as above.
+constexpr int kFewRows = 32;
+gmm_status few_rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_in,
+                            int d_out, int K, const int64_t* offsets, void* ws, cudaStream_t s);
 gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int d_in, int d_out,
                       int K, const int64_t* offsets, void* dW, int wdtype, void* ws,
                       cudaStream_t s);

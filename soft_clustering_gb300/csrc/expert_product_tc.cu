@@ -37,7 +37,10 @@ constexpr int kBox = 8192;                 // 64 rows x 128 bytes
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
 constexpr int kStageBytes = (kTileM + kTileN) * kTileK * 2;
 constexpr int kThreads = 192;              // fetch, issue, four read back
-constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kOutBytes = 4096;            // 32 rows x 128 bytes of dW on their way out
+constexpr int kOutAt = kStages * kStageBytes;            // two for each read-back warp
+constexpr int kBarsAt = kOutAt + 4 * 2 * kOutBytes;
+constexpr int kSmem = kBarsAt + 256 + 1024;
 constexpr uint32_t kWait = 2000000;        // polls of up to a microsecond
 
 enum { kProduct = 0, kDx = 1, kDw = 2 };
@@ -158,30 +161,31 @@ __device__ __forceinline__ void store_rows(const float* v, TO* out, int64_t ld, 
   }
 }
 
-// 32 consecutive outputs of this lane's row (dw), `left` of them wanted (a
-// multiple of 8).
-__device__ __forceinline__ void store_line(const float* v, float* out, int left) {
+// 128 bytes of this lane's row of dW (64 or 32 columns) into the warp's piece
+// in shared memory, 128-byte swizzled as the store's tensor map has it: eight
+// lanes fill all eight 16-byte places of a line.
+__device__ __forceinline__ void stage_line(const uint32_t* w, uint8_t* piece) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 32; j += 4)
-    if (j < left) *reinterpret_cast<float4*>(out + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(piece + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
-template <typename TO>
-__device__ __forceinline__ void store_line(const float* v, TO* out, int left) {
-#pragma unroll
-  for (int j = 0; j < 32; j += 8)
-    if (j < left)
-      *reinterpret_cast<uint4*>(out + j) =
-          make_uint4(Pair<TO>::pack(v[j], v[j + 1]), Pair<TO>::pack(v[j + 2], v[j + 3]),
-                     Pair<TO>::pack(v[j + 4], v[j + 5]), Pair<TO>::pack(v[j + 6], v[j + 7]));
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y,
+                                             int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::
+                   "l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(tc::smem_addr(src))
+               : "memory");
 }
 
 template <int MODE, typename T, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                 TO* __restrict__ out, TcArgs a) {
+                 const __grid_constant__ CUtensorMap map_out, TO* __restrict__ out, TcArgs a) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarsAt);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;     // [2]
@@ -208,6 +212,8 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  // the list (or the cleared status word) and everything before it is there
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int total = tile_total<MODE>(a);
 
   if (warp == 0) {
@@ -296,7 +302,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
     if (!ok && lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
-    uint32_t acc = 0;
+    uint32_t acc = 0, piece = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
       const Tile w = tile_at<MODE>(a, t);
       const int b = acc & 1;
@@ -309,18 +315,52 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         tc::tc_fence_after();
       }
       const uint32_t src = tmem + b * kTileN + ((uint32_t)(quarter * 32) << 16);
-      for (int c = 0; c < w.n; c += 32) {
-        float v[32];
-        if (w.len > 0) {
-          tc::tmem_ld32(src + c, v);
-        } else {
+      if constexpr (MODE == kDw) {
+        // pieces of 32 rows x 128 bytes, two in flight; the tensor map cuts
+        // off what is past dW's edges
+        constexpr int W = 128 / sizeof(TO);
+        uint8_t* pieces = smem + kOutAt + quarter * 2 * kOutBytes;
+        const int y = w.i0 + quarter * 32;
+        for (int c = 0; c < w.n && y < a.d_to; c += W, ++piece) {
+          uint32_t r[2][32];
+          if (w.len > 0) {
+            tc::tmem_ld32_issue(src + c, r[0]);
+            if (W == 64) tc::tmem_ld32_issue(src + c + 32, r[1]);
+            tc::tmem_wait32(r[0]);
+            if (W == 64) tc::tmem_wait32(r[1]);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            for (int j = 0; j < 32; ++j) r[0][j] = r[1][j] = 0u;
+          }
+          if constexpr (W == 64) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r[0][j] = Pair<TO>::pack(__uint_as_float(r[0][2 * j]), __uint_as_float(r[0][2 * j + 1]));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r[0][16 + j] = Pair<TO>::pack(__uint_as_float(r[1][2 * j]), __uint_as_float(r[1][2 * j + 1]));
+          }
+          uint8_t* at = pieces + (piece & 1) * kOutBytes;
+          if (lane == 0)  // the store before the last one has read its piece
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+          stage_line(r[0], at);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&map_out, at, w.j0 + c, y, w.k);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
         }
-        if constexpr (MODE == kDw) {
-          if (f < a.d_to)
-            store_line(v, out + ((int64_t)w.k * a.d_to + f) * a.d_from + w.j0 + c, w.n - c);
-        } else {
+      } else {
+        for (int c = 0; c < w.n; c += 32) {
+          float v[32];
+          if (w.len > 0) {
+            tc::tmem_ld32(src + c, v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
           store_rows(v, out + (w.row0 + c) * (int64_t)a.d_to, a.d_to, f, a.d_to, w.n - c);
         }
       }
@@ -331,6 +371,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         ++acc;
       }
     }
+    if (MODE == kDw && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncthreads();
   if (warp == 1) {
@@ -357,15 +398,18 @@ EncodeFn encoder() {
   return fn;
 }
 
-// Dense [d2][d1][d0] of 16-bit elements (d2 = 0: two dimensions), boxes of 64 x 64.
-bool encode(CUtensorMap* m, int xdtype, const void* base, int64_t d0, int64_t d1, int64_t d2) {
+// Dense [d2][d1][d0] (d2 = 0: two dimensions), boxes of rows x 128 bytes.
+bool encode(CUtensorMap* m, int type, const void* base, int64_t d0, int64_t d1, int64_t d2, int rows) {
   const EncodeFn fn = encoder();
   if (!fn) return false;
+  const cuuint64_t es = (cuuint64_t)dtype_size(type);
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-  const cuuint64_t strides[2] = {(cuuint64_t)d0 * 2, (cuuint64_t)d0 * (cuuint64_t)d1 * 2};
-  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
-  return fn(m, xdtype == GMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-            d2 ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
+  const cuuint64_t strides[2] = {(cuuint64_t)d0 * es, (cuuint64_t)d0 * (cuuint64_t)d1 * es};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = type == GMM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : type == GMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return fn(m, dt, d2 ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -379,15 +423,26 @@ int multiprocessors() {
 }
 
 template <int MODE, typename T, typename TO>
-gmm_status go(const CUtensorMap& mp, const CUtensorMap& mq, void* out, const TcArgs& a,
-              int64_t most, cudaStream_t s) {
+gmm_status go(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, void* out,
+              const TcArgs& a, int64_t most, cudaStream_t s) {
   const int sms = multiprocessors();
   if (sms < 1 || cudaFuncSetAttribute(expert_tc_kernel<MODE, T, TO>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return GMM_ERR_CUDA;
   const unsigned grid = (unsigned)(most < sms ? most : sms);
   ProfScope p(MODE == kProduct ? "expert_tc_kernel" : MODE == kDx ? "expert_tc_kernel(dx)" : "expert_tc_kernel(dw)", s);
-  expert_tc_kernel<MODE, T, TO><<<grid, kThreads, kSmem, s>>>(mp, mq, (TO*)out, a);
+  // may start while the kernel that makes its list runs
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, expert_tc_kernel<MODE, T, TO>, mp, mq, mo, (TO*)out, a);
   return launched();
 }
 
@@ -405,36 +460,38 @@ gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R,
   if (r != GMM_OK || R == 0) return r;
   CUtensorMap mp, mq;
   const int d_in = dx ? d_to : d_from, d_out = dx ? d_from : d_to;
-  if (!encode(&mp, xdtype, W, d_in, d_out, K) || !encode(&mq, xdtype, A, d_from, R, 0))
+  if (!encode(&mp, xdtype, W, d_in, d_out, K, 64) || !encode(&mq, xdtype, A, d_from, R, 0, 64))
     return GMM_ERR_CUDA;
   TcArgs a{offsets, at<int32_t>(ws, L.off_count), at<int4>(ws, L.off_tiles), at<DeviceStatus>(ws, 0),
            R, K, d_from, d_to};
   const int64_t most = ProductLayout::most_tiles(R, K, kTileN) * ((d_to + kTileM - 1) / kTileM);
   if (xdtype == GMM_BF16) {
     using T = __nv_bfloat16;
-    return dx ? go<kDx, T, T>(mp, mq, Y, a, most, s) : go<kProduct, T, T>(mp, mq, Y, a, most, s);
+    return dx ? go<kDx, T, T>(mp, mq, mq, Y, a, most, s) : go<kProduct, T, T>(mp, mq, mq, Y, a, most, s);
   }
   using T = __half;
-  return dx ? go<kDx, T, T>(mp, mq, Y, a, most, s) : go<kProduct, T, T>(mp, mq, Y, a, most, s);
+  return dx ? go<kDx, T, T>(mp, mq, mq, Y, a, most, s) : go<kProduct, T, T>(mp, mq, mq, Y, a, most, s);
 }
 
 gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int d_in, int d_out,
                       int K, const int64_t* offsets, void* dW, int wdtype, void* ws,
                       cudaStream_t s) {
-  CUtensorMap mp, mq;
-  if (!encode(&mp, xdtype, dY, d_out, R, 0) || !encode(&mq, xdtype, A, d_in, R, 0))
+  CUtensorMap mp, mq, mo;
+  if (!encode(&mp, xdtype, dY, d_out, R, 0, 64) || !encode(&mq, xdtype, A, d_in, R, 0, 64) ||
+      !encode(&mo, wdtype, dW, d_in, d_out, K, 32))
     return GMM_ERR_CUDA;
-  if (cudaMemsetAsync(ws, 0, sizeof(DeviceStatus), s) != cudaSuccess) return GMM_ERR_CUDA;
+  const gmm_status r = clear_status(ws, s);
+  if (r != GMM_OK) return r;
   TcArgs a{offsets, nullptr, nullptr, at<DeviceStatus>(ws, 0), R, K, d_in, d_out};
   const int64_t most =
       (int64_t)K * ((d_out + kTileM - 1) / kTileM) * ((d_in + kTileN - 1) / kTileN);
   if (most > INT32_MAX) return GMM_ERR_UNSUPPORTED;
   if (xdtype == GMM_BF16) {
     using T = __nv_bfloat16;
-    return wdtype == GMM_F32 ? go<kDw, T, float>(mp, mq, dW, a, most, s) : go<kDw, T, T>(mp, mq, dW, a, most, s);
+    return wdtype == GMM_F32 ? go<kDw, T, float>(mp, mq, mo, dW, a, most, s) : go<kDw, T, T>(mp, mq, mo, dW, a, most, s);
   }
   using T = __half;
-  return wdtype == GMM_F32 ? go<kDw, T, float>(mp, mq, dW, a, most, s) : go<kDw, T, T>(mp, mq, dW, a, most, s);
+  return wdtype == GMM_F32 ? go<kDw, T, float>(mp, mq, mo, dW, a, most, s) : go<kDw, T, T>(mp, mq, mo, dW, a, most, s);
 }
 
 }  // namespace gmm
