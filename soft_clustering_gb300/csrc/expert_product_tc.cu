@@ -32,16 +32,18 @@
 namespace gmm {
 namespace {
 
-constexpr int kStages = 4;
 constexpr int kBox = 8192;                 // 64 rows x 128 bytes
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kStageBytes = (kTileM + kTileN) * kTileK * 2;
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;   // kTileM: of one block
+constexpr int kRing = 192 * 1024;          // stages: 4 of 48 KB, or 6 of 32 KB in a pair
+template <int CG> constexpr int kStageBytes = (kTileM + kTileN / CG) * kTileK * 2;
+template <int CG> constexpr int kStages = kRing / kStageBytes<CG>;
 constexpr int kThreads = 192;              // fetch, issue, four read back
 constexpr int kOutBytes = 4096;            // 32 rows x 128 bytes of dW on their way out
-constexpr int kOutAt = kStages * kStageBytes;            // two for each read-back warp
+constexpr int kOutAt = kRing;              // two for each read-back warp
 constexpr int kBarsAt = kOutAt + 4 * 2 * kOutBytes;
 constexpr int kSmem = kBarsAt + 256 + 1024;
 constexpr uint32_t kWait = 2000000;        // polls of up to a microsecond
+constexpr uint64_t kWaitNs = 2000000000;   // of a pair
 
 enum { kProduct = 0, kDx = 1, kDw = 2 };
 
@@ -60,52 +62,199 @@ struct Tile {
   int64_t row0;
 };
 
-template <int MODE>
+template <int MODE, int CG>
 __device__ __forceinline__ int tile_total(const TcArgs& a) {
-  if (MODE == kDw) return a.K * ((a.d_to + kTileM - 1) / kTileM) * ((a.d_from + kTileN - 1) / kTileN);
-  return *a.count * ((a.d_to + kTileM - 1) / kTileM);
+  const int mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
+  if (MODE == kDw) return a.K * mt * ((a.d_from + kTileN - 1) / kTileN);
+  return *a.count * mt;
 }
 
-template <int MODE>
-__device__ __forceinline__ Tile tile_at(const TcArgs& a, int t) {
+// What of a tile has to come from memory; fetched a tile ahead by every role.
+struct TileRaw {
+  int4 q;
+  int64_t b, e;
+};
+template <int MODE, int CG>
+__device__ __forceinline__ TileRaw tile_raw(const TcArgs& a, int t, int total) {
+  TileRaw r;
+  r.q = make_int4(-1, 0, 0, 0);
+  r.b = r.e = 0;
+  if (t < total) {
+    const int mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
+    if (MODE == kDw) {
+      const int k = t / (mt * ((a.d_from + kTileN - 1) / kTileN));
+      r.b = a.offsets[k];
+      r.e = a.offsets[k + 1];
+    } else {
+      r.q = a.tiles[t / mt];
+    }
+  }
+  return r;
+}
+template <int MODE, int CG>
+__device__ __forceinline__ Tile tile_at(const TcArgs& a, int t, const TileRaw& raw) {
   Tile w;
-  const int mt = (a.d_to + kTileM - 1) / kTileM;
+  const int mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
   if (MODE == kDw) {
     const int nt = (a.d_from + kTileN - 1) / kTileN;
     w.k = t / (mt * nt);
     const int r = t % (mt * nt);
-    w.i0 = (r / nt) * kTileM;
+    w.i0 = (r / nt) * CG * kTileM;
     w.j0 = (r % nt) * kTileN;
     w.n = min(kTileN, a.d_from - w.j0);
-    const int64_t b = clamp_row(a.offsets[w.k], a.R), e = clamp_row(a.offsets[w.k + 1], a.R);
+    const int64_t b = clamp_row(raw.b, a.R), e = clamp_row(raw.e, a.R);
     w.row0 = b;
     w.len = e > b ? (int)(e - b) : 0;
   } else {
-    const int4 q = a.tiles[t / mt];
-    w.k = q.x;
-    w.row0 = q.y;
-    w.n = q.z;
-    w.i0 = (t % mt) * kTileM;
+    w.k = raw.q.x;
+    w.row0 = raw.q.y;
+    w.n = raw.q.z;
+    w.i0 = (t % mt) * CG * kTileM;
     w.j0 = 0;
-    w.len = q.x < 0 ? 0 : a.d_from;
+    w.len = raw.q.x < 0 ? 0 : a.d_from;
   }
   return w;
 }
 
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(tc::smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(tc::smem_addr(bar))
-      : "memory");
+// TMA of one box.  `bar`: a shared::cluster address; with PAIR it may be the
+// other block's of the pair.
+template <bool PAIR>
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(tc::smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(tc::smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                       uint64_t* bar) {
+                                       uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// One lane of a converged warp.  (Copies and products take their operands
+// from uniform registers; behind a test of the lane number each of them costs
+// 130 to 170 cycles to issue, more than a product of 128 x 256 x 16 takes.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_addr(bar))
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// ---- pairs of blocks (cta_group::2)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of this block's `p` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrival at a barrier of either block.  A release to the cluster waits for
+// every earlier access of the thread (about 1000 cycles): only where this
+// block's own writes have to be seen.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_release_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits for the phase with this parity, acquiring what either block of the
+// pair released; gives up after kWaitNs.
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity) {
+  uint64_t end = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15) == 15) {
+      uint64_t now;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (end == 0) end = now + kWaitNs;
+      else if (now > end) return false;
+    }
+  }
+}
+template <int CG>
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
+  return CG == 2 ? wait_pair(bar, parity) : tc::mbar_wait(bar, parity, kWait);
+}
+template <int CG>
+__device__ __forceinline__ void tmem_take(uint32_t* dst) {
+  if (CG == 1) {
+    tc::tmem_alloc(dst, 512);
+    tc::tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_addr(dst)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_give(uint32_t at) {
+  if (CG == 1) tc::tmem_dealloc(at, 512);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(512u) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t p, uint64_t q, uint32_t id, uint32_t add) {
+  if (CG == 1) {
+    tc::mma_f16(d, p, q, id, add);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(p), "l"(q), "r"(id), "r"(add)
+        : "memory");
+  }
+}
+// Arrives on `bar` (in a pair: of both blocks) when the products issued so
+// far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 1) {
+    tc::mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  }
 }
 
 // Descriptor of an MN-major operand in 128-byte swizzled boxes of 64 (MN) x
@@ -123,10 +272,10 @@ __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
 
 // Instruction descriptor: fp32 accumulator, both operands f16 or bf16, P / Q
 // MN-major where told (bits 15, 16).
-__device__ __forceinline__ uint32_t idesc(bool bf16, bool p_mn, bool q_mn, int n) {
+__device__ __forceinline__ uint32_t idesc(bool bf16, bool p_mn, bool q_mn, int m, int n) {
   const uint32_t f = bf16 ? 1u : 0u;
   return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)p_mn << 15) | ((uint32_t)q_mn << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 template <typename TO> struct Pair;
@@ -179,136 +328,200 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-template <int MODE, typename T, typename TO>
+// Rows left .. left + rows - 1 of `boxes` boxes from p: zeros (128 bytes each).
+__device__ __forceinline__ void zero_rows(uint8_t* p, int boxes, int left, int rows) {
+  for (int x = threadIdx.x & 31; x < boxes * rows * 8; x += 32) {
+    const int box = x / (rows * 8), r = left + (x / 8) % rows, c = x & 7;
+    *reinterpret_cast<uint4*>(p + box * kBox + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// CG = 2: a pair of blocks (a cluster, on two multiprocessors) on tiles of 256
+// rows; each block holds 128 of them, fetches half of the columns, and reads
+// its 128 rows of the accumulator back.  The first block issues the products;
+// the fetched bytes of both are counted on its barriers.
+template <int MODE, typename T, typename TO, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                  const __grid_constant__ CUtensorMap map_out, TO* __restrict__ out, TcArgs a) {
   extern __shared__ uint8_t raw[];
+  constexpr int S = kStages<CG>, B = kStageBytes<CG>;
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarsAt);
-  uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;   // [2]
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;         // [2]
   uint64_t* acc_empty = acc_full + 2;     // [2]
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* zeroed = acc_empty + 2;       // [S] the second block of a pair has zeroed its rows
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(zeroed + S);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kPmn = MODE != kProduct, kQmn = MODE == kDw;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < S; ++i) {
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&zeroed[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&acc_full[i], 1);
-      tc::mbar_init(&acc_empty[i], 4);
+      tc::mbar_init(&acc_empty[i], 4 * CG);
     }
     tc::mbar_fence_init();
   }
-  if (warp == 1) {
-    tc::tmem_alloc(tmem_at, 512);
-    tc::tmem_relinquish();
-  }
+  if (warp == 1) tmem_take<CG>(tmem_at);
   tc::tc_fence_before();
   __syncthreads();
+  __syncwarp();
+  if (CG == 2) cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_at;
   // the list (or the cleared status word) and everything before it is there
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = tile_total<MODE>(a);
+  const int total = tile_total<MODE, CG>(a);
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       uint32_t it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const Tile w = tile_at<MODE>(a, t);
-        const int boxes = (w.n + 63) / 64;
+      TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
+      for (int t = first; ok && t < total; t += step) {
+        const Tile w = tile_at<MODE, CG>(a, t, ahead);
+        ahead = tile_raw<MODE, CG>(a, t + step, total);
+        // this block's columns
+        const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
+        const int boxes = (cols + 63) / 64, at = (int)rank * cols;
+        const int i0 = w.i0 + (int)rank * kTileM;
         for (int l = 0; l < w.len; l += kTileK, ++it) {
-          const int s = it % kStages;
-          if (it >= kStages && !tc::mbar_wait(&empty[s], ((it / kStages) - 1) & 1, kWait)) {
-            raise_status(a.st, GMM_ERR_TIMEOUT);
+          const int s = it % S;
+          if (it >= S && !wait_on<CG>(&empty[s], ((it / S) - 1) & 1)) {
+            // the wait took far longer than the copies in flight can
+            if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
             ok = false;
             break;
           }
-          uint8_t* p = smem + s * kStageBytes;
-          uint8_t* q = p + kTileM * kTileK * 2;
-          tc::mbar_arrive_expect_tx(&full[s], (2 + boxes) * kBox);
-          if (MODE == kProduct) {
-            tma_3d(p, &map_p, l, w.i0, w.k, &full[s]);
-            tma_3d(p + kBox, &map_p, l, w.i0 + 64, w.k, &full[s]);
-          } else if (MODE == kDx) {
-            tma_3d(p, &map_p, w.i0, l, w.k, &full[s]);
-            tma_3d(p + kBox, &map_p, w.i0 + 64, l, w.k, &full[s]);
-          } else {
-            tma_2d(p, &map_p, w.i0, (int)w.row0 + l, &full[s]);
-            tma_2d(p + kBox, &map_p, w.i0 + 64, (int)w.row0 + l, &full[s]);
+          if (elect_one()) {
+            uint8_t* p = smem + s * B;
+            uint8_t* q = p + kTileM * kTileK * 2;
+            uint32_t bar = tc::smem_addr(&full[s]);
+            // the end of a component whose rows have to be zeroed first (below)
+            const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
+            const uint32_t bytes = (2 + boxes) * kBox;
+            if (CG == 1 || rank == 0) tc::mbar_arrive_expect_tx(&full[s], CG == 2 && !odd ? 2 * bytes : bytes);
+            else if (odd) tc::mbar_arrive_expect_tx(&full[s], bytes);  // its own barrier
+            else bar = in_block(&full[s], 0);
+            constexpr bool PAIR = CG == 2;
+            if (MODE == kProduct) {
+              tma_3d<PAIR>(p, &map_p, l, i0, w.k, bar);
+              tma_3d<PAIR>(p + kBox, &map_p, l, i0 + 64, w.k, bar);
+            } else if (MODE == kDx) {
+              tma_3d<PAIR>(p, &map_p, i0, l, w.k, bar);
+              tma_3d<PAIR>(p + kBox, &map_p, i0 + 64, l, w.k, bar);
+            } else {
+              tma_2d<PAIR>(p, &map_p, i0, (int)w.row0 + l, bar);
+              tma_2d<PAIR>(p + kBox, &map_p, i0 + 64, (int)w.row0 + l, bar);
+            }
+            for (int b = 0; b < boxes; ++b) {
+              if (MODE == kDw) tma_2d<PAIR>(q + b * kBox, &map_q, w.j0 + at + 64 * b, (int)w.row0 + l, bar);
+              else tma_2d<PAIR>(q + b * kBox, &map_q, l, (int)w.row0 + at + 64 * b, bar);
+            }
           }
-          for (int b = 0; b < boxes; ++b) {
-            if (MODE == kDw) tma_2d(q + b * kBox, &map_q, w.j0 + 64 * b, (int)w.row0 + l, &full[s]);
-            else tma_2d(q + b * kBox, &map_q, l, (int)w.row0 + 64 * b, &full[s]);
-          }
+          __syncwarp();
         }
       }
-      if (!ok)  // the copies in flight end before the block does
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-          tc::mbar_wait(&full[i % kStages], (i / kStages) & 1, kWait);
     }
-  } else if (warp == 1) {
-    uint32_t it = 0, acc = 0;
+  } else if (warp == 1 && rank == 0) {
+    uint32_t it = 0, acc = 0, odds = 0;  // odds: a bit for each of `zeroed`
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const Tile w = tile_at<MODE>(a, t);
+    TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
+    for (int t = first; ok && t < total; t += step) {
+      const Tile w = tile_at<MODE, CG>(a, t, ahead);
+      ahead = tile_raw<MODE, CG>(a, t + step, total);
       if (w.len == 0) continue;
       const int b = acc & 1;
-      if (acc >= 2 && !tc::mbar_wait(&acc_empty[b], ((acc >> 1) - 1) & 1, kWait)) ok = false;
+      if (acc >= 2 && !wait_on<CG>(&acc_empty[b], ((acc >> 1) - 1) & 1)) ok = false;
       const uint32_t d = tmem + b * kTileN;
-      const int n = (w.n + 15) & ~15;
-      const uint32_t id = idesc(std::is_same<T, __nv_bfloat16>::value, kPmn, kQmn, n);
+      const int n = CG == 2 ? (w.n + 31) & ~31 : (w.n + 15) & ~15;
+      const uint32_t id = idesc(std::is_same<T, __nv_bfloat16>::value, kPmn, kQmn, CG * kTileM, n);
       for (int l = 0; ok && l < w.len; l += kTileK, ++it) {
-        const int s = it % kStages;
-        if (!tc::mbar_wait(&full[s], (it / kStages) & 1, kWait)) {
+        const int s = it % S;
+        if (!wait_on<CG>(&full[s], (it / S) & 1)) {
           ok = false;
           break;
         }
-        uint8_t* p = smem + s * kStageBytes;
-        uint8_t* q = p + kTileM * kTileK * 2;
+        uint8_t* p = smem + s * B;
         const int left = min(kTileK, w.len - l);
         const int steps = (left + 15) / 16;
+        // rows of the next component, up to the next 16
         if (MODE == kDw && left < 16 * steps) {
-          // rows of the next component, up to the next 16: 128 bytes of each box
-          const int rows = 16 * steps - left, boxes = 2 + (w.n + 63) / 64;
-          for (int x = lane; x < boxes * rows * 8; x += 32) {
-            const int box = x / (rows * 8), r = left + (x / 8) % rows, c = x & 7;
-            *reinterpret_cast<uint4*>(p + box * kBox + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          zero_rows(p, 2 + (n / CG + 63) / 64, left, 16 * steps - left);
+          if (CG == 2) {
+            if (!wait_on<CG>(&zeroed[s], (odds >> s) & 1)) {
+              ok = false;
+              break;
+            }
+            odds ^= 1u << s;
           }
-          tc::fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) {
-          tc::tc_fence_after();
-          const uint32_t ps = tc::smem_addr(p), qs = tc::smem_addr(q);
-          for (int x = 0; x < steps; ++x) {
-            const uint64_t dp = kPmn ? sdesc_mn128(ps + x * 2048) : tc::sdesc_k128(ps + x * 32);
-            const uint64_t dq = kQmn ? sdesc_mn128(qs + x * 2048) : tc::sdesc_k128(qs + x * 32);
-            tc::mma_f16(d, dp, dq, id, (l > 0 || x > 0) ? 1u : 0u);
-          }
-          tc::mma_commit(&empty[s]);
-          if (l + kTileK >= w.len) tc::mma_commit(&acc_full[b]);
+        tc::tc_fence_after();
+        const uint32_t ps = tc::smem_addr(p), qs = ps + kTileM * kTileK * 2;
+        const uint64_t dp = kPmn ? sdesc_mn128(ps) : tc::sdesc_k128(ps);
+        const uint64_t dq = kQmn ? sdesc_mn128(qs) : tc::sdesc_k128(qs);
+        // a descriptor's address counts 16 bytes: 16 terms on
+        constexpr int kP = (kPmn ? 2048 : 32) / 16, kQ = (kQmn ? 2048 : 32) / 16;
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < kTileK / 16; ++x)
+            if (x < steps) mma<CG>(d, dp + x * kP, dq + x * kQ, id, (l > 0 || x > 0) ? 1u : 0u);
+          commit<CG>(&empty[s]);
+          if (l + kTileK >= w.len) commit<CG>(&acc_full[b]);
         }
         __syncwarp();
       }
       ++acc;
     }
     if (!ok && lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
+  } else if (warp == 1) {
+    // the second block of a pair: zeroes its share of the rows that belong to
+    // the next component, then tells the first
+    if (MODE == kDw) {
+      uint32_t it = 0, phases = 0;  // a bit for each stage's own barrier
+      TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
+      for (int t = first; t < total; t += step) {
+        const Tile w = tile_at<MODE, CG>(a, t, ahead);
+        ahead = tile_raw<MODE, CG>(a, t + step, total);
+        const int blocks = (w.len + kTileK - 1) / kTileK;
+        it += blocks;
+        const int left = w.len - (blocks - 1) * kTileK;
+        if (blocks == 0 || left % 16 == 0) continue;
+        const int s = (it - 1) % S;
+        if (!wait_on<CG>(&full[s], (phases >> s) & 1)) {
+          if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
+          break;
+        }
+        phases ^= 1u << s;
+        const int cols = ((w.n + 31) & ~31) / 2;
+        zero_rows(smem + s * B, 2 + (cols + 63) / 64, left, (left + 15) / 16 * 16 - left);
+        if (lane == 0) arrive_release_at(in_block(&zeroed[s], 0));
+        __syncwarp();
+      }
+    }
   } else {
     const int quarter = warp & 3;  // the TMEM lanes this warp may read
     uint32_t acc = 0, piece = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const Tile w = tile_at<MODE>(a, t);
+    TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
+    for (int t = first; t < total; t += step) {
+      Tile w = tile_at<MODE, CG>(a, t, ahead);
+      ahead = tile_raw<MODE, CG>(a, t + step, total);
+      w.i0 += (int)rank * kTileM;
       const int b = acc & 1;
       const int f = w.i0 + quarter * 32 + lane;
       if (w.len > 0) {
-        if (!tc::mbar_wait(&acc_full[b], (acc >> 1) & 1, kWait)) {
+        if (!wait_on<CG>(&acc_full[b], (acc >> 1) & 1)) {
           if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
           break;
         }
@@ -367,16 +580,21 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
       if (w.len > 0) {
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&acc_empty[b]);
+        if (lane == 0) {
+          if (CG == 2) arrive_at(in_block(&acc_empty[b], 0));
+          else tc::mbar_arrive(&acc_empty[b]);
+        }
         ++acc;
       }
     }
     if (MODE == kDw && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncthreads();
+  __syncwarp();
+  if (CG == 2) cluster_sync();  // neither block leaves while the other may reach it
   if (warp == 1) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(tmem, 512);
+    tmem_give<CG>(tmem);
   }
 }
 
@@ -422,28 +640,46 @@ int multiprocessors() {
   return n;
 }
 
-template <int MODE, typename T, typename TO>
-gmm_status go(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, void* out,
-              const TcArgs& a, int64_t most, cudaStream_t s) {
+template <int MODE, typename T, typename TO, int CG>
+gmm_status go_as(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, void* out,
+                 const TcArgs& a, int64_t most, cudaStream_t s) {
   const int sms = multiprocessors();
-  if (sms < 1 || cudaFuncSetAttribute(expert_tc_kernel<MODE, T, TO>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+  if (sms < CG || cudaFuncSetAttribute(expert_tc_kernel<MODE, T, TO, CG>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return GMM_ERR_CUDA;
-  const unsigned grid = (unsigned)(most < sms ? most : sms);
+  const int64_t tiles = most * ((a.d_to + CG * kTileM - 1) / (CG * kTileM));
+  const unsigned grid = (unsigned)(tiles < sms / CG ? tiles : sms / CG) * CG;
   ProfScope p(MODE == kProduct ? "expert_tc_kernel" : MODE == kDx ? "expert_tc_kernel(dx)" : "expert_tc_kernel(dw)", s);
   // may start while the kernel that makes its list runs
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, expert_tc_kernel<MODE, T, TO>, mp, mq, mo, (TO*)out, a);
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, expert_tc_kernel<MODE, T, TO, CG>, mp, mq, mo, (TO*)out, a);
   return launched();
+}
+
+// Pairs where the 256 rows of a tile are all there, or nearly so.
+bool pairs(int d_to) {
+  const int t = (d_to + 255) / 256 * 256;
+  return (t - d_to) * 8 <= t;
+}
+
+// most: row tiles at most (dw: components x column tiles).
+template <int MODE, typename T, typename TO>
+gmm_status go(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, void* out,
+              const TcArgs& a, int64_t most, cudaStream_t s) {
+  return pairs(a.d_to) ? go_as<MODE, T, TO, 2>(mp, mq, mo, out, a, most, s)
+                       : go_as<MODE, T, TO, 1>(mp, mq, mo, out, a, most, s);
 }
 
 }  // namespace
@@ -464,7 +700,8 @@ gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R,
     return GMM_ERR_CUDA;
   TcArgs a{offsets, at<int32_t>(ws, L.off_count), at<int4>(ws, L.off_tiles), at<DeviceStatus>(ws, 0),
            R, K, d_from, d_to};
-  const int64_t most = ProductLayout::most_tiles(R, K, kTileN) * ((d_to + kTileM - 1) / kTileM);
+  const int64_t most = ProductLayout::most_tiles(R, K, kTileN);
+  if (most * ((d_to + kTileM - 1) / kTileM) > INT32_MAX) return GMM_ERR_UNSUPPORTED;
   if (xdtype == GMM_BF16) {
     using T = __nv_bfloat16;
     return dx ? go<kDx, T, T>(mp, mq, mq, Y, a, most, s) : go<kProduct, T, T>(mp, mq, mq, Y, a, most, s);
@@ -483,9 +720,8 @@ gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int 
   const gmm_status r = clear_status(ws, s);
   if (r != GMM_OK) return r;
   TcArgs a{offsets, nullptr, nullptr, at<DeviceStatus>(ws, 0), R, K, d_in, d_out};
-  const int64_t most =
-      (int64_t)K * ((d_out + kTileM - 1) / kTileM) * ((d_in + kTileN - 1) / kTileN);
-  if (most > INT32_MAX) return GMM_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)K * ((d_in + kTileN - 1) / kTileN);
+  if (most * ((d_out + kTileM - 1) / kTileM) > INT32_MAX) return GMM_ERR_UNSUPPORTED;
   if (xdtype == GMM_BF16) {
     using T = __nv_bfloat16;
     return wdtype == GMM_F32 ? go<kDw, T, float>(mp, mq, mo, dW, a, most, s) : go<kDw, T, T>(mp, mq, mo, dW, a, most, s);
