@@ -16,6 +16,7 @@ namespace {
 constexpr int kT = 64;        // tile rows and columns of the CUDA-core kernel
 constexpr int kStep = 16;
 constexpr int kListThreads = 1024;
+constexpr int kListSmem = 4096;   // components whose first tiles fit in shared memory
 
 // Row tiles of T rows for every component, in order, then those of the rows
 // past offsets[K] (component -1: zeros).  Offsets are held within [0, R].
@@ -29,6 +30,7 @@ tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
   if (!tiles) return;
+  __shared__ uint32_t before[kListSmem + 1];
   const int G = K + 1;
   const int per = (G + kListThreads - 1) / kListThreads;
   const int k0 = min(G, (int)threadIdx.x * per), k1 = min(G, k0 + per);
@@ -38,6 +40,33 @@ tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T,
     if (b > a) mine += (uint32_t)((b - a + T - 1) / T);
   }
   uint32_t at = block_exclusive_1024(mine, wsum);
+  if (G <= kListSmem) {
+    // every thread writes tiles: the component of tile t is the last one that
+    // starts at or before it
+    for (int k = k0; k < k1; ++k) {
+      const int64_t a = clamp_row(offsets[k], R), b = k < K ? clamp_row(offsets[k + 1], R) : R;
+      before[k] = at;
+      if (b > a) at += (uint32_t)((b - a + T - 1) / T);
+    }
+    if (k1 == G && k0 < k1) {
+      before[G] = at;
+      *count = (int32_t)at;
+    }
+    __syncthreads();
+    const uint32_t total = before[G];
+    for (uint32_t t = threadIdx.x; t < total; t += kListThreads) {
+      int lo = 0, hi = G - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const int64_t a = clamp_row(offsets[lo], R), b = lo < K ? clamp_row(offsets[lo + 1], R) : R;
+      const int64_t r = a + (int64_t)(t - before[lo]) * T;
+      tiles[t] = make_int4(lo < K ? lo : -1, (int)r, (int)min((int64_t)T, b - r), 0);
+    }
+    return;
+  }
   for (int k = k0; k < k1; ++k) {
     const int64_t a = clamp_row(offsets[k], R), b = k < K ? clamp_row(offsets[k + 1], R) : R;
     for (int64_t r = a; r < b; r += T)

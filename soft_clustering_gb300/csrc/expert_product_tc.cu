@@ -37,10 +37,12 @@ constexpr int kTileM = 128, kTileN = 256, kTileK = 64;   // kTileM: of one block
 constexpr int kRing = 192 * 1024;          // stages: 4 of 48 KB, or 6 of 32 KB in a pair
 template <int CG> constexpr int kStageBytes = (kTileM + kTileN / CG) * kTileK * 2;
 template <int CG> constexpr int kStages = kRing / kStageBytes<CG>;
-constexpr int kThreads = 192;              // fetch, issue, four read back
-constexpr int kOutBytes = 4096;            // 32 rows x 128 bytes of dW on their way out
-constexpr int kOutAt = kRing;              // two for each read-back warp
-constexpr int kBarsAt = kOutAt + 4 * 2 * kOutBytes;
+constexpr int kBackWarps = 8;              // two for each quarter of the accumulator's lanes
+constexpr int kThreads = 64 + 32 * kBackWarps;  // fetch, issue, read back
+constexpr int kOutBytes = 4096;            // what a read-back warp has on its way out
+constexpr int kOutPitch = 80;              // bytes of a staged row of 32 outputs: no bank conflicts
+constexpr int kOutAt = kRing;
+constexpr int kBarsAt = kOutAt + kBackWarps * kOutBytes;
 constexpr int kSmem = kBarsAt + 256 + 1024;
 constexpr uint32_t kWait = 2000000;        // polls of up to a microsecond
 constexpr uint64_t kWaitNs = 2000000000;   // of a pair
@@ -62,59 +64,68 @@ struct Tile {
   int64_t row0;
 };
 
+// The tiles of one block (or pair), every `step`-th from `first`: row tiles
+// (dw: components) k, feature tiles i, and for dw column tiles j, the last
+// one running fastest.  What of a tile comes from memory is fetched a tile
+// ahead, and no division is done per tile: every role walks for itself, and
+// the time between a tile's last product and the next one's first is idle.
 template <int MODE, int CG>
-__device__ __forceinline__ int tile_total(const TcArgs& a) {
-  const int mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
-  if (MODE == kDw) return a.K * mt * ((a.d_from + kTileN - 1) / kTileN);
-  return *a.count * mt;
-}
-
-// What of a tile has to come from memory; fetched a tile ahead by every role.
-struct TileRaw {
+struct Walk {
+  int mt, nt, limit, k, i, j, dk, di, dj;
   int4 q;
   int64_t b, e;
-};
-template <int MODE, int CG>
-__device__ __forceinline__ TileRaw tile_raw(const TcArgs& a, int t, int total) {
-  TileRaw r;
-  r.q = make_int4(-1, 0, 0, 0);
-  r.b = r.e = 0;
-  if (t < total) {
-    const int mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
+  __device__ __forceinline__ Walk(const TcArgs& a, int first, int step) {
+    mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
+    nt = MODE == kDw ? (a.d_from + kTileN - 1) / kTileN : 1;
+    limit = MODE == kDw ? a.K : *a.count;
+    j = first % nt;
+    i = first / nt % mt;
+    k = first / nt / mt;
+    dj = step % nt;
+    di = step / nt % mt;
+    dk = step / nt / mt;
+    q = make_int4(-1, 0, 0, 0);
+    b = e = 0;
+    fetch(a);
+  }
+  __device__ __forceinline__ void fetch(const TcArgs& a) {
+    if (k >= limit) return;
     if (MODE == kDw) {
-      const int k = t / (mt * ((a.d_from + kTileN - 1) / kTileN));
-      r.b = a.offsets[k];
-      r.e = a.offsets[k + 1];
+      b = a.offsets[k];
+      e = a.offsets[k + 1];
     } else {
-      r.q = a.tiles[t / mt];
+      q = a.tiles[k];
     }
   }
-  return r;
-}
-template <int MODE, int CG>
-__device__ __forceinline__ Tile tile_at(const TcArgs& a, int t, const TileRaw& raw) {
-  Tile w;
-  const int mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
-  if (MODE == kDw) {
-    const int nt = (a.d_from + kTileN - 1) / kTileN;
-    w.k = t / (mt * nt);
-    const int r = t % (mt * nt);
-    w.i0 = (r / nt) * CG * kTileM;
-    w.j0 = (r % nt) * kTileN;
-    w.n = min(kTileN, a.d_from - w.j0);
-    const int64_t b = clamp_row(raw.b, a.R), e = clamp_row(raw.e, a.R);
-    w.row0 = b;
-    w.len = e > b ? (int)(e - b) : 0;
-  } else {
-    w.k = raw.q.x;
-    w.row0 = raw.q.y;
-    w.n = raw.q.z;
-    w.i0 = (t % mt) * CG * kTileM;
-    w.j0 = 0;
-    w.len = raw.q.x < 0 ? 0 : a.d_from;
+  __device__ __forceinline__ bool more() const { return k < limit; }
+  __device__ __forceinline__ Tile take(const TcArgs& a) {
+    Tile w;
+    w.i0 = i * CG * kTileM;
+    if (MODE == kDw) {
+      w.k = k;
+      w.j0 = j * kTileN;
+      w.n = min(kTileN, a.d_from - w.j0);
+      const int64_t lo = clamp_row(b, a.R), hi = clamp_row(e, a.R);
+      w.row0 = lo;
+      w.len = hi > lo ? (int)(hi - lo) : 0;
+    } else {
+      w.k = q.x;
+      w.row0 = q.y;
+      w.n = q.z;
+      w.j0 = 0;
+      w.len = q.x < 0 ? 0 : a.d_from;
+    }
+    if (MODE == kDw) {
+      j += dj;
+      if (j >= nt) { j -= nt; ++i; }
+    }
+    i += di;
+    if (i >= mt) { i -= mt; ++k; }
+    k += dk;
+    fetch(a);
+    return w;
   }
-  return w;
-}
+};
 
 // TMA of one box.  `bar`: a shared::cluster address; with PAIR it may be the
 // other block's of the pair.
@@ -292,22 +303,65 @@ template <> struct Pair<__nv_bfloat16> {
   }
 };
 
-// 32 columns (rows of the output) of this lane's feature; lanes exchange so
-// that each holds two neighbouring features of every other row.
+// Accumulator lanes `lanes` .. + 15 of 32 columns: register 4 c + 2 u + v is
+// lane 8 u + t / 4, column 8 c + 2 (t % 4) + v of thread t.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// 32 features x 32 columns of the accumulator (from `src`) as 32 rows of 32
+// outputs: transposed on their way into the warp's piece of shared memory (8 x
+// 8 at a time), then 64 bytes a row to memory.  `left` rows and `feats`
+// features of them are wanted (feats a multiple of 8).
 template <typename TO>
-__device__ __forceinline__ void store_rows(const float* v, TO* out, int64_t ld, int f, int d_to,
-                                           int left) {
+__device__ __forceinline__ void store_rows(uint32_t src, bool some, uint8_t* piece, TO* out, int64_t ld,
+                                           int left, int feats) {
   const int lane = threadIdx.x & 31;
-  const bool odd = lane & 1;
-  const bool live = f < d_to;  // d_to is even
-  TO* p = out + (f & ~1);
+  if (some) {
+    uint32_t r[2][16];
+    tmem_ld16x32(src, r[0]);
+    tmem_ld16x32(src + (16u << 16), r[1]);
+    tmem_wait16(r[0]);
+    tmem_wait16(r[1]);
+    uint32_t at = tc::smem_addr(piece) + (lane & 7) * kOutPitch + (lane >> 3) * 16;
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-    const uint32_t w = odd ? Pair<TO>::pack(got, v[j + 1]) : Pair<TO>::pack(v[j], got);
-    const int r = j + (odd ? 1 : 0);
-    if (live && r < left) *reinterpret_cast<uint32_t*>(p + (int64_t)r * ld) = w;
+    for (int c = 0; c < 4; ++c) {
+      uint32_t h[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        h[x] = Pair<TO>::pack(__uint_as_float(r[x >> 1][4 * c + 2 * (x & 1)]),
+                              __uint_as_float(r[x >> 1][4 * c + 2 * (x & 1) + 1]));
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                       at + c * 8 * kOutPitch),
+                   "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
+    }
+    __syncwarp();
   }
+  const int row = lane >> 2, chunk = lane & 3;
+  TO* p = out + row * ld + chunk * 8;
+  const bool mine = chunk * 8 < feats;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (some) v = *reinterpret_cast<const uint4*>(piece + (8 * x + row) * kOutPitch + chunk * 16);
+    if (mine && 8 * x + row < left) *reinterpret_cast<uint4*>(p + 8 * x * ld) = v;
+  }
+  __syncwarp();
 }
 
 // 128 bytes of this lane's row of dW (64 or 32 columns) into the warp's piece
@@ -368,7 +422,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&acc_full[i], 1);
-      tc::mbar_init(&acc_empty[i], 4 * CG);
+      tc::mbar_init(&acc_empty[i], kBackWarps * CG);
     }
     tc::mbar_fence_init();
   }
@@ -381,65 +435,58 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   const uint32_t tmem = *tmem_at;
   // the list (or the cleared status word) and everything before it is there
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = tile_total<MODE, CG>(a);
 
   if (warp == 0) {
-    {
-      uint32_t it = 0;
-      bool ok = true;
-      TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
-      for (int t = first; ok && t < total; t += step) {
-        const Tile w = tile_at<MODE, CG>(a, t, ahead);
-        ahead = tile_raw<MODE, CG>(a, t + step, total);
-        // this block's columns
-        const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
-        const int boxes = (cols + 63) / 64, at = (int)rank * cols;
-        const int i0 = w.i0 + (int)rank * kTileM;
-        for (int l = 0; l < w.len; l += kTileK, ++it) {
-          const int s = it % S;
-          if (it >= S && !wait_on<CG>(&empty[s], ((it / S) - 1) & 1)) {
-            // the wait took far longer than the copies in flight can
-            if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            uint8_t* p = smem + s * B;
-            uint8_t* q = p + kTileM * kTileK * 2;
-            uint32_t bar = tc::smem_addr(&full[s]);
-            // the end of a component whose rows have to be zeroed first (below)
-            const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
-            const uint32_t bytes = (2 + boxes) * kBox;
-            if (CG == 1 || rank == 0) tc::mbar_arrive_expect_tx(&full[s], CG == 2 && !odd ? 2 * bytes : bytes);
-            else if (odd) tc::mbar_arrive_expect_tx(&full[s], bytes);  // its own barrier
-            else bar = in_block(&full[s], 0);
-            constexpr bool PAIR = CG == 2;
-            if (MODE == kProduct) {
-              tma_3d<PAIR>(p, &map_p, l, i0, w.k, bar);
-              tma_3d<PAIR>(p + kBox, &map_p, l, i0 + 64, w.k, bar);
-            } else if (MODE == kDx) {
-              tma_3d<PAIR>(p, &map_p, i0, l, w.k, bar);
-              tma_3d<PAIR>(p + kBox, &map_p, i0 + 64, l, w.k, bar);
-            } else {
-              tma_2d<PAIR>(p, &map_p, i0, (int)w.row0 + l, bar);
-              tma_2d<PAIR>(p + kBox, &map_p, i0 + 64, (int)w.row0 + l, bar);
-            }
-            for (int b = 0; b < boxes; ++b) {
-              if (MODE == kDw) tma_2d<PAIR>(q + b * kBox, &map_q, w.j0 + at + 64 * b, (int)w.row0 + l, bar);
-              else tma_2d<PAIR>(q + b * kBox, &map_q, l, (int)w.row0 + at + 64 * b, bar);
-            }
-          }
-          __syncwarp();
+    uint32_t it = 0;
+    bool ok = true;
+    for (Walk<MODE, CG> walk(a, first, step); ok && walk.more();) {
+      const Tile w = walk.take(a);
+      // this block's columns
+      const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
+      const int boxes = (cols + 63) / 64, at = (int)rank * cols;
+      const int i0 = w.i0 + (int)rank * kTileM;
+      for (int l = 0; l < w.len; l += kTileK, ++it) {
+        const int s = it % S;
+        if (it >= S && !wait_on<CG>(&empty[s], ((it / S) - 1) & 1)) {
+          // the wait took far longer than the copies in flight can
+          if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
+          ok = false;
+          break;
         }
+        if (elect_one()) {
+          uint8_t* p = smem + s * B;
+          uint8_t* q = p + kTileM * kTileK * 2;
+          uint32_t bar = tc::smem_addr(&full[s]);
+          // the end of a component whose rows have to be zeroed first (below)
+          const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
+          const uint32_t bytes = (2 + boxes) * kBox;
+          if (CG == 1 || rank == 0) tc::mbar_arrive_expect_tx(&full[s], CG == 2 && !odd ? 2 * bytes : bytes);
+          else if (odd) tc::mbar_arrive_expect_tx(&full[s], bytes);  // its own barrier
+          else bar = in_block(&full[s], 0);
+          constexpr bool PAIR = CG == 2;
+          if (MODE == kProduct) {
+            tma_3d<PAIR>(p, &map_p, l, i0, w.k, bar);
+            tma_3d<PAIR>(p + kBox, &map_p, l, i0 + 64, w.k, bar);
+          } else if (MODE == kDx) {
+            tma_3d<PAIR>(p, &map_p, i0, l, w.k, bar);
+            tma_3d<PAIR>(p + kBox, &map_p, i0 + 64, l, w.k, bar);
+          } else {
+            tma_2d<PAIR>(p, &map_p, i0, (int)w.row0 + l, bar);
+            tma_2d<PAIR>(p + kBox, &map_p, i0 + 64, (int)w.row0 + l, bar);
+          }
+          for (int b = 0; b < boxes; ++b) {
+            if (MODE == kDw) tma_2d<PAIR>(q + b * kBox, &map_q, w.j0 + at + 64 * b, (int)w.row0 + l, bar);
+            else tma_2d<PAIR>(q + b * kBox, &map_q, l, (int)w.row0 + at + 64 * b, bar);
+          }
+        }
+        __syncwarp();
       }
     }
   } else if (warp == 1 && rank == 0) {
     uint32_t it = 0, acc = 0, odds = 0;  // odds: a bit for each of `zeroed`
     bool ok = true;
-    TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
-    for (int t = first; ok && t < total; t += step) {
-      const Tile w = tile_at<MODE, CG>(a, t, ahead);
-      ahead = tile_raw<MODE, CG>(a, t + step, total);
+    for (Walk<MODE, CG> walk(a, first, step); ok && walk.more();) {
+      const Tile w = walk.take(a);
       if (w.len == 0) continue;
       const int b = acc & 1;
       if (acc >= 2 && !wait_on<CG>(&acc_empty[b], ((acc >> 1) - 1) & 1)) ok = false;
@@ -490,10 +537,8 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
     // the next component, then tells the first
     if (MODE == kDw) {
       uint32_t it = 0, phases = 0;  // a bit for each stage's own barrier
-      TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
-      for (int t = first; t < total; t += step) {
-        const Tile w = tile_at<MODE, CG>(a, t, ahead);
-        ahead = tile_raw<MODE, CG>(a, t + step, total);
+      for (Walk<MODE, CG> walk(a, first, step); walk.more();) {
+        const Tile w = walk.take(a);
         const int blocks = (w.len + kTileK - 1) / kTileK;
         it += blocks;
         const int left = w.len - (blocks - 1) * kTileK;
@@ -511,15 +556,14 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
       }
     }
   } else {
-    const int quarter = warp & 3;  // the TMEM lanes this warp may read
-    uint32_t acc = 0, piece = 0;
-    TileRaw ahead = tile_raw<MODE, CG>(a, first, total);
-    for (int t = first; t < total; t += step) {
-      Tile w = tile_at<MODE, CG>(a, t, ahead);
-      ahead = tile_raw<MODE, CG>(a, t + step, total);
-      w.i0 += (int)rank * kTileM;
+    const int quarter = warp & 3;       // the TMEM lanes this warp may read
+    const int half = (warp - 2) >> 2;   // every other stretch of columns
+    uint8_t* piece = smem + kOutAt + (warp - 2) * kOutBytes;
+    uint32_t acc = 0;
+    for (Walk<MODE, CG> walk(a, first, step); walk.more();) {
+      const Tile w = walk.take(a);
       const int b = acc & 1;
-      const int f = w.i0 + quarter * 32 + lane;
+      const int i0 = w.i0 + (int)rank * kTileM + quarter * 32;
       if (w.len > 0) {
         if (!wait_on<CG>(&acc_full[b], (acc >> 1) & 1)) {
           if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
@@ -529,12 +573,10 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
       }
       const uint32_t src = tmem + b * kTileN + ((uint32_t)(quarter * 32) << 16);
       if constexpr (MODE == kDw) {
-        // pieces of 32 rows x 128 bytes, two in flight; the tensor map cuts
-        // off what is past dW's edges
+        // 32 rows x 128 bytes at a time; the tensor map cuts off what is past
+        // dW's edges
         constexpr int W = 128 / sizeof(TO);
-        uint8_t* pieces = smem + kOutAt + quarter * 2 * kOutBytes;
-        const int y = w.i0 + quarter * 32;
-        for (int c = 0; c < w.n && y < a.d_to; c += W, ++piece) {
+        for (int c = half * W; c < w.n && i0 < a.d_to; c += 2 * W) {
           uint32_t r[2][32];
           if (w.len > 0) {
             tc::tmem_ld32_issue(src + c, r[0]);
@@ -553,29 +595,21 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
             for (int j = 0; j < 16; ++j)
               r[0][16 + j] = Pair<TO>::pack(__uint_as_float(r[1][2 * j]), __uint_as_float(r[1][2 * j + 1]));
           }
-          uint8_t* at = pieces + (piece & 1) * kOutBytes;
-          if (lane == 0)  // the store before the last one has read its piece
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          if (lane == 0)  // the last store has read the piece
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
-          stage_line(r[0], at);
+          stage_line(r[0], piece);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&map_out, at, w.j0 + c, y, w.k);
+            tma_store_3d(&map_out, piece, w.j0 + c, i0, w.k);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         }
-      } else {
-        for (int c = 0; c < w.n; c += 32) {
-          float v[32];
-          if (w.len > 0) {
-            tc::tmem_ld32(src + c, v);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
-          }
-          store_rows(v, out + (w.row0 + c) * (int64_t)a.d_to, a.d_to, f, a.d_to, w.n - c);
-        }
+      } else if (i0 < a.d_to) {
+        for (int c = half * 32; c < w.n; c += 64)
+          store_rows(src + c, w.len > 0, piece, out + (w.row0 + c) * (int64_t)a.d_to + i0, a.d_to,
+                     w.n - c, a.d_to - i0);
       }
       if (w.len > 0) {
         tc::tc_fence_before();
