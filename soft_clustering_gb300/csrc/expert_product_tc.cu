@@ -38,7 +38,8 @@ constexpr int kRing = 192 * 1024;          // stages: 4 of 48 KB, or 6 of 32 KB 
 template <int CG> constexpr int kStageBytes = (kTileM + kTileN / CG) * kTileK * 2;
 template <int CG> constexpr int kStages = kRing / kStageBytes<CG>;
 constexpr int kBackWarps = 8;              // two for each quarter of the accumulator's lanes
-constexpr int kThreads = 64 + 32 * kBackWarps;  // fetch, issue, read back
+constexpr int kThreads = 64 + 32 * kBackWarps + 32;  // fetch, issue, read back, mend
+constexpr int kMendWarp = 2 + kBackWarps;  // dw: zeroes rows of the next component
 constexpr int kOutBytes = 4096;            // what a read-back warp has on its way out
 constexpr int kOutPitch = 80;              // bytes of a staged row of 32 outputs: no bank conflicts
 constexpr int kOutAt = kRing;
@@ -384,10 +385,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 
 // Rows left .. left + rows - 1 of `boxes` boxes from p: zeros (128 bytes each).
 __device__ __forceinline__ void zero_rows(uint8_t* p, int boxes, int left, int rows) {
-  for (int x = threadIdx.x & 31; x < boxes * rows * 8; x += 32) {
-    const int box = x / (rows * 8), r = left + (x / 8) % rows, c = x & 7;
-    *reinterpret_cast<uint4*>(p + box * kBox + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-  }
+  const int lane = threadIdx.x & 31;
+  for (int box = 0; box < boxes; ++box)
+    for (int r = lane >> 3; r < rows; r += 4)
+      *reinterpret_cast<uint4*>(p + box * kBox + (left + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async_smem();
   __syncwarp();
 }
@@ -407,8 +408,8 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;         // [2]
   uint64_t* acc_empty = acc_full + 2;     // [2]
-  uint64_t* zeroed = acc_empty + 2;       // [S] the second block of a pair has zeroed its rows
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(zeroed + S);
+  uint64_t* odd_full = acc_empty + 2;     // [S] there, but with rows to be zeroed first
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(odd_full + S);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kPmn = MODE != kProduct, kQmn = MODE == kDw;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -416,9 +417,9 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&full[i], CG);  // the fetching warp, or both blocks' mending warps
       tc::mbar_init(&empty[i], 1);
-      tc::mbar_init(&zeroed[i], 1);
+      tc::mbar_init(&odd_full[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&acc_full[i], 1);
@@ -457,12 +458,18 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
           uint8_t* p = smem + s * B;
           uint8_t* q = p + kTileM * kTileK * 2;
           uint32_t bar = tc::smem_addr(&full[s]);
-          // the end of a component whose rows have to be zeroed first (below)
+          // the end of a component, with rows of the next one up to the next 16
           const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
           const uint32_t bytes = (2 + boxes) * kBox;
-          if (CG == 1 || rank == 0) tc::mbar_arrive_expect_tx(&full[s], CG == 2 && !odd ? 2 * bytes : bytes);
-          else if (odd) tc::mbar_arrive_expect_tx(&full[s], bytes);  // its own barrier
-          else bar = in_block(&full[s], 0);
+          if (odd) {
+            tc::mbar_arrive_expect_tx(&odd_full[s], bytes);
+            bar = tc::smem_addr(&odd_full[s]);
+          } else if (rank == 0) {
+            tc::mbar_arrive_expect_tx(&full[s], CG * bytes);
+            if (CG == 2) tc::mbar_arrive(&full[s]);
+          } else {
+            bar = in_block(&full[s], 0);
+          }
           constexpr bool PAIR = CG == 2;
           if (MODE == kProduct) {
             tma_3d<PAIR>(p, &map_p, l, i0, w.k, bar);
@@ -483,7 +490,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
       }
     }
   } else if (warp == 1 && rank == 0) {
-    uint32_t it = 0, acc = 0, odds = 0;  // odds: a bit for each of `zeroed`
+    uint32_t it = 0, acc = 0;
     bool ok = true;
     for (Walk<MODE, CG> walk(a, first, step); ok && walk.more();) {
       const Tile w = walk.take(a);
@@ -502,17 +509,6 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         uint8_t* p = smem + s * B;
         const int left = min(kTileK, w.len - l);
         const int steps = (left + 15) / 16;
-        // rows of the next component, up to the next 16
-        if (MODE == kDw && left < 16 * steps) {
-          zero_rows(p, 2 + (n / CG + 63) / 64, left, 16 * steps - left);
-          if (CG == 2) {
-            if (!wait_on<CG>(&zeroed[s], (odds >> s) & 1)) {
-              ok = false;
-              break;
-            }
-            odds ^= 1u << s;
-          }
-        }
         __syncwarp();
         tc::tc_fence_after();
         const uint32_t ps = tc::smem_addr(p), qs = ps + kTileM * kTileK * 2;
@@ -532,11 +528,11 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
       ++acc;
     }
     if (!ok && lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
-  } else if (warp == 1) {
-    // the second block of a pair: zeroes its share of the rows that belong to
-    // the next component, then tells the first
+  } else if (warp == kMendWarp) {
+    // ahead of the products: zeroes this block's rows of the next component
+    // in a component's last stage and passes the stage on
     if (MODE == kDw) {
-      uint32_t it = 0, phases = 0;  // a bit for each stage's own barrier
+      uint32_t it = 0, phases = 0;  // a bit for each stage's barrier
       for (Walk<MODE, CG> walk(a, first, step); walk.more();) {
         const Tile w = walk.take(a);
         const int blocks = (w.len + kTileK - 1) / kTileK;
@@ -544,18 +540,21 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         const int left = w.len - (blocks - 1) * kTileK;
         if (blocks == 0 || left % 16 == 0) continue;
         const int s = (it - 1) % S;
-        if (!wait_on<CG>(&full[s], (phases >> s) & 1)) {
+        if (!wait_on<CG>(&odd_full[s], (phases >> s) & 1)) {
           if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
           break;
         }
         phases ^= 1u << s;
-        const int cols = ((w.n + 31) & ~31) / 2;
+        const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
         zero_rows(smem + s * B, 2 + (cols + 63) / 64, left, (left + 15) / 16 * 16 - left);
-        if (lane == 0) arrive_release_at(in_block(&zeroed[s], 0));
+        if (lane == 0) {
+          if (CG == 2) arrive_release_at(in_block(&full[s], 0));
+          else tc::mbar_arrive(&full[s]);
+        }
         __syncwarp();
       }
     }
-  } else {
+  } else if (warp >= 2) {
     const int quarter = warp & 3;       // the TMEM lanes this warp may read
     const int half = (warp - 2) >> 2;   // every other stretch of columns
     uint8_t* piece = smem + kOutAt + (warp - 2) * kOutBytes;
