@@ -20,8 +20,8 @@ constexpr int kListSmem = 4096;   // components whose first tiles fit in shared 
 
 // Row tiles of T rows for every component, in order, then those of the rows
 // past offsets[K] (component -1: zeros).  Offsets are held within [0, R].
-// `tiles` NULL: the status word alone.  The kernel after it may start at once
-// (its set-up overlaps this one) and waits for this one's end itself.
+// The kernel after it may start at once (its set-up overlaps this one) and
+// waits for this one's end itself.
 __global__ void __launch_bounds__(kListThreads)
 tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T,
                  DeviceStatus* __restrict__ st, int32_t* __restrict__ count,
@@ -29,7 +29,6 @@ tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T,
   __shared__ uint32_t wsum[32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
-  if (!tiles) return;
   __shared__ uint32_t before[kListSmem + 1];
   const int G = K + 1;
   const int per = (G + kListThreads - 1) / kListThreads;
@@ -215,11 +214,6 @@ gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
   return launched();
 }
 
-gmm_status clear_status(void* ws, cudaStream_t s) {
-  ProfScope p("tile_list_kernel(status)", s);
-  tile_list_kernel<<<1, 64, 0, s>>>(nullptr, 0, 0, 1, at<DeviceStatus>(ws, 0), nullptr, nullptr);
-  return launched();
-}
 
 }  // namespace gmm
 

@@ -32,7 +32,6 @@ struct ProductLayout {
 gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
                       const ProductLayout& L, cudaStream_t s);
 
-gmm_status clear_status(void* ws, cudaStream_t s);
 
 // The tensor-core forms (expert_product_tc.cu) and what they take.
 bool tc_product_ok(int xdtype, int64_t R, int d_in, int d_out, const void* a, const void* b, const void* c);

@@ -44,6 +44,9 @@ constexpr int kOutBytes = 4096;            // what a read-back warp has on its w
 constexpr int kOutPitch = 80;              // bytes of a staged row of 32 outputs: no bank conflicts
 constexpr int kOutAt = kRing;
 constexpr int kBarsAt = kOutAt + kBackWarps * kOutBytes;
+constexpr int kRowOut = 32 * kOutPitch;    // product, dx: the staged rows of a warp
+constexpr int kFirstAt = kOutAt + kBackWarps * kRowOut;  // ... and behind them, each component's first tile
+constexpr int kMostFirst = (kBarsAt - kFirstAt) / 4;     // components (and the rows past them) that fit
 constexpr int kSmem = kBarsAt + 256 + 1024;
 constexpr uint32_t kWait = 2000000;        // polls of up to a microsecond
 constexpr uint64_t kWaitNs = 2000000000;   // of a pair
@@ -52,8 +55,8 @@ enum { kProduct = 0, kDx = 1, kDw = 2 };
 
 struct TcArgs {
   const int64_t* offsets;
-  const int32_t* count;
-  const int4* tiles;
+  const int32_t* count;  // the list of row tiles, where the components do not
+  const int4* tiles;     // fit in shared memory (NULL: they do)
   DeviceStatus* st;
   int64_t R;
   int K, d_from, d_to;  // rows' width and the output's (dw: d_in, d_out)
@@ -72,19 +75,22 @@ struct Tile {
 // the time between a tile's last product and the next one's first is idle.
 template <int MODE, int CG>
 struct Walk {
-  int mt, nt, limit, k, i, j, dk, di, dj;
+  const uint32_t* before;  // product, dx: tiles before each component (shared memory)
+  int mt, nt, limit, k, i, j, dk, di, dj, g;
   int4 q;
   int64_t b, e;
-  __device__ __forceinline__ Walk(const TcArgs& a, int first, int step) {
+  __device__ __forceinline__ Walk(const TcArgs& a, const uint32_t* first_tiles, int first, int step)
+      : before(first_tiles) {
     mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
     nt = MODE == kDw ? (a.d_from + kTileN - 1) / kTileN : 1;
-    limit = MODE == kDw ? a.K : *a.count;
+    limit = MODE == kDw ? a.K : a.tiles ? *a.count : (int)before[a.K + 1];
     j = first % nt;
     i = first / nt % mt;
     k = first / nt / mt;
     dj = step % nt;
     di = step / nt % mt;
     dk = step / nt / mt;
+    g = 0;
     q = make_int4(-1, 0, 0, 0);
     b = e = 0;
     fetch(a);
@@ -94,8 +100,12 @@ struct Walk {
     if (MODE == kDw) {
       b = a.offsets[k];
       e = a.offsets[k + 1];
-    } else {
+    } else if (a.tiles) {
       q = a.tiles[k];
+    } else {
+      while (before[g + 1] <= (uint32_t)k) ++g;
+      b = a.offsets[g];
+      e = g < a.K ? a.offsets[g + 1] : a.R;
     }
   }
   __device__ __forceinline__ bool more() const { return k < limit; }
@@ -110,11 +120,17 @@ struct Walk {
       w.row0 = lo;
       w.len = hi > lo ? (int)(hi - lo) : 0;
     } else {
-      w.k = q.x;
-      w.row0 = q.y;
-      w.n = q.z;
       w.j0 = 0;
-      w.len = q.x < 0 ? 0 : a.d_from;
+      if (a.tiles) {
+        w.k = q.x;
+        w.row0 = q.y;
+        w.n = q.z;
+      } else {
+        w.k = g < a.K ? g : -1;
+        w.row0 = clamp_row(b, a.R) + (int64_t)(k - (int)before[g]) * kTileN;
+        w.n = (int)min((int64_t)kTileN, clamp_row(e, a.R) - w.row0);
+      }
+      w.len = w.k < 0 ? 0 : a.d_from;
     }
     if (MODE == kDw) {
       j += dj;
@@ -127,6 +143,38 @@ struct Walk {
     return w;
   }
 };
+
+// before[g]: row tiles of the components before g (g = K: the rows past them),
+// before[K + 1]: all of them.  By the whole block.
+__device__ __forceinline__ void count_tiles(const TcArgs& a, uint32_t* before) {
+  __shared__ uint32_t warp_sums[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.K + 1, per = (G + kThreads - 1) / kThreads;
+  const int k0 = min(G, (int)threadIdx.x * per), k1 = min(G, k0 + per);
+  uint32_t mine = 0;
+  for (int k = k0; k < k1; ++k) {
+    const int64_t b = clamp_row(a.offsets[k], a.R), e = k < a.K ? clamp_row(a.offsets[k + 1], a.R) : a.R;
+    const uint32_t n = e > b ? (uint32_t)((e - b + kTileN - 1) / kTileN) : 0u;
+    before[k] = n;
+    mine += n;
+  }
+  uint32_t sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  if (lane == 31) warp_sums[warp] = sum;
+  __syncthreads();
+  uint32_t at = sum - mine;
+  for (int w = 0; w < warp; ++w) at += warp_sums[w];
+  for (int k = k0; k < k1; ++k) {
+    const uint32_t n = before[k];
+    before[k] = at;
+    at += n;
+  }
+  if (k1 == G && k0 < k1) before[G] = at;
+}
 
 // TMA of one box.  `bar`: a shared::cluster address; with PAIR it may be the
 // other block's of the pair.
@@ -412,6 +460,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(odd_full + S);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kPmn = MODE != kProduct, kQmn = MODE == kDw;
+  uint32_t* before = reinterpret_cast<uint32_t*>(smem + kFirstAt);
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
@@ -428,19 +477,25 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
     tc::mbar_fence_init();
   }
   if (warp == 1) tmem_take<CG>(tmem_at);
+  if (a.tiles) {
+    // the list and everything before it is there
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else {
+    // no wait gives up in the time that this takes
+    if (blockIdx.x == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
+      reinterpret_cast<int32_t*>(a.st)[threadIdx.x] = 0;
+    if (MODE != kDw) count_tiles(a, before);
+  }
   tc::tc_fence_before();
   __syncthreads();
   __syncwarp();
   if (CG == 2) cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_at;
-  // the list (or the cleared status word) and everything before it is there
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
   if (warp == 0) {
     uint32_t it = 0;
     bool ok = true;
-    for (Walk<MODE, CG> walk(a, first, step); ok && walk.more();) {
+    for (Walk<MODE, CG> walk(a, before, first, step); ok && walk.more();) {
       const Tile w = walk.take(a);
       // this block's columns
       const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
@@ -492,7 +547,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   } else if (warp == 1 && rank == 0) {
     uint32_t it = 0, acc = 0;
     bool ok = true;
-    for (Walk<MODE, CG> walk(a, first, step); ok && walk.more();) {
+    for (Walk<MODE, CG> walk(a, before, first, step); ok && walk.more();) {
       const Tile w = walk.take(a);
       if (w.len == 0) continue;
       const int b = acc & 1;
@@ -533,7 +588,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
     // in a component's last stage and passes the stage on
     if (MODE == kDw) {
       uint32_t it = 0, phases = 0;  // a bit for each stage's barrier
-      for (Walk<MODE, CG> walk(a, first, step); walk.more();) {
+      for (Walk<MODE, CG> walk(a, before, first, step); walk.more();) {
         const Tile w = walk.take(a);
         const int blocks = (w.len + kTileK - 1) / kTileK;
         it += blocks;
@@ -557,9 +612,9 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   } else if (warp >= 2) {
     const int quarter = warp & 3;       // the TMEM lanes this warp may read
     const int half = (warp - 2) >> 2;   // every other stretch of columns
-    uint8_t* piece = smem + kOutAt + (warp - 2) * kOutBytes;
+    uint8_t* piece = smem + kOutAt + (warp - 2) * (MODE == kDw ? kOutBytes : kRowOut);
     uint32_t acc = 0;
-    for (Walk<MODE, CG> walk(a, first, step); walk.more();) {
+    for (Walk<MODE, CG> walk(a, before, first, step); walk.more();) {
       const Tile w = walk.take(a);
       const int b = acc & 1;
       const int i0 = w.i0 + (int)rank * kTileM + quarter * 32;
@@ -686,7 +741,7 @@ gmm_status go_as(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap
   // may start while the kernel that makes its list runs
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.programmaticStreamSerializationAllowed = a.tiles != nullptr;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = CG;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -725,14 +780,19 @@ bool tc_product_ok(int xdtype, int64_t R, int d_in, int d_out, const void* a, co
 gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
                    int d_to, int K, bool dx, const int64_t* offsets, void* ws, cudaStream_t s) {
   const ProductLayout L = ProductLayout::make(R, d_from, d_to, K);
-  const gmm_status r = list_tiles(offsets, K, R, kTileN, ws, L, s);
-  if (r != GMM_OK || R == 0) return r;
+  // (few thousand components: every block counts their tiles itself, 1 us in
+  // place of the 5 us of a kernel before it)
+  const bool listed = K + 2 > kMostFirst || R == 0;
+  if (listed) {
+    const gmm_status r = list_tiles(offsets, K, R, kTileN, ws, L, s);
+    if (r != GMM_OK || R == 0) return r;
+  }
   CUtensorMap mp, mq;
   const int d_in = dx ? d_to : d_from, d_out = dx ? d_from : d_to;
   if (!encode(&mp, xdtype, W, d_in, d_out, K, 64) || !encode(&mq, xdtype, A, d_from, R, 0, 64))
     return GMM_ERR_CUDA;
-  TcArgs a{offsets, at<int32_t>(ws, L.off_count), at<int4>(ws, L.off_tiles), at<DeviceStatus>(ws, 0),
-           R, K, d_from, d_to};
+  TcArgs a{offsets, at<int32_t>(ws, L.off_count), listed ? at<int4>(ws, L.off_tiles) : nullptr,
+           at<DeviceStatus>(ws, 0), R, K, d_from, d_to};
   const int64_t most = ProductLayout::most_tiles(R, K, kTileN);
   if (most * ((d_to + kTileM - 1) / kTileM) > INT32_MAX) return GMM_ERR_UNSUPPORTED;
   if (xdtype == GMM_BF16) {
@@ -750,8 +810,6 @@ gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int 
   if (!encode(&mp, xdtype, dY, d_out, R, 0, 64) || !encode(&mq, xdtype, A, d_in, R, 0, 64) ||
       !encode(&mo, wdtype, dW, d_in, d_out, K, 32))
     return GMM_ERR_CUDA;
-  const gmm_status r = clear_status(ws, s);
-  if (r != GMM_OK) return r;
   TcArgs a{offsets, nullptr, nullptr, at<DeviceStatus>(ws, 0), R, K, d_in, d_out};
   const int64_t most = (int64_t)K * ((d_in + kTileN - 1) / kTileN);
   if (most * ((d_out + kTileM - 1) / kTileM) > INT32_MAX) return GMM_ERR_UNSUPPORTED;
