@@ -14,8 +14,9 @@
 // atomics, the order does not matter), turns the counts into each segment's
 // first place, and then walks the segments in order, __match_any_sync ranking
 // the equal keys of 32 entries: fixed places, so the result never varies.
-// Ids are fetched kBatch at a time a lane, since the walk waits on memory
-// more than on anything else.
+// The walk waits on latencies more than on anything else: ids are fetched
+// kBatch at a time a lane, a batch ahead, and a batch's ranks are taken before
+// its places, which depend on one another.
 // Floor: 4 bytes read and 8 written per entry.
 #include "expert_internal.cuh"
 
@@ -23,7 +24,7 @@ namespace gmm {
 namespace {
 
 constexpr int kTinyE = 1024;
-constexpr int kCountThreads = 256;
+constexpr int kCountThreads = 1024;
 constexpr int kSlice = 24576;          // groups per shared-memory histogram pass
 constexpr int kBatch = 8;              // entries a lane fetches at once
 constexpr int kMaxWarps = 8;           // scatter warps per block
@@ -156,12 +157,15 @@ route_scan_groups_kernel(const uint32_t* __restrict__ tot, int K, int64_t* __res
 // hist[w][k]: entries of group k in the segments before warp w's, then with
 // the warp's running count; two counts to a word (a block holds at most 65535
 // entries).  base[k]: the block's first place of group k, in shared memory
-// where it fits (`base_here`).
+// where it fits (`base_here`); every block then adds up the groups' totals
+// itself and the first one writes offsets, which elsewhere are there already.
 __global__ void __launch_bounds__(kMaxWarps * 32)
 route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg, int base_here,
-                     const uint32_t* __restrict__ counts, const int64_t* __restrict__ offsets,
-                     int32_t* __restrict__ entry, int32_t* __restrict__ slot) {
+                     const uint32_t* __restrict__ counts, const uint32_t* __restrict__ tot,
+                     int64_t* __restrict__ offsets, int32_t* __restrict__ entry,
+                     int32_t* __restrict__ slot) {
   extern __shared__ uint32_t words[];
+  __shared__ uint32_t sums[kMaxWarps];
   const int G = K + 1, H = (G + 1) / 2;  // words of one warp's counts
   const int warps = blockDim.x >> 5;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -172,9 +176,9 @@ route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg,
   uint32_t* base = words + (size_t)warps * H;
   for (int i = threadIdx.x; i < warps * H; i += blockDim.x) words[i] = 0u;
   if (base_here)
-    for (int k = threadIdx.x; k < G; k += blockDim.x) base[k] = (uint32_t)offsets[k] + before[k];
+    for (int k = threadIdx.x; k < G; k += blockDim.x) base[k] = tot[k];
   __syncthreads();
-  if (warps > 1) {
+  if (warps > 1)
     for (int64_t e = e0 + lane; e < e1; e += kBatch * 32) {
       int k[kBatch];
 #pragma unroll
@@ -183,6 +187,34 @@ route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg,
       for (int j = 0; j < kBatch; ++j)
         if (k[j] >= 0) atomicAdd(&words[(size_t)w * H + (k[j] >> 1)], (k[j] & 1) ? 0x10000u : 1u);
     }
+  if (base_here) {
+    // prefix over the groups, each thread a stretch
+    const int per = (G + blockDim.x - 1) / blockDim.x;
+    const int k0 = min(G, (int)threadIdx.x * per), k1 = min(G, k0 + per);
+    uint32_t mine = 0;
+    for (int k = k0; k < k1; ++k) mine += base[k];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) sums[w] = incl;
+    __syncthreads();
+    uint32_t run = incl - mine;
+    for (int i = 0; i < w; ++i) run += sums[i];
+    for (int k = k0; k < k1; ++k) {
+      const uint32_t v = base[k];
+      base[k] = run;
+      run += v;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < G; k += blockDim.x) {
+      if (b == 0) offsets[k] = base[k];
+      base[k] += before[k];
+    }
+  }
+  if (warps > 1) {
     __syncthreads();
     for (int i = threadIdx.x; i < H; i += blockDim.x) {
       uint32_t run = 0;  // both halves at once: neither sum reaches 65536
@@ -192,28 +224,46 @@ route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg,
         run += v;
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
   uint16_t* mine = reinterpret_cast<uint16_t*>(words + (size_t)w * H);
+  int next[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    next[j] = e0 + lane + j * 32 < e1 ? group_of(ids[e0 + lane + j * 32], K) : -1;
   for (int64_t e = e0 + lane; e - lane < e1; e += kBatch * 32) {
     int k[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) k[j] = e + j * 32 < e1 ? group_of(ids[e + j * 32], K) : -1;
+    unsigned same[kBatch];
+    uint32_t first[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const unsigned same = __match_any_sync(0xffffffffu, k[j]);
-      uint32_t at = 0;
-      if (k[j] >= 0) {
-        at = mine[k[j]];
-        const uint32_t first = base_here ? base[k[j]] : (uint32_t)offsets[k[j]] + before[k[j]];
-        const uint32_t pos = first + at + __popc(same & ((1u << lane) - 1u));
-        slot[e + j * 32] = k[j] < K ? (int32_t)pos : -1;
-        entry[pos] = k[j] < K ? (int32_t)(e + j * 32) : -1;
-      }
-      __syncwarp();
-      if (k[j] >= 0 && lane == __ffs(same) - 1) mine[k[j]] = (uint16_t)(at + __popc(same));
-      __syncwarp();
+      k[j] = next[j];
+      const int64_t f = e + (kBatch + j) * 32;
+      next[j] = f < e1 ? group_of(ids[f], K) : -1;
     }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      same[j] = __match_any_sync(0xffffffffu, k[j]);
+      first[j] = 0;
+      if (k[j] >= 0)
+        first[j] = (base_here ? base[k[j]] : (uint32_t)offsets[k[j]] + before[k[j]]) +
+                   __popc(same[j] & ((1u << lane) - 1u));
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      uint32_t at = 0;
+      if (k[j] >= 0) at = mine[k[j]];
+      __syncwarp();
+      if (k[j] >= 0 && lane == __ffs(same[j]) - 1) mine[k[j]] = (uint16_t)(at + __popc(same[j]));
+      __syncwarp();
+      first[j] += at;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (k[j] >= 0) {
+        slot[e + j * 32] = k[j] < K ? (int32_t)first[j] : -1;
+        entry[first[j]] = k[j] < K ? (int32_t)(e + j * 32) : -1;
+      }
   }
 }
 
@@ -229,10 +279,11 @@ struct RouteLayout {
     while (L.warps > 1 && per_warp * L.warps + bases > kScatterSmem) L.warps >>= 1;
     L.base_here = per_warp * L.warps + bases <= kScatterSmem;
     L.smem = per_warp * L.warps + (L.base_here ? bases : 0);
-    // enough blocks for two a multiprocessor, up to 2048 entries a warp (a
-    // block's K counters are written, scanned and read once more)
+    // one wave of two blocks a multiprocessor, as far as a block's 16-bit
+    // counts reach (a block's K counters are written, scanned and read once
+    // more: few long blocks)
     int64_t seg = (E + (int64_t)L.warps * 304 - 1) / ((int64_t)L.warps * 304);
-    seg = seg < 256 ? 256 : seg > 2048 ? 2048 : (seg + 31) / 32 * 32;
+    seg = seg < 256 ? 256 : seg > 8160 ? 8160 : (seg + 31) / 32 * 32;
     L.seg = (int)seg;
     L.tile = L.warps * L.seg;
     L.nb = (E + L.tile - 1) / L.tile;
@@ -286,16 +337,18 @@ gmm_status gmm_route(const int32_t* ids, int64_t N, int m, int K, int64_t* offse
       cudaFuncSetAttribute(route_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)(sizeof(uint32_t) * kSlice)) != cudaSuccess)
     return GMM_ERR_CUDA;
-  ProfScope p("route_kernels", s, 4);
+  ProfScope p("route_kernels", s, L.base_here ? 3 : 4);
   gmm_status r;
   route_count_kernel<<<(unsigned)L.nb, kCountThreads, bins, s>>>(ids, E, K, L.tile, counts);
   if ((r = launched()) != GMM_OK) return r;
   route_scan_blocks_kernel<<<(K + 1 + 31) / 32, 1024, 0, s>>>(counts, L.nb, K + 1, tot);
   if ((r = launched()) != GMM_OK) return r;
-  route_scan_groups_kernel<<<1, 1024, 0, s>>>(tot, K, offsets);
-  if ((r = launched()) != GMM_OK) return r;
+  if (!L.base_here) {
+    route_scan_groups_kernel<<<1, 1024, 0, s>>>(tot, K, offsets);
+    if ((r = launched()) != GMM_OK) return r;
+  }
   route_scatter_kernel<<<(unsigned)L.nb, L.warps * 32, L.smem, s>>>(
-      ids, E, K, L.seg, L.base_here, counts, offsets, entry, slot);
+      ids, E, K, L.seg, L.base_here, counts, tot, offsets, entry, slot);
   return launched();
 }
 

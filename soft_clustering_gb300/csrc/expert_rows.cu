@@ -44,27 +44,39 @@ __device__ __forceinline__ void zero_tail(T* Y, int64_t R, int D, const int64_t*
 }
 
 // Points a thread has in flight: M rows of up to 16 bytes each for every one.
-__host__ __device__ constexpr int points_in_flight(int M) { return M >= 8 ? 1 : M >= 4 ? 2 : 4; }
+__host__ __device__ constexpr int points_in_flight(int M) { return M >= 4 ? 1 : M == 2 ? 2 : 4; }
+// Blocks a multiprocessor holds (what the registers of those points leave).
+__host__ __device__ constexpr int resident(int M) { return M >= 8 ? 2 : 4; }
 
 // The M slots (and weights) of point n; -1 past m, past N and outside [0, R).
 template <int M>
-__device__ __forceinline__ void load_slots(const int32_t* __restrict__ slot,
-                                           const float* __restrict__ gamma, int64_t n, int64_t N,
-                                           int m, int64_t R, int32_t (&at)[M], float (&w)[M]) {
+struct Slots {
+  int32_t at[M];
+  float w[M];
+  __device__ __forceinline__ void load(const int32_t* __restrict__ slot,
+                                       const float* __restrict__ gamma, int64_t n, int64_t N, int m) {
 #pragma unroll
-  for (int t = 0; t < M; ++t) {
-    at[t] = -1;
-    w[t] = 1.f;
-    if (t < m && n < N) {
-      const int32_t s = slot[n * m + t];
-      at[t] = (s >= 0 && s < R) ? s : -1;
-      if (gamma) w[t] = gamma[n * m + t];
+    for (int t = 0; t < M; ++t) {
+      at[t] = -1;
+      w[t] = 1.f;
+      if (t < m && n < N) {
+        at[t] = slot[n * m + t];
+        if (gamma) w[t] = gamma[n * m + t];
+      }
     }
   }
-}
+  __device__ __forceinline__ void check(int64_t R) {
+#pragma unroll
+    for (int t = 0; t < M; ++t)
+      if (at[t] >= R) at[t] = -1;
+  }
+};
 
+// Both kernels fetch the next turn's slots before they move this turn's rows:
+// a row's address waits on its slot, and the two latencies in a row halve the
+// bandwidth.
 template <typename T, int V, int M, bool DG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, resident(M))
 spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R,
               const int32_t* __restrict__ slot, const int64_t* __restrict__ offsets,
               const float* __restrict__ gamma, const T* __restrict__ Z, T* __restrict__ Y,
@@ -74,13 +86,20 @@ spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R
   const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2;
   const int rows = kThreads >> tx_log2;
   const int nv = D / V;
+  const int64_t stride = (int64_t)gridDim.x * rows * P;
+  int64_t n0 = (int64_t)blockIdx.x * rows * P;
+  Slots<M> next[P];
+#pragma unroll
+  for (int u = 0; u < P; ++u) next[u].load(slot, gamma, n0 + u * rows + ty, N, m);
   // every lane of a warp takes the same number of turns (shuffles below)
-  for (int64_t n0 = (int64_t)blockIdx.x * rows * P; n0 < N; n0 += (int64_t)gridDim.x * rows * P) {
-    int32_t at[P][M];
-    float w[P][M], dot[P][M];
+  for (; n0 < N; n0 += stride) {
+    Slots<M> s[P];
+    float dot[P][M];
 #pragma unroll
     for (int u = 0; u < P; ++u) {
-      load_slots<M>(slot, gamma, n0 + u * rows + ty, N, m, R, at[u], w[u]);
+      s[u] = next[u];
+      s[u].check(R);
+      next[u].load(slot, gamma, n0 + stride + u * rows + ty, N, m);
 #pragma unroll
       for (int t = 0; t < M; ++t) dot[u][t] = 0.f;
     }
@@ -93,15 +112,15 @@ spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R
         if (DG) {
 #pragma unroll
           for (int t = 0; t < M; ++t)
-            if (at[u][t] >= 0) z[u][t] = load_vec<T, V>(Z + (int64_t)at[u][t] * D + (int64_t)c * V);
+            if (s[u].at[t] >= 0) z[u][t] = load_vec<T, V>(Z + (int64_t)s[u].at[t] * D + (int64_t)c * V);
         }
       }
 #pragma unroll
       for (int u = 0; u < P; ++u) {
 #pragma unroll
         for (int t = 0; t < M; ++t) {
-          if (at[u][t] < 0) continue;
-          T* y = Y + (int64_t)at[u][t] * D + (int64_t)c * V;
+          if (s[u].at[t] < 0) continue;
+          T* y = Y + (int64_t)s[u].at[t] * D + (int64_t)c * V;
           if (DG) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -110,7 +129,7 @@ spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R
           if (gamma) {
             Vec<T, V> o;
 #pragma unroll
-            for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(to_f(x[u].v[i]) * w[u][t]);
+            for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(to_f(x[u].v[i]) * s[u].w[t]);
             store_vec<T, V>(y, o);
           } else {
             store_vec<T, V>(y, x[u]);
@@ -126,7 +145,7 @@ spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R
         for (int t = 0; t < M; ++t) {
           for (int o = TX >> 1; o > 0; o >>= 1)
             dot[u][t] += __shfl_xor_sync(0xffffffffu, dot[u][t], o);
-          if (t < m && n < N && tx == 0) dgamma[n * m + t] = at[u][t] >= 0 ? dot[u][t] : 0.f;
+          if (t < m && n < N && tx == 0) dgamma[n * m + t] = s[u].at[t] >= 0 ? dot[u][t] : 0.f;
         }
       }
     }
@@ -135,7 +154,7 @@ spread_kernel(const T* __restrict__ X, int64_t N, int D, int m, int K, int64_t R
 }
 
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, resident(M))
 collect_kernel(const T* __restrict__ Z, int64_t N, int D, int m, int64_t R,
                const int32_t* __restrict__ slot, const float* __restrict__ gamma,
                T* __restrict__ out, int tx_log2) {
@@ -144,19 +163,26 @@ collect_kernel(const T* __restrict__ Z, int64_t N, int D, int m, int64_t R,
   const int tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2;
   const int rows = kThreads >> tx_log2;
   const int nv = D / V;
-  for (int64_t n0 = (int64_t)blockIdx.x * rows * P; n0 < N; n0 += (int64_t)gridDim.x * rows * P) {
-    int32_t at[P][M];
-    float w[P][M];
+  const int64_t stride = (int64_t)gridDim.x * rows * P;
+  int64_t n0 = (int64_t)blockIdx.x * rows * P;
+  Slots<M> next[P];
 #pragma unroll
-    for (int u = 0; u < P; ++u)
-      load_slots<M>(slot, gamma, n0 + u * rows + ty, N, m, R, at[u], w[u]);
+  for (int u = 0; u < P; ++u) next[u].load(slot, gamma, n0 + u * rows + ty, N, m);
+  for (; n0 < N; n0 += stride) {
+    Slots<M> s[P];
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      s[u] = next[u];
+      s[u].check(R);
+      next[u].load(slot, gamma, n0 + stride + u * rows + ty, N, m);
+    }
     for (int c = tx; c < nv; c += TX) {
       Vec<T, V> z[P][M];
 #pragma unroll
       for (int u = 0; u < P; ++u)
 #pragma unroll
         for (int t = 0; t < M; ++t)
-          if (at[u][t] >= 0) z[u][t] = load_vec<T, V>(Z + (int64_t)at[u][t] * D + (int64_t)c * V);
+          if (s[u].at[t] >= 0) z[u][t] = load_vec<T, V>(Z + (int64_t)s[u].at[t] * D + (int64_t)c * V);
 #pragma unroll
       for (int u = 0; u < P; ++u) {
         const int64_t n = n0 + u * rows + ty;
@@ -165,9 +191,9 @@ collect_kernel(const T* __restrict__ Z, int64_t N, int D, int m, int64_t R,
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll
         for (int t = 0; t < M; ++t)
-          if (at[u][t] >= 0) {
+          if (s[u].at[t] >= 0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u][t], to_f(z[u][t].v[i]), acc[i]);
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(s[u].w[t], to_f(z[u][t].v[i]), acc[i]);
           }
         Vec<T, V> y;
 #pragma unroll
@@ -192,12 +218,11 @@ int tx_log2_for(int nv, int most) {
   return l;
 }
 
-// Blocks: one for every `rows * P` points, up to eight a multiprocessor's worth
-// of full blocks; with few points fewer of them share a block, so that the
-// points in flight do not take away from the blocks.
-int64_t grid_for(int64_t N, int rows, int P) {
+// Blocks: one for every `rows * P` points, up to those that are resident at
+// once, which then take turns.
+int64_t grid_for(int64_t N, int rows, int P, int most) {
   const int64_t g = (N + (int64_t)rows * P - 1) / ((int64_t)rows * P);
-  return g > 152 * 32 ? 152 * 32 : g;
+  return g > 152 * most ? 152 * most : g;
 }
 
 template <typename T, int V, int M>
@@ -205,9 +230,9 @@ void spread_launch_m(const void* X, int64_t N, int D, int m, int K, int64_t R, c
                      const int64_t* offsets, const float* gamma, const void* Z, void* Y,
                      float* dgamma, cudaStream_t s) {
   const int l = tx_log2_for(D / V, dgamma ? 5 : 8);
-  int64_t grid = grid_for(N, kThreads >> l, points_in_flight(M));
+  int64_t grid = grid_for(N, kThreads >> l, points_in_flight(M), resident(M));
   const int64_t tail = (R * (D / V) + kThreads * 8 - 1) / (kThreads * 8);  // if every row were zero
-  if (grid < tail) grid = tail > 152 * 8 ? (grid > 152 * 8 ? grid : 152 * 8) : tail;
+  if (grid < tail) grid = tail < 152 * resident(M) ? tail : 152 * resident(M);
   if (grid < 1) grid = 1;
   if (dgamma)
     spread_kernel<T, V, M, true><<<(unsigned)grid, kThreads, 0, s>>>(
@@ -221,7 +246,7 @@ template <typename T, int V, int M>
 void collect_launch_m(const void* Z, int64_t N, int D, int m, int64_t R, const int32_t* slot,
                       const float* gamma, void* out, cudaStream_t s) {
   const int l = tx_log2_for(D / V, 8);
-  const int64_t grid = grid_for(N, kThreads >> l, points_in_flight(M));
+  const int64_t grid = grid_for(N, kThreads >> l, points_in_flight(M), resident(M));
   collect_kernel<T, V, M><<<(unsigned)grid, kThreads, 0, s>>>((const T*)Z, N, D, m, R, slot, gamma,
                                                               (T*)out, l);
 }
