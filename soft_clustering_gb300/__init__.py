@@ -149,14 +149,23 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_raw_stream = None
+
+
 def _current_stream():
     """The current torch stream's handle, without a Stream object where torch
     offers that (3 us less a call)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # initialises CUDA
+        c = torch._C
+        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+            of, dev = c._cuda_getCurrentRawStream, c._cuda_getDevice
+            _raw_stream = lambda: of(dev())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def _check(status, what, raise_on_error=True):

@@ -46,6 +46,9 @@ class AdamW:
             _dense(p, "params[%d]" % i, p.numel(), tuple(TORCH_XDTYPE), self.params[0].device)
         self.state = self._state(state, master)
         self._table = (gmm_adamw_tensor * max(1, len(self.params)))()
+        self._rows = [(self._table[i], p.numel(), p.device) for i, p in enumerate(self.params)]
+        self._opts = gmm_adamw_opts()
+        self._opts.state_bits = state_bits
         for i, p in enumerate(self.params):
             e = self._table[i]
             e.param, e.n, e.param_dtype = p.data_ptr(), p.numel(), TORCH_XDTYPE[p.dtype]
@@ -84,20 +87,19 @@ class AdamW:
         not 0 (the step still counts)."""
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
-        table = self._table
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            if (g.dtype not in TORCH_XDTYPE or g.numel() != p.numel() or g.device != p.device
-                    or not g.is_contiguous()):
-                _dense(g, "grads[%d]" % i, p.numel(), tuple(TORCH_XDTYPE), p.device)
-            e = table[i]
-            e.grad, e.grad_dtype = g.data_ptr(), TORCH_XDTYPE[g.dtype]
+        for i, (g, (e, n, device)) in enumerate(zip(grads, self._rows)):
+            dt = TORCH_XDTYPE.get(g.dtype) if torch.is_tensor(g) else None
+            if dt is None or g.numel() != n or g.device != device or not g.is_contiguous():
+                _dense(g, "grads[%d]" % i, n, tuple(TORCH_XDTYPE), device)
+            e.grad, e.grad_dtype = g.data_ptr(), dt
         if skip is not None:
             _dense(skip, "skip", 1, (torch.int32,), self.params[0].device)
         self.steps += 1
-        o = gmm_adamw_opts(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                           grad_scale, self.steps, self.state_bits,
-                           skip.data_ptr() if skip is not None else None)
-        return gmm_adamw_step(table, len(self.params), o, stream=stream)
+        o = self._opts
+        o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
+        o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self.steps
+        o.skip = skip.data_ptr() if skip is not None else None
+        return gmm_adamw_step(self._table, len(self.params), o, stream=stream)
 
     def moments(self, m_out=None, v_out=None, stream=None):
         """The moments in float32: two lists of tensors (given ones are written)."""

@@ -227,19 +227,19 @@ route_scatter_kernel(const int32_t* __restrict__ ids, int64_t E, int K, int seg,
   }
   __syncthreads();
   uint16_t* mine = reinterpret_cast<uint16_t*>(words + (size_t)w * H);
-  int next[kBatch];
+  int32_t next[kBatch];  // ids as they are: what is done with them would wait for them
 #pragma unroll
   for (int j = 0; j < kBatch; ++j)
-    next[j] = e0 + lane + j * 32 < e1 ? group_of(ids[e0 + lane + j * 32], K) : -1;
+    if (e0 + lane + j * 32 < e1) next[j] = ids[e0 + lane + j * 32];
   for (int64_t e = e0 + lane; e - lane < e1; e += kBatch * 32) {
     int k[kBatch];
     unsigned same[kBatch];
     uint32_t first[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      k[j] = next[j];
+      k[j] = e + j * 32 < e1 ? group_of(next[j], K) : -1;
       const int64_t f = e + (kBatch + j) * 32;
-      next[j] = f < e1 ? group_of(ids[f], K) : -1;
+      if (f < e1) next[j] = ids[f];
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {

@@ -23,15 +23,16 @@ from .torch_api import TORCH_XDTYPE
 
 
 def _need(t, name, shape, dtype, device):
-    """A dense tensor of this shape, type and device, or ValueError."""
+    """A dense tensor of this shape (a tuple), type and device, or ValueError."""
+    if (torch.is_tensor(t) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t
     if not torch.is_tensor(t):
         raise ValueError("%s is not a tensor" % name)
-    if t.shape != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError("%s: expected %s %s on %s, got %s %s on %s"
-                         % (name, tuple(shape), dtype, device, tuple(t.shape), t.dtype, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s is not dense (strides %s)" % (name, t.stride()))
-    return t
+                         % (name, shape, dtype, device, tuple(t.shape), t.dtype, t.device))
+    raise ValueError("%s is not dense (strides %s)" % (name, t.stride()))
 
 
 def _device(device):
@@ -51,9 +52,16 @@ def _empty(shape, dtype, device, stream):
 
 
 def _xdtype(t, name):
-    if t.dtype not in TORCH_XDTYPE:
+    x = TORCH_XDTYPE.get(t.dtype)
+    if x is None:
         raise ValueError("%s: type %s is not supported" % (name, t.dtype))
-    return TORCH_XDTYPE[t.dtype]
+    return x
+
+
+def _width(t, name):
+    if not torch.is_tensor(t) or t.dim() != 2:
+        raise ValueError("%s: expected rows of one width" % name)
+    return t.shape[1]
 
 
 class Router:
@@ -87,20 +95,18 @@ class Router:
         """Y[slot[n, t]] = gamma[n, t] X[n] (gamma None: 1), zeros past the last
         row used.  With Z [N*m, D]: returns (Y, dgamma), dgamma[n, t] =
         <X[n], Z[slot[n, t]]>: with X = d out the gradient of ``collect``."""
-        if not torch.is_tensor(X) or X.dim() != 2 or X.shape[0] != self.N:
-            raise ValueError("X: expected [%d, D]" % self.N)
-        D, x = X.shape[1], _xdtype(X, "X")
+        D, x = _width(X, "X"), _xdtype(X, "X")
         _need(X, "X", (self.N, D), X.dtype, self.device)
         if gamma is not None:
             _need(gamma, "gamma", (self.N, self.m), torch.float32, self.device)
-        if Z is not None:
-            _need(Z, "Z", (self.rows, D), X.dtype, self.device)
-        if out is None:
-            out = _empty((self.rows, D), X.dtype, self.device, stream)
-        _need(out, "out", (self.rows, D), X.dtype, self.device)
         dgamma = None
         if Z is not None:
+            _need(Z, "Z", (self.rows, D), X.dtype, self.device)
             dgamma = _empty((self.N, self.m), torch.float32, self.device, stream)
+        if out is None:
+            out = _empty((self.rows, D), X.dtype, self.device, stream)
+        else:
+            _need(out, "out", (self.rows, D), X.dtype, self.device)
         gmm_spread(X, x, self.N, D, self.m, self.K, self.rows, self.slot, self.offsets, gamma, Z,
                    out, dgamma, stream=stream)
         return out if Z is None else (out, dgamma)
@@ -108,15 +114,14 @@ class Router:
     def collect(self, Z, gamma=None, out=None, stream=None):
         """out[n] = sum_t gamma[n, t] Z[slot[n, t]] (gamma None: 1): the answers
         of a point's components, or the gradient of ``spread``."""
-        if not torch.is_tensor(Z) or Z.dim() != 2:
-            raise ValueError("Z: expected [%d, D]" % self.rows)
-        D, x = Z.shape[1], _xdtype(Z, "Z")
+        D, x = _width(Z, "Z"), _xdtype(Z, "Z")
         _need(Z, "Z", (self.rows, D), Z.dtype, self.device)
         if gamma is not None:
             _need(gamma, "gamma", (self.N, self.m), torch.float32, self.device)
         if out is None:
             out = _empty((self.N, D), Z.dtype, self.device, stream)
-        _need(out, "out", (self.N, D), Z.dtype, self.device)
+        else:
+            _need(out, "out", (self.N, D), Z.dtype, self.device)
         gmm_collect(Z, x, self.N, D, self.m, self.rows, self.slot, gamma, out, stream=stream)
         return out
 
@@ -142,8 +147,9 @@ class ExpertProduct:
         if not torch.is_tensor(t) or t.dim() != 2 or t.shape[0] > self.max_rows:
             raise ValueError("%s: expected [rows, %d] with at most %d rows"
                              % (name, width, self.max_rows))
-        _need(t, name, (t.shape[0], width), self.dtype, self.device)
-        return t.shape[0]
+        R = t.shape[0]
+        _need(t, name, (R, width), self.dtype, self.device)
+        return R
 
     def _common(self, offsets, W):
         _need(offsets, "offsets", (self.K + 1,), torch.int64, self.device)
