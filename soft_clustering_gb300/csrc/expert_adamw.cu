@@ -267,7 +267,7 @@ template <int TOP>
 __device__ __forceinline__ float2 scale_of(float big) {
   if (!(big >= kTiny)) return make_float2(0.f, 0.f);
   return make_float2(__fmul_rn(big, (float)(1.0 / (TOP * TOP))),
-                     __fmul_rn(__fdiv_rn(1.f, big), (float)(TOP * TOP)));
+                     __fmul_rn(__frcp_rn(big), (float)(TOP * TOP)));
 }
 
 __device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
@@ -772,9 +772,8 @@ unsigned grid_for(int chunks) { return (unsigned)(chunks < 152 * 12 ? chunks : 1
 template <int BITS, bool PH, bool GH, int COUNT>
 void launch_step(const AdamwTable<COUNT>& t, cudaStream_t s) {
   const size_t smem = BITS == 8 ? ring_bytes<PH, GH>() : 0;
-  if (smem > 48 * 1024)
-    cudaFuncSetAttribute(adamw_kernel<BITS, PH, GH, COUNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)smem);
+  static std::atomic<uint64_t> allowed;
+  if (smem > 48 * 1024 && !allow_smem((const void*)adamw_kernel<BITS, PH, GH, COUNT>, smem, allowed)) return;
   adamw_kernel<BITS, PH, GH, COUNT><<<grid_for(t.k.chunks), kWarps * 32, smem, s>>>(t);
 }
 

@@ -4,7 +4,7 @@
 //
 // Block (x, r): row r's component is found by counting the offsets at or
 // before it; the component's first row does the work of all its rows, up to
-// kRows at a time, for 32 output features: a warp takes four of them, its
+// kRows at a time, for 32 output features (or twice that, one after the other): a warp takes four of them, its
 // lanes 8 input features of each at a time.  The 4 x kRows sums of a warp are
 // added across its lanes by halving: 31 shuffles for 16 sums.
 #include "expert_product.cuh"
@@ -94,10 +94,10 @@ __device__ __forceinline__ void few_rows(const T* __restrict__ A, const T* __res
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
                 const int64_t* __restrict__ offsets, const T* __restrict__ W, T* __restrict__ Y,
-                DeviceStatus* __restrict__ st) {
+                DeviceStatus* __restrict__ st, int turns) {
   __shared__ int counts[kThreads / 32];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
     reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
@@ -111,22 +111,26 @@ few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
   int k = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) k += counts[i];
-  const int f0 = blockIdx.x * kBlockFeats + warp * kFeats;
   if (k == K) {  // a row of nobody
-    const int f = blockIdx.x * kBlockFeats + threadIdx.x;
-    if (threadIdx.x < kBlockFeats && f < d_out) Y[row * d_out + f] = from_f<T>(0.f);
+    const int f0 = blockIdx.x * kBlockFeats * turns;
+    for (int f = f0 + threadIdx.x; f < min(d_out, f0 + kBlockFeats * turns); f += kThreads)
+      Y[row * d_out + f] = from_f<T>(0.f);
     return;
   }
-  if (clamp_row(offsets[k], R) != row || f0 >= d_out) return;
+  if (clamp_row(offsets[k], R) != row) return;
   const int n = (int)(clamp_row(offsets[k + 1], R) - row);
   const T* w = W + (int64_t)k * d_in * d_out;
   for (int g = 0; g < n; g += kRows) {
     const T* a = A + (row + g) * d_in;
     T* y = Y + (row + g) * d_out;
     const int rows = min(kRows, n - g);
-    if (rows == 1) few_rows<T, 1>(a, w, y, d_in, d_out, f0, rows);
-    else if (rows == 2) few_rows<T, 2>(a, w, y, d_in, d_out, f0, rows);
-    else few_rows<T, 4>(a, w, y, d_in, d_out, f0, rows);
+    for (int t = 0; t < turns; ++t) {
+      const int f0 = ((int)blockIdx.x * turns + t) * kBlockFeats + warp * kFeats;
+      if (f0 >= d_out) break;
+      if (rows == 1) few_rows<T, 1>(a, w, y, d_in, d_out, f0, rows);
+      else if (rows == 2) few_rows<T, 2>(a, w, y, d_in, d_out, f0, rows);
+      else few_rows<T, 4>(a, w, y, d_in, d_out, f0, rows);
+    }
   }
 }
 
@@ -134,15 +138,18 @@ few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
 
 gmm_status few_rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_in,
                             int d_out, int K, const int64_t* offsets, void* ws, cudaStream_t s) {
-  const dim3 grid((d_out + kBlockFeats - 1) / kBlockFeats, (unsigned)R);
+  // two stretches of features a block where three blocks a multiprocessor are
+  // left: fewer starts (16 rows x 2048 features: 15.0 -> 14.6 us a call)
+  const int turns = R * ((d_out + 2 * kBlockFeats - 1) / (2 * kBlockFeats)) >= 3 * 152 ? 2 : 1;
+  const dim3 grid((d_out + kBlockFeats * turns - 1) / (kBlockFeats * turns), (unsigned)R);
   ProfScope p("few_rows_kernel", s);
   DeviceStatus* st = at<DeviceStatus>(ws, 0);
   if (xdtype == GMM_BF16)
     few_rows_kernel<<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)A, R, d_in, d_out, K, offsets,
-                                              (const __nv_bfloat16*)W, (__nv_bfloat16*)Y, st);
+                                              (const __nv_bfloat16*)W, (__nv_bfloat16*)Y, st, turns);
   else
     few_rows_kernel<<<grid, kThreads, 0, s>>>((const __half*)A, R, d_in, d_out, K, offsets,
-                                              (const __half*)W, (__half*)Y, st);
+                                              (const __half*)W, (__half*)Y, st, turns);
   return launched();
 }
 

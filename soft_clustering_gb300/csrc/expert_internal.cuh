@@ -3,6 +3,8 @@
 
 #include <stdio.h>
 
+#include <atomic>
+
 #include "gmm_experts.h"
 #include "gmm_internal.cuh"
 
@@ -13,6 +15,19 @@ inline gmm_status launched() {
   if (e == cudaSuccess) return GMM_OK;
   fprintf(stderr, "libgmm: CUDA error %s\n", cudaGetErrorString(e));
   return GMM_ERR_CUDA;
+}
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `done` (one for each kernel, static) holds the devices that have it already.
+inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 inline bool dtype_ok(int t) { return t >= GMM_F32 && t <= GMM_BF16; }

@@ -237,14 +237,12 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival at a barrier of either block.  A release to the cluster waits for
-// every earlier access of the thread (about 1000 cycles): only where this
-// block's own writes have to be seen.
+// Arrival at a barrier of either block.  (Not a release to the cluster: that
+// waits about 1000 cycles for the thread's earlier accesses, and what a block
+// passes on here is in tensor memory, or in its own shared memory behind a
+// proxy fence.)
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void arrive_release_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Waits for the phase with this parity, acquiring what either block of the
 // pair released; gives up after kWaitNs.
@@ -603,7 +601,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
         zero_rows(smem + s * B, 2 + (cols + 63) / 64, left, (left + 15) / 16 * 16 - left);
         if (lane == 0) {
-          if (CG == 2) arrive_release_at(in_block(&full[s], 0));
+          if (CG == 2) arrive_at(in_block(&full[s], 0));
           else tc::mbar_arrive(&full[s]);
         }
         __syncwarp();
@@ -720,11 +718,14 @@ bool encode(CUtensorMap* m, int type, const void* base, int64_t d0, int64_t d1, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Of the current device; 0 where that cannot be told.
 int multiprocessors() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -732,8 +733,8 @@ template <int MODE, typename T, typename TO, int CG>
 gmm_status go_as(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& mo, void* out,
                  const TcArgs& a, int64_t most, cudaStream_t s) {
   const int sms = multiprocessors();
-  if (sms < CG || cudaFuncSetAttribute(expert_tc_kernel<MODE, T, TO, CG>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+  static std::atomic<uint64_t> allowed;
+  if (sms < CG || !allow_smem((const void*)expert_tc_kernel<MODE, T, TO, CG>, kSmem, allowed))
     return GMM_ERR_CUDA;
   const int64_t tiles = most * ((a.d_to + CG * kTileM - 1) / (CG * kTileM));
   const unsigned grid = (unsigned)(tiles < sms / CG ? tiles : sms / CG) * CG;

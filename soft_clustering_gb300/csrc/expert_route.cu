@@ -332,10 +332,9 @@ gmm_status gmm_route(const int32_t* ids, int64_t N, int m, int K, int64_t* offse
   uint32_t* tot = at<uint32_t>(ws, L.off_tot);
   const int G = K + 1;
   const size_t bins = sizeof(uint32_t) * (size_t)(G < kSlice ? G : kSlice);
-  if (cudaFuncSetAttribute(route_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kScatterSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(route_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)(sizeof(uint32_t) * kSlice)) != cudaSuccess)
+  static std::atomic<uint64_t> scatter_allowed, count_allowed;
+  if (!allow_smem((const void*)route_scatter_kernel, kScatterSmem, scatter_allowed) ||
+      !allow_smem((const void*)route_count_kernel, sizeof(uint32_t) * kSlice, count_allowed))
     return GMM_ERR_CUDA;
   ProfScope p("route_kernels", s, L.base_here ? 3 : 4);
   gmm_status r;
