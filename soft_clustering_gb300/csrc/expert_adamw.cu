@@ -765,16 +765,20 @@ gmm_status over_tables(const gmm_adamw_tensor* ts, int count, const AdamwConst& 
 }
 
 constexpr int kSmallTable = 16, kTable = 400;
-// Blocks: one a chunk, up to a few waves of resident ones, so that the last
-// blocks of long lists do not run alone.
-unsigned grid_for(int chunks) { return (unsigned)(chunks < 152 * 12 ? chunks : 152 * 12); }
+// Blocks: one a chunk, up to `most` a multiprocessor, each a contiguous
+// stretch of the list.  The step in 8 bits, which computes as much as it
+// waits, has the four that are resident (2e8 elements: 467 us; with 8 488 us);
+// what waits for memory alone several waves of smaller stretches (the step in
+// fp32, 1e8 elements: 422 us with 16, 441 with 2; moments from 8 bits, 2e8:
+// 317 us with 24, 340 with 4 or 12).
+unsigned grid_for(int chunks, int most) { return (unsigned)(chunks < 152 * most ? chunks : 152 * most); }
 
 template <int BITS, bool PH, bool GH, int COUNT>
 void launch_step(const AdamwTable<COUNT>& t, cudaStream_t s) {
   const size_t smem = BITS == 8 ? ring_bytes<PH, GH>() : 0;
   static std::atomic<uint64_t> allowed;
   if (smem > 48 * 1024 && !allow_smem((const void*)adamw_kernel<BITS, PH, GH, COUNT>, smem, allowed)) return;
-  adamw_kernel<BITS, PH, GH, COUNT><<<grid_for(t.k.chunks), kWarps * 32, smem, s>>>(t);
+  adamw_kernel<BITS, PH, GH, COUNT><<<grid_for(t.k.chunks, BITS == 8 ? 4 : 16), kWarps * 32, smem, s>>>(t);
 }
 
 }  // namespace
@@ -858,8 +862,8 @@ gmm_status gmm_adamw_moments(const gmm_adamw_tensor* ts, int count, int state_bi
   ProfScope p("adamw_moments_kernel", s);
   auto go = [&](const auto& t) {
     constexpr int C = sizeof(t.e) / sizeof(t.e[0]);
-    if (state_bits == 32) adamw_moments_kernel<32, C><<<grid_for(t.k.chunks), kWarps * 32, 0, s>>>(t);
-    else adamw_moments_kernel<8, C><<<grid_for(t.k.chunks), kWarps * 32, 0, s>>>(t);
+    if (state_bits == 32) adamw_moments_kernel<32, C><<<grid_for(t.k.chunks, 24), kWarps * 32, 0, s>>>(t);
+    else adamw_moments_kernel<8, C><<<grid_for(t.k.chunks, 24), kWarps * 32, 0, s>>>(t);
   };
   auto all = [](int) { return true; };
   return count <= kSmallTable ? over_tables<kSmallTable>(ts, count, AdamwConst{}, all, fill, go)
