@@ -537,3 +537,19 @@ def test_python_refusals(cuda):
                            torch.zeros(11, 8, dtype=torch.float16, device="cuda"), o)
     with pytest.raises(RuntimeError):
         LocalExperts(2, 1, 2, 8, 8, torch.float16).backward(torch.zeros(2, 8, device="cuda").half(), W)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_mixture_of_local_experts_learns(cuda, state_bits):
+    """The example end to end: EM, gate, experts, gradients, AdamW.  Answers that
+    are linear within each component are recovered to a small part of their
+    variance (bf16 products: relative error near 2^-8)."""
+    import importlib.util
+    import os
+    p = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "local_experts.py")
+    spec = importlib.util.spec_from_file_location("local_experts", p)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses = m.train(N=6000, K=8, steps=120, state_bits=state_bits, log=None)
+    assert all(np.isfinite(losses)) and losses[-1] < 0.05 * losses[0], (losses[0], losses[-1])
