@@ -130,12 +130,12 @@ def lib():
 
 def _ptr(x):
     """Device/host address of a torch tensor, numpy array or integer (None -> NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
+    if x is None or isinstance(x, int):
+        return x
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(type(x))

@@ -5,8 +5,10 @@
 // model.  A warp takes 256 consecutive elements of a tensor at a time, eight
 // to a lane: the block that shares one scale where the moments are held in 8
 // bits, so its largest value is a warp reduction away.  Blocks take
-// contiguous stretches of the list (one search of the table each) and fetch
-// the next turn's operands before they work on the present ones.
+// contiguous stretches of the list (one search of the table each), up to 16
+// turns a warp in one tensor, and fetch ahead: three turns through shared
+// memory where the moments are bytes (a lane has 24 bytes a turn, too little
+// in flight otherwise), one turn in registers where they are floats.
 //
 // Bound by HBM traffic: 28 bytes an element in fp32, 10 with 16-bit
 // parameters and gradients and 8-bit moments.  With fp32 moments every
@@ -21,7 +23,12 @@
 //     codes and scales are those of the exact roots;
 //   - the parameter's update uses the approximate root and reciprocal: a
 //     relative error of the update below 2^-21, under the rounding of the
-//     parameter.
+//     parameter;
+//   - products and sums go by pairs of elements (packed fp32 operations).
+// Measured: 1e8 elements in fp32 422 us (6.63 TB/s, 98 % of the copy rate);
+// 2e8 bf16 elements with 8-bit moments 467 us (4.3 TB/s: about 54
+// instructions an element, 45 % of the issue slots, four blocks a
+// multiprocessor); their moments in fp32 317 us (6.3 TB/s).
 #include <cmath>
 #include <type_traits>
 

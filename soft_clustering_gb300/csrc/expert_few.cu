@@ -7,6 +7,9 @@
 // kRows at a time, for 32 output features (or twice that, one after the other): a warp takes four of them, its
 // lanes 8 input features of each at a time.  The 4 x kRows sums of a warp are
 // added across its lanes by halving: 31 shuffles for 16 sums.
+// 16 rows, 14 of 64 components of 1024 x 2048 in bf16: 14 us (4.2 TB/s; the
+// weights alone 8.7 at the copy rate), of which the search, the first fetch
+// and the last blocks take about five.
 #include "expert_product.cuh"
 
 namespace gmm {

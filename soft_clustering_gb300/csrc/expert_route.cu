@@ -17,7 +17,10 @@
 // The walk waits on latencies more than on anything else: ids are fetched
 // kBatch at a time a lane, a batch ahead, and a batch's ranks are taken before
 // its places, which depend on one another.
-// Floor: 4 bytes read and 8 written per entry.
+// Floor: 4 bytes read and 8 written per entry.  8000012 entries to 4096
+// components: 12 + 7 + 92 us; the scatter is bound by latency (16 warps a
+// multiprocessor, as many as the counts' shared memory allows) and by its
+// 4-byte writes to scattered places.  4 entries: 3.6 us.
 #include "expert_internal.cuh"
 
 namespace gmm {
