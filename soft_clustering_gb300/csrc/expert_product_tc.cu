@@ -31,7 +31,7 @@
 // with single blocks, bound by shared memory, which has to take 192 bytes a
 // cycle).  Runs that last are bound by the power limit (about 350 us).
 // What the rest is bound by: 1000001 rows through 256 experts of 128 x 128 in
-// f16, HBM traffic (93 us a call, 5.6 TB/s); dX and dW of 16385 rows x 64
+// f16, HBM traffic (90 us a call, 5.8 TB/s); dX and dW of 16385 rows x 64
 // experts of 1024 x 2048, the weights' traffic (65 and 73 us; 54 each at the
 // measured copy rate).
 #include <cuda.h>
@@ -50,8 +50,9 @@ constexpr int kRing = 192 * 1024;          // stages: 4 of 48 KB, or 6 of 32 KB 
 template <int CG> constexpr int kStageBytes = (kTileM + kTileN / CG) * kTileK * 2;
 template <int CG> constexpr int kStages = kRing / kStageBytes<CG>;
 constexpr int kBackWarps = 8;              // two for each quarter of the accumulator's lanes
-constexpr int kThreads = 64 + 32 * kBackWarps + 32;  // fetch, issue, read back, mend
+constexpr int kThreads = 64 + 32 * kBackWarps + 64;  // fetch P, issue, read back, mend, fetch Q
 constexpr int kMendWarp = 2 + kBackWarps;  // dw: zeroes rows of the next component
+constexpr int kFetchQWarp = kMendWarp + 1;
 constexpr int kOutBytes = 4096;            // what a read-back warp has on its way out
 constexpr int kOutPitch = 80;              // bytes of a staged row of 32 outputs: no bank conflicts
 constexpr int kOutAt = kRing;
@@ -502,7 +503,11 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   if (CG == 2) cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_at;
-  if (warp == 0) {
+  if (warp == 0 || warp == kFetchQWarp) {
+    // P by one warp, which also counts on the barrier what is to come, Q by
+    // the other: a copy takes about 100 cycles to issue, and one warp's four
+    // to six a stage were what short contractions waited for
+    const bool fetch_p = warp == 0;
     uint32_t it = 0;
     bool ok = true;
     for (Walk<MODE, CG> walk(a, before, first, step); ok && walk.more();) {
@@ -522,33 +527,36 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         if (elect_one()) {
           uint8_t* p = smem + s * B;
           uint8_t* q = p + kTileM * kTileK * 2;
-          uint32_t bar = tc::smem_addr(&full[s]);
-          // the end of a component, with rows of the next one up to the next 16
+          // the end of a component, with rows of the next one up to the next
+          // 16: to the mending warp first
           const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
           const uint32_t bytes = (2 + boxes) * kBox;
-          if (odd) {
-            tc::mbar_arrive_expect_tx(&odd_full[s], bytes);
-            bar = tc::smem_addr(&odd_full[s]);
-          } else if (rank == 0) {
-            tc::mbar_arrive_expect_tx(&full[s], CG * bytes);
-            if (CG == 2) tc::mbar_arrive(&full[s]);
-          } else {
-            bar = in_block(&full[s], 0);
-          }
+          const uint32_t bar = odd                    ? tc::smem_addr(&odd_full[s])
+                               : CG == 2 && rank != 0 ? in_block(&full[s], 0)
+                                                      : tc::smem_addr(&full[s]);
           constexpr bool PAIR = CG == 2;
-          if (MODE == kProduct) {
-            tma_3d<PAIR>(p, &map_p, l, i0, w.k, bar);
-            tma_3d<PAIR>(p + kBox, &map_p, l, i0 + 64, w.k, bar);
-          } else if (MODE == kDx) {
-            tma_3d<PAIR>(p, &map_p, i0, l, w.k, bar);
-            tma_3d<PAIR>(p + kBox, &map_p, i0 + 64, l, w.k, bar);
+          if (fetch_p) {
+            if (odd) {
+              tc::mbar_arrive_expect_tx(&odd_full[s], bytes);
+            } else if (rank == 0) {
+              tc::mbar_arrive_expect_tx(&full[s], CG * bytes);
+              if (CG == 2) tc::mbar_arrive(&full[s]);
+            }
+            if (MODE == kProduct) {
+              tma_3d<PAIR>(p, &map_p, l, i0, w.k, bar);
+              tma_3d<PAIR>(p + kBox, &map_p, l, i0 + 64, w.k, bar);
+            } else if (MODE == kDx) {
+              tma_3d<PAIR>(p, &map_p, i0, l, w.k, bar);
+              tma_3d<PAIR>(p + kBox, &map_p, i0 + 64, l, w.k, bar);
+            } else {
+              tma_2d<PAIR>(p, &map_p, i0, (int)w.row0 + l, bar);
+              tma_2d<PAIR>(p + kBox, &map_p, i0 + 64, (int)w.row0 + l, bar);
+            }
           } else {
-            tma_2d<PAIR>(p, &map_p, i0, (int)w.row0 + l, bar);
-            tma_2d<PAIR>(p + kBox, &map_p, i0 + 64, (int)w.row0 + l, bar);
-          }
-          for (int b = 0; b < boxes; ++b) {
-            if (MODE == kDw) tma_2d<PAIR>(q + b * kBox, &map_q, w.j0 + at + 64 * b, (int)w.row0 + l, bar);
-            else tma_2d<PAIR>(q + b * kBox, &map_q, l, (int)w.row0 + at + 64 * b, bar);
+            for (int b = 0; b < boxes; ++b) {
+              if (MODE == kDw) tma_2d<PAIR>(q + b * kBox, &map_q, w.j0 + at + 64 * b, (int)w.row0 + l, bar);
+              else tma_2d<PAIR>(q + b * kBox, &map_q, l, (int)w.row0 + at + 64 * b, bar);
+            }
           }
         }
         __syncwarp();
