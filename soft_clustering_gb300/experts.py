@@ -58,10 +58,13 @@ def _xdtype(t, name):
     return x
 
 
-def _width(t, name):
-    if not torch.is_tensor(t) or t.dim() != 2:
-        raise ValueError("%s: expected rows of one width" % name)
-    return t.shape[1]
+def _rows_of(t, name):
+    """(rows, width) of a tensor with two dimensions."""
+    try:
+        rows, width = t.shape
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError("%s: expected a tensor of two dimensions" % name) from None
+    return rows, width
 
 
 class Router:
@@ -95,18 +98,18 @@ class Router:
         """Y[slot[n, t]] = gamma[n, t] X[n] (gamma None: 1), zeros past the last
         row used.  With Z [N*m, D]: returns (Y, dgamma), dgamma[n, t] =
         <X[n], Z[slot[n, t]]>: with X = d out the gradient of ``collect``."""
-        D, x = _width(X, "X"), _xdtype(X, "X")
-        _need(X, "X", (self.N, D), X.dtype, self.device)
+        D, x, dt, dev = _rows_of(X, "X")[1], _xdtype(X, "X"), X.dtype, self.device
+        _need(X, "X", (self.N, D), dt, dev)
         if gamma is not None:
-            _need(gamma, "gamma", (self.N, self.m), torch.float32, self.device)
+            _need(gamma, "gamma", (self.N, self.m), torch.float32, dev)
         dgamma = None
         if Z is not None:
-            _need(Z, "Z", (self.rows, D), X.dtype, self.device)
-            dgamma = _empty((self.N, self.m), torch.float32, self.device, stream)
+            _need(Z, "Z", (self.rows, D), dt, dev)
+            dgamma = _empty((self.N, self.m), torch.float32, dev, stream)
         if out is None:
-            out = _empty((self.rows, D), X.dtype, self.device, stream)
+            out = _empty((self.rows, D), dt, dev, stream)
         else:
-            _need(out, "out", (self.rows, D), X.dtype, self.device)
+            _need(out, "out", (self.rows, D), dt, dev)
         gmm_spread(X, x, self.N, D, self.m, self.K, self.rows, self.slot, self.offsets, gamma, Z,
                    out, dgamma, stream=stream)
         return out if Z is None else (out, dgamma)
@@ -114,14 +117,14 @@ class Router:
     def collect(self, Z, gamma=None, out=None, stream=None):
         """out[n] = sum_t gamma[n, t] Z[slot[n, t]] (gamma None: 1): the answers
         of a point's components, or the gradient of ``spread``."""
-        D, x = _width(Z, "Z"), _xdtype(Z, "Z")
-        _need(Z, "Z", (self.rows, D), Z.dtype, self.device)
+        D, x, dt, dev = _rows_of(Z, "Z")[1], _xdtype(Z, "Z"), Z.dtype, self.device
+        _need(Z, "Z", (self.rows, D), dt, dev)
         if gamma is not None:
-            _need(gamma, "gamma", (self.N, self.m), torch.float32, self.device)
+            _need(gamma, "gamma", (self.N, self.m), torch.float32, dev)
         if out is None:
-            out = _empty((self.N, D), Z.dtype, self.device, stream)
+            out = _empty((self.N, D), dt, dev, stream)
         else:
-            _need(out, "out", (self.N, D), Z.dtype, self.device)
+            _need(out, "out", (self.N, D), dt, dev)
         gmm_collect(Z, x, self.N, D, self.m, self.rows, self.slot, gamma, out, stream=stream)
         return out
 
@@ -142,19 +145,19 @@ class ExpertProduct:
             raise ValueError("unsupported sizes K=%d d_in=%d d_out=%d rows=%d"
                              % (K, d_in, d_out, max_rows))
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._offsets_shape, self._w_shape = (self.K + 1,), (self.K, self.d_out, self.d_in)
 
     def _rows(self, t, name, width):
-        if not torch.is_tensor(t) or t.dim() != 2 or t.shape[0] > self.max_rows:
-            raise ValueError("%s: expected [rows, %d] with at most %d rows"
-                             % (name, width, self.max_rows))
-        R = t.shape[0]
+        R = _rows_of(t, name)[0]
+        if R > self.max_rows:
+            raise ValueError("%s: %d rows, at most %d" % (name, R, self.max_rows))
         _need(t, name, (R, width), self.dtype, self.device)
         return R
 
     def _common(self, offsets, W):
-        _need(offsets, "offsets", (self.K + 1,), torch.int64, self.device)
+        _need(offsets, "offsets", self._offsets_shape, torch.int64, self.device)
         if W is not None:
-            _need(W, "W", (self.K, self.d_out, self.d_in), self.dtype, self.device)
+            _need(W, "W", self._w_shape, self.dtype, self.device)
 
     def _out(self, out, shape, dtype, stream):
         if out is None:
@@ -189,7 +192,7 @@ class ExpertProduct:
         wt = out_dtype or (out.dtype if out is not None else self.dtype)
         if wt not in (self.dtype, torch.float32):
             raise ValueError("out_dtype %s: expected %s or float32" % (wt, self.dtype))
-        out = self._out(out, (self.K, self.d_out, self.d_in), wt, stream)
+        out = self._out(out, self._w_shape, wt, stream)
         gmm_expert_product_dw(dY, A, self.xdtype, R, self.d_in, self.d_out, self.K, offsets, out,
                               GMM_F32 if wt == torch.float32 else self.xdtype, self.ws,
                               self.ws_bytes, stream=stream)

@@ -553,3 +553,45 @@ def test_mixture_of_local_experts_learns(cuda, state_bits):
     spec.loader.exec_module(m)
     losses = m.train(N=6000, K=8, steps=120, state_bits=state_bits, log=None)
     assert all(np.isfinite(losses)) and losses[-1] < 0.05 * losses[0], (losses[0], losses[-1])
+
+
+@pytest.mark.gpu
+def test_captured_in_a_graph(cuda):
+    """Forward, backward and the weights' step replayed from a CUDA graph."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    from soft_clustering_gb300.experts import LocalExperts
+    rng = np.random.default_rng(8)
+    N, m, K, d = 700, 2, 10, 256
+    ids = torch.from_numpy(_ids(rng, N, m, K, 0.1)).cuda()
+    gam = torch.from_numpy(rng.random((N, m)).astype(np.float32)).cuda()
+    X, g = _rand(rng, (N, d), "bf16"), _rand(rng, (N, d), "bf16")
+    W0 = _rand(rng, (K, d, d), "bf16")
+
+    def build():
+        W = W0.clone()
+        return W, LocalExperts(N, m, K, d, d, torch.bfloat16), AdamW([W], state_bits=8)
+
+    def once(W, layer, opt):
+        out = layer.forward(X, ids, gam, W)
+        dX, dg, dW = layer.backward(g, W)
+        opt.step([dW])
+        return out, dX, dg, dW
+
+    a = build()
+    eager = [t.clone() for t in once(*a)] + [a[0].clone()]
+    b = build()
+    once(*b)
+    W, layer, opt = b
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.steps = 0  # the captured step is step 1
+        outs = once(*b)
+    W.copy_(W0)
+    for k, ts in opt.state.items():
+        for t in ts:
+            t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(eager, [*outs, W]):
+        assert torch.equal(x, y)
