@@ -94,12 +94,13 @@ class AdamW:
             e.grad, e.grad_dtype = g.data_ptr(), dt
         if skip is not None:
             _dense(skip, "skip", 1, (torch.int32,), self.params[0].device)
-        self.steps += 1
         o = self._opts
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
-        o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self.steps
+        o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self.steps + 1
         o.skip = skip.data_ptr() if skip is not None else None
-        return gmm_adamw_step(self._table, len(self.params), o, stream=stream)
+        r = gmm_adamw_step(self._table, len(self.params), o, stream=stream)
+        self.steps += 1
+        return r
 
     def moments(self, m_out=None, v_out=None, stream=None):
         """The moments in float32: two lists of tensors (given ones are written)."""

@@ -141,13 +141,17 @@ rows_simt_kernel(const T* __restrict__ A, const T* __restrict__ W, T* __restrict
 template <typename T, typename TO>
 __global__ void __launch_bounds__(256)
 weights_simt_kernel(const T* __restrict__ dY, const T* __restrict__ A, TO* __restrict__ dW,
-                    int d_in, int d_out, const int64_t* __restrict__ offsets, int64_t R) {
-  const int k = blockIdx.z;
-  const int64_t a = clamp_row(offsets[k], R), b = clamp_row(offsets[k + 1], R);
-  const int i0 = blockIdx.x * kT, o0 = blockIdx.y * kT;
-  tile_product<T, TO>(dY + a * d_out + o0, 1, d_out, A + a * d_in + i0, 1, d_in,
-                      min(kT, d_out - o0), min(kT, d_in - i0), b > a ? b - a : 0,
-                      dW + ((int64_t)k * d_out + o0) * d_in + i0, d_in);
+                    int d_in, int d_out, int K, const int64_t* __restrict__ offsets, int64_t R,
+                    DeviceStatus* __restrict__ st) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
+    reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
+  const int o0 = blockIdx.x * kT, i0 = blockIdx.y * kT;
+  for (int k = blockIdx.z; k < K; k += gridDim.z) {
+    const int64_t a = clamp_row(offsets[k], R), b = clamp_row(offsets[k + 1], R);
+    tile_product<T, TO>(dY + a * d_out + o0, 1, d_out, A + a * d_in + i0, 1, d_in,
+                        min(kT, d_out - o0), min(kT, d_in - i0), b > a ? b - a : 0,
+                        dW + ((int64_t)k * d_out + o0) * d_in + i0, d_in);
+  }
 }
 
 bool sizes_ok(int xdtype, int64_t R, int d_in, int d_out, int K) {
@@ -183,11 +187,11 @@ gmm_status rows_simt(const void* A, const void* W, void* Y, int64_t R, int d_fro
 
 template <typename T, typename TO>
 gmm_status weights_simt(const void* dY, const void* A, void* dW, int64_t R, int d_in, int d_out,
-                        int K, const int64_t* offsets, cudaStream_t s) {
-  const dim3 grid((d_in + kT - 1) / kT, (d_out + kT - 1) / kT, K);
+                        int K, const int64_t* offsets, void* ws, cudaStream_t s) {
+  const dim3 grid((d_out + kT - 1) / kT, (d_in + kT - 1) / kT, K < 65535 ? K : 65535);
   ProfScope p("weights_simt_kernel", s);
   weights_simt_kernel<T, TO><<<grid, 256, 0, s>>>((const T*)dY, (const T*)A, (TO*)dW, d_in, d_out,
-                                                  offsets, R);
+                                                  K, offsets, R, at<DeviceStatus>(ws, 0));
   return launched();
 }
 
@@ -256,14 +260,14 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
   cudaStream_t s = (cudaStream_t)stream;
   if (R > 0 && tc_product_ok(xdtype, R, d_in, d_out, dY, A, dW))
     return tc_weights(dY, A, xdtype, R, d_in, d_out, K, offsets, dW, wdtype, ws, s);
-  if (K > 65535 || (d_out + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
-  if (xdtype == GMM_F32) return weights_simt<float, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+  if ((d_in + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
+  if (xdtype == GMM_F32) return weights_simt<float, float>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
   if (xdtype == GMM_F16) {
-    if (wdtype == GMM_F32) return weights_simt<__half, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
-    return weights_simt<__half, __half>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+    if (wdtype == GMM_F32) return weights_simt<__half, float>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
+    return weights_simt<__half, __half>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
   }
-  if (wdtype == GMM_F32) return weights_simt<__nv_bfloat16, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
-  return weights_simt<__nv_bfloat16, __nv_bfloat16>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+  if (wdtype == GMM_F32) return weights_simt<__nv_bfloat16, float>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
+  return weights_simt<__nv_bfloat16, __nv_bfloat16>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
 }
 
 }  // extern "C"

@@ -116,10 +116,23 @@ struct Walk {
     } else if (a.tiles) {
       q = a.tiles[k];
     } else {
-      while (before[g + 1] <= (uint32_t)k) ++g;
+      g = component_of((uint32_t)k, g, a.K);
       b = a.offsets[g];
       e = g < a.K ? a.offsets[g + 1] : a.R;
     }
+  }
+  // The component of row tile t, not before g: a few steps on, or a search.
+  __device__ __forceinline__ int component_of(uint32_t t, int g, int K) const {
+#pragma unroll
+    for (int x = 0; x < 3; ++x, ++g)
+      if (before[g + 1] > t) return g;
+    int hi = K;  // before[K + 1] > t
+    while (g < hi) {
+      const int mid = (g + hi) >> 1;
+      if (before[mid + 1] > t) hi = mid;
+      else g = mid + 1;
+    }
+    return g;
   }
   __device__ __forceinline__ bool more() const { return k < limit; }
   __device__ __forceinline__ Tile take(const TcArgs& a) {
