@@ -300,7 +300,7 @@ def _offsets(rng, K, R, tail):
 PRODUCTS = [(100, 0, 3, 8, 16), (100, 3, 2, 16, 8), (0, 0, 3, 16, 24), (1, 0, 1, 1, 1), (1, 0, 4, 128, 64), (5, 1, 4, 7, 9), (64, 0, 3, 64, 64),
             (16, 0, 64, 256, 136), (130, 3, 5, 33, 70), (777, 20, 6, 72, 200), (300, 0, 2, 128, 128),
             (1000, 17, 40, 128, 96), (20, 3, 5, 64, 40), (32, 0, 2, 264, 72), (33, 2, 2, 264, 72), (700, 9, 5, 256, 512),
-            (90, 0, 9, 1000, 256), (5000, 5, 4000, 64, 40), (2600, 3, 2, 512, 240), (1500, 40, 60, 240, 256), (7, 7, 3, 16, 8),
+            (90, 0, 9, 1000, 256), (5000, 5, 4000, 64, 40), (5000, 5, 900, 64, 40), (2600, 3, 2, 512, 240), (1500, 40, 60, 240, 256), (7, 7, 3, 16, 8),
             (2500, 0, 3, 320, 264), (513, 1, 1, 1024, 520), (40, 0, 3, 520, 1032)]
 
 
