@@ -4,12 +4,13 @@
 //
 // Block (x, r): row r's component is found by counting the offsets at or
 // before it; the component's first row does the work of all its rows, up to
-// kRows at a time, for 32 output features (or twice that, one after the other): a warp takes four of them, its
+// kRows at a time, for 32 output features: a warp takes four of them, its
 // lanes 8 input features of each at a time.  The 4 x kRows sums of a warp are
 // added across its lanes by halving: 31 shuffles for 16 sums.
-// 16 rows, 14 of 64 components of 1024 x 2048 in bf16: 14 us (4.2 TB/s; the
-// weights alone 8.7 at the copy rate), of which the search, the first fetch
-// and the last blocks take about five.
+// 16 rows, 14 of 64 components of 1024 x 2048 in bf16: 14.2 us a call (4.2
+// TB/s; the weights alone 8.7 us at the copy rate), of which the search, the
+// first fetch and the last blocks take about five.  Three blocks a
+// multiprocessor; with two, or with 64 features a block, 15 to 16.
 #include "expert_product.cuh"
 
 namespace gmm {
@@ -71,7 +72,8 @@ __device__ __forceinline__ void few_rows(const T* __restrict__ A, const T* __res
   const T* w[kFeats];
 #pragma unroll
   for (int f = 0; f < kFeats; ++f) w[f] = W + (int64_t)min(f0 + f, d_out - 1) * d_in;
-#pragma unroll 2
+  // one row: 16 loads a lane in flight; more rows take the registers
+#pragma unroll (NR == 1 ? 4 : NR == 2 ? 2 : 1)
   for (int c = lane * 8; c < d_in; c += 256) {
     uint4 q[kFeats];
 #pragma unroll
@@ -97,43 +99,56 @@ __device__ __forceinline__ void few_rows(const T* __restrict__ A, const T* __res
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
 few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
                 const int64_t* __restrict__ offsets, const T* __restrict__ W, T* __restrict__ Y,
-                DeviceStatus* __restrict__ st, int turns) {
-  __shared__ int counts[kThreads / 32];
+                DeviceStatus* __restrict__ st) {
+  __shared__ int found[3][kThreads / 32];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
     reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
   const int64_t row = blockIdx.y;
   const int warp = threadIdx.x >> 5;
-  int at_or_before = 0;
-  for (int k = threadIdx.x; k < K; k += kThreads) at_or_before += offsets[k + 1] <= row;
-  at_or_before = __reduce_add_sync(0xffffffffu, at_or_before);
-  if ((threadIdx.x & 31) == 0) counts[warp] = at_or_before;
+  // the offsets at or before the row: how many, and the last; the first after
+  int count = 0, last = (int)clamp_row(offsets[0], R), next = (int)R;
+  for (int k = threadIdx.x; k < K; k += kThreads) {
+    const int v = (int)clamp_row(offsets[k + 1], R);
+    const bool before = v <= row;
+    count += before;
+    if (before) last = max(last, v);
+    else next = min(next, v);
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  last = __reduce_max_sync(0xffffffffu, last);
+  next = __reduce_min_sync(0xffffffffu, next);
+  if ((threadIdx.x & 31) == 0) {
+    found[0][warp] = count;
+    found[1][warp] = last;
+    found[2][warp] = next;
+  }
   __syncthreads();
   int k = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) k += counts[i];
+  for (int i = 0; i < kThreads / 32; ++i) {
+    k += found[0][i];
+    last = max(last, found[1][i]);
+    next = min(next, found[2][i]);
+  }
   if (k == K) {  // a row of nobody
-    const int f0 = blockIdx.x * kBlockFeats * turns;
-    for (int f = f0 + threadIdx.x; f < min(d_out, f0 + kBlockFeats * turns); f += kThreads)
-      Y[row * d_out + f] = from_f<T>(0.f);
+    const int f = blockIdx.x * kBlockFeats + threadIdx.x;
+    if (threadIdx.x < kBlockFeats && f < d_out) Y[row * d_out + f] = from_f<T>(0.f);
     return;
   }
-  if (clamp_row(offsets[k], R) != row) return;
-  const int n = (int)(clamp_row(offsets[k + 1], R) - row);
+  const int f0 = blockIdx.x * kBlockFeats + warp * kFeats;
+  if (last != row || f0 >= d_out) return;
+  const int n = next - (int)row;
   const T* w = W + (int64_t)k * d_in * d_out;
   for (int g = 0; g < n; g += kRows) {
     const T* a = A + (row + g) * d_in;
     T* y = Y + (row + g) * d_out;
     const int rows = min(kRows, n - g);
-    for (int t = 0; t < turns; ++t) {
-      const int f0 = ((int)blockIdx.x * turns + t) * kBlockFeats + warp * kFeats;
-      if (f0 >= d_out) break;
-      if (rows == 1) few_rows<T, 1>(a, w, y, d_in, d_out, f0, rows);
-      else if (rows == 2) few_rows<T, 2>(a, w, y, d_in, d_out, f0, rows);
-      else few_rows<T, 4>(a, w, y, d_in, d_out, f0, rows);
-    }
+    if (rows == 1) few_rows<T, 1>(a, w, y, d_in, d_out, f0, rows);
+    else if (rows == 2) few_rows<T, 2>(a, w, y, d_in, d_out, f0, rows);
+    else few_rows<T, 4>(a, w, y, d_in, d_out, f0, rows);
   }
 }
 
@@ -141,18 +156,15 @@ few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
 
 gmm_status few_rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_in,
                             int d_out, int K, const int64_t* offsets, void* ws, cudaStream_t s) {
-  // two stretches of features a block where three blocks a multiprocessor are
-  // left: fewer starts (16 rows x 2048 features: 15.0 -> 14.6 us a call)
-  const int turns = R * ((d_out + 2 * kBlockFeats - 1) / (2 * kBlockFeats)) >= 3 * 152 ? 2 : 1;
-  const dim3 grid((d_out + kBlockFeats * turns - 1) / (kBlockFeats * turns), (unsigned)R);
+  const dim3 grid((d_out + kBlockFeats - 1) / kBlockFeats, (unsigned)R);
   ProfScope p("few_rows_kernel", s);
   DeviceStatus* st = at<DeviceStatus>(ws, 0);
   if (xdtype == GMM_BF16)
     few_rows_kernel<<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)A, R, d_in, d_out, K, offsets,
-                                              (const __nv_bfloat16*)W, (__nv_bfloat16*)Y, st, turns);
+                                              (const __nv_bfloat16*)W, (__nv_bfloat16*)Y, st);
   else
     few_rows_kernel<<<grid, kThreads, 0, s>>>((const __half*)A, R, d_in, d_out, K, offsets,
-                                              (const __half*)W, (__half*)Y, st, turns);
+                                              (const __half*)W, (__half*)Y, st);
   return launched();
 }
 

@@ -38,7 +38,7 @@ bool tc_product_ok(int xdtype, int64_t R, int d_in, int d_out, const void* a, co
 gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
                    int d_to, int K, bool dx, const int64_t* offsets, void* ws, cudaStream_t s);
 // ... and the one for few rows, 16-bit types as above.  Experts of 1024 x 2048
-// in bf16, a call: 16 rows over 64 components 15.4 us, 32 rows 22.3 (the
+// in bf16, a call: 16 rows over 64 components 14.2 us, 32 rows 22.3 (the
 // tensor-core form 19.0 and 25.4); 64 rows 35.1 (33.8); 32 rows over 8
 // components, several to a component, 21.7 (15.8).  Its blocks count the
 // offsets themselves, 256 at a time: worth it for a few thousand components.

@@ -18,7 +18,7 @@
 // terms of a sum (product_dw) they are zeroed in shared memory first, in both
 // operands, so no infinity or NaN passes from one component to another.
 //
-// A persistent block per multiprocessor: one warp fetches (192 KB of stages in
+// A persistent block per multiprocessor: two warps fetch (192 KB of stages in
 // flight), one issues the products into one of two 256-column accumulators,
 // eight read the other one back and store it, and for product_dw one zeroes
 // the rows of the next component ahead of the products.  Sums are fp32 in
@@ -31,7 +31,7 @@
 // with single blocks, bound by shared memory, which has to take 192 bytes a
 // cycle).  Runs that last are bound by the power limit (about 350 us).
 // What the rest is bound by: 1000001 rows through 256 experts of 128 x 128 in
-// f16, HBM traffic (90 us a call, 5.8 TB/s); dX and dW of 16385 rows x 64
+// f16, HBM traffic (87 us a call, 6.0 TB/s); dX and dW of 16385 rows x 64
 // experts of 1024 x 2048, the weights' traffic (65 and 73 us; 54 each at the
 // measured copy rate).
 #include <cuda.h>
