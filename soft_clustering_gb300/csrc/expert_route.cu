@@ -286,7 +286,8 @@ struct RouteLayout {
     // counts reach (a block's K counters are written, scanned and read once
     // more: few long blocks)
     int64_t seg = (E + (int64_t)L.warps * 304 - 1) / ((int64_t)L.warps * 304);
-    seg = seg < 256 ? 256 : seg > 8160 ? 8160 : (seg + 31) / 32 * 32;
+    const int64_t most = 65535 / L.warps / 32 * 32;
+    seg = seg < 256 ? 256 : seg > most ? most : (seg + 31) / 32 * 32;
     L.seg = (int)seg;
     L.tile = L.warps * L.seg;
     L.nb = (E + L.tile - 1) / L.tile;

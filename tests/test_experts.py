@@ -200,6 +200,45 @@ def test_route(cuda, N, m, K, drop):
     assert np.array_equal(r.slot.cpu().numpy(), s)
 
 
+def _route_fast(ids, K):
+    """route_ref for long tables: a stable sort of the keys."""
+    flat = ids.reshape(-1).astype(np.int64)
+    key = np.where((flat >= 0) & (flat < K), flat, K)
+    order = np.argsort(key, kind="stable")
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=K + 1)[:K])]).astype(np.int64)
+    used = offsets[-1]
+    entry = np.full(flat.size, -1, dtype=np.int32)
+    entry[:used] = order[:used]
+    slot = np.full(flat.size, -1, dtype=np.int32)
+    slot[order[:used]] = np.arange(used)
+    return offsets, entry, slot.reshape(ids.shape)
+
+
+def test_route_references_agree():
+    rng = np.random.default_rng(1)
+    ids = _ids(rng, 500, 3, 40, 0.2)
+    for a, b in zip(route_ref(ids, 40), _route_fast(ids, 40)):
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,m,K", [(3_000_001, 4, 300), (1_500_000, 8, 20_000), (25_000_003, 1, 65_536)])
+def test_route_long_tables(cuda, N, m, K):
+    """Segments at the length that the 16-bit counts allow, one key in half of
+    the entries."""
+    import torch
+    from soft_clustering_gb300.experts import Router
+    rng = np.random.default_rng(K)
+    ids = rng.integers(-1, K + 1, (N, m)).astype(np.int32)
+    ids[rng.random(N) < 0.5] = K // 2
+    r = Router(N, m, K)
+    r.route(torch.from_numpy(ids).cuda())
+    o, e, s = _route_fast(ids, K)
+    assert np.array_equal(r.offsets.cpu().numpy(), o)
+    assert np.array_equal(r.entry.cpu().numpy(), e)
+    assert np.array_equal(r.slot.cpu().numpy(), s)
+
+
 @pytest.mark.gpu
 def test_route_one_component_takes_all(cuda):
     import torch
