@@ -29,7 +29,7 @@ constexpr int kListSmem = 4096;   // components whose first tiles fit in shared 
 __global__ void __launch_bounds__(kListThreads)
 tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T, uint32_t room,
                  DeviceStatus* __restrict__ st, int32_t* __restrict__ count,
-                 int4* __restrict__ tiles) {
+                 uint32_t* __restrict__ first, int4* __restrict__ tiles) {
   __shared__ uint32_t wsum[32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
@@ -49,6 +49,7 @@ tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T, u
     for (int k = k0; k < k1; ++k) {
       const int64_t a = clamp_row(offsets[k], R), b = k < K ? clamp_row(offsets[k + 1], R) : R;
       before[k] = at;
+      first[k] = min(at, room);
       if (b > a) at += (uint32_t)((b - a + T - 1) / T);
     }
     if (k1 == G && k0 < k1) {
@@ -72,6 +73,7 @@ tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T, u
   }
   for (int k = k0; k < k1; ++k) {
     const int64_t a = clamp_row(offsets[k], R), b = k < K ? clamp_row(offsets[k + 1], R) : R;
+    first[k] = min(at, room);
     for (int64_t r = a; r < b; r += T, ++at)
       if (at < room) tiles[at] = make_int4(k < K ? k : -1, (int)r, (int)min((int64_t)T, b - r), 0);
   }
@@ -218,7 +220,7 @@ gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
   ProfScope p("tile_list_kernel", s);
   tile_list_kernel<<<1, kListThreads, 0, s>>>(
       offsets, K, R, T, (uint32_t)ProductLayout::most_tiles(R, K, T), at<DeviceStatus>(ws, 0),
-      at<int32_t>(ws, L.off_count), at<int4>(ws, L.off_tiles));
+      at<int32_t>(ws, L.off_count), at<uint32_t>(ws, L.off_first), at<int4>(ws, L.off_tiles));
   return launched();
 }
 

@@ -11,24 +11,48 @@ __host__ __device__ inline int64_t clamp_row(int64_t v, int64_t R) {
   return v < 0 ? 0 : v > R ? R : v;
 }
 
+// dW has a tile for every component and 128 x 256 of its matrix, each a sum
+// over all the component's rows.  Where those are fewer than four a
+// multiprocessor and the sums long, a component's rows are cut into stretches
+// with a partial sum each, added in order afterwards: about this many
+// stretches in all.  Cut and joined against whole: 522711 rows to 22
+// components of 64 x 128 76 us (406), 200000 to 16 of 512 x 256 90 (189),
+// 1000001 to 256 of 128 x 128 126 (128); but 16385 to 8 of 1024 x 1024 57
+// (40): hence kDwLong rows a component.
+constexpr int kDwTiles = 4 * 152, kDwLong = 4096;
+inline int dw_stretches(int d_in, int d_out) {
+  const int64_t tiles = (int64_t)((d_out + 127) / 128) * ((d_in + 255) / 256);
+  return tiles > kDwTiles ? 0 : (int)(kDwTiles / tiles);
+}
+// Rows of a stretch; 0: components are not cut.
+inline int64_t dw_stretch_rows(int64_t R, int d_in, int d_out, int K) {
+  const int n = dw_stretches(d_in, d_out);
+  if (n <= K || R < (int64_t)kDwLong * K) return 0;
+  const int64_t each = (R + (n - K) - 1) / (n - K);
+  const int64_t rows = each < 256 ? 256 : (each + 63) / 64 * 64;
+  return rows < R ? rows : 0;
+}
+
 struct ProductLayout {
-  size_t off_count, off_tiles, bytes;  // the DeviceStatus comes first
+  size_t off_count, off_first, off_tiles, off_part, bytes;  // the DeviceStatus comes first
   // row tiles of K components and of the rows past them
   static int64_t most_tiles(int64_t R, int K, int T) { return R / T + K + 1; }
   static ProductLayout make(int64_t R, int d_in, int d_out, int K) {
-    (void)d_in;
-    (void)d_out;
     ProductLayout L;
     size_t o = align_up(sizeof(DeviceStatus));
     L.off_count = o; o = align_up(o + sizeof(int32_t));
+    L.off_first = o; o = align_up(o + sizeof(uint32_t) * ((size_t)K + 2));
     L.off_tiles = o; o = align_up(o + sizeof(int4) * (size_t)most_tiles(R, K, kLeastTile));
+    L.off_part = o;
+    if (dw_stretch_rows(R, d_in, d_out, K) > 0)
+      o = align_up(o + sizeof(float) * (size_t)d_in * d_out * (dw_stretches(d_in, d_out) + 1));
     L.bytes = o;
     return L;
   }
 };
 
-// Fills the tile list {component or -1, first row, rows, 0} and its length,
-// and clears the workspace's status word.
+// Fills the tile list {component or -1, first row, rows, 0}, its length and
+// each component's first tile, and clears the workspace's status word.
 gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
                       const ProductLayout& L, cudaStream_t s);
 

@@ -83,7 +83,7 @@ struct Tile {
 };
 
 // The tiles of one block (or pair), every `step`-th from `first`: row tiles
-// (dw: components) k, feature tiles i, and for dw column tiles j, the last
+// (dw: components, or stretches of their rows) k, feature tiles i, and for dw column tiles j, the last
 // one running fastest.  What of a tile comes from memory is fetched a tile
 // ahead, and no division is done per tile: every role walks for itself, and
 // the time between a tile's last product and the next one's first is idle.
@@ -97,7 +97,7 @@ struct Walk {
       : before(first_tiles) {
     mt = (a.d_to + CG * kTileM - 1) / (CG * kTileM);
     nt = MODE == kDw ? (a.d_from + kTileN - 1) / kTileN : 1;
-    limit = MODE == kDw ? a.K : a.tiles ? *a.count : (int)before[a.K + 1];
+    limit = a.tiles ? *a.count : MODE == kDw ? a.K : (int)before[a.K + 1];
     j = first % nt;
     i = first / nt % mt;
     k = first / nt / mt;
@@ -111,11 +111,11 @@ struct Walk {
   }
   __device__ __forceinline__ void fetch(const TcArgs& a) {
     if (k >= limit) return;
-    if (MODE == kDw) {
+    if (a.tiles) {
+      q = a.tiles[k];
+    } else if (MODE == kDw) {
       b = a.offsets[k];
       e = a.offsets[k + 1];
-    } else if (a.tiles) {
-      q = a.tiles[k];
     } else {
       g = component_of((uint32_t)k, g, a.K);
       b = a.offsets[g];
@@ -143,9 +143,14 @@ struct Walk {
       w.k = k;
       w.j0 = j * kTileN;
       w.n = min(kTileN, a.d_from - w.j0);
-      const int64_t lo = clamp_row(b, a.R), hi = clamp_row(e, a.R);
-      w.row0 = lo;
-      w.len = hi > lo ? (int)(hi - lo) : 0;
+      if (a.tiles) {  // a stretch of a component's rows
+        w.row0 = q.y;
+        w.len = q.x < 0 ? 0 : q.z;
+      } else {
+        const int64_t lo = clamp_row(b, a.R), hi = clamp_row(e, a.R);
+        w.row0 = lo;
+        w.len = hi > lo ? (int)(hi - lo) : 0;
+      }
     } else {
       w.j0 = 0;
       if (a.tiles) {
@@ -718,6 +723,42 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   }
 }
 
+// dW[k] = the sum of its stretches' partial sums, in order.
+template <typename TO>
+__global__ void __launch_bounds__(256)
+join_kernel(const float* __restrict__ part, const uint32_t* __restrict__ first, int64_t quads,
+            TO* __restrict__ dW) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const int k = blockIdx.y;
+  const uint32_t s0 = first[k], s1 = first[k + 1];
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* p = reinterpret_cast<const float4*>(part) + i;
+#pragma unroll 8
+  for (uint32_t s = s0; s < s1; ++s) {
+    const float4 v = p[(int64_t)s * quads];
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  TO* o = dW + ((int64_t)k * quads + i) * 4;
+  if constexpr (sizeof(TO) == 4)
+    *reinterpret_cast<float4*>(o) = sum;
+  else
+    *reinterpret_cast<uint2*>(o) = make_uint2(Pair<TO>::pack(sum.x, sum.y), Pair<TO>::pack(sum.z, sum.w));
+}
+
+template <typename TO>
+gmm_status join(const void* ws, const ProductLayout& L, int K, int d_in, int d_out, void* dW,
+                cudaStream_t s) {
+  const int64_t quads = (int64_t)d_in * d_out / 4;
+  ProfScope p("join_kernel", s);
+  join_kernel<TO><<<dim3((unsigned)((quads + 255) / 256), K), 256, 0, s>>>(
+      at<float>(ws, L.off_part), at<uint32_t>(ws, L.off_first), quads, (TO*)dW);
+  return launched();
+}
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -845,11 +886,30 @@ gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int 
                       int K, const int64_t* offsets, void* dW, int wdtype, void* ws,
                       cudaStream_t s) {
   CUtensorMap mp, mq, mo;
-  if (!encode(&mp, xdtype, dY, d_out, R, 0, 64) || !encode(&mq, xdtype, A, d_in, R, 0, 64) ||
-      !encode(&mo, wdtype, dW, d_in, d_out, K, 32))
+  if (!encode(&mp, xdtype, dY, d_out, R, 0, 64) || !encode(&mq, xdtype, A, d_in, R, 0, 64))
     return GMM_ERR_CUDA;
+  const int64_t nt = (d_in + kTileN - 1) / kTileN;
   TcArgs a{offsets, nullptr, nullptr, at<DeviceStatus>(ws, 0), R, K, d_in, d_out};
-  const int64_t most = (int64_t)K * ((d_in + kTileN - 1) / kTileN);
+  const int64_t stretch = dw_stretch_rows(R, d_in, d_out, K);
+  if (stretch > 0) {
+    // few tiles of long sums
+    const ProductLayout L = ProductLayout::make(R, d_in, d_out, K);
+    const int64_t most = ProductLayout::most_tiles(R, K, (int)stretch);
+    float* part = at<float>(ws, L.off_part);
+    if (!encode(&mo, GMM_F32, part, d_in, d_out, most, 32)) return GMM_ERR_CUDA;
+    gmm_status r = list_tiles(offsets, K, R, (int)stretch, ws, L, s);
+    if (r != GMM_OK) return r;
+    a.count = at<int32_t>(ws, L.off_count);
+    a.tiles = at<int4>(ws, L.off_tiles);
+    r = xdtype == GMM_BF16 ? go<kDw, __nv_bfloat16, float>(mp, mq, mo, part, a, most * nt, s)
+                           : go<kDw, __half, float>(mp, mq, mo, part, a, most * nt, s);
+    if (r != GMM_OK) return r;
+    if (wdtype == GMM_F32) return join<float>(ws, L, K, d_in, d_out, dW, s);
+    if (wdtype == GMM_BF16) return join<__nv_bfloat16>(ws, L, K, d_in, d_out, dW, s);
+    return join<__half>(ws, L, K, d_in, d_out, dW, s);
+  }
+  if (!encode(&mo, wdtype, dW, d_in, d_out, K, 32)) return GMM_ERR_CUDA;
+  const int64_t most = (int64_t)K * nt;
   if (most * ((d_out + kTileM - 1) / kTileM) > INT32_MAX) return GMM_ERR_UNSUPPORTED;
   if (xdtype == GMM_BF16) {
     using T = __nv_bfloat16;

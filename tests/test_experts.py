@@ -336,7 +336,7 @@ def _offsets(rng, K, R, tail):
     return np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
 
 
-PRODUCTS = [(100, 0, 3, 8, 16), (100, 3, 2, 16, 8), (0, 0, 3, 16, 24), (1, 0, 1, 1, 1), (1, 0, 4, 128, 64), (5, 1, 4, 7, 9), (64, 0, 3, 64, 64),
+PRODUCTS = [(30000, 5, 3, 64, 128), (40000, 0, 5, 256, 40), (9001, 0, 1, 264, 264), (9001, 0, 3, 264, 264), (100, 0, 3, 8, 16), (100, 3, 2, 16, 8), (0, 0, 3, 16, 24), (1, 0, 1, 1, 1), (1, 0, 4, 128, 64), (5, 1, 4, 7, 9), (64, 0, 3, 64, 64),
             (16, 0, 64, 256, 136), (130, 3, 5, 33, 70), (777, 20, 6, 72, 200), (300, 0, 2, 128, 128),
             (1000, 17, 40, 128, 96), (20, 3, 5, 64, 40), (32, 0, 2, 264, 72), (33, 2, 2, 264, 72), (700, 9, 5, 256, 512),
             (90, 0, 9, 1000, 256), (5000, 5, 4000, 64, 40), (5000, 5, 900, 64, 40), (2600, 3, 2, 512, 240), (1500, 40, 60, 240, 256), (7, 7, 3, 16, 8),
@@ -379,7 +379,7 @@ def test_product_of_whole_numbers_is_exact(cuda, dtype, R, tail, K, d_in, d_out)
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("R,tail,K,d_in,d_out", [(16, 0, 64, 256, 136), (777, 20, 6, 72, 200),
-                                                 (2500, 0, 3, 320, 264), (40, 0, 3, 33, 65)])
+                                                 (2500, 0, 3, 320, 264), (40, 0, 3, 33, 65), (20000, 0, 3, 64, 72), (20000, 0, 5, 64, 72)])
 def test_product_of_real_numbers(cuda, dtype, R, tail, K, d_in, d_out):
     import torch
     rng = np.random.default_rng(R)
