@@ -269,12 +269,20 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival at a barrier of either block.  (Not a release to the cluster: that
-// waits about 1000 cycles for the thread's earlier accesses, and what a block
-// passes on here is in tensor memory, or in its own shared memory behind a
-// proxy fence.)
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
+// Arrival at a barrier of either block that passes on an accumulator read
+// back.  (Not a release to the cluster, which waits about 1000 cycles for the
+// thread's earlier stores to global memory: no write is handed over here.
+// tcgen05.wait::ld has the values in registers before the arrival, so nothing
+// of the accumulator is still to be read when the next products go there.)
+__device__ __forceinline__ void arrive_read(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrival at a barrier of either block that passes on writes to this block's
+// shared memory: the products that read them are issued by the other block, so
+// the arrival is a release to the cluster (without a scope it would be one to
+// this block alone), and wait_pair acquires there.
+__device__ __forceinline__ void arrive_written(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Waits for the phase with this parity, acquiring what either block of the
 // pair released; gives up after kWaitNs.
@@ -640,7 +648,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         const int cols = CG == 2 ? ((w.n + 31) & ~31) / 2 : w.n;
         zero_rows(smem + s * B, 2 + (cols + 63) / 64, left, (left + 15) / 16 * 16 - left);
         if (lane == 0) {
-          if (CG == 2) arrive_at(in_block(&full[s], 0));
+          if (CG == 2) arrive_written(in_block(&full[s], 0));
           else tc::mbar_arrive(&full[s]);
         }
         __syncwarp();
@@ -706,7 +714,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (CG == 2) arrive_at(in_block(&acc_empty[b], 0));
+          if (CG == 2) arrive_read(in_block(&acc_empty[b], 0));
           else tc::mbar_arrive(&acc_empty[b]);
         }
         ++acc;

@@ -1,0 +1,47 @@
+"""Local experts as programs use them: batches that overlap, buffers that are
+written again, other streams, neighbours that are not finite.
+
+References and tolerances are those of test_experts.py: products of small whole
+numbers are exact, and what is compared with itself has to be equal.
+"""
+import numpy as np
+import pytest
+
+import soft_clustering_gb300 as G
+from test_experts import _f64, _ids, _rand, dw_ref
+
+
+@pytest.fixture(scope="module")
+def cuda():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from soft_clustering_gb300 import build
+    build.build()
+    return torch.device("cuda", 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d_in,d_out", [(64, 256), (264, 512), (512, 240)])
+def test_ragged_ends_in_pairs_of_blocks(cuda, d_in, d_out):
+    """dW where two blocks share a tile and every component ends inside a stage:
+    the rows of the next component, infinities and NaN, reach no sum, time after
+    time."""
+    import torch
+    from soft_clustering_gb300.experts import ExpertProduct
+    rng = np.random.default_rng(d_out)
+    n = [1, 15, 17, 63, 65, 127, 40, 200, 3, 90] * 8
+    o = np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
+    K, R = len(n), sum(n)
+    A, dY = _rand(rng, (R, d_in), "bf16", True), _rand(rng, (R, d_out), "bf16", True)
+    odd = np.repeat(np.arange(K) % 2 == 1, n)
+    ref = dw_ref(_f64(dY), _f64(A), o, K)[::2]
+    A[torch.from_numpy(odd).cuda()] = float("inf")
+    dY[torch.from_numpy(odd).cuda()] = float("nan")
+    e = ExpertProduct(K, d_in, d_out, torch.bfloat16, R)
+    od = torch.from_numpy(o).cuda()
+    for _ in range(20):
+        dW = e.backward_weights(dY, A, od, out_dtype=torch.float32)
+        assert np.array_equal(_f64(dW[::2]), ref)
+        assert torch.isnan(dW[1::2]).all()
+    assert e.device_status() == G.GMM_OK
