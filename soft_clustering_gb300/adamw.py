@@ -6,6 +6,7 @@
 from __future__ import annotations
 
 import ctypes
+from operator import is_
 
 import torch
 
@@ -28,9 +29,14 @@ class AdamW:
     CUDA tensors, updated in place.
 
     state_bits: 32 (float moments) or 8 (codes with a scale per 256 elements).
-    master: hold 16-bit parameters in float32 as well (``self.master``).
+    master: hold 16-bit parameters in float32 as well (``self.state["master"]``;
+    None for a float32 one).
     state, step: resume; a dict of lists m, v (and m_scale, v_scale in 8 bits,
     master with master=True) as ``self.state`` holds them, and the steps taken.
+
+    ``params`` and the lists of ``state`` are the caller's to change between
+    calls: every call goes to the tensors that they hold then, wherever those
+    have their storage, and refuses ones of another size or type.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
@@ -43,17 +49,55 @@ class AdamW:
         for i, p in enumerate(self.params):
             if not torch.is_tensor(p) or p.device.type != "cuda":
                 raise ValueError("params[%d] is not a CUDA tensor" % i)
-            _dense(p, "params[%d]" % i, p.numel(), tuple(TORCH_XDTYPE), self.params[0].device)
+        self._device = self.params[0].device if self.params else None
+        self._given = [(p.numel(), p.dtype) for p in self.params]
+        self._check_params()
         self.state = self._state(state, master)
-        self._table = (gmm_adamw_tensor * max(1, len(self.params)))()
-        self._rows = [(self._table[i], p.numel(), p.device) for i, p in enumerate(self.params)]
+        self._master = "master" in self.state
         self._opts = gmm_adamw_opts()
         self._opts.state_bits = state_bits
+        self._fill_table()
+
+    def _check_params(self):
+        if len(self.params) != len(self._given):
+            raise ValueError("%d parameters, %d at first" % (len(self.params), len(self._given)))
+        for i, (p, (n, dt)) in enumerate(zip(self.params, self._given)):
+            _dense(p, "params[%d]" % i, n, (dt,) if dt in TORCH_XDTYPE else tuple(TORCH_XDTYPE),
+                   self._device)
+
+    def _flat(self):
+        out = list(self.params)
+        for ts in self.state.values():
+            out += ts
+        return out
+
+    def _fill_table(self):
+        """The tensors' addresses for the library, and what `_bind` knows them by."""
+        self._table = (gmm_adamw_tensor * max(1, len(self.params)))()
+        self._rows = [(self._table[i], n, self._device) for i, (n, _) in enumerate(self._given)]
         for i, p in enumerate(self.params):
             e = self._table[i]
             e.param, e.n, e.param_dtype = p.data_ptr(), p.numel(), TORCH_XDTYPE[p.dtype]
             for k, ts in self.state.items():
                 setattr(e, k, ts[i].data_ptr() if ts[i] is not None else None)
+        self._held = self._flat()
+        self._lookups = [t.data_ptr for t in self._held if t is not None]
+        for p in self.params:
+            self._lookups += [p.numel, p.is_contiguous]
+        self._found = [f() for f in self._lookups]
+        self._types = [p.dtype for p in self.params]
+
+    def _bind(self):
+        """Brings the table up to date where a list holds another tensor than at
+        the last call, or a tensor has other storage."""
+        flat = self._flat()
+        if (len(flat) == len(self._held) and all(map(is_, flat, self._held))
+                and [f() for f in self._lookups] == self._found
+                and [p.dtype for p in self.params] == self._types):
+            return
+        self._check_params()
+        self.state = self._state(self.state, self._master)
+        self._fill_table()
 
     def _state(self, given, master):
         bits = self.state_bits
@@ -87,13 +131,14 @@ class AdamW:
         not 0 (the step still counts)."""
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
+        self._bind()
         for i, (g, (e, n, device)) in enumerate(zip(grads, self._rows)):
             dt = TORCH_XDTYPE.get(g.dtype) if torch.is_tensor(g) else None
             if dt is None or g.numel() != n or g.device != device or not g.is_contiguous():
                 _dense(g, "grads[%d]" % i, n, tuple(TORCH_XDTYPE), device)
             e.grad, e.grad_dtype = g.data_ptr(), dt
         if skip is not None:
-            _dense(skip, "skip", 1, (torch.int32,), self.params[0].device)
+            _dense(skip, "skip", 1, (torch.int32,), self._device or skip.device)
         o = self._opts
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
         o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self.steps + 1
@@ -104,6 +149,7 @@ class AdamW:
 
     def moments(self, m_out=None, v_out=None, stream=None):
         """The moments in float32: two lists of tensors (given ones are written)."""
+        self._bind()
         def outs(ts, name):
             if ts is None:
                 return [torch.empty(p.shape, dtype=torch.float32, device=p.device)
