@@ -144,12 +144,14 @@ class AdamW:
         o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self.steps + 1
         o.skip = skip.data_ptr() if skip is not None else None
         r = gmm_adamw_step(self._table, len(self.params), o, stream=stream)
+        torch.autograd.graph.increment_version(self.params)  # autograd sees the change
         self.steps += 1
         return r
 
     def moments(self, m_out=None, v_out=None, stream=None):
         """The moments in float32: two lists of tensors (given ones are written)."""
         self._bind()
+
         def outs(ts, name):
             if ts is None:
                 return [torch.empty(p.shape, dtype=torch.float32, device=p.device)

@@ -112,3 +112,16 @@ def test_changes_that_are_refused(cuda):
     refused(lambda: opt.params.append(p[0]), opt.params.pop)
     opt.step(grads[0])
     assert opt.steps == 1
+
+
+@pytest.mark.gpu
+def test_autograd_sees_the_step(cuda):
+    """A backward pass that saved the parameter before the step refuses."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    x = torch.ones(8, device="cuda", requires_grad=True)
+    y = (w * x).sum()
+    AdamW([w]).step([torch.ones(8, device="cuda")])
+    with pytest.raises(RuntimeError):
+        y.backward()
