@@ -14,6 +14,8 @@ happens here.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (GMM_F32, gmm_collect, gmm_expert_product, gmm_expert_product_dw,
@@ -42,12 +44,19 @@ def _device(device):
     return d
 
 
+def _on(stream):
+    """torch work within goes to `stream` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream))
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor for work on `stream` (None: the current one)."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(s):
+    with _on(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -206,30 +215,36 @@ class LocalExperts:
     """A layer of K experts y = sum_t gamma[n, t] W[ids[n, t]] x[n] for N points.
 
     W [K, d_out, d_in] is the caller's (``adamw.AdamW`` trains it).  ``forward``
-    keeps what ``backward`` needs until the next ``forward``.
+    keeps what ``backward`` needs until the next ``forward``, gamma by value: its
+    buffer may be written again in between (the next batch's assignment).
     """
 
     def __init__(self, N, m, K, d_in, d_out, dtype, device="cuda"):
         self.router = Router(N, m, K, device)
         self.product = ExpertProduct(K, d_in, d_out, dtype, self.router.rows, device)
+        self._gamma = torch.empty(self.router.N, self.router.m, dtype=torch.float32,
+                                  device=self.router.device)
         self._kept = None
 
     def forward(self, X, ids, gamma, W, stream=None):
         """X [N, d_in], ids and gamma [N, m] as ``Assigner`` holds them -> [N, d_out]."""
         r = self.router
+        _need(gamma, "gamma", (r.N, r.m), torch.float32, r.device)
         r.route(ids, stream=stream)
         A = r.spread(X, stream=stream)
         Y = self.product.forward(A, r.offsets, W, stream=stream)
-        self._kept = (A, Y, gamma)
+        with _on(stream):
+            self._gamma.copy_(gamma)
+        self._kept = (A, Y)
         return r.collect(Y, gamma, stream=stream)
 
     def backward(self, dout, W, weight_dtype=None, stream=None):
         """(dX, dgamma, dW) of the last ``forward`` for the answer's gradient."""
         if self._kept is None:
             raise RuntimeError("backward before forward")
-        A, Y, gamma = self._kept
+        A, Y = self._kept
         r = self.router
-        dY, dgamma = r.spread(dout, gamma, Y, stream=stream)
+        dY, dgamma = r.spread(dout, self._gamma, Y, stream=stream)
         dA = self.product.backward_rows(dY, r.offsets, W, stream=stream)
         dW = self.product.backward_weights(dY, A, r.offsets, out_dtype=weight_dtype, stream=stream)
         return r.collect(dA, stream=stream), dgamma, dW

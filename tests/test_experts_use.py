@@ -45,3 +45,35 @@ def test_ragged_ends_in_pairs_of_blocks(cuda, d_in, d_out):
         assert np.array_equal(_f64(dW[::2]), ref)
         assert torch.isnan(dW[1::2]).all()
     assert e.device_status() == G.GMM_OK
+
+
+def _layer(seed=0, N=300, m=2, K=6, d=64, drop=0.1):
+    import torch
+    from soft_clustering_gb300.experts import LocalExperts
+    rng = np.random.default_rng(seed)
+    ids = torch.from_numpy(_ids(rng, N, m, K, drop)).cuda()
+    gam = torch.from_numpy(rng.random((N, m)).astype(np.float32)).cuda()
+    X, W, c = _rand(rng, (N, d), "bf16"), _rand(rng, (K, d, d), "bf16"), _rand(rng, (N, d), "bf16")
+    return ids, gam, X, W, c, LocalExperts(N, m, K, d, d, torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("side", [False, True])
+def test_gate_buffers_written_between_forward_and_backward(cuda, side):
+    """The next batch's ids and gamma in the buffers that forward was given."""
+    import torch
+    ids, gam, X, W, c, layer = _layer()
+    s = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    layer.forward(X, ids, gam, W)
+    want = layer.backward(c, W)
+    torch.cuda.synchronize()
+    layer.forward(X, ids, gam, W, stream=s)
+    torch.cuda.synchronize()
+    gam.fill_(float("nan"))
+    ids.fill_(3)
+    torch.cuda.synchronize()
+    got = layer.backward(c, W, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
