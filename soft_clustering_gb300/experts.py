@@ -96,10 +96,12 @@ class Router:
         self.entry = torch.full((self.rows,), -1, dtype=torch.int32, device=dev)
         self.slot = torch.full((self.N, self.m), -1, dtype=torch.int32, device=dev)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+        self.routes = 0  # calls of ``route`` so far
 
     def route(self, ids, stream=None):
         """ids: [N, m] int32, as ``Assigner.ids``."""
         _need(ids, "ids", (self.N, self.m), torch.int32, self.device)
+        self.routes += 1
         gmm_route(ids, self.N, self.m, self.K, self.offsets, self.entry, self.slot, self.ws,
                   self.ws_bytes, stream=stream)
 
@@ -230,20 +232,23 @@ class LocalExperts:
         """X [N, d_in], ids and gamma [N, m] as ``Assigner`` holds them -> [N, d_out]."""
         r = self.router
         _need(gamma, "gamma", (r.N, r.m), torch.float32, r.device)
+        self._kept = None  # its rows lose their places now
         r.route(ids, stream=stream)
         A = r.spread(X, stream=stream)
         Y = self.product.forward(A, r.offsets, W, stream=stream)
         with _on(stream):
             self._gamma.copy_(gamma)
-        self._kept = (A, Y)
+        self._kept = (A, Y, r.routes)
         return r.collect(Y, gamma, stream=stream)
 
     def backward(self, dout, W, weight_dtype=None, stream=None):
         """(dX, dgamma, dW) of the last ``forward`` for the answer's gradient."""
         if self._kept is None:
             raise RuntimeError("backward before forward")
-        A, Y = self._kept
+        A, Y, routes = self._kept
         r = self.router
+        if r.routes != routes:
+            raise RuntimeError("the router was given other ids after forward")
         dY, dgamma = r.spread(dout, self._gamma, Y, stream=stream)
         dA = self.product.backward_rows(dY, r.offsets, W, stream=stream)
         dW = self.product.backward_weights(dY, A, r.offsets, out_dtype=weight_dtype, stream=stream)

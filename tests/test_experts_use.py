@@ -77,3 +77,28 @@ def test_gate_buffers_written_between_forward_and_backward(cuda, side):
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_backward_of_rows_that_lost_their_places(cuda):
+    """Other ids in the layer's router, or a forward that failed half way: no
+    backward pass of the rows before."""
+    import torch
+    ids, gam, X, W, c, layer = _layer()
+    other = ids.flip(0).contiguous()
+    want = layer.forward(X, ids, gam, W)
+    layer.router.route(other)
+    with pytest.raises(RuntimeError):
+        layer.backward(c, W)
+    assert torch.equal(layer.forward(X, ids, gam, W), want)
+    layer.backward(c, W)
+    for bad in ((X, other, gam, W[:, :, :32].contiguous()), (X.float(), other, gam, W)):
+        layer.forward(X, ids, gam, W)
+        with pytest.raises(ValueError):
+            layer.forward(*bad)
+        with pytest.raises(RuntimeError):
+            layer.backward(c, W)
+    layer.forward(X, ids, gam, W)
+    with pytest.raises(ValueError):  # refused before anything changed
+        layer.forward(X, other, gam[:, :1], W)
+    layer.backward(c, W)
