@@ -48,8 +48,14 @@ def _on(stream):
     """torch work within goes to `stream` (None: the current one)."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(stream))
+    return torch.cuda.stream(_current(stream, None))
+
+
+def _current(stream, device):
+    """`stream` as torch's Stream (None: the current one)."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -238,17 +244,22 @@ class LocalExperts:
         Y = self.product.forward(A, r.offsets, W, stream=stream)
         with _on(stream):
             self._gamma.copy_(gamma)
-        self._kept = (A, Y, r.routes)
+        self._kept = (A, Y, r.routes, _current(stream, r.device).cuda_stream)
         return r.collect(Y, gamma, stream=stream)
 
     def backward(self, dout, W, weight_dtype=None, stream=None):
         """(dX, dgamma, dW) of the last ``forward`` for the answer's gradient."""
         if self._kept is None:
             raise RuntimeError("backward before forward")
-        A, Y, routes = self._kept
+        A, Y, routes, made_on = self._kept
         r = self.router
         if r.routes != routes:
             raise RuntimeError("the router was given other ids after forward")
+        s = _current(stream, r.device)
+        if s.cuda_stream != made_on:
+            # their memory goes back to the stream they were made on
+            A.record_stream(s)
+            Y.record_stream(s)
         dY, dgamma = r.spread(dout, self._gamma, Y, stream=stream)
         dA = self.product.backward_rows(dY, r.offsets, W, stream=stream)
         dW = self.product.backward_weights(dY, A, r.offsets, out_dtype=weight_dtype, stream=stream)

@@ -102,3 +102,25 @@ def test_backward_of_rows_that_lost_their_places(cuda):
     with pytest.raises(ValueError):  # refused before anything changed
         layer.forward(X, other, gam[:, :1], W)
     layer.backward(c, W)
+
+
+@pytest.mark.gpu
+def test_kept_rows_outlive_a_backward_on_another_stream(cuda):
+    """Memory of the kept rows is not handed out again while a backward pass on
+    another stream may still read it."""
+    import torch
+    ids, gam, X, W, c, layer = _layer()
+    layer.forward(X, ids, gam, W)
+    want = [t.clone() for t in layer.backward(c, W)]
+    layer.forward(X, ids, gam, W)
+    shape, side = layer._kept[0].shape, torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+        got = layer.backward(c, W)
+    layer._kept = None  # as the next forward does first
+    taken = [torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert len(taken) == 4
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
