@@ -69,7 +69,7 @@ def train(N=20000, D=64, K=16, d_out=32, steps=150, state_bits=8, seed=0, log=pr
         opt.step([dW])
         if log and i % 25 == 0:
             log("step %4d  mean squared error %.5f" % (i, losses[-1]))
-    assert layer.product.device_status() == G.GMM_OK
+    assert layer.device_status() == G.GMM_OK
     return losses
 
 

@@ -90,8 +90,10 @@ gmm_status gmm_collect(const void* Z, gmm_dtype xdtype, int64_t N, int D, int m,
  * 16-bit rows of a multiple of 16 bytes at 16-byte aligned addresses use the
  * tensor cores; other sizes and GMM_F32 use CUDA cores in fp32.
  * ws: gmm_expert_ws_bytes(R, d_in, d_out, K, xdtype) bytes, 256-byte
- *     aligned, of one call at a time (calls that overlap need one each);
- *     gmm_last_device_status(ws, stream) reports a wait that gave up.
+ *     aligned, of one call at a time (calls that overlap need one each).  Its
+ *     first 256 bytes are the status word's: zero them once, before the first
+ *     call.  gmm_last_device_status(ws, stream) then reports the first wait
+ *     that gave up in any of the calls since; no call resets the word.
  * d_in, d_out >= 1 with d_in*d_out <= 2^31 - 1, 1 <= K <= 65536, R <= 2^31 - 1.
  * More than 65535 blocks of 64 columns on CUDA cores, or 2^31 - 1 tiles on the
  * tensor cores, are GMM_ERR_UNSUPPORTED.

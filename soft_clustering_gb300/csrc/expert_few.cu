@@ -101,11 +101,8 @@ __device__ __forceinline__ void few_rows(const T* __restrict__ A, const T* __res
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 3)
 few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
-                const int64_t* __restrict__ offsets, const T* __restrict__ W, T* __restrict__ Y,
-                DeviceStatus* __restrict__ st) {
+                const int64_t* __restrict__ offsets, const T* __restrict__ W, T* __restrict__ Y) {
   __shared__ int found[3][kThreads / 32];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
-    reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
   const int64_t row = blockIdx.y;
   const int warp = threadIdx.x >> 5;
   // the offsets at or before the row: how many, and the last; the first after
@@ -155,16 +152,15 @@ few_rows_kernel(const T* __restrict__ A, int64_t R, int d_in, int d_out, int K,
 }  // namespace
 
 gmm_status few_rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_in,
-                            int d_out, int K, const int64_t* offsets, void* ws, cudaStream_t s) {
+                            int d_out, int K, const int64_t* offsets, cudaStream_t s) {
   const dim3 grid((d_out + kBlockFeats - 1) / kBlockFeats, (unsigned)R);
   ProfScope p("few_rows_kernel", s);
-  DeviceStatus* st = at<DeviceStatus>(ws, 0);
   if (xdtype == GMM_BF16)
     few_rows_kernel<<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)A, R, d_in, d_out, K, offsets,
-                                              (const __nv_bfloat16*)W, (__nv_bfloat16*)Y, st);
+                                              (const __nv_bfloat16*)W, (__nv_bfloat16*)Y);
   else
     few_rows_kernel<<<grid, kThreads, 0, s>>>((const __half*)A, R, d_in, d_out, K, offsets,
-                                              (const __half*)W, (__half*)Y, st);
+                                              (const __half*)W, (__half*)Y);
   return launched();
 }
 

@@ -28,11 +28,9 @@ constexpr int kListSmem = 4096;   // components whose first tiles fit in shared 
 // waits for this one's end itself.
 __global__ void __launch_bounds__(kListThreads)
 tile_list_kernel(const int64_t* __restrict__ offsets, int K, int64_t R, int T, uint32_t room,
-                 DeviceStatus* __restrict__ st, int32_t* __restrict__ count,
-                 uint32_t* __restrict__ first, int4* __restrict__ tiles) {
+                 int32_t* __restrict__ count, uint32_t* __restrict__ first, int4* __restrict__ tiles) {
   __shared__ uint32_t wsum[32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
   __shared__ uint32_t before[kListSmem + 1];
   const int G = K + 1;
   const int per = (G + kListThreads - 1) / kListThreads;
@@ -143,10 +141,7 @@ rows_simt_kernel(const T* __restrict__ A, const T* __restrict__ W, T* __restrict
 template <typename T, typename TO>
 __global__ void __launch_bounds__(256)
 weights_simt_kernel(const T* __restrict__ dY, const T* __restrict__ A, TO* __restrict__ dW,
-                    int d_in, int d_out, int K, const int64_t* __restrict__ offsets, int64_t R,
-                    DeviceStatus* __restrict__ st) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
-    reinterpret_cast<int32_t*>(st)[threadIdx.x] = 0;
+                    int d_in, int d_out, int K, const int64_t* __restrict__ offsets, int64_t R) {
   const int o0 = blockIdx.x * kT, i0 = blockIdx.y * kT;
   for (int k = blockIdx.z; k < K; k += gridDim.z) {
     const int64_t a = clamp_row(offsets[k], R), b = clamp_row(offsets[k + 1], R);
@@ -189,11 +184,11 @@ gmm_status rows_simt(const void* A, const void* W, void* Y, int64_t R, int d_fro
 
 template <typename T, typename TO>
 gmm_status weights_simt(const void* dY, const void* A, void* dW, int64_t R, int d_in, int d_out,
-                        int K, const int64_t* offsets, void* ws, cudaStream_t s) {
+                        int K, const int64_t* offsets, cudaStream_t s) {
   const dim3 grid((d_out + kT - 1) / kT, (d_in + kT - 1) / kT, K < 65535 ? K : 65535);
   ProfScope p("weights_simt_kernel", s);
   weights_simt_kernel<T, TO><<<grid, 256, 0, s>>>((const T*)dY, (const T*)A, (TO*)dW, d_in, d_out,
-                                                  K, offsets, R, at<DeviceStatus>(ws, 0));
+                                                  K, offsets, R);
   return launched();
 }
 
@@ -202,7 +197,7 @@ gmm_status rows_product(const void* A, int xdtype, const void* W, void* Y, int64
                         cudaStream_t s) {
   const bool tc = tc_product_ok(xdtype, R, d_from, d_to, A, W, Y);
   if (tc && !dx && few_rows(R, K))
-    return few_rows_product(A, xdtype, W, Y, R, d_from, d_to, K, offsets, ws, s);
+    return few_rows_product(A, xdtype, W, Y, R, d_from, d_to, K, offsets, s);
   if (tc)
     return tc_rows(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
   if ((d_to + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
@@ -219,8 +214,8 @@ gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
                       const ProductLayout& L, cudaStream_t s) {
   ProfScope p("tile_list_kernel", s);
   tile_list_kernel<<<1, kListThreads, 0, s>>>(
-      offsets, K, R, T, (uint32_t)ProductLayout::most_tiles(R, K, T), at<DeviceStatus>(ws, 0),
-      at<int32_t>(ws, L.off_count), at<uint32_t>(ws, L.off_first), at<int4>(ws, L.off_tiles));
+      offsets, K, R, T, (uint32_t)ProductLayout::most_tiles(R, K, T), at<int32_t>(ws, L.off_count),
+      at<uint32_t>(ws, L.off_first), at<int4>(ws, L.off_tiles));
   return launched();
 }
 
@@ -263,13 +258,13 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
   if (R > 0 && tc_product_ok(xdtype, R, d_in, d_out, dY, A, dW))
     return tc_weights(dY, A, xdtype, R, d_in, d_out, K, offsets, dW, wdtype, ws, s);
   if ((d_in + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
-  if (xdtype == GMM_F32) return weights_simt<float, float>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
+  if (xdtype == GMM_F32) return weights_simt<float, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
   if (xdtype == GMM_F16) {
-    if (wdtype == GMM_F32) return weights_simt<__half, float>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
-    return weights_simt<__half, __half>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
+    if (wdtype == GMM_F32) return weights_simt<__half, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+    return weights_simt<__half, __half>(dY, A, dW, R, d_in, d_out, K, offsets, s);
   }
-  if (wdtype == GMM_F32) return weights_simt<__nv_bfloat16, float>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
-  return weights_simt<__nv_bfloat16, __nv_bfloat16>(dY, A, dW, R, d_in, d_out, K, offsets, ws, s);
+  if (wdtype == GMM_F32) return weights_simt<__nv_bfloat16, float>(dY, A, dW, R, d_in, d_out, K, offsets, s);
+  return weights_simt<__nv_bfloat16, __nv_bfloat16>(dY, A, dW, R, d_in, d_out, K, offsets, s);
 }
 
 }  // extern "C"

@@ -52,7 +52,7 @@ struct ProductLayout {
 };
 
 // Fills the tile list {component or -1, first row, rows, 0}, its length and
-// each component's first tile, and clears the workspace's status word.
+// each component's first tile.
 gmm_status list_tiles(const int64_t* offsets, int K, int64_t R, int T, void* ws,
                       const ProductLayout& L, cudaStream_t s);
 
@@ -68,7 +68,7 @@ gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R,
 // offsets themselves, 256 at a time: worth it for a few thousand components.
 inline bool few_rows(int64_t R, int K) { return R > 0 && R <= 32 && R <= 2 * (int64_t)K && K <= 4096; }
 gmm_status few_rows_product(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_in,
-                            int d_out, int K, const int64_t* offsets, void* ws, cudaStream_t s);
+                            int d_out, int K, const int64_t* offsets, cudaStream_t s);
 gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int d_in, int d_out,
                       int K, const int64_t* offsets, void* dW, int wdtype, void* ws,
                       cudaStream_t s);

@@ -518,11 +518,8 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
   if (a.tiles) {
     // the list and everything before it is there
     asm volatile("griddepcontrol.wait;" ::: "memory");
-  } else {
-    // no wait gives up in the time that this takes
-    if (blockIdx.x == 0 && threadIdx.x < sizeof(DeviceStatus) / 4)
-      reinterpret_cast<int32_t*>(a.st)[threadIdx.x] = 0;
-    if (MODE != kDw) count_tiles(a, before);
+  } else if (MODE != kDw) {
+    count_tiles(a, before);
   }
   tc::tc_fence_before();
   __syncthreads();

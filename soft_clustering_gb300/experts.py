@@ -23,6 +23,8 @@ from . import (GMM_F32, gmm_collect, gmm_expert_product, gmm_expert_product_dw,
                gmm_route_ws_bytes, gmm_spread)
 from .torch_api import TORCH_XDTYPE
 
+STATUS_BYTES = 256  # of a products' workspace, at its head
+
 
 def _need(t, name, shape, dtype, device):
     """A dense tensor of this shape (a tuple), type and device, or ValueError."""
@@ -216,7 +218,13 @@ class ExpertProduct:
         return out
 
     def device_status(self, stream=None):
+        """The first failure on the device in any call so far, or GMM_OK; it
+        stays until ``clear_status``.  Waits for `stream`."""
         return gmm_last_device_status(self.ws, stream)
+
+    def clear_status(self, stream=None):
+        with _on(stream):
+            self.ws[:STATUS_BYTES].zero_()
 
 
 class LocalExperts:
@@ -264,3 +272,7 @@ class LocalExperts:
         dA = self.product.backward_rows(dY, r.offsets, W, stream=stream)
         dW = self.product.backward_weights(dY, A, r.offsets, out_dtype=weight_dtype, stream=stream)
         return r.collect(dA, stream=stream), dgamma, dW
+
+    def device_status(self, stream=None):
+        """``ExpertProduct.device_status`` of all three products."""
+        return self.product.device_status(stream)

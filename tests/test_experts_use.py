@@ -124,3 +124,31 @@ def test_kept_rows_outlive_a_backward_on_another_stream(cuda):
     assert len(taken) == 4
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,N,K,d", [("bf16", 300, 6, 64), ("bf16", 4, 20, 64), ("bf16", 900, 1500, 256),
+                                         ("bf16", 20000, 3, 64), ("f32", 60, 4, 24), ("f16", 0, 4, 64)])
+def test_a_failure_outlives_the_products_after_it(cuda, dtype, N, K, d):
+    """A status raised in one product is there after the others, in every form
+    of the product, until it is cleared."""
+    import torch
+    from soft_clustering_gb300.experts import LocalExperts
+    rng = np.random.default_rng(N)
+    ids = torch.from_numpy(rng.integers(0, K, (N, 1)).astype(np.int32)).cuda()
+    X, W, c = _rand(rng, (N, d), dtype), _rand(rng, (K, d, d), dtype), _rand(rng, (N, d), dtype)
+    layer = LocalExperts(N, 1, K, d, d, X.dtype)
+    gam = torch.ones(N, 1, device="cuda")
+
+    def step():
+        layer.forward(X, ids, gam, W)
+        layer.backward(c, W)
+
+    step()
+    assert layer.device_status() == G.GMM_OK
+    layer.product.ws[:4].view(torch.int32).fill_(G.GMM_ERR_TIMEOUT)
+    step()
+    assert layer.device_status() == G.GMM_ERR_TIMEOUT
+    layer.product.clear_status()
+    step()
+    assert layer.device_status() == G.GMM_OK
