@@ -131,7 +131,8 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
  * skip: optional device int32; when it is not 0 the call changes nothing
  *   (the caller's check for non-finite gradients; without it a non-finite
  *   gradient goes into the parameter and the moments as the formula says, and
- *   in 8 bits spoils its block).
+ *   in 8 bits, where a moment that is not finite has no code, every value of
+ *   that moment in its block becomes NaN).
  * tensors_host: host array, read before the call returns.
  * Arrays need the alignment of their element type only; 16-byte aligned
  * ones (8-byte for 8-bit moments) are faster.

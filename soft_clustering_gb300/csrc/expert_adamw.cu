@@ -29,6 +29,7 @@
 // 2e8 bf16 elements with 8-bit moments 467 us (4.3 TB/s: about 54
 // instructions an element, 45 % of the issue slots, four blocks a
 // multiprocessor); their moments in fp32 317 us (6.3 TB/s).
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -269,10 +270,13 @@ __device__ __forceinline__ float rcp_near(float x) {
 constexpr float kNear = 0.5f - 1.5e-4f;
 constexpr float kMagic = 12582912.f;  // 1.5 2^23: x + kMagic holds rint(x) in its low bits
 
-// Scale of a block whose largest magnitude is `big`, and its inverse.
+// Scale of a block whose largest magnitude is `big`, and its inverse.  A value
+// that is not finite has no code: the scale is NaN then, and so is every value
+// of the block from there on.
 template <int TOP>
 __device__ __forceinline__ float2 scale_of(float big) {
-  if (!(big >= kTiny)) return make_float2(0.f, 0.f);
+  if (big < kTiny) return make_float2(0.f, 0.f);
+  if (!(big <= FLT_MAX)) return make_float2(NAN, NAN);
   return make_float2(__fmul_rn(big, (float)(1.0 / (TOP * TOP))),
                      __fmul_rn(__frcp_rn(big), (float)(TOP * TOP)));
 }
@@ -353,7 +357,13 @@ __device__ __forceinline__ uint2 encode_root(const float2* v, const float2* root
   return make_uint2(a, b);
 }
 
-// Largest of the warp's non-negative values (their bits order them).
+// The larger of two values, NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Largest of the warp's non-negative values (their bits order them, NaN last).
 __device__ __forceinline__ float warp_max_pos(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
@@ -471,8 +481,8 @@ __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry
   float mb = 0.f, vb = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    mb = fmaxf(mb, fmaxf(fabsf(m[j].x), fabsf(m[j].y)));
-    vb = fmaxf(vb, fmaxf(v[j].x, v[j].y));
+    mb = max_nan(mb, max_nan(fabsf(m[j].x), fabsf(m[j].y)));
+    vb = max_nan(vb, max_nan(v[j].x, v[j].y));
   }
   const float2 ms = scale_of<127>(warp_max_pos(mb));
   const float2 vs = scale_of<255>(__fsqrt_rn(warp_max_pos(vb)));

@@ -125,3 +125,34 @@ def test_autograd_sees_the_step(cuda):
     AdamW([w]).step([torch.ones(8, device="cuda")])
     with pytest.raises(RuntimeError):
         y.backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("at,n", [(300, 1024), (0, 256), (511, 700), (699, 700)])
+def test_gradients_that_are_not_finite(cuda, bad, dtype, at, n):
+    """32 bits: the element alone.  8 bits: its parameter at once, both moments
+    of its block, and nothing else."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    block = slice(at // 256 * 256, min(n, at // 256 * 256 + 256))
+    for bits in (32, 8):
+        p = torch.zeros(n, device="cuda")
+        opt = AdamW([p], state_bits=bits)
+        opt.step([torch.linspace(-1, 1, n, device="cuda").to(getattr(torch, dtype))])
+        g = torch.ones(n, device="cuda", dtype=getattr(torch, dtype))
+        g[at] = bad
+        opt.step([g])
+        hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+        hit[at] = True
+        assert torch.equal(~torch.isfinite(p), hit)
+        if bits == 8:
+            hit[block] = True
+        for x in opt.moments():
+            assert torch.equal(~torch.isfinite(x[0]), hit)
+            if bits == 8:
+                assert torch.isnan(x[0][block]).all()
+        opt.step([torch.ones(n, device="cuda")])
+        assert torch.equal(~torch.isfinite(p), hit)
+        assert torch.equal(~torch.isfinite(opt.moments()[0][0]), hit)
