@@ -11,6 +11,7 @@ from operator import is_
 import torch
 
 from . import (gmm_adamw_moments, gmm_adamw_opts, gmm_adamw_step, gmm_adamw_tensor)
+from .experts import _empty
 from .torch_api import TORCH_XDTYPE
 
 BLOCK = 256  # elements that share one scale of an 8-bit moment
@@ -154,8 +155,7 @@ class AdamW:
 
         def outs(ts, name):
             if ts is None:
-                return [torch.empty(p.shape, dtype=torch.float32, device=p.device)
-                        for p in self.params]
+                return [_empty(p.shape, torch.float32, p.device, stream) for p in self.params]
             if len(ts) != len(self.params):
                 raise ValueError("%s: %d tensors for %d parameters" % (name, len(ts), len(self.params)))
             for i, (t, p) in enumerate(zip(ts, self.params)):

@@ -156,3 +156,26 @@ def test_gradients_that_are_not_finite(cuda, bad, dtype, at, n):
         opt.step([torch.ones(n, device="cuda")])
         assert torch.equal(~torch.isfinite(p), hit)
         assert torch.equal(~torch.isfinite(opt.moments()[0][0]), hit)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_on_another_stream(cuda, bits):
+    """Outputs that `moments` makes for another stream are not memory that the
+    current one still writes."""
+    import torch
+    n = 1 << 20
+    p, _, opt = _make(n=(n,), bits=bits)
+    opt.step([torch.ones(n, device="cuda")])
+    want = [t[0].clone() for t in opt.moments()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    x = [torch.empty(n, device="cuda") for _ in range(2)]
+    torch.cuda._sleep(200_000_000)  # about a tenth of a second
+    for t in x:
+        t.fill_(3.0)
+    del x, t
+    got = opt.moments(stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b[0])
