@@ -134,6 +134,9 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
  *   in 8 bits, where a moment that is not finite has no code, every value of
  *   that moment in its block becomes NaN).
  * tensors_host: host array, read before the call returns.
+ * opts->step and both corrections made from it are fixed by the call: a call
+ * captured in a graph takes the same step at every replay.  For graphs there
+ * is gmm_adamw_step_counted.
  * Arrays need the alignment of their element type only; 16-byte aligned
  * ones (8-byte for 8-bit moments) are faster.
  */
@@ -159,6 +162,15 @@ typedef struct {
 
 gmm_status gmm_adamw_step(const gmm_adamw_tensor* tensors_host, int count,
                           const gmm_adamw_opts* opts, void* stream);
+
+/*
+ * gmm_adamw_step_counted - the same step, counted on the device: `steps`
+ * (device, 8-byte aligned) holds the steps taken so far, this one is number
+ * *steps + 1, and the call adds one to it after its last launch, also where
+ * `skip` leaves everything else as it was.  opts->step is not read.
+ */
+gmm_status gmm_adamw_step_counted(const gmm_adamw_tensor* tensors_host, int count,
+                                  const gmm_adamw_opts* opts, int64_t* steps, void* stream);
 
 /* The moments in fp32, whatever holds them (for checkpoints and inspection):
  * m_out_host[i], v_out_host[i] are device pointers to n floats each, written.

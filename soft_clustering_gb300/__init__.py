@@ -29,7 +29,7 @@ EXPORTS = (
     "gmm_profile_reset", "gmm_em_step_noalloc", "gmm_debug_tc_gemm", "gmm_ivf_lists_ws_bytes",
     "gmm_ivf_lists", "gmm_route_ws_bytes", "gmm_route", "gmm_spread", "gmm_collect",
     "gmm_expert_ws_bytes", "gmm_expert_product", "gmm_expert_product_dx",
-    "gmm_expert_product_dw", "gmm_adamw_step", "gmm_adamw_moments",
+    "gmm_expert_product_dw", "gmm_adamw_step", "gmm_adamw_step_counted", "gmm_adamw_moments",
 )
 
 
@@ -111,6 +111,7 @@ def lib():
         L.gmm_expert_product_dw.argtypes = [vp, vp, i32, i64, i32, i32, i32, vp, vp, i32, vp, sz,
                                             vp]
         L.gmm_adamw_step.argtypes = [P(gmm_adamw_tensor), i32, P(gmm_adamw_opts), vp]
+        L.gmm_adamw_step_counted.argtypes = [P(gmm_adamw_tensor), i32, P(gmm_adamw_opts), vp, vp]
         L.gmm_adamw_moments.argtypes = [P(gmm_adamw_tensor), i32, i32, P(vp), P(vp), vp]
         L.gmm_profile_enable.argtypes = [i32]
         L.gmm_profile_enable.restype = None
@@ -122,7 +123,7 @@ def lib():
                   "gmm_last_device_status", "gmm_em_step_noalloc", "gmm_ivf_lists",
                   "gmm_route", "gmm_spread", "gmm_collect", "gmm_expert_product",
                   "gmm_expert_product_dx", "gmm_expert_product_dw", "gmm_adamw_step",
-                  "gmm_adamw_moments"):
+                  "gmm_adamw_step_counted", "gmm_adamw_moments"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -315,6 +316,13 @@ def gmm_adamw_step(tensors, count, opts, stream=None, raise_on_error=True):
     """tensors: a ctypes array of gmm_adamw_tensor; opts: gmm_adamw_opts."""
     st = lib().gmm_adamw_step(tensors, count, ctypes.byref(opts), _stream(stream))
     return _check(st, "gmm_adamw_step", raise_on_error)
+
+
+def gmm_adamw_step_counted(tensors, count, opts, steps, stream=None, raise_on_error=True):
+    """As gmm_adamw_step, with the steps taken in a device int64."""
+    st = lib().gmm_adamw_step_counted(tensors, count, ctypes.byref(opts), _ptr(steps),
+                                      _stream(stream))
+    return _check(st, "gmm_adamw_step_counted", raise_on_error)
 
 
 def gmm_adamw_moments(tensors, count, state_bits, m_out, v_out, stream=None,

@@ -6,11 +6,13 @@
 from __future__ import annotations
 
 import ctypes
+import warnings
 from operator import is_
 
 import torch
 
-from . import (gmm_adamw_moments, gmm_adamw_opts, gmm_adamw_step, gmm_adamw_tensor)
+from . import (gmm_adamw_moments, gmm_adamw_opts, gmm_adamw_step, gmm_adamw_step_counted,
+               gmm_adamw_tensor)
 from .experts import _empty
 from .torch_api import TORCH_XDTYPE
 
@@ -35,29 +37,49 @@ class AdamW:
     state, step: resume; a dict of lists m, v (and m_scale, v_scale in 8 bits,
     master with master=True) as ``self.state`` holds them, and the steps taken.
 
+    capturable: the steps taken are counted on the device, so that a step
+    captured in a CUDA graph goes on at every replay; otherwise the number is
+    part of the captured call, and every replay is that one step again.
+    ``steps`` is the number of steps taken (capturable: reading it waits for the
+    device).
+
     ``params`` and the lists of ``state`` are the caller's to change between
     calls: every call goes to the tensors that they hold then, wherever those
     have their storage, and refuses ones of another size or type.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
-                 state_bits=32, master=False, state=None, step=0):
+                 state_bits=32, master=False, state=None, step=0, capturable=False):
         self.params = list(params)
         if state_bits not in (8, 32):
             raise ValueError("state_bits %s: expected 8 or 32" % (state_bits,))
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.state_bits, self.steps = state_bits, int(step)
+        self.state_bits, self._count, self._steps = state_bits, None, int(step)
         for i, p in enumerate(self.params):
             if not torch.is_tensor(p) or p.device.type != "cuda":
                 raise ValueError("params[%d] is not a CUDA tensor" % i)
         self._device = self.params[0].device if self.params else None
         self._given = [(p.numel(), p.dtype) for p in self.params]
         self._check_params()
+        if capturable:
+            self._count = torch.full((1,), int(step), dtype=torch.int64,
+                                     device=self._device or "cuda")
         self.state = self._state(state, master)
         self._master = "master" in self.state
         self._opts = gmm_adamw_opts()
         self._opts.state_bits = state_bits
         self._fill_table()
+
+    @property
+    def steps(self):
+        return self._steps if self._count is None else int(self._count.item())
+
+    @steps.setter
+    def steps(self, n):
+        if self._count is None:
+            self._steps = int(n)
+        else:
+            self._count.fill_(int(n))
 
     def _check_params(self):
         if len(self.params) != len(self._given):
@@ -142,11 +164,18 @@ class AdamW:
             _dense(skip, "skip", 1, (torch.int32,), self._device or skip.device)
         o = self._opts
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
-        o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self.steps + 1
+        o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self._steps + 1
         o.skip = skip.data_ptr() if skip is not None else None
-        r = gmm_adamw_step(self._table, len(self.params), o, stream=stream)
+        if self._count is None:
+            if torch.cuda.is_current_stream_capturing():
+                warnings.warn("AdamW.step captured without capturable=True: every replay of the "
+                              "graph takes step %d again" % o.step, stacklevel=2)
+            r = gmm_adamw_step(self._table, len(self.params), o, stream=stream)
+            self._steps += 1
+        else:
+            r = gmm_adamw_step_counted(self._table, len(self.params), o, self._count,
+                                       stream=stream)
         torch.autograd.graph.increment_version(self.params)  # autograd sees the change
-        self.steps += 1
         return r
 
     def moments(self, m_out=None, v_out=None, stream=None):

@@ -63,6 +63,9 @@ struct AdamwConst {
   int count, chunks, turns;
   int eps_covers;    // eps is far above the root of a subnormal
   const int32_t* skip;
+  // a step counted on the device: taken so far (NULL: root and rate are there)
+  const int64_t* steps;
+  double lr, beta1, beta2;
 };
 
 template <int COUNT>
@@ -620,13 +623,33 @@ __device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry&
   return turns;
 }
 
-// PH, GH: 16-bit parameters (no master) and gradients.
-template <int BITS, bool PH, bool GH, int COUNT>
-__global__ void __launch_bounds__(kWarps * 32, BITS == 8 ? 4 : 2)
+// Both bias corrections of a step that is counted on the device, by one thread.
+__device__ __forceinline__ void correct_by_count(AdamwConst& k) {
+  __shared__ float at[2];
+  if (threadIdx.x == 0) {
+    const int64_t taken = *k.steps;
+    const double n = (double)((taken < 0 ? 0 : taken) + 1);
+    at[0] = (float)pow(1.0 - pow(k.beta2, n), -0.5);
+    at[1] = (float)(k.lr / (1.0 - pow(k.beta1, n)));
+  }
+  __syncthreads();
+  k.root = at[0];
+  k.rate = at[1];
+}
+
+// PH, GH: 16-bit parameters (no master) and gradients.  MORE: the step may be
+// counted on the device.  That is a kernel of its own, since what it computes
+// takes registers that the 8-bit step lacks.
+template <bool MORE> using ConstOf = std::conditional_t<MORE, AdamwConst, const AdamwConst&>;
+template <int BITS, bool PH, bool GH, bool MORE, int COUNT>
+__global__ void __launch_bounds__(kWarps * 32, BITS == 8 ? (MORE ? 3 : 4) : 2)
 adamw_kernel(const __grid_constant__ AdamwTable<COUNT> t) {
   extern __shared__ __align__(16) uint8_t rings[];
-  const AdamwConst& k = t.k;
+  ConstOf<MORE> k = t.k;
   if (k.skip && *k.skip != 0) return;
+  if constexpr (MORE) {
+    if (k.steps) correct_by_count(k);
+  }
   const int warp = threadIdx.x >> 5;
   uint8_t* ring = rings + warp * (kAhead + 1) * stage_bytes<PH, GH>();
   const int c0 = (int)((int64_t)k.chunks * blockIdx.x / gridDim.x);
@@ -790,25 +813,22 @@ constexpr int kSmallTable = 16, kTable = 400;
 // 317 us with 24, 340 with 4 or 12).
 unsigned grid_for(int chunks, int most) { return (unsigned)(chunks < 152 * most ? chunks : 152 * most); }
 
-template <int BITS, bool PH, bool GH, int COUNT>
+template <int BITS, bool PH, bool GH, bool MORE, int COUNT>
 void launch_step(const AdamwTable<COUNT>& t, cudaStream_t s) {
   const size_t smem = BITS == 8 ? ring_bytes<PH, GH>() : 0;
   static std::atomic<uint64_t> allowed;
-  if (smem > 48 * 1024 && !allow_smem((const void*)adamw_kernel<BITS, PH, GH, COUNT>, smem, allowed)) return;
-  adamw_kernel<BITS, PH, GH, COUNT><<<grid_for(t.k.chunks, BITS == 8 ? 4 : 16), kWarps * 32, smem, s>>>(t);
+  const auto kernel = adamw_kernel<BITS, PH, GH, MORE, COUNT>;
+  if (smem > 48 * 1024 && !allow_smem((const void*)kernel, smem, allowed)) return;
+  kernel<<<grid_for(t.k.chunks, BITS == 8 ? (MORE ? 3 : 4) : 16), kWarps * 32, smem, s>>>(t);
 }
 
-}  // namespace
-}  // namespace gmm
+__global__ void count_step_kernel(int64_t* steps) { *steps = (*steps < 0 ? 0 : *steps) + 1; }
 
-using namespace gmm;
-
-extern "C" {
-
-gmm_status gmm_adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw_opts* o,
-                          void* stream) {
+// steps: of a step that is counted on the device, or NULL.
+gmm_status adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw_opts* o, int64_t* steps,
+                      void* stream) {
   if (!o || !tensors_ok(ts, count, o->state_bits, true)) return GMM_ERR_INVALID_ARG;
-  if (o->step < 1 || !(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) ||
+  if ((!steps && o->step < 1) || !(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) ||
       !(o->eps >= 0) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay) ||
       !std::isfinite(o->grad_scale) || !std::isfinite(o->eps))
     return GMM_ERR_INVALID_ARG;
@@ -820,13 +840,21 @@ gmm_status gmm_adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw
   k.c1 = (float)(1.0 - o->beta1);
   k.b2 = (float)o->beta2;
   k.c2 = (float)(1.0 - o->beta2);
-  k.root = (float)std::pow(1.0 - std::pow(o->beta2, (double)o->step), -0.5);
+  if (steps) {
+    k.steps = steps;
+    k.lr = o->lr;
+    k.beta1 = o->beta1;
+    k.beta2 = o->beta2;
+  } else {
+    k.root = (float)std::pow(1.0 - std::pow(o->beta2, (double)o->step), -0.5);
+    k.rate = (float)(o->lr / (1.0 - std::pow(o->beta1, (double)o->step)));
+  }
   k.eps = (float)o->eps;
   k.decay = (float)(1.0 - o->lr * o->weight_decay);
-  k.rate = (float)(o->lr / (1.0 - std::pow(o->beta1, (double)o->step)));
   k.skip = o->skip;
   k.eps_covers = o->eps >= 1e-10;
   const int bits = o->state_bits;
+  const bool more = steps != nullptr;
   auto fill = [&](int i, AdamwEntry& e) {
     const gmm_adamw_tensor& t = ts[i];
     e.p = t.param; e.g = t.grad; e.master = t.master; e.m = t.m; e.v = t.v;
@@ -845,19 +873,43 @@ gmm_status gmm_adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw
       return (ts[i].param_dtype != GMM_F32 && !ts[i].master) == ph && (ts[i].grad_dtype != GMM_F32) == gh;
     };
     auto go = [&](const auto& t) {
-#define GMM_GO(B)                                  \
-  if (ph && gh) launch_step<B, true, true>(t, s);   \
-  else if (ph) launch_step<B, true, false>(t, s);   \
-  else if (gh) launch_step<B, false, true>(t, s);   \
-  else launch_step<B, false, false>(t, s);
-      if (bits == 32) { GMM_GO(32) } else { GMM_GO(8) }
+#define GMM_GO(B, M)                                  \
+  if (ph && gh) launch_step<B, true, true, M>(t, s);   \
+  else if (ph) launch_step<B, true, false, M>(t, s);   \
+  else if (gh) launch_step<B, false, true, M>(t, s);   \
+  else launch_step<B, false, false, M>(t, s);
+      if (more) {
+        if (bits == 32) { GMM_GO(32, true) } else { GMM_GO(8, true) }
+      } else {
+        if (bits == 32) { GMM_GO(32, false) } else { GMM_GO(8, false) }
+      }
 #undef GMM_GO
     };
     const gmm_status r = count <= kSmallTable ? over_tables<kSmallTable>(ts, count, k, take, fill, go)
                                               : over_tables<kTable>(ts, count, k, take, fill, go);
     if (r != GMM_OK) return r;
   }
-  return GMM_OK;
+  if (!steps) return GMM_OK;
+  count_step_kernel<<<1, 1, 0, s>>>(steps);
+  return launched();
+}
+
+}  // namespace
+}  // namespace gmm
+
+using namespace gmm;
+
+extern "C" {
+
+gmm_status gmm_adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw_opts* o,
+                          void* stream) {
+  return adamw_step(ts, count, o, nullptr, stream);
+}
+
+gmm_status gmm_adamw_step_counted(const gmm_adamw_tensor* ts, int count, const gmm_adamw_opts* o,
+                                  int64_t* steps, void* stream) {
+  if (!steps || (uintptr_t)steps % 8) return GMM_ERR_INVALID_ARG;
+  return adamw_step(ts, count, o, steps, stream);
 }
 
 gmm_status gmm_adamw_moments(const gmm_adamw_tensor* ts, int count, int state_bits,

@@ -4,10 +4,19 @@ streams, graphs, values that are not finite, long schedules.
 Every comparison is with the same step taken another way, equal to the bit,
 unless a test derives its bound.
 """
+import ctypes
+
 import numpy as np
 import pytest
 
 import soft_clustering_gb300 as G
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from soft_clustering_gb300 import build
+    build.build()
+    return G.lib()
 
 
 @pytest.fixture(scope="module")
@@ -179,3 +188,95 @@ def test_moments_on_another_stream(cuda, bits):
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b[0])
+
+
+def test_refusals_of_the_counted_step(lib):
+    e = (G.gmm_adamw_tensor * 1)(G.gmm_adamw_tensor(param=256, grad=256, m=256, v=256, n=8))
+    o = lambda **k: ctypes.byref(G.gmm_adamw_opts(**{**dict(  # noqa: E731
+        lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0, state_bits=32), **k}))
+    call = lambda steps, **k: lib.gmm_adamw_step_counted(e, 1, o(**k), steps, None)  # noqa: E731
+    assert call(None) == G.GMM_ERR_INVALID_ARG
+    assert call(260) == G.GMM_ERR_INVALID_ARG
+    assert lib.gmm_adamw_step_counted(e, 1, None, 256, None) == G.GMM_ERR_INVALID_ARG
+    assert lib.gmm_adamw_step_counted(None, 1, o(), 256, None) == G.GMM_ERR_INVALID_ARG
+    for bad in (dict(beta1=1.0), dict(beta2=-0.5), dict(lr=float("nan")), dict(state_bits=8)):
+        assert call(256, **bad) == G.GMM_ERR_INVALID_ARG, bad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype,master", [("float32", False), ("bfloat16", True), ("float16", False)])
+def test_replays_count_their_steps(cuda, bits, dtype, master):
+    """A captured step that counts on the device: every replay is the next step,
+    equal to the same steps without a graph.  Against the step counted on the
+    host the moments are equal; the two corrections are each the rounding of a
+    double that may differ in its last place, so one unit of fp32 apart, 2^-23 of
+    the update each, and its at most six operations round differently: 2^-20 of
+    an update of at most 10 lr (the first steps' moments are of one size), and
+    2^-23 of the parameter for its own two roundings, a step."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    dt, lr, steps = getattr(torch, dtype), 0.01, 7
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    n = (3000, 17, 600)
+    p0 = [torch.randn(k, device="cuda", generator=g).to(dt) for k in n]
+    grads = [[torch.randn(k, device="cuda", generator=g) for k in n] for _ in range(steps)]
+
+    def made(**kw):
+        p = [t.clone() for t in p0]
+        return p, AdamW(p, lr=lr, state_bits=bits, master=master, **kw)
+
+    p, opt = made(capturable=True)
+    q, eager = made(capturable=True)
+    r, host = made()
+    buf = [t.clone() for t in grads[0]]
+    opt.step(buf)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step(buf)
+    for x in grads[1:]:
+        for b, t in zip(buf, x):
+            b.copy_(t)
+        graph.replay()
+    for x in grads:
+        eager.step(x)
+        host.step(x)
+    assert opt.steps == eager.steps == host.steps == steps
+    same = lambda a, b: all(torch.equal(x, y) for k in a.state for x, y in zip(a.state[k], b.state[k])  # noqa: E731
+                            if x is not None and k != "master")
+    assert same(opt, eager) and same(opt, host)
+    for a, b in zip(p, q):
+        assert torch.equal(a, b)
+    if dtype != "float16":  # held in fp32
+        get = lambda o, w: w if dtype == "float32" else o.state["master"]  # noqa: E731
+        for a, b in zip(get(opt, p), get(host, r)):
+            bound = steps * (2.0 ** -20 * 10 * lr + 2.0 ** -23 * (b.abs() + 10 * lr * steps))
+            assert ((a - b).abs() <= bound).all()
+
+
+@pytest.mark.gpu
+def test_steps_of_a_counted_optimiser(cuda):
+    """Set, resumed, and counted where a step is skipped."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    p = torch.zeros(8, device="cuda")
+    opt = AdamW([p], capturable=True, step=3)
+    assert opt.steps == 3
+    opt.step([p.clone()], skip=torch.ones(1, dtype=torch.int32, device="cuda"))
+    assert opt.steps == 4 and not p.any()
+    opt.steps = 10
+    opt.step([torch.ones_like(p)])
+    assert opt.steps == 11 and p.all()
+
+
+@pytest.mark.gpu
+def test_capture_with_a_fixed_step_warns(cuda):
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    p, g = torch.zeros(8, device="cuda"), torch.ones(8, device="cuda")
+    opt = AdamW([p])
+    opt.step([g])
+    with pytest.warns(UserWarning, match="capturable"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            opt.step([g])
