@@ -818,7 +818,8 @@ void launch_step(const AdamwTable<COUNT>& t, cudaStream_t s) {
   const size_t smem = BITS == 8 ? ring_bytes<PH, GH>() : 0;
   static std::atomic<uint64_t> allowed;
   const auto kernel = adamw_kernel<BITS, PH, GH, MORE, COUNT>;
-  if (smem > 48 * 1024 && !allow_smem((const void*)kernel, smem, allowed)) return;
+  // what the kernel has of its own counts too: 48 KB of rings may be too much
+  if (smem > 0 && !allow_smem((const void*)kernel, smem, allowed)) return;
   kernel<<<grid_for(t.k.chunks, BITS == 8 ? (MORE ? 3 : 4) : 16), kWarps * 32, smem, s>>>(t);
 }
 

@@ -206,7 +206,8 @@ def test_refusals_of_the_counted_step(lib):
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("dtype,master", [("float32", False), ("bfloat16", True), ("float16", False)])
-def test_replays_count_their_steps(cuda, bits, dtype, master):
+@pytest.mark.parametrize("grad", ["float32", "bfloat16"])
+def test_replays_count_their_steps(cuda, bits, dtype, master, grad):
     """A captured step that counts on the device: every replay is the next step,
     equal to the same steps without a graph.  Against the step counted on the
     host the moments are equal; the two corrections are each the rounding of a
@@ -221,7 +222,7 @@ def test_replays_count_their_steps(cuda, bits, dtype, master):
     g.manual_seed(5)
     n = (3000, 17, 600)
     p0 = [torch.randn(k, device="cuda", generator=g).to(dt) for k in n]
-    grads = [[torch.randn(k, device="cuda", generator=g) for k in n] for _ in range(steps)]
+    grads = [[torch.randn(k, device="cuda", generator=g).to(getattr(torch, grad)) for k in n] for _ in range(steps)]
 
     def made(**kw):
         p = [t.clone() for t in p0]
