@@ -59,7 +59,8 @@ def train(N=20000, D=64, K=16, d_out=32, steps=150, state_bits=8, seed=0, log=pr
     gate = fit_gate(X, K)
     W = torch.zeros(K, d_out, D, dtype=torch.bfloat16, device=X.device)
     layer = LocalExperts(N, gate.m, K, D, d_out, torch.bfloat16)
-    opt = AdamW([W], lr=1e-2, weight_decay=0.0, state_bits=state_bits, master=True)
+    opt = AdamW([W], lr=1e-2, weight_decay=0.0, state_bits=state_bits, master=True,
+                rounding="seeded")
     losses = []
     for i in range(steps):
         off = layer.forward(X, gate.ids, gate.gamma, W).float() - y

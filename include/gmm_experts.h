@@ -128,6 +128,18 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
  *   a positive v keeps a code above zero.  A block whose largest value is
  *   below 1e-30 is held as zeros.  The step uses the new m and v before they
  *   are rounded.  m_scale, v_scale: ceil(n / 256) floats.
+ * rounding (8 bits): how that root is rounded.
+ *   GMM_ROUND_NEAREST (0): to the nearest code.  What a step changes by less
+ *   than half a code stays as it is, so these are no averages over more than a
+ *   few steps: with beta2 = 0.999 v does not fall but with its block's largest,
+ *   rises only from gradients of several times its root, and m of an element
+ *   whose gradients end stays at up to 81 S with beta1 = 0.9.
+ *   GMM_ROUND_SEEDED (1): to one of the two codes around it, at random, so
+ *   that m and v (above its smallest code) are held without bias and move at
+ *   their own rate: the rounding to train with.  The random numbers depend on
+ *   the step, the tensor's place in the list and the element alone (Philox4x32
+ *   with ten rounds; counter: element / 8, its high word, the tensor, 0 for m
+ *   or 1 for v; key: the step; 16 bits an element), so results repeat.
  * skip: optional device int32; when it is not 0 the call changes nothing
  *   (the caller's check for non-finite gradients; without it a non-finite
  *   gradient goes into the parameter and the moments as the formula says, and
@@ -153,10 +165,14 @@ typedef struct {
   gmm_dtype grad_dtype;
 } gmm_adamw_tensor;
 
+#define GMM_ROUND_NEAREST 0
+#define GMM_ROUND_SEEDED 1
+
 typedef struct {
   double lr, beta1, beta2, eps, weight_decay, grad_scale;
   int64_t step;        /* 1 at the first step */
   int state_bits;      /* 32 or 8 */
+  int rounding;        /* of 8-bit moments: GMM_ROUND_NEAREST or _SEEDED */
   const int32_t* skip; /* NULL: never */
 } gmm_adamw_opts;
 

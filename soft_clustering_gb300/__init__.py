@@ -54,7 +54,8 @@ class gmm_adamw_opts(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("grad_scale", ctypes.c_double), ("step", ctypes.c_int64),
-                ("state_bits", ctypes.c_int), ("skip", ctypes.c_void_p)]
+                ("state_bits", ctypes.c_int), ("rounding", ctypes.c_int),
+                ("skip", ctypes.c_void_p)]
 
 
 class GmmError(RuntimeError):

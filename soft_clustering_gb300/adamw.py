@@ -17,6 +17,7 @@ from .experts import _empty
 from .torch_api import TORCH_XDTYPE
 
 BLOCK = 256  # elements that share one scale of an 8-bit moment
+ROUNDINGS = {"nearest": 0, "seeded": 1}
 
 
 def _dense(t, name, n, dtypes, device):
@@ -32,6 +33,12 @@ class AdamW:
     CUDA tensors, updated in place.
 
     state_bits: 32 (float moments) or 8 (codes with a scale per 256 elements).
+    rounding, of 8-bit moments: "seeded" rounds up or down by random numbers of
+    the step, the tensor's place in the list and the element (results repeat), so
+    that both averages are held without bias: the one to train with.  "nearest"
+    (what None stands for, with a warning) loses every change below half a code:
+    v does not fall again and m does not end, so it is for comparisons and a few
+    steps.
     master: hold 16-bit parameters in float32 as well (``self.state["master"]``;
     None for a float32 one).
     state, step: resume; a dict of lists m, v (and m_scale, v_scale in 8 bits,
@@ -49,10 +56,17 @@ class AdamW:
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
-                 state_bits=32, master=False, state=None, step=0, capturable=False):
+                 state_bits=32, master=False, state=None, step=0, capturable=False,
+                 rounding=None):
         self.params = list(params)
         if state_bits not in (8, 32):
             raise ValueError("state_bits %s: expected 8 or 32" % (state_bits,))
+        if rounding is not None and rounding not in ROUNDINGS:
+            raise ValueError("rounding %r: expected one of %s" % (rounding, tuple(ROUNDINGS)))
+        if rounding is None and state_bits == 8:
+            warnings.warn("8-bit moments rounded to the nearest code do not follow their averages "
+                          "over more than a few steps: train with rounding=\"seeded\"",
+                          stacklevel=2)
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.state_bits, self._count, self._steps = state_bits, None, int(step)
         for i, p in enumerate(self.params):
@@ -67,7 +81,7 @@ class AdamW:
         self.state = self._state(state, master)
         self._master = "master" in self.state
         self._opts = gmm_adamw_opts()
-        self._opts.state_bits = state_bits
+        self._opts.state_bits, self._opts.rounding = state_bits, ROUNDINGS[rounding or "nearest"]
         self._fill_table()
 
     @property

@@ -53,6 +53,7 @@ struct AdamwEntry {
   float* vs;
   int64_t n;
   int32_t first;     // the tensor's first chunk in this launch (kWarps x turns of 256 elements)
+  int32_t index;     // the tensor's place in the caller's list
   int8_t pt, gt;     // gmm_dtype
   int8_t wide;       // every array aligned for eight-element accesses
   int8_t pad;
@@ -62,9 +63,11 @@ struct AdamwConst {
   float gs, b1, c1, b2, c2, root, eps, decay, rate;
   int count, chunks, turns;
   int eps_covers;    // eps is far above the root of a subnormal
+  int seeded;        // 8 bits: codes by random numbers of (step, tensor, element)
   const int32_t* skip;
   // a step counted on the device: taken so far (NULL: root and rate are there)
   const int64_t* steps;
+  int64_t number;    // of this step
   double lr, beta1, beta2;
 };
 
@@ -366,6 +369,74 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// Sixteen random bits for each of eight values: Philox4x32 with ten rounds
+// (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+// 2011), a function of the counter and the key alone.
+__device__ __forceinline__ uint4 philox(uint4 c, uint2 key) {
+#pragma unroll
+  for (int round = 0; round < 10; ++round) {
+    const uint32_t h0 = __umulhi(0xD2511F53u, c.x), l0 = 0xD2511F53u * c.x;
+    const uint32_t h1 = __umulhi(0xCD9E8D57u, c.z), l1 = 0xCD9E8D57u * c.z;
+    c = make_uint4(h1 ^ c.y ^ key.x, l1, h0 ^ c.w ^ key.y, l0);
+    key.x += 0x9E3779B9u;
+    key.y += 0xBB67AE85u;
+  }
+  return c;
+}
+
+// Seeded codes of eight values: the next code up with the probability that
+// makes the held value's expectation the value itself, so that an average that
+// moves by less than a code a step still moves at its own rate.  x = value / S
+// lies between c^2 and (c + 1)^2; the value held is linear in c^2 for m, and
+// for v, whose root is held, v is linear in c^4.  `which` 0: m, 1: v.
+template <int TOP, bool SQUARE>
+__device__ __forceinline__ void seeded_codes(const float* x, const AdamwConst& k, const AdamwEntry& e,
+                                             int64_t block, float* code) {
+  const uint64_t unit = (uint64_t)block * 32 + (threadIdx.x & 31);
+  const uint4 r = philox(make_uint4((uint32_t)unit, (uint32_t)(unit >> 32), (uint32_t)e.index, SQUARE),
+                         make_uint2((uint32_t)k.number, (uint32_t)((uint64_t)k.number >> 32)));
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float u = ((float)((w[j >> 1] >> (16 * (j & 1))) & 0xffffu) + 0.5f) * (1.f / 65536.f);
+    const float c = floorf(sqrt_near(x[j])), c2 = c * c, step = 2.f * c + 1.f;
+    const bool up = SQUARE ? u * step * (2.f * c2 + step) < (x[j] - c2) * (x[j] + c2) : u * step < x[j] - c2;
+    code[j] = fminf(up ? c + 1.f : c, (float)TOP);
+  }
+}
+__device__ __forceinline__ uint2 seeded_m(const float2* m, float inv, const AdamwConst& k,
+                                          const AdamwEntry& e, int64_t block) {
+  float x[8], c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(fabsf(j & 1 ? m[j >> 1].y : m[j >> 1].x), inv);
+  seeded_codes<127, false>(x, k, e, block, c);
+  float2 t[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    t[j] = make_float2(with_sign(c[2 * j], m[j].x) + kMagic, with_sign(c[2 * j + 1], m[j].y) + kMagic);
+  return make_uint2(low_bytes(t[0], t[1]), low_bytes(t[2], t[3]));
+}
+// v > 0 keeps a code above zero, as in encode_root; where S is as small as the
+// root of a subnormal the roots are taken again.
+__device__ __forceinline__ uint2 seeded_root(const float2* v, const float2* root, float inv,
+                                             const AdamwConst& k, const AdamwEntry& e, int64_t block) {
+  float x[8], c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float r = j & 1 ? root[j >> 1].y : root[j >> 1].x;
+    if (inv > 1e18f) r = __fsqrt_rn(j & 1 ? v[j >> 1].y : v[j >> 1].x);
+    x[j] = __fmul_rn(r, inv);
+  }
+  seeded_codes<255, true>(x, k, e, block, c);
+  float2 t[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    t[j].x = (v[j].x > 0.f ? fmaxf(c[2 * j], 1.f) : c[2 * j]) + kMagic;
+    t[j].y = (v[j].y > 0.f ? fmaxf(c[2 * j + 1], 1.f) : c[2 * j + 1]) + kMagic;
+  }
+  return make_uint2(low_bytes(t[0], t[1]), low_bytes(t[2], t[3]));
+}
+
 // Largest of the warp's non-negative values (their bits order them, NaN last).
 __device__ __forceinline__ float warp_max_pos(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
@@ -423,7 +494,7 @@ __device__ __forceinline__ void fetch_all(Operands<BITS, PH, GH>& o, const Adamw
 }
 
 // fp32 moments: the documented operations, one by one.
-template <bool PH, bool GH>
+template <bool MORE, bool PH, bool GH>
 __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry& e, const Place& q,
                                            const Operands<32, PH, GH>& o) {
   float g[8], p[8], m[8], v[8];
@@ -445,7 +516,7 @@ __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry
 }
 
 // 8-bit moments: pairs of elements, each half rounded as one by one.
-template <bool PH, bool GH>
+template <bool MORE, bool PH, bool GH>
 __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry& e, const Place& q,
                                            const Operands<8, PH, GH>& o) {
   float g[8], p[8];
@@ -489,8 +560,13 @@ __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry
   }
   const float2 ms = scale_of<127>(warp_max_pos(mb));
   const float2 vs = scale_of<255>(__fsqrt_rn(warp_max_pos(vb)));
-  put_codes(e.m, i, q.left, q.full, encode_m(m, ms.y));
-  put_codes(e.v, i, q.left, q.full, encode_root(v, root, vs.y));
+  if (MORE && k.seeded) {
+    put_codes(e.m, i, q.left, q.full, seeded_m(m, ms.y, k, e, q.block));
+    put_codes(e.v, i, q.left, q.full, seeded_root(v, root, vs.y, k, e, q.block));
+  } else {
+    put_codes(e.m, i, q.left, q.full, encode_m(m, ms.y));
+    put_codes(e.v, i, q.left, q.full, encode_root(v, root, vs.y));
+  }
   if ((threadIdx.x & 31) == 0) {
     e.ms[q.block] = ms.x;
     e.vs[q.block] = vs.x;
@@ -498,13 +574,13 @@ __device__ __forceinline__ void step_block(const AdamwConst& k, const AdamwEntry
 }
 
 // The odd blocks: a tensor's end, or arrays that are not aligned.
-template <int BITS, bool PH, bool GH>
+template <int BITS, bool PH, bool GH, bool MORE>
 __device__ __noinline__ void odd_block(const AdamwConst& k, const AdamwEntry& e, int64_t block) {
   const Place q = place_of(e, block);
   if (q.left == 0) return;
   Operands<BITS, PH, GH> o;
   fetch_all(o, e, q);
-  step_block(k, e, q, o);
+  step_block<MORE>(k, e, q, o);
 }
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
@@ -569,7 +645,7 @@ __device__ __forceinline__ void stage_read(Operands<8, PH, GH>& o, const uint8_t
 }
 
 // The full blocks of a warp's turns in one chunk; returns how many it did.
-template <bool PH, bool GH>
+template <bool MORE, bool PH, bool GH>
 __device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry& e, int64_t block,
                                           uint8_t* ring, std::integral_constant<int, 8>) {
   constexpr int B = stage_bytes<PH, GH>();
@@ -597,7 +673,7 @@ __device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry&
     }
     copy_wait<kAhead>();
     stage_read(o, ring + slot * B);
-    step_block(k, e, Place{kBlockElems, true, block}, o);
+    step_block<MORE>(k, e, Place{kBlockElems, true, block}, o);
     slot = slot == kAhead ? 0 : slot + 1;
     ahead = ahead == kAhead ? 0 : ahead + 1;
   }
@@ -605,7 +681,7 @@ __device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry&
 }
 
 // fp32 moments: a turn's operands are fetched into registers a turn ahead.
-template <bool PH, bool GH>
+template <bool MORE, bool PH, bool GH>
 __device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry& e, int64_t block,
                                           uint8_t*, std::integral_constant<int, 32>) {
   const int64_t fulls = e.wide ? e.n / kBlockElems : 0;
@@ -617,18 +693,20 @@ __device__ __forceinline__ int full_turns(const AdamwConst& k, const AdamwEntry&
   for (int turn = 0; turn < turns; ++turn, block += kWarps) {
     Operands<32, PH, GH> next;
     if (turn + 1 < turns) fetch_all(next, e, Place{kBlockElems, true, block + kWarps});
-    step_block(k, e, Place{kBlockElems, true, block}, o);
+    step_block<MORE>(k, e, Place{kBlockElems, true, block}, o);
     o = next;
   }
   return turns;
 }
 
-// Both bias corrections of a step that is counted on the device, by one thread.
+// The number of a step that is counted on the device, and both bias
+// corrections by one thread.
 __device__ __forceinline__ void correct_by_count(AdamwConst& k) {
   __shared__ float at[2];
+  const int64_t taken = *k.steps;
+  k.number = (taken < 0 ? 0 : taken) + 1;
   if (threadIdx.x == 0) {
-    const int64_t taken = *k.steps;
-    const double n = (double)((taken < 0 ? 0 : taken) + 1);
+    const double n = (double)k.number;
     at[0] = (float)pow(1.0 - pow(k.beta2, n), -0.5);
     at[1] = (float)(k.lr / (1.0 - pow(k.beta1, n)));
   }
@@ -638,8 +716,8 @@ __device__ __forceinline__ void correct_by_count(AdamwConst& k) {
 }
 
 // PH, GH: 16-bit parameters (no master) and gradients.  MORE: the step may be
-// counted on the device.  That is a kernel of its own, since what it computes
-// takes registers that the 8-bit step lacks.
+// counted on the device, and codes may be seeded.  That is a kernel of its own,
+// since what it computes takes registers that the 8-bit step lacks.
 template <bool MORE> using ConstOf = std::conditional_t<MORE, AdamwConst, const AdamwConst&>;
 template <int BITS, bool PH, bool GH, bool MORE, int COUNT>
 __global__ void __launch_bounds__(kWarps * 32, BITS == 8 ? (MORE ? 3 : 4) : 2)
@@ -660,9 +738,9 @@ adamw_kernel(const __grid_constant__ AdamwTable<COUNT> t) {
     while (at + 1 < k.count && t.e[at + 1].first <= c) ++at;
     const AdamwEntry e = t.e[at];
     const int64_t block = (int64_t)(c - e.first) * kWarps * k.turns + warp;
-    for (int turn = full_turns<PH, GH>(k, e, block, ring, std::integral_constant<int, BITS>());
+    for (int turn = full_turns<MORE, PH, GH>(k, e, block, ring, std::integral_constant<int, BITS>());
          turn < k.turns; ++turn)
-      odd_block<BITS, PH, GH>(k, t.e[at], block + turn * kWarps);
+      odd_block<BITS, PH, GH, MORE>(k, t.e[at], block + turn * kWarps);
   }
 }
 
@@ -829,6 +907,7 @@ __global__ void count_step_kernel(int64_t* steps) { *steps = (*steps < 0 ? 0 : *
 gmm_status adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw_opts* o, int64_t* steps,
                       void* stream) {
   if (!o || !tensors_ok(ts, count, o->state_bits, true)) return GMM_ERR_INVALID_ARG;
+  if (o->rounding != 0 && o->rounding != 1) return GMM_ERR_INVALID_ARG;
   if ((!steps && o->step < 1) || !(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) ||
       !(o->eps >= 0) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay) ||
       !std::isfinite(o->grad_scale) || !std::isfinite(o->eps))
@@ -855,11 +934,14 @@ gmm_status adamw_step(const gmm_adamw_tensor* ts, int count, const gmm_adamw_opt
   k.skip = o->skip;
   k.eps_covers = o->eps >= 1e-10;
   const int bits = o->state_bits;
-  const bool more = steps != nullptr;
+  k.number = o->step;
+  k.seeded = bits == 8 && o->rounding == 1;
+  const bool more = steps != nullptr || k.seeded;
   auto fill = [&](int i, AdamwEntry& e) {
     const gmm_adamw_tensor& t = ts[i];
     e.p = t.param; e.g = t.grad; e.master = t.master; e.m = t.m; e.v = t.v;
     e.ms = t.m_scale; e.vs = t.v_scale;
+    e.index = i;
     e.pt = (int8_t)t.param_dtype; e.gt = (int8_t)t.grad_dtype;
     const uintptr_t mv = (uintptr_t)t.m | (uintptr_t)t.v;
     const uintptr_t rest = (uintptr_t)t.param | (uintptr_t)t.grad | (uintptr_t)t.master;

@@ -281,3 +281,196 @@ def test_capture_with_a_fixed_step_warns(cuda):
     with pytest.warns(UserWarning, match="capturable"):
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             opt.step([g])
+
+
+# ------------------------------------------------- 8-bit moments, seeded codes
+
+def _philox(c, k):
+    """Philox4x32-10 of counters c [..., 4] and a key of two words, in numpy."""
+    c = [c[..., i].astype(np.uint64) for i in range(4)]
+    k0, k1, low = k[0], k[1], np.uint64(0xffffffff)
+    for _ in range(10):
+        a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k0), b & low,
+             (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k1), a & low]
+        k0, k1 = (k0 + 0x9E3779B9) & 0xffffffff, (k1 + 0xBB67AE85) & 0xffffffff
+    return np.stack(c, -1)
+
+
+def _uniform(n, step, tensor, which):
+    """The sixteen bits of each of n elements as (h + 1/2) / 65536."""
+    units = np.arange(-(-n // 8), dtype=np.uint64)
+    c = np.stack([units & np.uint64(0xffffffff), units >> np.uint64(32),
+                  np.full_like(units, tensor), np.full_like(units, which)], -1)
+    w = _philox(c, (step & 0xffffffff, step >> 32))
+    h = np.stack([w & np.uint64(0xffff), w >> np.uint64(16)], -1).reshape(-1)[:n]
+    return (h.astype(np.float64) + 0.5) / 65536
+
+
+def test_generator_known_answers():
+    """The published vectors of Philox4x32-10."""
+    c = lambda *x: np.array([x], dtype=np.uint64)  # noqa: E731
+    f = 0xffffffff
+    assert [hex(x) for x in _philox(c(0, 0, 0, 0), (0, 0))[0]] == ["0x6627e8d5", "0xe169c58d", "0xbc57ac4c", "0x9b00dbd8"]
+    assert [hex(x) for x in _philox(c(f, f, f, f), (f, f))[0]] == ["0x408f276d", "0x41c83b0e", "0xa20bc7c6", "0x6d5451fd"]
+
+
+def test_refusals_of_roundings(lib):
+    e = (G.gmm_adamw_tensor * 1)(G.gmm_adamw_tensor(param=256, grad=256, m=256, v=256, m_scale=256, v_scale=256, n=8))
+    for r in (-1, 2):
+        o = G.gmm_adamw_opts(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0, step=1, state_bits=8, rounding=r)
+        assert lib.gmm_adamw_step(e, 1, ctypes.byref(o), None) == G.GMM_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes,capturable", [([300_001], False), ([256 * 40, 7, 1000], False), ([5000, 3000], True)])
+def test_seeded_codes_are_those_of_the_rule(cuda, sizes, capturable):
+    """Each code is c or c + 1, c^2 <= value / S < (c + 1)^2, by u < p.  The new
+    moments are the documented fp32 operations (numpy's float32 ones); p follows
+    from them in 64 bits.  The kernel's p is off by at most 2^-24 x + 3 roundings
+    of c^2 over 2 c + 1 for m (below 127 2^-23) and by the near root's 2^-22 of
+    x, twice for its square, over 4 c^3 / c^4 and as many roundings for v (below
+    255 2^-21): 2e-4 covers both, and closer ones may fall either way."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    f, near = np.float32, 2e-4
+    rng = np.random.default_rng(sum(sizes))
+    p = [torch.zeros(n, device="cuda") for n in sizes]
+    opt = AdamW(p, betas=(0.9, 0.999), weight_decay=0.0, state_bits=8, rounding="seeded", capturable=capturable,
+                step=2 ** 33 + 5)
+    for step in range(2 ** 33 + 6, 2 ** 33 + 10):
+        gs = [(rng.standard_normal(n) * np.exp(2 * rng.standard_normal(n))).astype(f) for n in sizes]
+        held = [[opt.state[k][i].cpu().numpy().astype(f) for k in ("m", "v", "m_scale", "v_scale")] for i in range(len(sizes))]
+        opt.step([torch.from_numpy(g).cuda() for g in gs])
+        for i, (n, g) in enumerate(zip(sizes, gs)):
+            per = lambda s: np.repeat(s, 256)[:n]  # noqa: E731
+            m, v, ms, vs = held[i]
+            m, r = m * np.abs(m) * per(ms), v * v * per(vs)
+            m = m * f(0.9) + g * f(1 - 0.9)
+            v = (r * r) * f(0.999) + (g * g) * f(1 - 0.999)
+            for x, top, which, name in ((m, 127, 0, "m"), (np.sqrt(v), 255, 1, "v")):
+                big = np.array([np.abs(x[j:j + 256]).max() for j in range(0, n, 256)])
+                scale = big * f(1.0 / (top * top))
+                assert np.array_equal(opt.state[name + "_scale"][i].cpu().numpy(), scale)
+                y = (np.abs(x) * per((f(1) / big) * f(top * top))).astype(np.float64)
+                c = np.floor(np.sqrt(y))
+                prob = (y - c * c) / (2 * c + 1) if which == 0 else (y ** 2 - c ** 4) / ((c + 1) ** 4 - c ** 4)
+                u = _uniform(n, step, i, which)
+                want = np.minimum(c + (u < prob), top)
+                got = np.abs(opt.state[name][i].cpu().numpy().astype(np.float64))
+                if which == 1:
+                    want = np.where(x > 0, np.maximum(want, 1), want)
+                else:
+                    sign = np.sign(opt.state[name][i].cpu().numpy().astype(f))
+                    assert ((sign == np.sign(x)) | (sign == 0)).all()
+                off = got != want
+                assert not (off & (np.abs(u - prob) > near)).any(), (step, name, np.flatnonzero(off & (np.abs(u - prob) > near))[:5])
+                assert (np.abs(got - want) <= 1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [0.3, 0.011, 1e-4])
+def test_seeded_codes_are_unbiased(cuda, value):
+    """One step from zero of n equal gradients beside each block's largest: the
+    mean of what is held is the value, up to six standard deviations of the mean
+    of n independent choices between two neighbours (half their distance each)."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    blocks = 4000
+    g = torch.full((blocks, 256), value, device="cuda")
+    g[:, 0] = 1.0
+    p = torch.zeros(blocks * 256, device="cuda")
+    opt = AdamW([p], state_bits=8, rounding="seeded")
+    opt.step([g.reshape(-1)])
+    m, v = (t[0].double().reshape(blocks, 256)[:, 1:] for t in opt.moments())
+    n = m.numel()
+    for got, want, top, power in ((m, 0.1 * value, 127, 1), (v, 0.001 * value ** 2, 255, 2)):
+        c = int(top * value ** 0.5)  # root of (value / largest) x top^2
+        unit = (0.1 / 127 ** 2) if power == 1 else 0.001 ** 0.5 / 255 ** 2
+        gap = ((c + 1) ** 2 * unit) ** power - (c ** 2 * unit) ** power
+        assert c > 0 and abs(float(got.mean()) - want) <= 6 * gap / 2 / n ** 0.5 + 1e-5 * want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("later", [0.01, 0.0])
+def test_averages_fall_again(cuda, later):
+    """Half of every block's gradients shrink, or end, after 1000 of 10000 steps.
+    v held in 8 bits follows the average in fp32: a code's steps are a walk with
+    p (1 - p) near 0.00025 c a step over some 500 steps, a relative deviation of
+    v of about 1.4 / sqrt(c), 0.3 at c = 25, so the mean of 2048 independent ones
+    deviates by 0.7 %: 10 % is fourteen of these.  Where the gradients end m is
+    zero (0.9^9000 of a code of 127^2 is no chance) and the parameters rest."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    n = 4096
+    p, q = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    a = AdamW([p], weight_decay=0.0, state_bits=8, rounding="seeded")
+    b = AdamW([q], weight_decay=0.0)
+    half = torch.arange(n, device="cuda") % 2 == 0
+    for t in range(10000):
+        x = torch.randn(n, device="cuda", generator=g)
+        if t >= 1000:
+            x = torch.where(half, x * later, x)
+        a.step([x])
+        b.step([x])
+        if t == 6000:
+            at = p.clone()
+    (m8,), (v8,) = a.moments()
+    (_,), (v,) = b.moments()
+    # v's smallest code holds (max root / 255^2)^2 whatever the average
+    least = (v.max().sqrt() / 255 ** 2) ** 2
+    for part in (half, ~half):
+        want = v[part].double().mean()
+        assert abs(v8[part].double().mean() - want) <= 0.1 * want + 2 * least
+    if later == 0:
+        assert not m8[half].any()
+        assert torch.equal(p[half], at[half])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("master", [False, True])
+@pytest.mark.parametrize("grad", ["float32", "bfloat16"])
+def test_seeded_steps_repeat_and_resume(cuda, grad, master):
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    p0 = [torch.randn(k, device="cuda", generator=g).bfloat16() for k in (3000, 700)]
+    grads = [[torch.randn(k, device="cuda", generator=g).to(getattr(torch, grad)) for k in (3000, 700)] for _ in range(4)]
+
+    def run(stop=4, p=None, **kw):
+        p = [t.clone() for t in p0] if p is None else p
+        opt = AdamW(p, state_bits=8, rounding="seeded", master=master, **kw)
+        for x in grads[opt.steps:stop]:
+            opt.step(x)
+        return p, opt
+
+    p, one = run()
+    q, two = run(capturable=True)
+    h, half = run(stop=2)
+    h, rest = run(p=h, step=half.steps, state={k: [t.clone() for t in ts] for k, ts in half.state.items()})
+    for k in ("m", "v", "m_scale", "v_scale"):
+        for x, y, z in zip(one.state[k], two.state[k], rest.state[k]):
+            assert torch.equal(x, y) and torch.equal(x, z), k
+    for x, z in zip(p, h):
+        assert torch.equal(x, z)
+    assert not torch.equal(one.state["m"][0][:700], one.state["m"][1])
+
+
+@pytest.mark.gpu
+def test_rounding_of_8_bits_is_asked_for(cuda):
+    import torch
+    import warnings
+    from soft_clustering_gb300.adamw import AdamW
+    p = [torch.zeros(8, device="cuda")]
+    with pytest.raises(ValueError):
+        AdamW(p, state_bits=8, rounding="up")
+    with pytest.warns(UserWarning, match="seeded"):
+        AdamW(p, state_bits=8)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        AdamW(p, state_bits=8, rounding="nearest")
+        AdamW(p, state_bits=8, rounding="seeded")
+        AdamW(p)
