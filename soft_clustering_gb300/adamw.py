@@ -13,7 +13,7 @@ import torch
 
 from . import (gmm_adamw_moments, gmm_adamw_opts, gmm_adamw_step, gmm_adamw_step_counted,
                gmm_adamw_tensor)
-from .experts import _empty
+from .experts import _empty, _here
 from .torch_api import TORCH_XDTYPE
 
 BLOCK = 256  # elements that share one scale of an 8-bit moment
@@ -127,6 +127,8 @@ class AdamW:
     def _bind(self):
         """Brings the table up to date where a list holds another tensor than at
         the last call, or a tensor has other storage."""
+        if self._device is not None:
+            _here(self._device)
         flat = self._flat()
         if (len(flat) == len(self._held) and all(map(is_, flat, self._held))
                 and [f() for f in self._lookups] == self._found

@@ -41,9 +41,19 @@ def _need(t, name, shape, dtype, device):
 
 def _device(device):
     d = torch.device(device)
-    if d.type == "cuda" and d.index is None:
+    if d.type != "cuda":
+        raise ValueError("device %s: expected a CUDA device" % d)
+    if d.index is None:
         d = torch.device("cuda", torch.cuda.current_device())
     return d
+
+
+def _here(device):
+    """The library launches on the current device: ValueError if that is not the
+    tensors' one."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError("tensors are on %s, the current device is cuda:%d"
+                         % (device, torch.cuda.current_device()))
 
 
 def _on(stream):
@@ -109,6 +119,7 @@ class Router:
     def route(self, ids, stream=None):
         """ids: [N, m] int32, as ``Assigner.ids``."""
         _need(ids, "ids", (self.N, self.m), torch.int32, self.device)
+        _here(self.device)
         self.routes += 1
         gmm_route(ids, self.N, self.m, self.K, self.offsets, self.entry, self.slot, self.ws,
                   self.ws_bytes, stream=stream)
@@ -119,6 +130,7 @@ class Router:
         <X[n], Z[slot[n, t]]>: with X = d out the gradient of ``collect``."""
         D, x, dt, dev = _rows_of(X, "X")[1], _xdtype(X, "X"), X.dtype, self.device
         _need(X, "X", (self.N, D), dt, dev)
+        _here(dev)
         if gamma is not None:
             _need(gamma, "gamma", (self.N, self.m), torch.float32, dev)
         dgamma = None
@@ -138,6 +150,7 @@ class Router:
         of a point's components, or the gradient of ``spread``."""
         D, x, dt, dev = _rows_of(Z, "Z")[1], _xdtype(Z, "Z"), Z.dtype, self.device
         _need(Z, "Z", (self.rows, D), dt, dev)
+        _here(dev)
         if gamma is not None:
             _need(gamma, "gamma", (self.N, self.m), torch.float32, dev)
         if out is None:
@@ -174,6 +187,7 @@ class ExpertProduct:
         return R
 
     def _common(self, offsets, W):
+        _here(self.device)
         _need(offsets, "offsets", self._offsets_shape, torch.int64, self.device)
         if W is not None:
             _need(W, "W", self._w_shape, self.dtype, self.device)

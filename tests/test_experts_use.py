@@ -152,3 +152,34 @@ def test_a_failure_outlives_the_products_after_it(cuda, dtype, N, K, d):
     layer.product.clear_status()
     step()
     assert layer.device_status() == G.GMM_OK
+
+
+def test_only_the_current_cuda_device(monkeypatch):
+    """The launch goes to the current device: other tensors are refused before
+    it, on the host or on another GPU."""
+    import torch
+    from soft_clustering_gb300 import adamw, experts
+    for make in (lambda: experts.Router(4, 2, 3, device="cpu"),
+                 lambda: experts.ExpertProduct(3, 8, 8, torch.float16, 4, device="cpu"),
+                 lambda: experts.LocalExperts(4, 2, 3, 8, 8, torch.float16, device="cpu")):
+        with pytest.raises(ValueError, match="CUDA device"):
+            make()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    experts._here(torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="current device"):
+        experts._here(torch.device("cuda", 1))
+
+    # every call looks: objects of another device, as they would be there
+    other = torch.device("cuda", 1)
+    monkeypatch.setattr(experts, "_need", lambda t, *a: t)
+    x = torch.zeros(4, 8, dtype=torch.float16)
+    r, e, o = (object.__new__(c) for c in (experts.Router, experts.ExpertProduct, adamw.AdamW))
+    r.N, r.m, r.rows, r.K, r.device = 4, 1, 4, 3, other
+    e.max_rows, e.dtype, e.device, e.d_in, e.d_out = 4, torch.float16, other, 8, 8
+    e._offsets_shape = e._w_shape = None
+    o.params, o._device = [x], other
+    for call in (lambda: r.route(x), lambda: r.spread(x), lambda: r.collect(x), lambda: e.forward(x, x, x),
+                 lambda: e.backward_rows(x, x, x), lambda: e.backward_weights(x, x, x), lambda: o.step([x]),
+                 lambda: o.moments()):
+        with pytest.raises(ValueError, match="current device"):
+            call()
