@@ -22,6 +22,7 @@
  * errors returned before anything is queued.  Arrays are dense and
  * row-major; element types of rows and weights are gmm_dtype values, sums
  * are held in 32 bits and rounded once.  Results are bitwise reproducible.
+ * Every array is aligned to its element type (GMM_ERR_INVALID_ARG if not).
  * N and R may be 0.
  */
 #ifndef GMM_EXPERTS_H

@@ -30,6 +30,12 @@ inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& 
   return true;
 }
 
+// Whether each address is a multiple of `bytes` (NULL is).
+template <typename... P>
+inline bool aligned(size_t bytes, const P*... p) {
+  return ((... | (uintptr_t)p) & (bytes - 1)) == 0;
+}
+
 inline bool dtype_ok(int t) { return t >= GMM_F32 && t <= GMM_BF16; }
 inline int dtype_size(int t) { return t == GMM_F32 ? 4 : 2; }
 

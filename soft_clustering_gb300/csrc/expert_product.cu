@@ -162,7 +162,7 @@ gmm_status check(int xdtype, int64_t R, int d_in, int d_out, int K, const int64_
   if (R > 0 && (!rows1 || !rows2)) return GMM_ERR_INVALID_ARG;
   if (((uintptr_t)rows1 | (uintptr_t)rows2 | (uintptr_t)w) % dtype_size(xdtype))
     return GMM_ERR_INVALID_ARG;
-  if ((uintptr_t)ws % kAlign) return GMM_ERR_INVALID_ARG;
+  if (!aligned(kAlign, ws) || !aligned(8, offsets)) return GMM_ERR_INVALID_ARG;
   if (ws_bytes < ProductLayout::make(R, d_in, d_out, K).bytes) return GMM_ERR_WORKSPACE;
   return GMM_OK;
 }

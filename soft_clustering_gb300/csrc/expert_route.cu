@@ -319,6 +319,7 @@ gmm_status gmm_route(const int32_t* ids, int64_t N, int m, int K, int64_t* offse
                      int32_t* entry, int32_t* slot, void* ws, size_t ws_bytes, void* stream) {
   if (!route_sizes_ok(N, m, K) || !offsets || !ws) return GMM_ERR_INVALID_ARG;
   if (N > 0 && (!ids || !entry || !slot)) return GMM_ERR_INVALID_ARG;
+  if (!aligned(4, ids, entry, slot, ws) || !aligned(8, offsets)) return GMM_ERR_INVALID_ARG;
   const int64_t E = N * m;
   const RouteLayout L = RouteLayout::make(E, K);
   if (ws_bytes < L.bytes) return GMM_ERR_WORKSPACE;

@@ -307,6 +307,7 @@ gmm_status gmm_spread(const void* X, gmm_dtype xdtype, int64_t N, int D, int m, 
   if ((N > 0 && R > 0) && (!Z != !dgamma)) return GMM_ERR_INVALID_ARG;
   const uintptr_t bits = (uintptr_t)X | (uintptr_t)Y | (uintptr_t)Z;
   if (bits % dtype_size(xdtype)) return GMM_ERR_INVALID_ARG;
+  if (!aligned(4, slot, gamma, dgamma) || !aligned(8, offsets)) return GMM_ERR_INVALID_ARG;
   if (N == 0 && R == 0) return GMM_OK;
   cudaStream_t s = (cudaStream_t)stream;
   const int v = vec_width(D, dtype_size(xdtype), X, Y, Z);
@@ -323,6 +324,7 @@ gmm_status gmm_collect(const void* Z, gmm_dtype xdtype, int64_t N, int D, int m,
   if (N == 0) return GMM_OK;
   if (!slot || !out || (R > 0 && !Z)) return GMM_ERR_INVALID_ARG;
   if (((uintptr_t)Z | (uintptr_t)out) % dtype_size(xdtype)) return GMM_ERR_INVALID_ARG;
+  if (!aligned(4, slot, gamma)) return GMM_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   const int v = vec_width(D, dtype_size(xdtype), Z, out, nullptr);
   ProfScope p("collect_kernel", s);

@@ -12,6 +12,13 @@ from test_experts import _f64, _ids, _rand, dw_ref
 
 
 @pytest.fixture(scope="module")
+def lib():
+    from soft_clustering_gb300 import build
+    build.build()
+    return G.lib()
+
+
+@pytest.fixture(scope="module")
 def cuda():
     import torch
     if not torch.cuda.is_available():
@@ -183,3 +190,21 @@ def test_only_the_current_cuda_device(monkeypatch):
                  lambda: o.moments()):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+def test_addresses_that_are_not_aligned(lib):
+    """Refused before anything is queued, for every array of every call."""
+    bad, P, big = G.GMM_ERR_INVALID_ARG, 4096, 1 << 40
+
+    def each(f, args, where):
+        for i, by in where.items():
+            a = list(args)
+            a[i] += by
+            assert f(*a) == bad, (f.__name__, i)
+
+    each(lib.gmm_route, (P, 10, 2, 4, P, P, P, P, big, None), {0: 2, 4: 4, 5: 1, 6: 2, 7: 2})
+    each(lib.gmm_spread, (P, 1, 5, 8, 2, 3, 10, P, P, P, P, P, P, None), {0: 1, 7: 2, 8: 4, 9: 2, 10: 1, 11: 1, 12: 2})
+    each(lib.gmm_collect, (P, 1, 5, 8, 2, 10, P, P, P, None), {0: 1, 6: 2, 7: 1, 8: 1})
+    for f in (lib.gmm_expert_product, lib.gmm_expert_product_dx):
+        each(f, (P, 1, 4, 8, 8, 2, P, P, P, P, big, None), {0: 1, 6: 4, 7: 1, 8: 1, 9: 128})
+    each(lib.gmm_expert_product_dw, (P, P, 1, 4, 8, 8, 2, P, P, 0, P, big, None), {0: 1, 1: 1, 7: 4, 8: 2, 10: 128})
