@@ -533,6 +533,7 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
     // to six a stage were what short contractions waited for
     const bool fetch_p = warp == 0;
     uint32_t it = 0;
+    uint32_t odd_fills = 0, last_odd = 0;  // a bit a stage: an odd number of odd fills; the last one is odd
     bool ok = true;
     for (Walk<MODE, CG> walk(a, before, first, step); ok && walk.more();) {
       const Tile w = walk.take(a);
@@ -548,12 +549,16 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
           ok = false;
           break;
         }
+        // the end of a component, with rows of the next one up to the next
+        // 16: to the mending warp first
+        const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
+        if (MODE == kDw) {
+          last_odd = (last_odd & ~(1u << s)) | ((uint32_t)odd << s);
+          odd_fills ^= (uint32_t)odd << s;
+        }
         if (elect_one()) {
           uint8_t* p = smem + s * B;
           uint8_t* q = p + kTileM * kTileK * 2;
-          // the end of a component, with rows of the next one up to the next
-          // 16: to the mending warp first
-          const bool odd = MODE == kDw && w.len - l < kTileK && (w.len - l) % 16 != 0;
           const uint32_t bytes = (2 + boxes) * kBox;
           const uint32_t bar = odd                    ? tc::smem_addr(&odd_full[s])
                                : CG == 2 && rank != 0 ? in_block(&full[s], 0)
@@ -586,6 +591,19 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
         __syncwarp();
       }
     }
+    // No copy is in flight when the blocks end, also where a wait gave up: the
+    // last copies to each stage, of both warps, are on the barrier of its fill
+    // (a pair's on the first block's, and neither block leaves before the other).
+    if (fetch_p)
+      for (uint32_t s = 0; s < S && s < it; ++s) {
+        const bool odd = (last_odd >> s) & 1;
+        if (!odd && rank != 0) continue;
+        const uint32_t fill = (it - 1 - s) / S;  // of this stage
+        if (!wait_on<CG>(odd ? &odd_full[s] : &full[s], odd ? ((odd_fills >> s) & 1) ^ 1 : fill & 1)) {
+          if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
+          break;
+        }
+      }
   } else if (warp == 1 && rank == 0) {
     uint32_t it = 0, acc = 0;
     bool ok = true;
@@ -624,7 +642,11 @@ expert_tc_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constan
       }
       ++acc;
     }
-    if (!ok && lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
+    if (!ok) {
+      if (lane == 0) raise_status(a.st, GMM_ERR_TIMEOUT);
+      // the products issued so far end before their memory is given back
+      if (it > 0) wait_on<CG>(&empty[(it - 1) % S], ((it - 1) / S) & 1);
+    }
   } else if (warp == kMendWarp) {
     // ahead of the products: zeroes this block's rows of the next component
     // in a component's last stage and passes the stage on
