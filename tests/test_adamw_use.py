@@ -324,7 +324,8 @@ def test_refusals_of_roundings(lib):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("sizes,capturable", [([300_001], False), ([256 * 40, 7, 1000], False), ([5000, 3000], True)])
-def test_seeded_codes_are_those_of_the_rule(cuda, sizes, capturable):
+@pytest.mark.parametrize("scale_of_gradients", [1.0, 1e-20])
+def test_seeded_codes_are_those_of_the_rule(cuda, sizes, capturable, scale_of_gradients):
     """Each code is c or c + 1, c^2 <= value / S < (c + 1)^2, by u < p.  The new
     moments are the documented fp32 operations (numpy's float32 ones); p follows
     from them in 64 bits.  The kernel's p is off by at most 2^-24 x + 3 roundings
@@ -339,7 +340,7 @@ def test_seeded_codes_are_those_of_the_rule(cuda, sizes, capturable):
     opt = AdamW(p, betas=(0.9, 0.999), weight_decay=0.0, state_bits=8, rounding="seeded", capturable=capturable,
                 step=2 ** 33 + 5)
     for step in range(2 ** 33 + 6, 2 ** 33 + 10):
-        gs = [(rng.standard_normal(n) * np.exp(2 * rng.standard_normal(n))).astype(f) for n in sizes]
+        gs = [(scale_of_gradients * rng.standard_normal(n) * np.exp(2 * rng.standard_normal(n))).astype(f) for n in sizes]
         held = [[opt.state[k][i].cpu().numpy().astype(f) for k in ("m", "v", "m_scale", "v_scale")] for i in range(len(sizes))]
         opt.step([torch.from_numpy(g).cuda() for g in gs])
         for i, (n, g) in enumerate(zip(sizes, gs)):
@@ -474,3 +475,65 @@ def test_rounding_of_8_bits_is_asked_for(cuda):
         AdamW(p, state_bits=8, rounding="nearest")
         AdamW(p, state_bits=8, rounding="seeded")
         AdamW(p)
+
+
+# ---------------------------------------------- values at the ends of the range
+
+def _step32(held, g, n, b1=0.9, b2=0.999):
+    """The new fp32 moments (m, v) from 8-bit state, each operation rounded once."""
+    f = np.float32
+    m, v, ms, vs = held
+    per = lambda s: np.repeat(s, 256)[:n]  # noqa: E731
+    m, r = m * np.abs(m) * per(ms), v * v * per(vs)
+    return m * f(b1) + g * f(1 - b1), (r * r) * f(b2) + (g * g) * f(1 - b2)
+
+
+TINY = [1e-17, 1e-18, 1e-19, 4e-20, 1e-20, 3e-21, 1e-21, 1e-22, 1e-25, 1e-29, 1e-36]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eps", [0.0, 1e-12, 1e-10, 1e-8])
+@pytest.mark.parametrize("beside", [0.0, 1e-15, 1.0])
+def test_small_values_in_8_bits(cuda, eps, beside):
+    """Gradients whose v is subnormal or nearly so, alone in a block and beside
+    larger ones: scales and codes are those of the documented fp32 operations,
+    and the update is the formula's of those moments in 64 bits.  Its error: the
+    near root and reciprocal 2^-23 each, the roundings of the two corrections,
+    eps, two products and a sum 2^-24 each: 10 x 2^-24 of the update, and 2^-24
+    of the parameter for each of decay, its product and the difference."""
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    f, lr, wd = np.float32, 0.01, 0.1
+    rng = np.random.default_rng(int(beside) + 1)
+    n = 256 * len(TINY) + 77
+    size = np.concatenate([np.repeat(TINY, 256), np.full(77, 1e-20)])
+    p = torch.from_numpy(rng.standard_normal(n).astype(f)).cuda()
+    opt = AdamW([p], lr=lr, betas=(0.9, 0.999), eps=eps, weight_decay=wd, state_bits=8, rounding="nearest")
+    with np.errstate(all="ignore"):
+        for step in range(1, 4):
+            g = (size * np.sign(rng.standard_normal(n)) * (1 + rng.random(n))).astype(f)
+            if beside:
+                g[::64] = beside
+            held = [opt.state[k][0].cpu().numpy().astype(f) for k in ("m", "v", "m_scale", "v_scale")]
+            before = p.double().cpu().numpy()
+            opt.step([torch.from_numpy(g).cuda()])
+            m, v = _step32(held, g, n)
+            root = np.sqrt(v)
+            for x, top, name in ((m, 127, "m"), (root, 255, "v")):
+                big = np.array([np.abs(x[j:j + 256]).max() for j in range(0, n, 256)])
+                scale = np.where(big >= f(1e-30), big * f(1.0 / (top * top)), f(0))
+                assert np.array_equal(opt.state[name + "_scale"][0].cpu().numpy(), scale), (step, name)
+                inv = np.where(scale > 0, (f(1) / big) * f(top * top), f(0)).astype(f)
+                c = np.rint(np.sqrt(np.abs(x) * np.repeat(inv, 256)[:n]))
+                c = np.where((x > 0) & (c < 1), f(1), c) if name == "v" else c * np.sign(x)
+                got = opt.state[name][0].cpu().numpy().astype(f)
+                assert np.array_equal(got, c), (step, name, np.flatnonzero(got != c)[:5])
+            with np.errstate(all="ignore"):
+                m, v = m.astype(np.float64), v.astype(np.float64)
+                up = lr / (1 - 0.9 ** step) * m / (np.sqrt(v) / np.sqrt(1 - 0.999 ** step) + eps)
+            ok = (v > 0) | (eps > 0)  # elsewhere the formula divides by zero
+            after = before * (1 - lr * wd) - up
+            bound = 1.01 * 2.0 ** -24 * (10 * np.abs(up) + 3 * (np.abs(before) + np.abs(up)))
+            off = np.abs(p.double().cpu().numpy() - after)
+            assert (off[ok] <= bound[ok]).all(), (step, size[ok][(off[ok] - bound[ok]).argmax()])
+            p[torch.from_numpy(~ok).cuda()] = 1.0  # infinite there, as the formula says
