@@ -163,14 +163,14 @@ gmm_status check(int xdtype, int64_t R, int d_in, int d_out, int K, const int64_
   if (((uintptr_t)rows1 | (uintptr_t)rows2 | (uintptr_t)w) % dtype_size(xdtype))
     return GMM_ERR_INVALID_ARG;
   if (!aligned(kAlign, ws) || !aligned(8, offsets)) return GMM_ERR_INVALID_ARG;
-  if (ws_bytes < ProductLayout::make(R, d_in, d_out, K).bytes) return GMM_ERR_WORKSPACE;
+  if (ws_bytes < ProductLayout::make(R, d_in, d_out, K, xdtype).bytes) return GMM_ERR_WORKSPACE;
   return GMM_OK;
 }
 
 template <typename T>
-gmm_status rows_simt(const void* A, const void* W, void* Y, int64_t R, int d_from, int d_to, int K,
-                     bool dx, const int64_t* offsets, void* ws, cudaStream_t s) {
-  const ProductLayout L = ProductLayout::make(R, d_from, d_to, K);
+gmm_status rows_simt(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
+                     int d_to, int K, bool dx, const int64_t* offsets, void* ws, cudaStream_t s) {
+  const ProductLayout L = ProductLayout::make(R, d_from, d_to, K, xdtype);
   gmm_status r = list_tiles(offsets, K, R, kT, ws, L, s);
   if (r != GMM_OK || R == 0) return r;
   const dim3 grid((unsigned)ProductLayout::most_tiles(R, K, kT), (d_to + kT - 1) / kT);
@@ -202,9 +202,9 @@ gmm_status rows_product(const void* A, int xdtype, const void* W, void* Y, int64
     return tc_rows(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
   if ((d_to + kT - 1) / kT > 65535) return GMM_ERR_UNSUPPORTED;
   switch (xdtype) {
-    case GMM_F32: return rows_simt<float>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
-    case GMM_F16: return rows_simt<__half>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
-    default: return rows_simt<__nv_bfloat16>(A, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
+    case GMM_F32: return rows_simt<float>(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
+    case GMM_F16: return rows_simt<__half>(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
+    default: return rows_simt<__nv_bfloat16>(A, xdtype, W, Y, R, d_from, d_to, K, dx, offsets, ws, s);
   }
 }
 
@@ -228,7 +228,7 @@ extern "C" {
 
 size_t gmm_expert_ws_bytes(int64_t R, int d_in, int d_out, int K, gmm_dtype xdtype) {
   if (!sizes_ok(xdtype, R, d_in, d_out, K)) return 0;
-  return ProductLayout::make(R, d_in, d_out, K).bytes;
+  return ProductLayout::make(R, d_in, d_out, K, xdtype).bytes;
 }
 
 gmm_status gmm_expert_product(const void* A, gmm_dtype xdtype, int64_t R, int d_in, int d_out,

@@ -33,18 +33,23 @@ inline int64_t dw_stretch_rows(int64_t R, int d_in, int d_out, int K) {
   return rows < R ? rows : 0;
 }
 
+// What the tensor-core forms take, as far as types and widths say.
+inline bool tc_widths_ok(int xdtype, int d_in, int d_out) {
+  return xdtype != GMM_F32 && d_in % 8 == 0 && d_out % 8 == 0;
+}
+
 struct ProductLayout {
   size_t off_count, off_first, off_tiles, off_part, bytes;  // the DeviceStatus comes first
   // row tiles of K components and of the rows past them
   static int64_t most_tiles(int64_t R, int K, int T) { return R / T + K + 1; }
-  static ProductLayout make(int64_t R, int d_in, int d_out, int K) {
+  static ProductLayout make(int64_t R, int d_in, int d_out, int K, int xdtype) {
     ProductLayout L;
     size_t o = align_up(sizeof(DeviceStatus));
     L.off_count = o; o = align_up(o + sizeof(int32_t));
     L.off_first = o; o = align_up(o + sizeof(uint32_t) * ((size_t)K + 2));
     L.off_tiles = o; o = align_up(o + sizeof(int4) * (size_t)most_tiles(R, K, kLeastTile));
     L.off_part = o;
-    if (dw_stretch_rows(R, d_in, d_out, K) > 0)
+    if (tc_widths_ok(xdtype, d_in, d_out) && dw_stretch_rows(R, d_in, d_out, K) > 0)
       o = align_up(o + sizeof(float) * (size_t)d_in * d_out * (dw_stretches(d_in, d_out) + 1));
     L.bytes = o;
     return L;

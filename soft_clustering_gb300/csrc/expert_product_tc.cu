@@ -877,13 +877,12 @@ gmm_status go(const CUtensorMap& mp, const CUtensorMap& mq, const CUtensorMap& m
 }  // namespace
 
 bool tc_product_ok(int xdtype, int64_t R, int d_in, int d_out, const void* a, const void* b, const void* c) {
-  return xdtype != GMM_F32 && R <= INT32_MAX - 256 && d_in % 8 == 0 && d_out % 8 == 0 &&
-         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) % 16 == 0;
+  return tc_widths_ok(xdtype, d_in, d_out) && R <= INT32_MAX - 256 && aligned(16, a, b, c);
 }
 
 gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R, int d_from,
                    int d_to, int K, bool dx, const int64_t* offsets, void* ws, cudaStream_t s) {
-  const ProductLayout L = ProductLayout::make(R, d_from, d_to, K);
+  const ProductLayout L = ProductLayout::make(R, d_from, d_to, K, xdtype);
   // Up to kMostCounted components every block counts their tiles itself in
   // place of a kernel that lists them: experts of 128 x 128 in bf16, 30000
   // rows, a call: 12.8 us (listed 16.3) with 600 components, 17.6 (16.7) with
@@ -920,7 +919,7 @@ gmm_status tc_weights(const void* dY, const void* A, int xdtype, int64_t R, int 
   const int64_t stretch = dw_stretch_rows(R, d_in, d_out, K);
   if (stretch > 0) {
     // few tiles of long sums
-    const ProductLayout L = ProductLayout::make(R, d_in, d_out, K);
+    const ProductLayout L = ProductLayout::make(R, d_in, d_out, K, xdtype);
     const int64_t most = ProductLayout::most_tiles(R, K, (int)stretch);
     float* part = at<float>(ws, L.off_part);
     if (!encode(&mo, GMM_F32, part, d_in, d_out, most, 32)) return GMM_ERR_CUDA;

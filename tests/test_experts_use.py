@@ -208,3 +208,17 @@ def test_addresses_that_are_not_aligned(lib):
     for f in (lib.gmm_expert_product, lib.gmm_expert_product_dx):
         each(f, (P, 1, 4, 8, 8, 2, P, P, P, P, big, None), {0: 1, 6: 4, 7: 1, 8: 1, 9: 128})
     each(lib.gmm_expert_product_dw, (P, P, 1, 4, 8, 8, 2, P, P, 0, P, big, None), {0: 1, 1: 1, 7: 4, 8: 2, 10: 128})
+
+
+def test_workspace_holds_what_the_product_uses(lib):
+    """Partial sums of dW only where the tensor cores can make them, and never
+    less for fewer rows of the same product."""
+    R, K = 522711, 22
+    part = 4 * 64 * 128 * 100  # a hundred partial sums at least
+    assert G.gmm_expert_ws_bytes(R, 64, 128, K, G.GMM_BF16) > part
+    for d_in, d_out, x in ((64, 128, G.GMM_F32), (60, 128, G.GMM_BF16), (64, 124, G.GMM_F16)):
+        assert G.gmm_expert_ws_bytes(R, d_in, d_out, K, x) < part
+    for x in (G.GMM_F32, G.GMM_F16):
+        for d_in, d_out, K in ((64, 128, 22), (512, 256, 16), (8, 8, 1), (128, 128, 600), (2048, 2048, 3)):
+            sizes = [G.gmm_expert_ws_bytes(r, d_in, d_out, K, x) for r in range(0, 4_000_000, 4093)]
+            assert sizes == sorted(sizes) and sizes[0] > 0
