@@ -28,6 +28,15 @@ def _dense(t, name, n, dtypes, device):
     return t
 
 
+def _apart(named):
+    """ValueError if two of the tensors (name, tensor) have memory in common."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+                   for name, t in named if t is not None and t.numel())
+    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError("%s and %s have memory in common" % (a, b))
+
+
 class AdamW:
     """Decoupled weight decay Adam on `params`, dense float32 / float16 / bfloat16
     CUDA tensors, updated in place.
@@ -110,6 +119,10 @@ class AdamW:
 
     def _fill_table(self):
         """The tensors' addresses for the library, and what `_bind` knows them by."""
+        # one launch writes them all, in no order
+        _apart([("params[%d]" % i, p) for i, p in enumerate(self.params)]
+               + [("state[%s][%d]" % (k, i), t) for k, ts in self.state.items()
+                  for i, t in enumerate(ts)])
         self._table = (gmm_adamw_tensor * max(1, len(self.params)))()
         self._rows = [(self._table[i], n, self._device) for i, (n, _) in enumerate(self._given)]
         for i, p in enumerate(self.params):

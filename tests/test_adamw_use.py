@@ -537,3 +537,29 @@ def test_small_values_in_8_bits(cuda, eps, beside):
             off = np.abs(p.double().cpu().numpy() - after)
             assert (off[ok] <= bound[ok]).all(), (step, size[ok][(off[ok] - bound[ok]).argmax()])
             p[torch.from_numpy(~ok).cuda()] = 1.0  # infinite there, as the formula says
+
+
+def test_tensors_with_memory_in_common_are_refused():
+    """One launch would write them twice, in no order."""
+    import torch
+    from soft_clustering_gb300.adamw import _apart
+    x = torch.zeros(100)
+    _apart([("a", x[:50]), ("b", x[50:]), ("c", None), ("d", x[:0]), ("e", torch.zeros(3))])
+    _apart([])
+    for a, b in ((x, x), (x[:51], x[50:]), (x, x[10:20]), (x[99:], x)):
+        with pytest.raises(ValueError, match="memory in common"):
+            _apart([("a", a), ("x", torch.zeros(4)), ("b", b)])
+
+
+@pytest.mark.gpu
+def test_a_parameter_given_twice_is_refused(cuda):
+    import torch
+    from soft_clustering_gb300.adamw import AdamW
+    p = torch.zeros(100, device="cuda")
+    with pytest.raises(ValueError, match="memory in common"):
+        AdamW([p, p[90:]])
+    opt = AdamW([p, torch.zeros(100, device="cuda")])
+    opt.state["v"][1] = opt.state["m"][0]
+    with pytest.raises(ValueError, match="memory in common"):
+        opt.step([p, p])
+    assert not p.any() and opt.steps == 0
