@@ -89,7 +89,7 @@ class AdamW:
                                      device=self._device or "cuda")
         self.state = self._state(state, master)
         self._master = "master" in self.state
-        self._opts = gmm_adamw_opts()
+        self._opts, self._values = gmm_adamw_opts(), None
         self._opts.state_bits, self._opts.rounding = state_bits, ROUNDINGS[rounding or "nearest"]
         self._fill_table()
 
@@ -124,7 +124,7 @@ class AdamW:
                + [("state[%s][%d]" % (k, i), t) for k, ts in self.state.items()
                   for i, t in enumerate(ts)])
         self._table = (gmm_adamw_tensor * max(1, len(self.params)))()
-        self._rows = [(self._table[i], n, self._device) for i, (n, _) in enumerate(self._given)]
+        self._rows = [(self._table[i], n, self._device.index) for i, (n, _) in enumerate(self._given)]
         for i, p in enumerate(self.params):
             e = self._table[i]
             e.param, e.n, e.param_dtype = p.data_ptr(), p.numel(), TORCH_XDTYPE[p.dtype]
@@ -184,16 +184,23 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(self.params)))
         self._bind()
-        for i, (g, (e, n, device)) in enumerate(zip(grads, self._rows)):
-            dt = TORCH_XDTYPE.get(g.dtype) if torch.is_tensor(g) else None
-            if dt is None or g.numel() != n or g.device != device or not g.is_contiguous():
-                _dense(g, "grads[%d]" % i, n, tuple(TORCH_XDTYPE), device)
-            e.grad, e.grad_dtype = g.data_ptr(), dt
+        for g, (e, n, index) in zip(grads, self._rows):
+            try:
+                e.grad, e.grad_dtype = g.data_ptr(), TORCH_XDTYPE[g.dtype]
+                if g.numel() == n and g.get_device() == index and g.is_contiguous():
+                    continue
+            except (AttributeError, KeyError, TypeError):
+                pass
+            for i, (g, (n, _)) in enumerate(zip(grads, self._given)):  # says which and why
+                _dense(g, "grads[%d]" % i, n, tuple(TORCH_XDTYPE), self._device)
         if skip is not None:
             _dense(skip, "skip", 1, (torch.int32,), self._device or skip.device)
         o = self._opts
-        o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
-        o.weight_decay, o.grad_scale, o.step = self.weight_decay, grad_scale, self._steps + 1
+        values = (self.lr, self.betas, self.eps, self.weight_decay, grad_scale)
+        if values != self._values:
+            o.lr, (o.beta1, o.beta2), o.eps, o.weight_decay, o.grad_scale = values
+            self._values = values
+        o.step = self._steps + 1
         o.skip = skip.data_ptr() if skip is not None else None
         if self._count is None:
             if torch.cuda.is_current_stream_capturing():

@@ -563,3 +563,24 @@ def test_a_parameter_given_twice_is_refused(cuda):
     with pytest.raises(ValueError, match="memory in common"):
         opt.step([p, p])
     assert not p.any() and opt.steps == 0
+
+
+@pytest.mark.gpu
+def test_gradients_that_are_refused(cuda):
+    """Anything but a dense tensor of the parameter's size on its device, first
+    or last in the list; nothing is changed."""
+    import torch
+    p, grads, opt = _make()
+    kept = [t.clone() for t in p]
+    for at in (0, 1):
+        n = p[at].numel()
+        for bad in (None, 3, np.zeros(n, np.float32), torch.zeros(n), torch.zeros(n + 1, device="cuda"),
+                    torch.zeros(2 * n, device="cuda")[::2], torch.zeros(n, device="cuda", dtype=torch.int32),
+                    torch.zeros(n, device="cuda", dtype=torch.float64)):
+            g = list(grads[0])
+            g[at] = bad
+            with pytest.raises(ValueError, match="grads.%d" % at):
+                opt.step(g)
+    assert opt.steps == 0
+    for a, b in zip(p, kept):
+        assert torch.equal(a, b)
