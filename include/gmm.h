@@ -229,7 +229,7 @@ gmm_status gmm_ivf_lists(const int32_t* ids, const float* gamma, int64_t N, int 
 /* Synchronises `stream` and returns the device status word of `ws`: the
  * first device-side failure of the most recent gmm_em_step, gmm_em_step_host
  * or gmm_assign_topm call on that workspace (each call resets the word), or
- * GMM_OK. */
+ * GMM_OK.  (The products of gmm_experts.h do not reset theirs.) */
 gmm_status gmm_last_device_status(void* ws, void* stream);
 
 /*

@@ -112,9 +112,10 @@ gmm_status gmm_expert_product_dw(const void* dY, const void* A, gmm_dtype xdtype
 
 /*
  * gmm_adamw_step - one step of Adam with decoupled weight decay (Kingma and
- * Ba 2015; Loshchilov and Hutter 2019) over `count` tensors.  In fp32, each
- * operation rounded once and in this order (with 8-bit moments the update
- * m / (...) may differ by 2^-21 of itself; the moments do not):
+ * Ba 2015; Loshchilov and Hutter 2019) over `count` tensors, no two of their
+ * arrays with memory in common.  In fp32, each operation rounded once and in
+ * this order (with 8-bit moments the update m / (...) may differ by 2^-21 of
+ * itself; the moments do not):
  *   g = grad_scale grad
  *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
  *   p = (1 - lr weight_decay) p
@@ -169,6 +170,7 @@ typedef struct {
 #define GMM_ROUND_NEAREST 0
 #define GMM_ROUND_SEEDED 1
 
+/* Zero all of it before the fields are set. */
 typedef struct {
   double lr, beta1, beta2, eps, weight_decay, grad_scale;
   int64_t step;        /* 1 at the first step */

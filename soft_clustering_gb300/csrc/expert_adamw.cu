@@ -10,25 +10,28 @@
 // memory where the moments are bytes (a lane has 24 bytes a turn, too little
 // in flight otherwise), one turn in registers where they are floats.
 //
-// Bound by HBM traffic: 28 bytes an element in fp32, 10 with 16-bit
-// parameters and gradients and 8-bit moments.  With fp32 moments every
-// operation is the IEEE one in the documented order.  With 8-bit moments the
-// arithmetic competes with the traffic (10 bytes leave about 50 instructions
-// an element), so there
+// Bound by HBM traffic in fp32, 28 bytes an element, where every operation is
+// the IEEE one in the documented order.  With 16-bit parameters and gradients
+// and 8-bit moments an element is 10 bytes, which leave time for about 40
+// instructions, so there the arithmetic is the bound, and
 //   - bytes become floats and floats codes by adding 2^23 (or 1.5 2^23), on
 //     the FP32 pipe instead of the conversion unit;
 //   - square roots are approximate (2 units in the last place) wherever the
 //     rounding to a code cannot depend on it: a root within kNear of halfway
 //     between two codes, about one in 2500, is taken again exactly, so the
 //     codes and scales are those of the exact roots;
-//   - the parameter's update uses the approximate root and reciprocal: a
-//     relative error of the update below 2^-21, under the rounding of the
-//     parameter;
+//   - the parameter's update uses the approximate root and reciprocal, which
+//     add 2^-21 of the update: under the rounding of a 16-bit parameter, not
+//     under that of an fp32 one (or master) near zero;
 //   - products and sums go by pairs of elements (packed fp32 operations).
-// Measured: 1e8 elements in fp32 422 us (6.63 TB/s, 98 % of the copy rate);
-// 2e8 bf16 elements with 8-bit moments 467 us (4.3 TB/s: about 54
-// instructions an element, 45 % of the issue slots, four blocks a
-// multiprocessor); their moments in fp32 317 us (6.3 TB/s).
+// Rounding codes to the nearest loses every change below half a code; seeded
+// rounding does not, and takes random bits for both moments of every element.
+// Measured: 1e8 elements in fp32 419 us (6.68 TB/s, 98 % of the copy rate),
+// counted on the device 446.  2e8 bf16 elements with 8-bit moments, nearest,
+// 473 us (4.2 TB/s): 66 instructions an element, issue slots 75 % busy, four
+// blocks a multiprocessor; seeded 802 us: 108 instructions, 72 %, three blocks.
+// With a master copy and fp32 gradients 1008 and 1164 us.  Their moments in
+// fp32 317 us (6.3 TB/s).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>

@@ -31,9 +31,10 @@
 // with single blocks, bound by shared memory, which has to take 192 bytes a
 // cycle).  Runs that last are bound by the power limit (about 350 us).
 // What the rest is bound by: 1000001 rows through 256 experts of 128 x 128 in
-// f16, HBM traffic (87 us a call, 6.0 TB/s); dX and dW of 16385 rows x 64
-// experts of 1024 x 2048, the weights' traffic (65 and 73 us; 54 each at the
-// measured copy rate).
+// f16, HBM traffic (87 us a call, 6.0 TB/s); dX of 16385 rows x 64 experts of
+// 1024 x 2048, the weights' traffic (70 us a call, 54 at the measured copy
+// rate); dW of them (88 us, 54) the stages' latency, four or five a tile before
+// it is stored, and at a component's end the hand-over of mended rows.
 #include <cuda.h>
 
 #include <type_traits>
@@ -280,7 +281,10 @@ __device__ __forceinline__ void arrive_read(uint32_t bar) {
 // Arrival at a barrier of either block that passes on writes to this block's
 // shared memory: the products that read them are issued by the other block, so
 // the arrival is a release to the cluster (without a scope it would be one to
-// this block alone), and wait_pair acquires there.
+// this block alone), and wait_pair acquires there.  It takes about half a
+// microsecond a ragged end: 82 us of the kernel's time for dW of 16385 rows x
+// 64 experts of 1024 x 2048, where single blocks take as long and lose more
+// elsewhere (65536 rows x 32 experts of 2048 x 2048: 325 us, single 366).
 __device__ __forceinline__ void arrive_written(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -886,7 +890,8 @@ gmm_status tc_rows(const void* A, int xdtype, const void* W, void* Y, int64_t R,
   // Up to kMostCounted components every block counts their tiles itself in
   // place of a kernel that lists them: experts of 128 x 128 in bf16, 30000
   // rows, a call: 12.8 us (listed 16.3) with 600 components, 17.6 (16.7) with
-  // 1000, 27.1 (23.6) with 2000.
+  // 1000, 27.1 (23.6) with 2000.  The crossing is somewhat below 1000, where the
+  // room for their first tiles ends.
   const bool listed = K > kMostCounted || R == 0;
   if (listed) {
     const gmm_status r = list_tiles(offsets, K, R, kTileN, ws, L, s);

@@ -246,7 +246,8 @@ class LocalExperts:
 
     W [K, d_out, d_in] is the caller's (``adamw.AdamW`` trains it).  ``forward``
     keeps what ``backward`` needs until the next ``forward``, gamma by value: its
-    buffer may be written again in between (the next batch's assignment).
+    buffer may be written again in between (the next batch's assignment).  autograd
+    records neither: gradients are what ``backward`` returns.
     """
 
     def __init__(self, N, m, K, d_in, d_out, dtype, device="cuda"):
