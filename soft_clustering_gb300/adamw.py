@@ -49,7 +49,8 @@ class AdamW:
     v does not fall again and m does not end, so it is for comparisons and a few
     steps.
     master: hold 16-bit parameters in float32 as well (``self.state["master"]``;
-    None for a float32 one).
+    None for a float32 one).  A step reads them there, so a parameter that is
+    written by hand is written there too.
     state, step: resume; a dict of lists m, v (and m_scale, v_scale in 8 bits,
     master with master=True) as ``self.state`` holds them, and the steps taken.
 
