@@ -1,5 +1,6 @@
-"""Python binding of libgmm (include/gmm.h, include/gmm_experts.h): the fused
-GMM EM step, top-m soft assignment, and local experts behind it, on one GB300.
+"""Python binding of libgmm (include/gmm.h, gmm_experts.h, gmm_gate.h): the
+fused GMM EM step, top-m soft assignment, local experts behind it and a learned
+gate in its place, on one GB300.
 
 Argument marshalling only.  Every function here has the name of the C entry
 point it calls and forwards device pointers taken from torch tensors (or
@@ -21,6 +22,9 @@ GMM_OK, GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED, GMM_ERR_NOT_PD = 0, 1, 2, 3
 GMM_ERR_NONFINITE, GMM_ERR_WORKSPACE, GMM_ERR_TIMEOUT, GMM_ERR_CUDA = 4, 5, 6, 7
 GMM_FLAG_RIDGE, GMM_FLAG_NOT_PD, GMM_FLAG_FLOOR, GMM_FLAG_EMPTY = 1, 2, 4, 8
 GMM_OPT_CUDA_CORES = 1
+GMM_GATE_NORMALISED = 1
+GMM_TEACHER_LOGITS, GMM_TEACHER_GAMMA = 0, 1
+GMM_DISTILL_ADD = 1
 
 EXPORTS = (
     "gmm_default_opts", "gmm_status_string", "gmm_workspace_bytes", "gmm_prepared_bytes",
@@ -30,6 +34,8 @@ EXPORTS = (
     "gmm_ivf_lists", "gmm_route_ws_bytes", "gmm_route", "gmm_spread", "gmm_collect",
     "gmm_expert_ws_bytes", "gmm_expert_product", "gmm_expert_product_dx",
     "gmm_expert_product_dw", "gmm_adamw_step", "gmm_adamw_step_counted", "gmm_adamw_moments",
+    "gmm_gate_ws_bytes", "gmm_gate", "gmm_gate_grad", "gmm_distill_ws_bytes", "gmm_distill",
+    "gmm_layer_norm", "gmm_layer_norm_ws_bytes", "gmm_layer_norm_grad",
 )
 
 
@@ -114,6 +120,21 @@ def lib():
         L.gmm_adamw_step.argtypes = [P(gmm_adamw_tensor), i32, P(gmm_adamw_opts), vp]
         L.gmm_adamw_step_counted.argtypes = [P(gmm_adamw_tensor), i32, P(gmm_adamw_opts), vp, vp]
         L.gmm_adamw_moments.argtypes = [P(gmm_adamw_tensor), i32, i32, P(vp), P(vp), vp]
+        f64 = ctypes.c_double
+        L.gmm_gate_ws_bytes.argtypes = [i64, i32, i32]
+        L.gmm_gate_ws_bytes.restype = sz
+        L.gmm_gate.argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                               vp]
+        L.gmm_gate_grad.argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, f64, vp, vp]
+        L.gmm_distill_ws_bytes.argtypes = []
+        L.gmm_distill_ws_bytes.restype = sz
+        L.gmm_distill.argtypes = [vp, i32, i64, i32, i32, i32, i32, f64, f64, vp, vp, vp, vp, vp,
+                                  vp, vp, sz, vp]
+        L.gmm_layer_norm.argtypes = [vp, i32, i64, i32, f64, vp, vp, i32, vp, vp]
+        L.gmm_layer_norm_ws_bytes.argtypes = [i32]
+        L.gmm_layer_norm_ws_bytes.restype = sz
+        L.gmm_layer_norm_grad.argtypes = [vp, vp, i32, i64, i32, f64, vp, i32, vp, vp, vp, vp, sz,
+                                          vp]
         L.gmm_profile_enable.argtypes = [i32]
         L.gmm_profile_enable.restype = None
         L.gmm_profile_read.argtypes = [P(ctypes.c_char_p), P(ctypes.c_double), P(ctypes.c_long),
@@ -124,7 +145,8 @@ def lib():
                   "gmm_last_device_status", "gmm_em_step_noalloc", "gmm_ivf_lists",
                   "gmm_route", "gmm_spread", "gmm_collect", "gmm_expert_product",
                   "gmm_expert_product_dx", "gmm_expert_product_dw", "gmm_adamw_step",
-                  "gmm_adamw_step_counted", "gmm_adamw_moments"):
+                  "gmm_adamw_step_counted", "gmm_adamw_moments", "gmm_gate", "gmm_gate_grad",
+                  "gmm_distill", "gmm_layer_norm", "gmm_layer_norm_grad"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -331,6 +353,56 @@ def gmm_adamw_moments(tensors, count, state_bits, m_out, v_out, stream=None,
     """m_out, v_out: ctypes arrays of device addresses."""
     st = lib().gmm_adamw_moments(tensors, count, state_bits, m_out, v_out, _stream(stream))
     return _check(st, "gmm_adamw_moments", raise_on_error)
+
+
+def gmm_gate_ws_bytes(N, K, m) -> int:
+    return int(lib().gmm_gate_ws_bytes(N, K, m))
+
+
+def gmm_gate(L, xdtype, N, K, m, flags, live, ids, gamma, lse, counts, mass, share, loss, ws,
+             ws_bytes, stream=None, raise_on_error=True):
+    st = lib().gmm_gate(_ptr(L), xdtype, N, K, m, flags, _ptr(live), _ptr(ids), _ptr(gamma),
+                        _ptr(lse), _ptr(counts), _ptr(mass), _ptr(share), _ptr(loss), _ptr(ws),
+                        ws_bytes, _stream(stream))
+    return _check(st, "gmm_gate", raise_on_error)
+
+
+def gmm_gate_grad(L, xdtype, N, K, m, flags, live, ids, gamma, dgamma, share, coef, dL,
+                  stream=None, raise_on_error=True):
+    st = lib().gmm_gate_grad(_ptr(L), xdtype, N, K, m, flags, _ptr(live), _ptr(ids), _ptr(gamma),
+                             _ptr(dgamma), _ptr(share), coef, _ptr(dL), _stream(stream))
+    return _check(st, "gmm_gate_grad", raise_on_error)
+
+
+def gmm_distill_ws_bytes() -> int:
+    return int(lib().gmm_distill_ws_bytes())
+
+
+def gmm_distill(L, xdtype, N, K, m, kind, flags, temperature, scale, ids, values, weights, rows,
+                loss, dL, ws, ws_bytes, stream=None, raise_on_error=True):
+    st = lib().gmm_distill(_ptr(L), xdtype, N, K, m, kind, flags, temperature, scale, _ptr(ids),
+                           _ptr(values), _ptr(weights), _ptr(rows), _ptr(loss), _ptr(dL), _ptr(ws),
+                           ws_bytes, _stream(stream))
+    return _check(st, "gmm_distill", raise_on_error)
+
+
+def gmm_layer_norm(X, xdtype, N, D, eps, weight, bias, wdtype, Y, stream=None,
+                   raise_on_error=True):
+    st = lib().gmm_layer_norm(_ptr(X), xdtype, N, D, eps, _ptr(weight), _ptr(bias), wdtype,
+                              _ptr(Y), _stream(stream))
+    return _check(st, "gmm_layer_norm", raise_on_error)
+
+
+def gmm_layer_norm_ws_bytes(D) -> int:
+    return int(lib().gmm_layer_norm_ws_bytes(D))
+
+
+def gmm_layer_norm_grad(dY, X, xdtype, N, D, eps, weight, wdtype, dX, dweight, dbias, ws, ws_bytes,
+                        stream=None, raise_on_error=True):
+    st = lib().gmm_layer_norm_grad(_ptr(dY), _ptr(X), xdtype, N, D, eps, _ptr(weight), wdtype,
+                                   _ptr(dX), _ptr(dweight), _ptr(dbias), _ptr(ws), ws_bytes,
+                                   _stream(stream))
+    return _check(st, "gmm_layer_norm_grad", raise_on_error)
 
 
 def gmm_last_device_status(ws, stream=None) -> int:
