@@ -1,4 +1,9 @@
 // gate_internal.cuh - helpers shared by the learned gate's kernels.
+//
+// A row is held in registers by a team of threads: 1 to 32 lanes of a warp for
+// short rows, a block, or a cluster of blocks for long ones.  Vector j of lane i
+// of a team of `size` is number j * size + i of the row, V elements each: 16
+// bytes where every row starts on such a boundary, else one element.
 #pragma once
 
 #include "expert_internal.cuh"
@@ -9,6 +14,169 @@ namespace gate {
 
 constexpr int kMaxTop = 8;       // entries of a gate's row
 constexpr int kMaxTeacher = 64;  // entries of a teacher's row
+constexpr int kSms = 152;
+
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
+
+// Elements of one vector of a row: 16 bytes where the row length and all
+// addresses allow it.
+template <typename T> constexpr int kWide = 16 / (int)sizeof(T);
+template <typename T, typename... P>
+inline bool wide(int64_t width, const P*... p) {
+  return width % kWide<T> == 0 && aligned(16, (const char*)p...);
+}
+
+// Two elements of a row in fp32, and back.
+__device__ __forceinline__ float2 to_f2(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ float2 to_f2(__half a, __half b) { return __half22float2(__halves2half2(a, b)); }
+__device__ __forceinline__ float2 to_f2(__nv_bfloat16 a, __nv_bfloat16 b) {
+  return __bfloat1622float2(__halves2bfloat162(a, b));
+}
+__device__ __forceinline__ void from_f2(float2 f, float& a, float& b) { a = f.x, b = f.y; }
+__device__ __forceinline__ void from_f2(float2 f, __half& a, __half& b) {
+  const __half2 h = __float22half2_rn(f);
+  a = __low2half(h), b = __high2half(h);
+}
+__device__ __forceinline__ void from_f2(float2 f, __nv_bfloat16& a, __nv_bfloat16& b) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(f);
+  a = __low2bfloat16(h), b = __high2bfloat16(h);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// What a lane has of a row, as it is stored; its elements in order are pairs
+// of fp32 numbers to the arithmetic.
+template <typename T, int V, int NV>
+struct Row {
+  static constexpr int E = V * NV;
+  static_assert(E % 2 == 0, "pairs");
+  Vec<T, V> r[NV];
+  __device__ __forceinline__ void fill(T none) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) r[j].v[e] = none;
+  }
+  __device__ __forceinline__ void store(T* __restrict__ p, int lane, int size, int nv) const {
+    p += (int64_t)lane * V;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j * size + lane < nv) *reinterpret_cast<Vec<T, V>*>(p + j * size * V) = r[j];
+  }
+  __device__ __forceinline__ T& at(int i) { return r[i / V].v[i % V]; }
+  __device__ __forceinline__ const T& at(int i) const { return r[i / V].v[i % V]; }
+  __device__ __forceinline__ void get(float2 (&f)[E / 2]) const {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) f[i] = to_f2(at(2 * i), at(2 * i + 1));
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[E / 2]) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) from_f2(f[i], at(2 * i), at(2 * i + 1));
+  }
+};
+
+// A lane's own vectors of the rows ahead, of NA arrays of one shape.  Wide ones
+// wait in shared memory, put there by asynchronous copies kStages - 1 rows before
+// they are used: the bytes in flight that HBM needs, without registers for them.
+// A lane reads what it copied itself, so there is nothing to synchronise.  Single
+// elements (rows that do not start on 16 bytes) wait in registers, one row ahead.
+template <typename T, int V, int NV, int NA>
+struct Feed {
+  static constexpr bool kAsync = sizeof(T) * V == 16;
+  // 512 threads' rows fit a multiprocessor's shared memory
+  static constexpr int kStages = NA * NV >= 8 ? 3 : 4;
+  static constexpr size_t bytes(int threads) { return kAsync ? (size_t)kStages * NA * NV * threads * 16 : 0; }
+  const T* from[NA];  // the next row to be fetched, at this lane's first vector
+  int64_t step;       // elements from a row to the next
+  int left, size, lane, nv;
+  char* slot;         // this thread's, [stage][array][vector][thread] of 16 bytes
+  uint32_t stage;
+  Row<T, V, NV> ahead[kAsync ? 1 : NA];
+
+  // Rows `row`, row + stride, ... below N of arrays of `width`-element rows; nv:
+  // vectors of a row, those that a lane has past them are `none`.
+  __device__ __forceinline__ void start(char* smem, const T* const (&array)[NA], int64_t row, int64_t stride, int64_t N,
+                                        int64_t width, int lane_, int size_, int nv_, T none) {
+    lane = lane_, size = size_, nv = nv_, stage = 0, step = stride * width;
+    left = row < N ? (int)((N - row + stride - 1) / stride) : 0;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) from[a] = array[a] + row * width + (int64_t)lane * V;
+#pragma unroll
+    for (int a = 0; a < (kAsync ? 1 : NA); ++a) ahead[a].fill(none);
+    if constexpr (kAsync) {
+      slot = smem + threadIdx.x * 16;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (j * size + lane >= nv)
+          for (int s = 0; s < kStages * NA; ++s)
+            *reinterpret_cast<Vec<T, V>*>(slot + (size_t)(s * NV + j) * blockDim.x * 16) = ahead[0].r[j];
+#pragma unroll
+      for (int s = 0; s < kStages - 1; ++s) fetch(s);
+    } else {
+      fetch(0);
+    }
+  }
+  __device__ __forceinline__ void fetch(uint32_t into) {
+    if (left > 0) {
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (j * size + lane < nv) {
+            if constexpr (kAsync)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(
+                               slot + (size_t)((into * NA + a) * NV + j) * blockDim.x * 16)),
+                           "l"(from[a] + j * size * V)
+                           : "memory");
+            else
+              ahead[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(from[a] + j * size * V);
+          }
+    }
+    if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+    --left;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) from[a] += step;
+  }
+  // The next row; past the last one, what was there before.
+  __device__ __forceinline__ void next(Row<T, V, NV> (&row)[NA]) {
+    if constexpr (kAsync) {
+      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          row[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)((stage * NA + a) * NV + j) * blockDim.x * 16);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int a = 0; a < NA; ++a) row[a] = ahead[a];
+      fetch(0);
+    }
+  }
+};
+
+// Whether a lane's element i (of the pairs above) is one of the row's.
+template <int V>
+__device__ __forceinline__ bool inside(int i, int lane, int size, int nv) {
+  return (i / V) * size + lane < nv;
+}
+// The column of a lane's element i.
+template <int V>
+__device__ __forceinline__ int column(int i, int lane, int size) {
+  return ((i / V) * size + lane) * V + i % V;
+}
+
+// A lane's columns of a vector of numbers; `none` where there is none.
+template <int V, int NV, typename W>
+__device__ __forceinline__ void load_columns(float2 (&c)[V * NV / 2], const W* __restrict__ p, int lane,
+                                             int size, int nv, float none) {
+  float f[V * NV];
+#pragma unroll
+  for (int i = 0; i < V * NV; ++i)
+    f[i] = p && inside<V>(i, lane, size, nv) ? to_f(p[column<V>(i, lane, size)]) : none;
+#pragma unroll
+  for (int i = 0; i < V * NV / 2; ++i) c[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
 
 // Order of floats as unsigned numbers: -0 and 0 are one, every NaN is the largest.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -43,6 +211,123 @@ __device__ __forceinline__ T block_reduce(T v, T none, Op op, T* part) {
   __syncthreads();
   const int lane = threadIdx.x & 31;
   return warp_reduce(lane < (int)(blockDim.x >> 5) ? part[lane] : none, op);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A part of a warp (or all of it): `size` lanes, a power of two.
+struct WarpTeam {
+  int lane, size;
+  template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      if (size > o) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
+      }
+  }
+};
+
+// A block, or a cluster of up to 8.  Each warp's sums of Q numbers go to shared
+// memory (of every block of the cluster), where every warp adds them up.  A
+// lane ends with one of the Q, so that 4 take 6 shuffles and not 20.  The words
+// are in one of two halves in turn: who writes a half again has passed the
+// barrier before which the others had read it.
+template <bool CLUSTER>
+struct BlockTeam {
+  static constexpr int kWarps = CLUSTER ? 128 : 16;  // of the team
+  static constexpr int kWords = 2 * 4 * kWarps;
+  int lane, size;
+  int all;  // warps
+  float* part;
+  uint32_t turn;
+
+  __device__ __forceinline__ explicit BlockTeam(float* p) : part(p), turn(0) {
+    if (CLUSTER) {
+      lane = (int)(cluster_rank() * blockDim.x + threadIdx.x);
+      size = (int)(cluster_blocks() * blockDim.x);
+    } else {
+      lane = (int)threadIdx.x;
+      size = (int)blockDim.x;
+    }
+    all = size >> 5;
+  }
+  template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
+    static_assert(Q == 1 || Q == 2 || Q == 4, "a power of two");
+    constexpr int G = 32 / Q;  // lanes that end with the same one
+    const int l = threadIdx.x & 31, q = l / G, c = l % G;
+    float x;
+    if (Q == 4) {
+      const bool hi = l & 16, odd = l & 8;
+      float a = hi ? v[Q - 2] : v[0], b = hi ? v[Q - 1] : v[Q / 4];
+      const float sa = hi ? v[0] : v[Q - 2], sb = hi ? v[Q / 4] : v[Q - 1];
+      a += __shfl_xor_sync(0xffffffffu, sa, 16);
+      b += __shfl_xor_sync(0xffffffffu, sb, 16);
+      x = odd ? b : a;
+      x += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+    } else if (Q == 2) {
+      const bool hi = l & 16;
+      x = hi ? v[Q - 1] : v[0];
+      x += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[Q - 1], 16);
+    } else {
+      x = v[0];
+    }
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    float* p = part + 4 * kWarps * turn + q * kWarps;
+    turn ^= 1;
+    if (CLUSTER) {
+      if (c < (int)cluster_blocks()) {
+        uint32_t there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(there)
+                     : "r"((uint32_t)__cvta_generic_to_shared(p + (lane >> 5))), "r"(c));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(x) : "memory");
+      }
+      cluster_barrier();
+    } else {
+      if (c == 0) p[threadIdx.x >> 5] = x;
+      __syncthreads();
+    }
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; i += G)
+      if (c + i < all) x += p[c + i];
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+    for (int k = 0; k < Q; ++k) v[k] = Q == 1 ? x : __shfl_sync(0xffffffffu, x, k * G);
+  }
+};
+
+// Launches `kernel` as clusters of `cluster` blocks (1: without any).
+template <typename... P, typename... A>
+inline void launch_clusters(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                            cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = threads;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 }  // namespace gate
