@@ -62,6 +62,13 @@ struct Row {
     for (int j = 0; j < NV; ++j)
       if (j * size + lane < nv) *reinterpret_cast<Vec<T, V>*>(p + j * size * V) = r[j];
   }
+  // What is inside the row; the rest is not written.
+  __device__ __forceinline__ void read(const T* __restrict__ p, int lane, int size, int nv) {
+    p += (int64_t)lane * V;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j * size + lane < nv) r[j] = *reinterpret_cast<const Vec<T, V>*>(p + j * size * V);
+  }
   __device__ __forceinline__ T& at(int i) { return r[i / V].v[i % V]; }
   __device__ __forceinline__ const T& at(int i) const { return r[i / V].v[i % V]; }
   __device__ __forceinline__ void get(float2 (&f)[E / 2]) const {
@@ -79,7 +86,23 @@ struct Row {
 // they are used: the bytes in flight that HBM needs, without registers for them.
 // A lane reads what it copied itself, so there is nothing to synchronise.  Single
 // elements (rows that do not start on 16 bytes) wait in registers, one row ahead.
-template <typename T, int V, int NV, int NA>
+// Which rows are fetched at all.
+struct EveryRow {
+  static constexpr bool kMasked = false;
+  __device__ __forceinline__ bool operator()(int64_t) const { return true; }
+};
+struct LiveRows {  // bytes, or NULL
+  static constexpr bool kMasked = true;
+  const uint8_t* live;
+  __device__ __forceinline__ bool operator()(int64_t n) const { return !live || live[n] != 0; }
+};
+struct WeightedRows {  // weights, or NULL
+  static constexpr bool kMasked = true;
+  const float* weights;
+  __device__ __forceinline__ bool operator()(int64_t n) const { return !weights || weights[n] != 0.f; }
+};
+
+template <typename T, int V, int NV, int NA, typename Rows = EveryRow>
 struct Feed {
   static constexpr bool kAsync = sizeof(T) * V == 16;
   // 512 threads' rows fit a multiprocessor's shared memory
@@ -90,16 +113,22 @@ struct Feed {
   int left, size, lane, nv;
   char* slot;         // this thread's, [stage][array][vector][thread] of 16 bytes
   uint32_t stage;
+  Rows rows;
+  int64_t row, stride;  // the next one to be fetched (of masked rows alone)
+  bool on;              // and whether it is
+  uint32_t were;        // whether the last ones were, a bit each
   Row<T, V, NV> ahead[kAsync ? 1 : NA];
 
   // Rows `row`, row + stride, ... below N of arrays of `width`-element rows; nv:
   // vectors of a row, those that a lane has past them are `none`.
-  __device__ __forceinline__ void start(char* smem, const T* const (&array)[NA], int64_t row, int64_t stride, int64_t N,
-                                        int64_t width, int lane_, int size_, int nv_, T none) {
-    lane = lane_, size = size_, nv = nv_, stage = 0, step = stride * width;
+  __device__ __forceinline__ void start(char* smem, const T* const (&array)[NA], int64_t row_, int64_t stride_, int64_t N,
+                                        int64_t width, int lane_, int size_, int nv_, T none, Rows rows_ = Rows()) {
+    lane = lane_, size = size_, nv = nv_, stage = 0, step = stride_ * width;
+    rows = rows_, row = row_, stride = stride_, were = 0;
     left = row < N ? (int)((N - row + stride - 1) / stride) : 0;
+    on = left > 0 && rows(row);
 #pragma unroll
-    for (int a = 0; a < NA; ++a) from[a] = array[a] + row * width + (int64_t)lane * V;
+    for (int a = 0; a < NA; ++a) from[a] = array[a] + row_ * width + (int64_t)lane * V;
 #pragma unroll
     for (int a = 0; a < (kAsync ? 1 : NA); ++a) ahead[a].fill(none);
     if constexpr (kAsync) {
@@ -116,7 +145,9 @@ struct Feed {
     }
   }
   __device__ __forceinline__ void fetch(uint32_t into) {
-    if (left > 0) {
+    const bool there = Rows::kMasked ? on : left > 0;
+    were = were << 1 | (uint32_t)there;
+    if (there) {
 #pragma unroll
       for (int a = 0; a < NA; ++a)
 #pragma unroll
@@ -133,11 +164,16 @@ struct Feed {
     }
     if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
     --left;
+    if (Rows::kMasked) {
+      row += stride;
+      on = left > 0 && rows(row);
+    }
 #pragma unroll
     for (int a = 0; a < NA; ++a) from[a] += step;
   }
-  // The next row; past the last one, what was there before.
-  __device__ __forceinline__ void next(Row<T, V, NV> (&row)[NA]) {
+  // The next row and true; what was there before and false past the last one and
+  // for a row that is not fetched.
+  __device__ __forceinline__ bool next(Row<T, V, NV> (&out)[NA]) {
     if constexpr (kAsync) {
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -145,13 +181,14 @@ struct Feed {
       for (int a = 0; a < NA; ++a)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-          row[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)((stage * NA + a) * NV + j) * blockDim.x * 16);
+          out[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)((stage * NA + a) * NV + j) * blockDim.x * 16);
       stage = stage == kStages - 1 ? 0 : stage + 1;
     } else {
 #pragma unroll
-      for (int a = 0; a < NA; ++a) row[a] = ahead[a];
+      for (int a = 0; a < NA; ++a) out[a] = ahead[a];
       fetch(0);
     }
+    return were >> (kAsync ? kStages - 1 : 1) & 1u;
   }
 };
 
@@ -176,6 +213,57 @@ __device__ __forceinline__ void load_columns(float2 (&c)[V * NV / 2], const W* _
     f[i] = p && inside<V>(i, lane, size, nv) ? to_f(p[column<V>(i, lane, size)]) : none;
 #pragma unroll
   for (int i = 0; i < V * NV / 2; ++i) c[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// The larger; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float y;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
+}
+// A lane's largest element, in the row's own type.
+template <int V, int NV>
+__device__ __forceinline__ float lane_max(const Row<float, V, NV>& r) {
+  float m = r.at(0);
+#pragma unroll
+  for (int i = 1; i < V * NV; ++i) m = max_nan(m, r.at(i));
+  return m;
+}
+template <int V, int NV>
+__device__ __forceinline__ float lane_max(const Row<__half, V, NV>& r) {
+  __half2 m = __halves2half2(r.at(0), r.at(1));
+#pragma unroll
+  for (int i = 2; i < V * NV; i += 2) m = __hmax2_nan(m, __halves2half2(r.at(i), r.at(i + 1)));
+  return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+}
+template <int V, int NV>
+__device__ __forceinline__ float lane_max(const Row<__nv_bfloat16, V, NV>& r) {
+  __nv_bfloat162 m = __halves2bfloat162(r.at(0), r.at(1));
+#pragma unroll
+  for (int i = 2; i < V * NV; i += 2) m = __hmax2_nan(m, __halves2bfloat162(r.at(i), r.at(i + 1)));
+  return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+}
+// x -> 2^((x - top) k); top not -inf
+template <int P>
+__device__ __forceinline__ void exponentials(float2 (&x)[P], float top, float k) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    x[i] = mul2(sub2(x[i], both(top)), both(k));
+    x[i] = make_float2(ex2(x[i].x), ex2(x[i].y));
+  }
 }
 
 // Order of floats as unsigned numbers: -0 and 0 are one, every NaN is the largest.
@@ -230,6 +318,20 @@ __device__ __forceinline__ void cluster_barrier() {
 // A part of a warp (or all of it): `size` lanes, a power of two.
 struct WarpTeam {
   int lane, size;
+  // `v`: a lane's sums of exponentials 2^((x - top) k) with its `top`.  After
+  // it top is the team's and v the team's sums with it; own: what takes the
+  // lane's exponentials there.
+  __device__ __forceinline__ float top(float m) {
+    if (size == 32) return warp_max(m);
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+      if (size > o) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  }
+  template <int Q> __device__ __forceinline__ float join(float (&v)[Q], float& top, float) {
+    sum(v);
+    return 1.f;
+  }
   template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -253,6 +355,38 @@ struct BlockTeam {
   int all;  // warps
   float* part;
   uint32_t turn;
+
+  __device__ __forceinline__ float top(float m) { return warp_max(m); }
+  // As WarpTeam's, where `top` was the warp's.
+  template <int Q> __device__ __forceinline__ float join(float (&v)[Q], float& top, float k) {
+    static_assert(!CLUSTER && (Q == 1 || Q == 2), "one or two sums, and the maxima");
+    constexpr int G = 32 / Q;
+    const int l = threadIdx.x & 31, q = l / G, c = l % G;
+    float x = v[0];
+    if (Q == 2) {
+      const bool hi = l & 16;
+      x = hi ? v[Q - 1] : v[0];
+      x += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[Q - 1], 16);
+    }
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    float* p = part + 4 * kWarps * turn;
+    turn ^= 1;
+    if (c == 0) {
+      p[q * kWarps + (threadIdx.x >> 5)] = x;
+      if (q == 0) p[2 * kWarps + (threadIdx.x >> 5)] = top;
+    }
+    __syncthreads();
+    const float mine = top, there = c < all ? p[2 * kWarps + c] : -INFINITY;
+    top = warp_max(there);
+    const float low = top == -INFINITY ? 0.f : top;
+    x = c < all ? p[q * kWarps + c] * ex2((there - low) * k) : 0.f;
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+    for (int i = 0; i < Q; ++i) v[i] = Q == 1 ? x : __shfl_sync(0xffffffffu, x, i * G);
+    return ex2((mine - low) * k);
+  }
 
   __device__ __forceinline__ explicit BlockTeam(float* p) : part(p), turn(0) {
     if (CLUSTER) {
