@@ -18,6 +18,10 @@ using namespace gate;
 
 constexpr int kWarpThreads = 256;
 constexpr int kWarpK = 512;
+#ifndef PER16
+#define PER16 64
+#endif
+constexpr int kPer16 = PER16;
 constexpr int kBlockThreads = 512;
 constexpr int kBlockK = 16 * kBlockThreads;
 constexpr int kMaxGrid = 8 * kSms;
@@ -45,27 +49,32 @@ struct Entries {
   float old[MT];  // what the gradient is added to
   float q[MT];
 
-  template <typename T>
-  __device__ __forceinline__ void load(const Args& a, int64_t n, bool on, int lane, int size) {
-    const T* L = (const T*)a.L + n * a.K;
-    const T* dL = (const T*)a.dL + n * a.K;
+  // Row n's ids and values as they are, for `take` a row later.
+  __device__ __forceinline__ void fetch(const Args& a, int64_t n, int lane, int size) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int t = i * size + lane;
       id[i] = -1;
-      float v = 0.f;
-      if (on && t < a.m) {
+      b[i] = 0.f;
+      if (n < a.N && t < a.m) {
         id[i] = a.ids[n * a.m + t];
-        v = a.values[n * a.m + t];
+        b[i] = a.values[n * a.m + t];
       }
-      if ((uint32_t)id[i] >= (uint32_t)a.K) id[i] = -1;
-      b[i] = (a.gammas ? log2f(v) : v * kLog2E) * a.inv;
-      if (id[i] < 0 || b[i] == -INFINITY) id[i] = -1, b[i] = -INFINITY;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void take(const Args& a, const T* L, const T* dL, bool on) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (!on || (uint32_t)id[i] >= (uint32_t)a.K) id[i] = -1;
       x[i] = old[i] = 0.f;
       if (id[i] >= 0) {
         x[i] = to_f(L[id[i]]);
         if (a.add) old[i] = to_f(dL[id[i]]);
       }
+      b[i] = (a.gammas ? lg2(b[i]) : b[i] * kLog2E) * a.inv;
+      if (id[i] < 0) b[i] = -INFINITY;
+      if (b[i] == -INFINITY) id[i] = -1;
     }
   }
   // q, and whether there is an entry.
@@ -83,9 +92,10 @@ struct Entries {
       s[0] += q[i];
     }
     team.sum(s);
-    logsum = log2f(s[0]);
+    logsum = lg2(s[0]);
+    const float r = some ? rcp(s[0]) : 0.f;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) q[i] = some ? q[i] / s[0] : 0.f;
+    for (int i = 0; i < MT; ++i) q[i] *= r;
     return some;
   }
   // sum_t q_t (b_t - (x_t - top) k)
@@ -99,7 +109,7 @@ struct Entries {
   }
   // The gradient's elements at the entries, c (p - q) with the q of every entry
   // of that element, into q; the id stays with the first of them alone.
-  __device__ __forceinline__ void gradient(WarpTeam team, int m, float c, float top, float k, float sum) {
+  __device__ __forceinline__ void gradient(WarpTeam team, int m, float c, float top, float k, float rsum) {
     const int l = threadIdx.x & 31, base = l & ~(team.size - 1);
     float w[MT];
     bool first[MT];
@@ -130,8 +140,7 @@ struct Entries {
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const float p = sum == 0.f ? 0.f : ex2((x[i] - top) * k) / sum;
-      q[i] = fmaf(c, p - w[i], old[i]);
+      q[i] = fmaf(c, ex2((x[i] - top) * k) * rsum - w[i], old[i]);
       if (!first[i]) id[i] = -1;
     }
   }
@@ -153,8 +162,11 @@ __device__ __forceinline__ void store_total(const Args& a, double total) {
 __device__ __forceinline__ float row_loss(const Args& a, float w, float divergence, float logsum, float sum) {
   // a row with no student at all is infinitely far
   if (sum == 0.f) return w * INFINITY;
-  return w * a.T * a.T * kLn2 * (divergence - logsum + log2f(sum));
+  return w * a.T * a.T * kLn2 * (divergence - logsum + lg2(sum));
 }
+
+// 1 / the sum; no student: p = 0
+__device__ __forceinline__ float rsum_of(float sum) { return sum == 0.f ? 0.f : rcp(sum); }
 
 template <typename T, int V, int NV, int MT>
 __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int size) {
@@ -169,17 +181,19 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
   int64_t n = warp * per + l / size;
   Feed<T, V, NV, 1, WeightedRows> feed;
   feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, size, nv, none, WeightedRows{a.weights});
+  Entries<MT> ahead;
+  ahead.fetch(a, n, team.lane, size);
+  const T* L = (const T*)a.L + n * K;
+  T* d = (T*)a.dL + n * K;
   double total = 0.0;
-  for (int64_t end = warp * per; end < a.N; n += stride, end += stride) {
+  for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
     Row<T, V, NV> row[1], old;
     const bool on = feed.next(row);
     const float w = on ? (a.weights ? a.weights[n] : 1.f) : 0.f;
-    Entries<MT> e;
-    e.template load<T>(a, n, on, team.lane, size);
-    T* d = (T*)a.dL + n * K;
+    Entries<MT> e = ahead;
+    e.take(a, L, d, on);
+    ahead.fetch(a, n + stride, team.lane, size);
     if (a.add && n < a.N) old.read(d, team.lane, size, nv);
-    float logsum;
-    const bool some = e.normalise(team, logsum);
     float top = team.top(lane_max(row[0]));
     if (top == -INFINITY) top = 0.f;
     float2 x[P];
@@ -190,30 +204,30 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
     for (int i = 1; i < P; ++i) t = add2(t, x[i]);
     float s[1] = {t.x + t.y};
     team.sum(s);
+    float logsum;
+    const bool some = e.normalise(team, logsum) && on;
     const float divergence = e.divergence(team, top, k);
     if (team.lane == 0 && n < a.N) {
-      const float r = on && some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
+      const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
       a.rows[n] = r;
       total += r;
     }
     if (!a.dL) continue;
-    const float c = a.scale * w * a.T;
-    e.gradient(team, a.m, c, top, k, s[0]);
-    const float f = s[0] == 0.f ? 0.f : c / s[0];
-    if (n < a.N && (!a.add || (on && some))) {
+    const float c = a.scale * w * a.T, rsum = rsum_of(s[0]);
+    e.gradient(team, a.m, c, top, k, rsum);
+    if (n < a.N && (!a.add || some)) {
+      const float2 f = both(c * rsum);
       if (a.add) {
         float2 o[P];
         old.get(o);
 #pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = fma2(x[i], both(f), o[i]);
-      } else if (on && some) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], both(f));
+        for (int i = 0; i < P; ++i) x[i] = fma2(x[i], f, o[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = both(0.f);
+        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], f);
       }
       row[0].set(x);
+      if (!some) row[0].fill(from_f<T>(0.f));
       row[0].store(d, team.lane, size, nv);
     }
     __syncwarp();
@@ -222,234 +236,308 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
   store_total(a, total);
 }
 
-// The first warp has the entries.
+// The last warp has the entries, and no part of the row: what it waits for and
+// works out goes beside the others' work.  It puts a row's elements right after
+// the next row's barrier, before which the others have stored the row.
 template <typename T, int V, int NV, int MT>
-__global__ void __launch_bounds__(kBlockThreads) distill_block_kernel(Args a, int) {
+__global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float part[BlockTeam<false>::kWords];
   __shared__ int some_s[2];
   constexpr int P = V * NV / 2;
   const int K = a.K, nv = K / V;
-  const bool teacher = threadIdx.x < 32;
-  BlockTeam<false> team(part);
-  const WarpTeam first{(int)threadIdx.x & 31, 32};
+  BlockTeam<false> team(part, blockDim.x - 32);
   const float k = kLog2E * a.inv;
   const T none = from_f<T>(-INFINITY);
-  Feed<T, V, NV, 1, WeightedRows> feed;
-  feed.start(smem, {(const T*)a.L}, blockIdx.x, gridDim.x, a.N, K, team.lane, team.size, nv, none,
-             WeightedRows{a.weights});
-  double total = 0.0;
-  Entries<MT> late;  // elements to be put right once the row before is stored
-#pragma unroll
-  for (int i = 0; i < MT; ++i) late.id[i] = -1, late.q[i] = 0.f;
   uint32_t turn = 0;
-  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
-    Row<T, V, NV> row[1], old;
-    const bool on = feed.next(row);
-    const float w = on ? (a.weights ? a.weights[n] : 1.f) : 0.f;
-    T* d = (T*)a.dL + n * K;
-    Entries<MT> e;
-    float logsum = 0.f;
-    if (teacher) e.template load<T>(a, n, on, first.lane, 32);
-    if (a.add) old.read(d, team.lane, team.size, nv);
-    float top = team.top(lane_max(row[0]));
-    const float low = top == -INFINITY ? 0.f : top;
-    float2 x[P];
-    row[0].get(x);
-    exponentials(x, low, k);
-    float2 t = x[0];
+  double total = 0.0;
+  const int64_t step = (int64_t)gridDim.x * K;
+  T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
+  if ((int)threadIdx.x >= team.size) {
+    const WarpTeam warp{(int)threadIdx.x & 31, 32};
+    const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
+    Entries<MT> ahead, late;  // of the next row and of the last one
+    ahead.fetch(a, blockIdx.x, warp.lane, 32);
 #pragma unroll
-    for (int i = 1; i < P; ++i) t = add2(t, x[i]);
-    float s[1] = {t.x + t.y};
-    if (teacher) {
-      const bool some = e.normalise(first, logsum);
-      if (threadIdx.x == 0) some_s[turn] = some;
-    }
-    const float own = team.join(s, top, k);
-    if (top == -INFINITY) top = 0.f;
-    const bool some = on && some_s[turn];
-    const float c = a.scale * w * a.T;
-    if (teacher) {
-      if (a.dL) late.store(d - (int64_t)gridDim.x * K);  // that row was stored before the barrier
-      const float divergence = e.divergence(first, top, k);
-      if (threadIdx.x == 0) {
+    for (int i = 0; i < MT; ++i) late.id[i] = -1;
+    float wn = !a.weights || blockIdx.x >= a.N ? 1.f : a.weights[blockIdx.x];
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
+      const float w = wn;
+      Entries<MT> e = ahead;
+      e.take(a, L, d, w != 0.f);
+      ahead.fetch(a, n + gridDim.x, warp.lane, 32);
+      if (a.weights && n + gridDim.x < a.N) wn = a.weights[n + gridDim.x];
+      float logsum, top, s[1];
+      const bool some = e.normalise(warp, logsum);
+      if (warp.lane == 0) some_s[turn] = some;
+      __syncthreads();
+      if (a.dL) late.store(d - step);
+      team.hear(s, top, 0.f, k);
+      const float divergence = e.divergence(warp, top, k);
+      if (warp.lane == 0) {
         const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
         a.rows[n] = r;
         total += r;
       }
       if (a.dL) {
-        e.gradient(first, a.m, c, top, k, s[0]);
+        e.gradient(warp, a.m, a.scale * w * a.T, top, k, rsum_of(s[0]));
         late = e;
       }
     }
-    if (!a.dL || (a.add && !some)) continue;
-    const float f = s[0] == 0.f ? 0.f : c * own / s[0];
-    if (a.add) {
-      float2 o[P];
-      old.get(o);
+    __syncthreads();
+    if (a.dL) late.store(d - step);
+  } else {
+    Feed<T, V, NV, 1, WeightedRows> feed;
+    feed.start(smem, {(const T*)a.L}, blockIdx.x, gridDim.x, a.N, K, team.lane, team.size, nv, none,
+               WeightedRows{a.weights});
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, d += step, turn ^= 1) {
+      Row<T, V, NV> row[1], old;
+      const bool on = feed.next(row);
+      const float w = on ? (a.weights ? a.weights[n] : 1.f) : 0.f;
+      if (a.add) old.read(d, team.lane, team.size, nv);
+      const float mine = team.top(lane_max(row[0])), low = mine == -INFINITY ? 0.f : mine;
+      float2 x[P];
+      row[0].get(x);
+      exponentials(x, low, k);
+      float2 t = x[0];
 #pragma unroll
-      for (int i = 0; i < P; ++i) x[i] = fma2(x[i], both(f), o[i]);
-    } else if (some) {
+      for (int i = 1; i < P; ++i) t = add2(t, x[i]);
+      float s[1] = {t.x + t.y}, top;
+      team.tell(s, mine);
+      __syncthreads();
+      if (!a.dL) {
+        team.turn ^= 1;
+        continue;
+      }
+      const bool some = on && some_s[turn];
+      const float own = team.hear(s, top, mine, k);
+      if (a.add && !some) continue;
+      const float2 f = both(a.scale * w * a.T * own * rsum_of(s[0]));
+      if (a.add) {
+        float2 o[P];
+        old.get(o);
 #pragma unroll
-      for (int i = 0; i < P; ++i) x[i] = mul2(x[i], both(f));
-    } else {
+        for (int i = 0; i < P; ++i) x[i] = fma2(x[i], f, o[i]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < P; ++i) x[i] = both(0.f);
+        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], f);
+      }
+      row[0].set(x);
+      if (!some) row[0].fill(from_f<T>(0.f));
+      row[0].store(d, team.lane, team.size, nv);
     }
-    row[0].set(x);
-    row[0].store(d, team.lane, team.size, nv);
-  }
-  __syncthreads();
-  if (teacher && a.dL && blockIdx.x < a.N) {
-    const int64_t last = blockIdx.x + (a.N - 1 - blockIdx.x) / gridDim.x * gridDim.x;
-    late.store((T*)a.dL + last * K);
+    __syncthreads();
   }
   store_total(a, total);
 }
 
-// Rows that no block holds, at any address: 16-byte vectors between the row's
-// first and last boundary, single elements before and behind.
+// Rows that no block holds, at any address.  The 16-byte vectors between a row's
+// first and last boundary go through shared memory as a Feed's do, kDepth copies
+// a thread ahead, and without a break from the first reading of a row to the
+// second (out of L2) and on to the next row; the elements before and behind,
+// fewer than a vector, belong to one thread each.
+constexpr int kStreamThreads = 512;
+constexpr int kStreamVectors = 2;  // a copy
+constexpr int kDepth = 4;
+
 template <typename T>
-struct Cover {
-  static constexpr int V = kWide<T>;
-  const T* row;
-  int shift, K, nv;  // elements before the row in its first vector; vectors
-  __device__ __forceinline__ Cover(const T* p, int K_) : row(p), K(K_) {
-    shift = (int)((uintptr_t)p / sizeof(T) % V);
-    nv = (shift + K + V - 1) / V;
+struct Stream {
+  static constexpr int V = kWide<T>, U = kStreamVectors;
+  const T* L;
+  int64_t n, N, stride, row_step;
+  int K, passes;
+  // the copy to be asked for next
+  const T* body;
+  int nv, at, pass;
+  uint32_t slot_in, slot_out;
+  char* slot;
+  int threads;
+
+  // The row's vectors begin `head` elements in; nv of them.
+  static __device__ __forceinline__ int head_of(const T* p, int K) {
+    const int h = (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T);
+    return h < K ? h : K;
   }
-  __device__ __forceinline__ bool whole(int v) const { return v * V >= shift && (v + 1) * V <= shift + K; }
-  // Vector v of `p`, a row as this one but for its address.
-  __device__ __forceinline__ void load(Vec<T, V>& x, const T* p, int v, T none, bool same = true) const {
-    if (same && whole(v)) {
-      x = *reinterpret_cast<const Vec<T, V>*>(p + v * V - shift);
-    } else {
+  __device__ __forceinline__ void row() {
+    const int h = head_of(L, K);
+    body = L + h;
+    nv = (K - h) / V;
+  }
+  __device__ __forceinline__ void start(char* smem, const T* L_, int64_t n_, int64_t stride_, int64_t N_, int K_, int passes_,
+                                        int threads_) {
+    L = L_ + n_ * K_, n = n_, N = N_, stride = stride_, row_step = stride_ * K_, K = K_, passes = passes_;
+    threads = threads_;
+    at = (int)threadIdx.x, pass = 0, slot_in = slot_out = 0;
+    slot = smem + threadIdx.x * 16;
+    row();
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int c = v * V + e - shift;
-        x.v[e] = c >= 0 && c < K ? p[c] : none;
+    for (int i = 0; i < kDepth - 1; ++i) ask();
+  }
+  __device__ __forceinline__ void ask() {
+    if (n < N) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (at + u * threads < nv)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(
+                           slot + (size_t)(slot_in * U + u) * threads * 16)),
+                       "l"(body + (int64_t)(at + u * threads) * V)
+                       : "memory");
+      at += U * threads;
+      if (at - (int)threadIdx.x >= nv) {
+        at = (int)threadIdx.x;
+        if (++pass == passes) {
+          pass = 0;
+          n += stride;
+          L += row_step;
+          if (n < N) row();
+        }
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    slot_in = slot_in == kDepth - 1 ? 0 : slot_in + 1;
   }
-  __device__ __forceinline__ void store(const Vec<T, V>& x, T* p, int v, bool same) const {
-    if (same && whole(v)) {
-      *reinterpret_cast<Vec<T, V>*>(p + v * V - shift) = x;
-    } else {
+  __device__ __forceinline__ void next(Row<T, V, U>& x) {
+    ask();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int c = v * V + e - shift;
-        if (c >= 0 && c < K) p[c] = x.v[e];
-      }
-    }
+    for (int u = 0; u < U; ++u)
+      x.r[u] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)(slot_out * U + u) * threads * 16);
+    slot_out = slot_out == kDepth - 1 ? 0 : slot_out + 1;
   }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kBlockThreads) distill_stream_kernel(Args a, int) {
+__global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(Args a) {
+  extern __shared__ __align__(16) char smem[];
   __shared__ float part[BlockTeam<false>::kWords];
-  __shared__ int some_s;
-  constexpr int V = kWide<T>, U = 4, MT = 2;
+  __shared__ int some_s[2];
+  constexpr int V = kWide<T>, U = kStreamVectors, P = U * V / 2, MT = 2;
   const int K = a.K;
-  const bool teacher = threadIdx.x < 32;
-  BlockTeam<false> team(part);
-  const WarpTeam first{(int)threadIdx.x & 31, 32};
+  BlockTeam<false> team(part, kStreamThreads);
   const float k = kLog2E * a.inv;
   const T none = from_f<T>(-INFINITY);
+  const int64_t step = (int64_t)gridDim.x * K;
+  const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
+  T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
+  uint32_t turn = 0;
   double total = 0.0;
-  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-    const float w = a.weights ? a.weights[n] : 1.f;
-    const bool on = w != 0.f;
-    const T* L = (const T*)a.L + n * K;
-    T* d = (T*)a.dL + n * K;
-    Entries<MT> e;
-    float logsum = 0.f;
-    if (teacher) {
-      e.template load<T>(a, n, on, first.lane, 32);
-      const bool some = e.normalise(first, logsum);
-      if (threadIdx.x == 0) some_s = some;
-    }
-    const Cover<T> row(L, K);
-    float top = -INFINITY;
-    float2 sum = both(0.f);
-    if (on)
-      for (int v0 = threadIdx.x; v0 < row.nv; v0 += U * kBlockThreads) {
-        Row<T, V, U> x;
+  if ((int)threadIdx.x >= kStreamThreads) {
+    const WarpTeam warp{(int)threadIdx.x & 31, 32};
+    Entries<MT> ahead, late;
+    ahead.fetch(a, blockIdx.x, warp.lane, 32);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int v = v0 + u * kBlockThreads;
-          if (v < row.nv) {
-            row.load(x.r[u], L, v, none);
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x.r[u].v[i] = none;
-          }
-        }
-        const float m = max_nan(top, lane_max(x));
-        if (m == -INFINITY) continue;
-        sum = mul2(sum, both(ex2((top - m) * k)));
-        top = m;
-        float2 f[U * V / 2];
-        x.get(f);
-        exponentials(f, top, k);
-#pragma unroll
-        for (int i = 0; i < U * V / 2; ++i) sum = add2(sum, f[i]);
-      }
-    // the warp's, then the block's
-    float s[1] = {sum.x + sum.y};
-    const float lane_top = top;
-    top = warp_max(top);
-    if (lane_top != -INFINITY) s[0] *= ex2((lane_top - top) * k);
-    team.join(s, top, k);
-    if (top == -INFINITY) top = 0.f;
-    const bool some = on && some_s;
-    const float c = a.scale * w * a.T;
-    if (teacher) {
-      const float divergence = e.divergence(first, top, k);
-      if (threadIdx.x == 0) {
+    for (int i = 0; i < MT; ++i) late.id[i] = -1;
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
+      const float w = a.weights ? a.weights[n] : 1.f;
+      Entries<MT> e = ahead;
+      e.take(a, L, d, w != 0.f);
+      ahead.fetch(a, n + gridDim.x, warp.lane, 32);
+      float logsum, top, s[1];
+      const bool some = e.normalise(warp, logsum);
+      if (warp.lane == 0) some_s[turn] = some;
+      __syncthreads();
+      if (a.dL) late.store(d - step);
+      team.hear(s, top, 0.f, k);
+      const float divergence = e.divergence(warp, top, k);
+      if (warp.lane == 0) {
         const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
         a.rows[n] = r;
         total += r;
       }
-      if (a.dL) e.gradient(first, a.m, c, top, k, s[0]);
+      if (a.dL) {
+        e.gradient(warp, a.m, a.scale * w * a.T, top, k, rsum_of(s[0]));
+        late = e;
+      }
     }
-    if (a.dL && (!a.add || some)) {
-      const float f = s[0] == 0.f ? 0.f : c / s[0];
+    __syncthreads();
+    if (a.dL) late.store(d - step);
+  } else {
+    const int t = threadIdx.x;
+    Stream<T> feed;
+    feed.start(smem, (const T*)a.L, blockIdx.x, gridDim.x, a.N, K, a.dL ? 2 : 1, kStreamThreads);
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
+      const float w = a.weights ? a.weights[n] : 1.f;
+      const int head = Stream<T>::head_of(L, K), nv = (K - head) / V, tail = head + nv * V;
+      const int turns = (nv + U * kStreamThreads - 1) / (U * kStreamThreads);
+      // the elements outside the vectors, one a thread
+      const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;
+      const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
+      float top = xe;
+      float2 sum = make_float2(xe == -INFINITY ? 0.f : ex2((xe - xe) * k), 0.f);
+      for (int i = 0; i < turns; ++i) {
+        Row<T, V, U> x;
+        feed.next(x);
+        const int v0 = i * U * kStreamThreads + t;
+        if (i == turns - 1) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * kStreamThreads >= nv)
+#pragma unroll
+              for (int e = 0; e < V; ++e) x.r[u].v[e] = none;
+        }
+        const float m = max_nan(top, lane_max(x));
+        if (m != top) {
+          if (m != -INFINITY) sum = mul2(sum, both(ex2((top - m) * k)));
+          top = m;
+        }
+        float2 f[P];
+        x.get(f);
+        exponentials(f, top == -INFINITY ? 0.f : top, k);
+#pragma unroll
+        for (int j = 0; j < P; ++j) sum = add2(sum, f[j]);
+      }
+      // the warp's, then the block's
+      const float mine = warp_max(top);
+      float s[1] = {top == -INFINITY ? 0.f : (sum.x + sum.y) * ex2((top - mine) * k)};
+      team.tell(s, mine);
+      __syncthreads();
+      if (!a.dL) {
+        team.turn ^= 1;
+        continue;
+      }
+      const bool some = w != 0.f && some_s[turn];
+      team.hear(s, top, mine, k);
+      const float c = some ? a.scale * w * a.T * rsum_of(s[0]) : 0.f;
+      const float2 f = both(c);
       const bool same = (((uintptr_t)L ^ (uintptr_t)d) & 15) == 0;
-      // backwards: what was read last is nearest
-      const int turns = (row.nv + U * kBlockThreads - 1) / (U * kBlockThreads);
-      for (int i = turns - 1; i >= 0; --i) {
-        const int v0 = i * U * kBlockThreads + threadIdx.x;
-        Row<T, V, U> x, o;
+      if (edge >= 0 && (some || !a.add)) {
+        float y = some ? ex2((xe - top) * k) * c : 0.f;
+        if (a.add) y += to_f(d[edge]);
+        d[edge] = from_f<T>(y);
+      }
+      for (int i = 0; i < turns; ++i) {
+        Row<T, V, U> x;
+        feed.next(x);
+        float2 y[P];
+        x.get(y);
+        exponentials(y, top, k);
+#pragma unroll
+        for (int j = 0; j < P; ++j) y[j] = some ? mul2(y[j], f) : both(0.f);
+        const int v0 = i * U * kStreamThreads + t;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int v = v0 + u * kBlockThreads;
-          if (v < row.nv) {
-            if (some) row.load(x.r[u], L, v, none);
-            if (a.add) row.load(o.r[u], d, v, none, same);
+          const int v = v0 + u * kStreamThreads;
+          if (v >= nv || (a.add && !some)) continue;
+          T* out = d + head + (int64_t)v * V;
+          Vec<T, V> o;
+          if (a.add) {
+            if (same) o = *reinterpret_cast<const Vec<T, V>*>(out);
+            else
+#pragma unroll
+              for (int e = 0; e < V; ++e) o.v[e] = out[e];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) y[u * V / 2 + e] = add2(y[u * V / 2 + e], to_f2(o.v[2 * e], o.v[2 * e + 1]));
           }
-        }
-        float2 y[U * V / 2];
-        if (some) {
-          x.get(y);
-          exponentials(y, top, k);
-          float2 z[U * V / 2];
-          o.get(z);
 #pragma unroll
-          for (int j = 0; j < U * V / 2; ++j) y[j] = a.add ? fma2(y[j], both(f), z[j]) : mul2(y[j], both(f));
-        } else {
+          for (int e = 0; e < V / 2; ++e) from_f2(y[u * V / 2 + e], o.v[2 * e], o.v[2 * e + 1]);
+          if (same) *reinterpret_cast<Vec<T, V>*>(out) = o;
+          else
 #pragma unroll
-          for (int j = 0; j < U * V / 2; ++j) y[j] = both(0.f);
-        }
-        x.set(y);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int v = v0 + u * kBlockThreads;
-          if (v < row.nv) row.store(x.r[u], d, v, same);
+            for (int e = 0; e < V; ++e) out[e] = o.v[e];
         }
       }
     }
     __syncthreads();
-    if (teacher && a.dL) e.store(d);
   }
   store_total(a, total);
 }
@@ -469,19 +557,15 @@ template <typename T, int V, int NV, int MT>
 bool launch_block(const Args& a, int threads, int64_t grid, cudaStream_t s) {
   static std::atomic<uint64_t> done;
   using F = Feed<T, V, NV, 1, WeightedRows>;
-  if (F::bytes(threads) > 48 * 1024 - 4096 &&
-      !allow_smem((const void*)distill_block_kernel<T, V, NV, MT>, F::bytes(kBlockThreads), done))
-    return false;
-  distill_block_kernel<T, V, NV, MT><<<(unsigned)grid, threads, F::bytes(threads), s>>>(a, 0);
+  if (!allow_smem((const void*)distill_block_kernel<T, V, NV, MT>, F::bytes(kBlockThreads + 32), done)) return false;
+  distill_block_kernel<T, V, NV, MT><<<(unsigned)grid, threads, F::bytes(threads), s>>>(a);
   return true;
 }
 template <typename T, int V, int NV, int MT>
 bool launch_warp(const Args& a, int size, int64_t grid, cudaStream_t s) {
   static std::atomic<uint64_t> done;
   using F = Feed<T, V, NV, 1, WeightedRows>;
-  if (F::bytes(kWarpThreads) > 48 * 1024 - 4096 &&
-      !allow_smem((const void*)distill_warp_kernel<T, V, NV, MT>, F::bytes(kWarpThreads), done))
-    return false;
+  if (!allow_smem((const void*)distill_warp_kernel<T, V, NV, MT>, F::bytes(kWarpThreads), done)) return false;
   distill_warp_kernel<T, V, NV, MT><<<(unsigned)grid, kWarpThreads, F::bytes(kWarpThreads), s>>>(a, size);
   return true;
 }
@@ -491,19 +575,22 @@ template <typename T, int V>
 int64_t launch(const Args& a, cudaStream_t s) {
   const int K = a.K, m = a.m;
   if (K <= kWarpK) {
-    const int per = K <= (V == 1 ? 256 : 8) ? 8 : 16;
+    const int per = V == 1 ? (K <= 256 ? 8 : 16) : K <= 8 ? 8 : K <= kPer16 ? 16 : 32;
     int size = 1;
     while (size < 32 && size * (V == 1 ? 1 : per) < K) size <<= 1;
     while (size * 8 < m) size <<= 1;  // at most eight entries a lane
     const int64_t rows = kWarpThreads / size, need = (a.N + rows - 1) / rows;
     const int64_t grid = need < 1 ? 1 : need < 4 * kSms ? need : 4 * kSms;
-    const bool ok = per == 8 ? (m <= size ? launch_warp<T, V, 8 / V, 1>(a, size, grid, s)
-                                          : launch_warp<T, V, 8 / V, 8>(a, size, grid, s))
-                             : (m <= size ? launch_warp<T, V, 16 / V, 1>(a, size, grid, s)
-                                          : launch_warp<T, V, 16 / V, 8>(a, size, grid, s));
+    bool ok;
+    if (per == 8)
+      ok = m <= size ? launch_warp<T, V, 8 / V, 1>(a, size, grid, s) : launch_warp<T, V, 8 / V, 8>(a, size, grid, s);
+    else if (per == 16)
+      ok = m <= size ? launch_warp<T, V, 16 / V, 1>(a, size, grid, s) : launch_warp<T, V, 16 / V, 8>(a, size, grid, s);
+    else if constexpr (V > 1)
+      ok = m <= size ? launch_warp<T, V, 32 / V, 1>(a, size, grid, s) : launch_warp<T, V, 32 / V, 8>(a, size, grid, s);
     return ok ? grid : 0;
   }
-  const int threads = ((K + 15) / 16 + 31) / 32 * 32;
+  const int threads = ((K + 15) / 16 + 31) / 32 * 32 + 32;
   const int resident = 1024 / threads < 8 ? 1024 / threads : 8;
   const int64_t grid = a.N < 1 ? 1 : a.N < (int64_t)resident * kSms ? a.N : (int64_t)resident * kSms;
   const bool ok = m <= 32 ? launch_block<T, V, 16 / V, 1>(a, threads, grid, s)
@@ -514,8 +601,11 @@ int64_t launch(const Args& a, cudaStream_t s) {
 template <typename T>
 int64_t launch_typed(const Args& a, cudaStream_t s) {
   if (a.K > kBlockK) {
+    static std::atomic<uint64_t> done;
+    const size_t smem = (size_t)kDepth * kStreamVectors * kStreamThreads * 16;
+    if (!allow_smem((const void*)distill_stream_kernel<T>, smem, done)) return 0;
     const int64_t grid = a.N < 1 ? 1 : a.N < 2 * kSms ? a.N : 2 * kSms;
-    distill_stream_kernel<T><<<(unsigned)grid, kBlockThreads, 0, s>>>(a, 0);
+    distill_stream_kernel<T><<<(unsigned)grid, kStreamThreads + 32, smem, s>>>(a);
     return grid;
   }
   return wide<T>(a.K, (const char*)a.L, (const char*)a.dL) ? launch<T, kWide<T>>(a, s) : launch<T, 1>(a, s);

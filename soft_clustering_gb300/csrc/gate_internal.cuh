@@ -221,6 +221,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 1 / x for x of 1 to 2^20 (or NaN) to an ulp, and log2 x to 2^-21.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The larger; NaN if either is.
@@ -318,19 +329,13 @@ __device__ __forceinline__ void cluster_barrier() {
 // A part of a warp (or all of it): `size` lanes, a power of two.
 struct WarpTeam {
   int lane, size;
-  // `v`: a lane's sums of exponentials 2^((x - top) k) with its `top`.  After
-  // it top is the team's and v the team's sums with it; own: what takes the
-  // lane's exponentials there.
+  // The largest of the team's.
   __device__ __forceinline__ float top(float m) {
     if (size == 32) return warp_max(m);
 #pragma unroll
     for (int o = 8; o; o >>= 1)
       if (size > o) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
-  }
-  template <int Q> __device__ __forceinline__ float join(float (&v)[Q], float& top, float) {
-    sum(v);
-    return 1.f;
   }
   template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
 #pragma unroll
@@ -356,9 +361,21 @@ struct BlockTeam {
   float* part;
   uint32_t turn;
 
+  // `threads` of each block, from the first on; the others may listen.
+  __device__ __forceinline__ BlockTeam(float* p, int threads) : part(p), turn(0) {
+    if (CLUSTER) {
+      lane = (int)(cluster_rank() * blockDim.x + threadIdx.x);
+      size = (int)cluster_blocks() * threads;
+    } else {
+      lane = (int)threadIdx.x;
+      size = threads;
+    }
+    all = size >> 5;
+  }
   __device__ __forceinline__ float top(float m) { return warp_max(m); }
-  // As WarpTeam's, where `top` was the warp's.
-  template <int Q> __device__ __forceinline__ float join(float (&v)[Q], float& top, float k) {
+  // As WarpTeam's, where `top` was the warp's: what a warp tells, and what every
+  // warp, of the team or not, makes of it after the block's barrier.
+  template <int Q> __device__ __forceinline__ void tell(const float (&v)[Q], float top) {
     static_assert(!CLUSTER && (Q == 1 || Q == 2), "one or two sums, and the maxima");
     constexpr int G = 32 / Q;
     const int l = threadIdx.x & 31, q = l / G, c = l % G;
@@ -371,32 +388,27 @@ struct BlockTeam {
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     float* p = part + 4 * kWarps * turn;
-    turn ^= 1;
     if (c == 0) {
       p[q * kWarps + (threadIdx.x >> 5)] = x;
       if (q == 0) p[2 * kWarps + (threadIdx.x >> 5)] = top;
     }
-    __syncthreads();
-    const float mine = top, there = c < all ? p[2 * kWarps + c] : -INFINITY;
+  }
+  // The team's top and sums with it (0 for -inf); what takes a warp of top
+  // `mine` there.
+  template <int Q> __device__ __forceinline__ float hear(float (&v)[Q], float& top, float mine, float k) {
+    constexpr int G = 32 / Q;
+    const int l = threadIdx.x & 31, q = l / G, c = l % G;
+    const float* p = part + 4 * kWarps * turn;
+    turn ^= 1;
+    const float there = c < all ? p[2 * kWarps + c] : -INFINITY;
     top = warp_max(there);
-    const float low = top == -INFINITY ? 0.f : top;
-    x = c < all ? p[q * kWarps + c] * ex2((there - low) * k) : 0.f;
+    if (top == -INFINITY) top = 0.f;
+    float x = c < all ? p[q * kWarps + c] * ex2((there - top) * k) : 0.f;
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
 #pragma unroll
     for (int i = 0; i < Q; ++i) v[i] = Q == 1 ? x : __shfl_sync(0xffffffffu, x, i * G);
-    return ex2((mine - low) * k);
-  }
-
-  __device__ __forceinline__ explicit BlockTeam(float* p) : part(p), turn(0) {
-    if (CLUSTER) {
-      lane = (int)(cluster_rank() * blockDim.x + threadIdx.x);
-      size = (int)(cluster_blocks() * blockDim.x);
-    } else {
-      lane = (int)threadIdx.x;
-      size = (int)blockDim.x;
-    }
-    all = size >> 5;
+    return ex2((mine - top) * k);
   }
   template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
     static_assert(Q == 1 || Q == 2 || Q == 4, "a power of two");

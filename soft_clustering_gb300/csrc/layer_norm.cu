@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kBlockThreads) norm_block_kernel(Args a, int b
   __shared__ float part[BlockTeam<CLUSTER>::kWords];
   const uint32_t c = blockIdx.x / blocks;
   if (CLUSTER) cluster_barrier();  // every block of the cluster runs
-  norm_rows<T, W, V, NV>(a, smem, BlockTeam<CLUSTER>(part), c, gridDim.x / blocks, c);
+  norm_rows<T, W, V, NV>(a, smem, BlockTeam<CLUSTER>(part, blockDim.x), c, gridDim.x / blocks, c);
   if (CLUSTER) cluster_barrier();  // nothing is on its way to a block that has ended
 }
 
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kBlockThreads) norm_grad_block_kernel(Args a, 
   __shared__ float part[BlockTeam<CLUSTER>::kWords];
   float2 dw[E / 2], db[E / 2];
   const uint32_t at = blockIdx.x / blocks;
-  const BlockTeam<CLUSTER> team(part);
+  const BlockTeam<CLUSTER> team(part, blockDim.x);
   if (CLUSTER) cluster_barrier();  // every block of the cluster runs
   grad_rows<T, W, V, NV>(a, smem, team, at, gridDim.x / blocks, at, dw, db);
   if (a.sums) {
