@@ -4,11 +4,12 @@
 //   dL    = scale w T (p - q)
 //
 // One pass over the logits: a row stays in registers from its load to the
-// gradient's store.  Rows of up to 512 logits belong to lanes of a warp, of up
-// to 8192 to a block, 16 logits a thread; longer ones are streamed by a block
-// twice, the second time out of L2.  The gradient is stored as p alone first;
-// the lane that holds a teacher's entry puts that element right afterwards,
-// from the logit that it read with the entry.  All exponents are of base 2.
+// gradient's store, 32 logits a thread.  Rows of up to 1024 logits belong to
+// lanes of a warp, of up to 16384 to a block; longer ones are streamed by a block
+// twice, the second time out of L2.  Rows that do not start on 16 bytes are read
+// by single elements, 8 or 16 a thread, up to 8192.  The gradient is p alone
+// first; the lane that holds a teacher's entry puts that element right.  All
+// exponents are of base 2.
 #include "gate_internal.cuh"
 
 namespace gmm {
@@ -17,13 +18,7 @@ namespace {
 using namespace gate;
 
 constexpr int kWarpThreads = 256;
-constexpr int kWarpK = 512;
-#ifndef PER16
-#define PER16 64
-#endif
-constexpr int kPer16 = PER16;
 constexpr int kBlockThreads = 512;
-constexpr int kBlockK = 16 * kBlockThreads;
 constexpr int kMaxGrid = 8 * kSms;
 constexpr int kStudent = 1 << 18;
 
@@ -62,23 +57,34 @@ struct Entries {
       }
     }
   }
-  template <typename T>
-  __device__ __forceinline__ void take(const Args& a, const T* L, const T* dL, bool on) {
+  __device__ __forceinline__ void check(const Args& a, bool on) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (!on || (uint32_t)id[i] >= (uint32_t)a.K) id[i] = -1;
-      x[i] = old[i] = 0.f;
-      if (id[i] >= 0) {
-        x[i] = to_f(L[id[i]]);
-        if (a.add) old[i] = to_f(dL[id[i]]);
-      }
       b[i] = (a.gammas ? lg2(b[i]) : b[i] * kLog2E) * a.inv;
       if (id[i] < 0) b[i] = -INFINITY;
       if (b[i] == -INFINITY) id[i] = -1;
+      x[i] = old[i] = 0.f;
+    }
+  }
+  // The student's logits at the entries, from `at(id)`.
+  template <typename At>
+  __device__ __forceinline__ void gather(At at) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (id[i] >= 0) x[i] = to_f(*at(id[i]));
+  }
+  template <typename T>
+  __device__ __forceinline__ void gather_old(const Args& a, const T* dL) {
+    if (a.add) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        if (id[i] >= 0) old[i] = to_f(dL[id[i]]);
     }
   }
   // q, and whether there is an entry.
-  __device__ __forceinline__ bool normalise(WarpTeam team, float& logsum) {
+  template <typename Team>
+  __device__ __forceinline__ bool normalise(Team team, float& logsum) {
     float top = b[0];
 #pragma unroll
     for (int i = 1; i < MT; ++i) top = max_nan(top, b[i]);
@@ -98,28 +104,49 @@ struct Entries {
     for (int i = 0; i < MT; ++i) q[i] *= r;
     return some;
   }
-  // sum_t q_t (b_t - (x_t - top) k)
-  __device__ __forceinline__ float divergence(WarpTeam team, float top, float k) {
+  // sum_t q_t (b_t - (x_t k - base))
+  template <typename Team>
+  __device__ __forceinline__ float divergence(Team team, const Base& base, float k) {
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (id[i] >= 0 && q[i] != 0.f) s[0] += q[i] * (b[i] - (x[i] - top) * k);
+      if (id[i] >= 0 && q[i] != 0.f) s[0] += q[i] * (b[i] - base(x[i], k));
     team.sum(s);
     return s[0];
   }
+  // Whether two entries of some row in the warp are of one element.
+  template <typename Team>
+  __device__ __forceinline__ bool twice(Team team) const {
+    if (MT > 1) return true;
+    const int l = threadIdx.x & 31, group = l & ~(team.size - 1);
+    const unsigned same = __match_any_sync(0xffffffffu, id[0] >= 0 ? id[0] << 5 | group : -1 - l);
+    return __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+  }
+  // The same by the elements' own words, which hold nothing of use any more:
+  // of two lanes that write one, the one whose number is not there sees it.
+  template <typename At>
+  __device__ __forceinline__ bool twice_at(At at) const {
+    using W = unsigned short;
+    bool other = false;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (id[i] >= 0) *reinterpret_cast<W*>(at(id[i])) = (W)(i * 32 + (threadIdx.x & 31));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      if (id[i] >= 0) other |= *reinterpret_cast<const W*>(at(id[i])) != (W)(i * 32 + (threadIdx.x & 31));
+    return __any_sync(0xffffffffu, other);
+  }
   // The gradient's elements at the entries, c (p - q) with the q of every entry
   // of that element, into q; the id stays with the first of them alone.
-  __device__ __forceinline__ void gradient(WarpTeam team, int m, float c, float top, float k, float rsum) {
-    const int l = threadIdx.x & 31, base = l & ~(team.size - 1);
+  template <typename Team>
+  __device__ __forceinline__ void gradient(Team team, int m, float c, const Base& base, float k, float rsum,
+                                           bool twice) {
+    const int l = threadIdx.x & 31, group = l & ~(team.size - 1);
     float w[MT];
     bool first[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) w[i] = q[i], first[i] = true;
-    bool twice = MT > 1;
-    if (MT == 1) {
-      const unsigned same = __match_any_sync(0xffffffffu, id[0] >= 0 ? id[0] << 5 | base : -1 - l);
-      twice = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
-    }
     if (twice) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) w[i] = 0.f;
@@ -127,8 +154,8 @@ struct Entries {
       for (int j = 0; j < MT; ++j) {
         if (j * team.size >= m) break;
         for (int o = 0; o < team.size; ++o) {
-          const int id_o = __shfl_sync(0xffffffffu, id[j], base + o);
-          const float q_o = __shfl_sync(0xffffffffu, q[j], base + o);
+          const int id_o = __shfl_sync(0xffffffffu, id[j], group + o);
+          const float q_o = __shfl_sync(0xffffffffu, q[j], group + o);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
             if (id_o == id[i]) {
@@ -140,15 +167,15 @@ struct Entries {
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      q[i] = fmaf(c, ex2((x[i] - top) * k) * rsum - w[i], old[i]);
+      q[i] = fmaf(c, ex2(base(x[i], k)) * rsum - w[i], old[i]);
       if (!first[i]) id[i] = -1;
     }
   }
-  template <typename T>
-  __device__ __forceinline__ void store(T* d) const {
+  template <typename T, typename At>
+  __device__ __forceinline__ void store(At at) const {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (id[i] >= 0) d[id[i]] = from_f<T>(q[i]);
+      if (id[i] >= 0) *at(id[i]) = from_f<T>(q[i]);
   }
 };
 
@@ -168,72 +195,105 @@ __device__ __forceinline__ float row_loss(const Args& a, float w, float divergen
 // 1 / the sum; no student: p = 0
 __device__ __forceinline__ float rsum_of(float sum) { return sum == 0.f ? 0.f : rcp(sum); }
 
-template <typename T, int V, int NV, int MT>
-__global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int size) {
+// The gradient's elements at the entries are put into the row while it is in
+// shared memory (read from there too): in device memory a scattered store and a
+// scattered load for each took 127 of 296 us on 1000003 rows of 256 f16.
+template <typename T, int V, int NV, int MT, int S>
+__global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int size_) {
   extern __shared__ __align__(16) char smem[];
   constexpr int P = V * NV / 2;
+  using F = Feed<T, V, NV, 1, WeightedRows>;
+  const int size = S ? S : size_;
   const int l = threadIdx.x & 31, per = 32 / size, K = a.K, nv = K / V;
   const int64_t warp = ((int64_t)blockIdx.x * kWarpThreads + threadIdx.x) >> 5;
   const int64_t stride = (int64_t)gridDim.x * (kWarpThreads / 32) * per;
-  WarpTeam team{l & (size - 1), size};
+  WarpTeam<S> team(l & (size - 1), size);
   const float k = kLog2E * a.inv;
   const T none = from_f<T>(-INFINITY);
   int64_t n = warp * per + l / size;
-  Feed<T, V, NV, 1, WeightedRows> feed;
+  F feed;
   feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, size, nv, none, WeightedRows{a.weights});
   Entries<MT> ahead;
   ahead.fetch(a, n, team.lane, size);
   const T* L = (const T*)a.L + n * K;
   T* d = (T*)a.dL + n * K;
-  double total = 0.0;
+  float wn = a.weights && n < a.N ? a.weights[n] : 1.f;
+  double losses = 0.0;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
-    Row<T, V, NV> row[1], old;
+    Row<T, V, NV> row[1];
     const bool on = feed.next(row);
-    const float w = on ? (a.weights ? a.weights[n] : 1.f) : 0.f;
     Entries<MT> e = ahead;
-    e.take(a, L, d, on);
+    e.check(a, on);
     ahead.fetch(a, n + stride, team.lane, size);
-    if (a.add && n < a.N) old.read(d, team.lane, size, nv);
-    float top = team.top(lane_max(row[0]));
-    if (top == -INFINITY) top = 0.f;
+    const float w = wn;
+    if (a.weights && n + stride < a.N) wn = a.weights[n + stride];
+    bool twice;
+    if constexpr (F::kAsync) {
+      __syncwarp();
+      e.gather([&](int i) { return feed.peer(i); });
+      __syncwarp();
+      twice = a.dL && e.twice_at([&](int i) { return feed.peer(i); });
+    } else {
+      e.gather([&](int i) { return L + i; });
+      twice = a.dL && e.twice(team);
+    }
+    e.gather_old(a, d);
+    const Base base(team.top(lane_max(row[0])), k);
     float2 x[P];
     row[0].get(x);
-    exponentials(x, top, k);
-    float2 t = x[0];
-#pragma unroll
-    for (int i = 1; i < P; ++i) t = add2(t, x[i]);
-    float s[1] = {t.x + t.y};
+    exponentials(x, base, k);
+    float s[1] = {total(x)};
     team.sum(s);
     float logsum;
     const bool some = e.normalise(team, logsum) && on;
-    const float divergence = e.divergence(team, top, k);
+    const float divergence = e.divergence(team, base, k);
     if (team.lane == 0 && n < a.N) {
       const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
       a.rows[n] = r;
-      total += r;
+      losses += r;
     }
     if (!a.dL) continue;
     const float c = a.scale * w * a.T, rsum = rsum_of(s[0]);
-    e.gradient(team, a.m, c, top, k, rsum);
-    if (n < a.N && (!a.add || some)) {
-      const float2 f = both(c * rsum);
-      if (a.add) {
-        float2 o[P];
-        old.get(o);
+    e.gradient(team, a.m, c, base, k, rsum, twice);
+    const bool write = n < a.N && (!a.add || some);
+    const float2 f = both(c * rsum);
+    if (a.add) {
+      Row<T, V, NV> old;
+      old.fill(none);
+      if (write) old.read(d, team.lane, team.size, nv);
+      float2 o[P];
+      old.get(o);
 #pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = fma2(x[i], f, o[i]);
-      } else {
+      for (int i = 0; i < P; ++i) x[i] = fma2(x[i], f, o[i]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], f);
-      }
-      row[0].set(x);
-      if (!some) row[0].fill(from_f<T>(0.f));
-      row[0].store(d, team.lane, size, nv);
+      for (int i = 0; i < P; ++i) x[i] = mul2(x[i], f);
     }
-    __syncwarp();
-    e.store(d);
+    row[0].set(x);
+    if (!some) row[0].fill(from_f<T>(0.f));
+    if constexpr (F::kAsync) {
+      feed.put(row[0]);
+      __syncwarp();
+      e.template store<T>([&](int i) { return feed.peer(i); });
+      __syncwarp();
+      feed.again(row[0]);
+      if (write) row[0].store(d, team.lane, size, nv);
+      // what is no part of the row is no logit
+      if (nv < NV * size) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (j * size + team.lane >= nv)
+#pragma unroll
+            for (int i = 0; i < V; ++i) row[0].r[j].v[i] = none;
+        feed.put(row[0]);
+      }
+    } else {
+      if (write) row[0].store(d, team.lane, size, nv);
+      __syncwarp();
+      e.template store<T>([&](int i) { return d + i; });
+    }
   }
-  store_total(a, total);
+  store_total(a, losses);
 }
 
 // The last warp has the entries, and no part of the row: what it waits for and
@@ -250,11 +310,11 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
   const float k = kLog2E * a.inv;
   const T none = from_f<T>(-INFINITY);
   uint32_t turn = 0;
-  double total = 0.0;
+  double losses = 0.0;
   const int64_t step = (int64_t)gridDim.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   if ((int)threadIdx.x >= team.size) {
-    const WarpTeam warp{(int)threadIdx.x & 31, 32};
+    const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
     const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
     Entries<MT> ahead, late;  // of the next row and of the last one
     ahead.fetch(a, blockIdx.x, warp.lane, 32);
@@ -264,45 +324,47 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
     for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
       const float w = wn;
       Entries<MT> e = ahead;
-      e.take(a, L, d, w != 0.f);
+      e.check(a, w != 0.f);
+      e.gather([&](int i) { return L + i; });
+      e.gather_old(a, d);
       ahead.fetch(a, n + gridDim.x, warp.lane, 32);
       if (a.weights && n + gridDim.x < a.N) wn = a.weights[n + gridDim.x];
       float logsum, top, s[1];
       const bool some = e.normalise(warp, logsum);
       if (warp.lane == 0) some_s[turn] = some;
       __syncthreads();
-      if (a.dL) late.store(d - step);
+      if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
       team.hear(s, top, 0.f, k);
-      const float divergence = e.divergence(warp, top, k);
+      const Base base(top, k);
+      const float divergence = e.divergence(warp, base, k);
       if (warp.lane == 0) {
         const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
         a.rows[n] = r;
-        total += r;
+        losses += r;
       }
       if (a.dL) {
-        e.gradient(warp, a.m, a.scale * w * a.T, top, k, rsum_of(s[0]));
+        e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]),
+                   e.twice(warp));
         late = e;
       }
     }
     __syncthreads();
-    if (a.dL) late.store(d - step);
+    if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
   } else {
     Feed<T, V, NV, 1, WeightedRows> feed;
     feed.start(smem, {(const T*)a.L}, blockIdx.x, gridDim.x, a.N, K, team.lane, team.size, nv, none,
                WeightedRows{a.weights});
+    float wn = a.weights && blockIdx.x < a.N ? a.weights[blockIdx.x] : 1.f;
     for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, d += step, turn ^= 1) {
-      Row<T, V, NV> row[1], old;
+      Row<T, V, NV> row[1];
       const bool on = feed.next(row);
-      const float w = on ? (a.weights ? a.weights[n] : 1.f) : 0.f;
-      if (a.add) old.read(d, team.lane, team.size, nv);
-      const float mine = team.top(lane_max(row[0])), low = mine == -INFINITY ? 0.f : mine;
+      const float w = wn;
+      if (a.weights && n + gridDim.x < a.N) wn = a.weights[n + gridDim.x];
+      const float mine = team.top(lane_max(row[0]));
       float2 x[P];
       row[0].get(x);
-      exponentials(x, low, k);
-      float2 t = x[0];
-#pragma unroll
-      for (int i = 1; i < P; ++i) t = add2(t, x[i]);
-      float s[1] = {t.x + t.y}, top;
+      exponentials(x, Base(mine, k), k);
+      float s[1] = {total(x)}, top;
       team.tell(s, mine);
       __syncthreads();
       if (!a.dL) {
@@ -314,6 +376,8 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
       if (a.add && !some) continue;
       const float2 f = both(a.scale * w * a.T * own * rsum_of(s[0]));
       if (a.add) {
+        Row<T, V, NV> old;
+        old.read(d, team.lane, team.size, nv);
         float2 o[P];
         old.get(o);
 #pragma unroll
@@ -328,7 +392,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
     }
     __syncthreads();
   }
-  store_total(a, total);
+  store_total(a, losses);
 }
 
 // Rows that no block holds, at any address.  The 16-byte vectors between a row's
@@ -337,8 +401,8 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
 // second (out of L2) and on to the next row; the elements before and behind,
 // fewer than a vector, belong to one thread each.
 constexpr int kStreamThreads = 512;
-constexpr int kStreamVectors = 2;  // a copy
-constexpr int kDepth = 4;
+constexpr int kStreamVectors = 4;  // a copy
+constexpr int kDepth = 3;
 
 template <typename T>
 struct Stream {
@@ -420,9 +484,9 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
   const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   uint32_t turn = 0;
-  double total = 0.0;
+  double losses = 0.0;
   if ((int)threadIdx.x >= kStreamThreads) {
-    const WarpTeam warp{(int)threadIdx.x & 31, 32};
+    const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
     Entries<MT> ahead, late;
     ahead.fetch(a, blockIdx.x, warp.lane, 32);
 #pragma unroll
@@ -430,27 +494,31 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
     for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
       const float w = a.weights ? a.weights[n] : 1.f;
       Entries<MT> e = ahead;
-      e.take(a, L, d, w != 0.f);
+      e.check(a, w != 0.f);
+      e.gather([&](int i) { return L + i; });
+      e.gather_old(a, d);
       ahead.fetch(a, n + gridDim.x, warp.lane, 32);
       float logsum, top, s[1];
       const bool some = e.normalise(warp, logsum);
       if (warp.lane == 0) some_s[turn] = some;
       __syncthreads();
-      if (a.dL) late.store(d - step);
+      if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
       team.hear(s, top, 0.f, k);
-      const float divergence = e.divergence(warp, top, k);
+      const Base base(top, k);
+      const float divergence = e.divergence(warp, base, k);
       if (warp.lane == 0) {
         const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
         a.rows[n] = r;
-        total += r;
+        losses += r;
       }
       if (a.dL) {
-        e.gradient(warp, a.m, a.scale * w * a.T, top, k, rsum_of(s[0]));
+        e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]),
+                   e.twice(warp));
         late = e;
       }
     }
     __syncthreads();
-    if (a.dL) late.store(d - step);
+    if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
   } else {
     const int t = threadIdx.x;
     Stream<T> feed;
@@ -467,8 +535,8 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
       for (int i = 0; i < turns; ++i) {
         Row<T, V, U> x;
         feed.next(x);
-        const int v0 = i * U * kStreamThreads + t;
         if (i == turns - 1) {
+          const int v0 = i * U * kStreamThreads + t;
 #pragma unroll
           for (int u = 0; u < U; ++u)
             if (v0 + u * kStreamThreads >= nv)
@@ -477,18 +545,18 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
         }
         const float m = max_nan(top, lane_max(x));
         if (m != top) {
-          if (m != -INFINITY) sum = mul2(sum, both(ex2((top - m) * k)));
+          sum = mul2(sum, both(BlockTeam<false>::between(top, m, k)));
           top = m;
         }
         float2 f[P];
         x.get(f);
-        exponentials(f, top == -INFINITY ? 0.f : top, k);
+        exponentials(f, Base(top, k), k);
 #pragma unroll
         for (int j = 0; j < P; ++j) sum = add2(sum, f[j]);
       }
       // the warp's, then the block's
       const float mine = warp_max(top);
-      float s[1] = {top == -INFINITY ? 0.f : (sum.x + sum.y) * ex2((top - mine) * k)};
+      float s[1] = {(sum.x + sum.y) * BlockTeam<false>::between(top, mine == -INFINITY ? 0.f : mine, k)};
       team.tell(s, mine);
       __syncthreads();
       if (!a.dL) {
@@ -497,49 +565,57 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
       }
       const bool some = w != 0.f && some_s[turn];
       team.hear(s, top, mine, k);
+      const Base base(top, k);
       const float c = some ? a.scale * w * a.T * rsum_of(s[0]) : 0.f;
       const float2 f = both(c);
       const bool same = (((uintptr_t)L ^ (uintptr_t)d) & 15) == 0;
       if (edge >= 0 && (some || !a.add)) {
-        float y = some ? ex2((xe - top) * k) * c : 0.f;
+        float y = some ? ex2(base(xe, k)) * c : 0.f;
         if (a.add) y += to_f(d[edge]);
         d[edge] = from_f<T>(y);
       }
-      for (int i = 0; i < turns; ++i) {
+      T* out = d + head + (int64_t)t * V;
+      for (int i = 0; i < turns; ++i, out += U * kStreamThreads * V) {
         Row<T, V, U> x;
         feed.next(x);
+        if (a.add && !some) continue;
         float2 y[P];
         x.get(y);
-        exponentials(y, top, k);
+        exponentials(y, base, k);
+        if (a.add) {
+          Row<T, V, U> o;
+          o.fill(none);
 #pragma unroll
-        for (int j = 0; j < P; ++j) y[j] = some ? mul2(y[j], f) : both(0.f);
-        const int v0 = i * U * kStreamThreads + t;
+          for (int u = 0; u < U; ++u)
+            if (i * U * kStreamThreads + t + u * kStreamThreads < nv) {
+              if (same) o.r[u] = *reinterpret_cast<const Vec<T, V>*>(out + u * kStreamThreads * V);
+              else
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int v = v0 + u * kStreamThreads;
-          if (v >= nv || (a.add && !some)) continue;
-          T* out = d + head + (int64_t)v * V;
-          Vec<T, V> o;
-          if (a.add) {
-            if (same) o = *reinterpret_cast<const Vec<T, V>*>(out);
+                for (int e = 0; e < V; ++e) o.r[u].v[e] = out[u * kStreamThreads * V + e];
+            }
+          float2 z[P];
+          o.get(z);
+#pragma unroll
+          for (int j = 0; j < P; ++j) y[j] = fma2(y[j], f, z[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < P; ++j) y[j] = mul2(y[j], f);
+        }
+        x.set(y);
+        if (!some) x.fill(from_f<T>(0.f));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i * U * kStreamThreads + t + u * kStreamThreads < nv) {
+            if (same) *reinterpret_cast<Vec<T, V>*>(out + u * kStreamThreads * V) = x.r[u];
             else
 #pragma unroll
-              for (int e = 0; e < V; ++e) o.v[e] = out[e];
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) y[u * V / 2 + e] = add2(y[u * V / 2 + e], to_f2(o.v[2 * e], o.v[2 * e + 1]));
+              for (int e = 0; e < V; ++e) out[u * kStreamThreads * V + e] = x.r[u].v[e];
           }
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) from_f2(y[u * V / 2 + e], o.v[2 * e], o.v[2 * e + 1]);
-          if (same) *reinterpret_cast<Vec<T, V>*>(out) = o;
-          else
-#pragma unroll
-            for (int e = 0; e < V; ++e) out[e] = o.v[e];
-        }
       }
     }
     __syncthreads();
   }
-  store_total(a, total);
+  store_total(a, losses);
 }
 
 // The blocks' sums in order, in 64 bits.
@@ -561,46 +637,55 @@ bool launch_block(const Args& a, int threads, int64_t grid, cudaStream_t s) {
   distill_block_kernel<T, V, NV, MT><<<(unsigned)grid, threads, F::bytes(threads), s>>>(a);
   return true;
 }
-template <typename T, int V, int NV, int MT>
+template <typename T, int V, int E, int MT, int S>
 bool launch_warp(const Args& a, int size, int64_t grid, cudaStream_t s) {
   static std::atomic<uint64_t> done;
-  using F = Feed<T, V, NV, 1, WeightedRows>;
-  if (!allow_smem((const void*)distill_warp_kernel<T, V, NV, MT>, F::bytes(kWarpThreads), done)) return false;
-  distill_warp_kernel<T, V, NV, MT><<<(unsigned)grid, kWarpThreads, F::bytes(kWarpThreads), s>>>(a, size);
+  using F = Feed<T, V, E / V, 1, WeightedRows>;
+  if (!allow_smem((const void*)distill_warp_kernel<T, V, E / V, MT, S>, F::bytes(kWarpThreads), done)) return false;
+  distill_warp_kernel<T, V, E / V, MT, S><<<(unsigned)grid, kWarpThreads, F::bytes(kWarpThreads), s>>>(a, size);
   return true;
+}
+// With as many lanes as hold the row, but for entries: at most eight a lane.
+template <typename T, int V, int E, int S>
+int64_t launch_lanes(const Args& a, int size, cudaStream_t s) {
+  const int64_t rows = kWarpThreads / size, need = (a.N + rows - 1) / rows;
+  const int64_t grid = need < 1 ? 1 : need < 4 * kSms ? need : 4 * kSms;
+  const bool ok = a.m <= size ? launch_warp<T, V, E, 1, S>(a, size, grid, s) : launch_warp<T, V, E, 8, S>(a, size, grid, s);
+  return ok ? grid : 0;
 }
 
 // Returns the blocks launched; 0: none.
 template <typename T, int V>
 int64_t launch(const Args& a, cudaStream_t s) {
   const int K = a.K, m = a.m;
-  if (K <= kWarpK) {
-    const int per = V == 1 ? (K <= 256 ? 8 : 16) : K <= 8 ? 8 : K <= kPer16 ? 16 : 32;
-    int size = 1;
-    while (size < 32 && size * (V == 1 ? 1 : per) < K) size <<= 1;
-    while (size * 8 < m) size <<= 1;  // at most eight entries a lane
-    const int64_t rows = kWarpThreads / size, need = (a.N + rows - 1) / rows;
-    const int64_t grid = need < 1 ? 1 : need < 4 * kSms ? need : 4 * kSms;
-    bool ok;
-    if (per == 8)
-      ok = m <= size ? launch_warp<T, V, 8 / V, 1>(a, size, grid, s) : launch_warp<T, V, 8 / V, 8>(a, size, grid, s);
-    else if (per == 16)
-      ok = m <= size ? launch_warp<T, V, 16 / V, 1>(a, size, grid, s) : launch_warp<T, V, 16 / V, 8>(a, size, grid, s);
-    else if constexpr (V > 1)
-      ok = m <= size ? launch_warp<T, V, 32 / V, 1>(a, size, grid, s) : launch_warp<T, V, 32 / V, 8>(a, size, grid, s);
-    return ok ? grid : 0;
+  if constexpr (V == 1) {
+    // single elements: read 32 at a time where the row has as many
+    if (K <= 512) {
+      int size = 1;
+      while (size < 32 && (size < K || size * 8 < m)) size <<= 1;
+      return K <= 256 ? launch_lanes<T, 1, 8, 0>(a, size, s) : launch_lanes<T, 1, 16, 0>(a, size, s);
+    }
+  } else {
+    if (K <= 8 && m <= 8) return launch_lanes<T, V, 8, 1>(a, 1, s);
+    if (K <= 64 && m <= 32) return launch_lanes<T, V, 16, 4>(a, 4, s);
+    if (K <= 128 && m <= 32) return launch_lanes<T, V, 32, 4>(a, 4, s);
+    if (K <= 256) return launch_lanes<T, V, 32, 8>(a, 8, s);
+    if (K <= 512) return launch_lanes<T, V, 32, 16>(a, 16, s);
+    if (K <= 1024) return launch_lanes<T, V, 32, 32>(a, 32, s);
   }
-  const int threads = ((K + 15) / 16 + 31) / 32 * 32 + 32;
+  constexpr int E = V > 1 ? 32 : 16;
+  const int threads = ((K + E - 1) / E + 31) / 32 * 32 + 32;
   const int resident = 1024 / threads < 8 ? 1024 / threads : 8;
   const int64_t grid = a.N < 1 ? 1 : a.N < (int64_t)resident * kSms ? a.N : (int64_t)resident * kSms;
-  const bool ok = m <= 32 ? launch_block<T, V, 16 / V, 1>(a, threads, grid, s)
-                          : launch_block<T, V, 16 / V, 2>(a, threads, grid, s);
+  const bool ok = m <= 32 ? launch_block<T, V, E / V, 1>(a, threads, grid, s)
+                          : launch_block<T, V, E / V, 2>(a, threads, grid, s);
   return ok ? grid : 0;
 }
 
 template <typename T>
 int64_t launch_typed(const Args& a, cudaStream_t s) {
-  if (a.K > kBlockK) {
+  const bool vectors = wide<T>(a.K, (const char*)a.L, (const char*)a.dL);
+  if (a.K > (vectors ? 32 : 16) * kBlockThreads) {
     static std::atomic<uint64_t> done;
     const size_t smem = (size_t)kDepth * kStreamVectors * kStreamThreads * 16;
     if (!allow_smem((const void*)distill_stream_kernel<T>, smem, done)) return 0;
@@ -608,7 +693,7 @@ int64_t launch_typed(const Args& a, cudaStream_t s) {
     distill_stream_kernel<T><<<(unsigned)grid, kStreamThreads + 32, smem, s>>>(a);
     return grid;
   }
-  return wide<T>(a.K, (const char*)a.L, (const char*)a.dL) ? launch<T, kWide<T>>(a, s) : launch<T, 1>(a, s);
+  return vectors ? launch<T, kWide<T>>(a, s) : launch<T, 1>(a, s);
 }
 
 }  // namespace

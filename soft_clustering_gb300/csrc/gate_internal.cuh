@@ -171,6 +171,28 @@ struct Feed {
 #pragma unroll
     for (int a = 0; a < NA; ++a) from[a] += step;
   }
+  // Element `at` of the row (of this thread's team) that `next` gave last, in the
+  // words of whoever holds it, until the next call; between lanes it takes a
+  // __syncwarp.
+  __device__ __forceinline__ T* peer(int at) const {
+    static_assert(kAsync, "in shared memory");
+    const int v = at / V, j = v / size;
+    const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
+    return reinterpret_cast<T*>(slot + ((int64_t)(s * NA * NV + j) * blockDim.x + (v - j * size) - lane) * 16) + at % V;
+  }
+  // This thread's part of that row, written and read again.
+  __device__ __forceinline__ void put(const Row<T, V, NV>& r) const {
+    const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      *reinterpret_cast<Vec<T, V>*>(slot + (size_t)(s * NA * NV + j) * blockDim.x * 16) = r.r[j];
+  }
+  __device__ __forceinline__ void again(Row<T, V, NV>& r) const {
+    const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      r.r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)(s * NA * NV + j) * blockDim.x * 16);
+  }
   // The next row and true; what was there before and false past the last one and
   // for a row that is not fetched.
   __device__ __forceinline__ bool next(Row<T, V, NV> (&out)[NA]) {
@@ -267,14 +289,36 @@ __device__ __forceinline__ float lane_max(const Row<__nv_bfloat16, V, NV>& r) {
   for (int i = 2; i < V * NV; i += 2) m = __hmax2_nan(m, __halves2bfloat162(r.at(i), r.at(i + 1)));
   return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
 }
-// x -> 2^((x - top) k); top not -inf
-template <int P>
-__device__ __forceinline__ void exponentials(float2 (&x)[P], float top, float k) {
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    x[i] = mul2(sub2(x[i], both(top)), both(k));
-    x[i] = make_float2(ex2(x[i].x), ex2(x[i].y));
+// x -> 2^(x k - base) with base = top k rounded: its rounding is a factor that
+// all of a row have in common, so shares do not see it, and a logarithm of their
+// sum takes base itself.  A top so large, or so low, that base is not finite is
+// taken off first.
+struct Base {
+  float top, base;
+  __device__ __forceinline__ Base(float t, float k) : top(t == -INFINITY ? 0.f : t), base(top * k) {}
+  __device__ __forceinline__ float operator()(float x, float k) const {
+    return fabsf(base) == INFINITY ? (x - top) * k : fmaf(x, k, -base);
   }
+};
+template <int P>
+__device__ __forceinline__ void exponentials(float2 (&x)[P], const Base& b, float k) {
+  if (fabsf(b.base) == INFINITY) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = mul2(sub2(x[i], both(b.top)), both(k));
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = fma2(x[i], both(k), both(-b.base));
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) x[i] = make_float2(ex2(x[i].x), ex2(x[i].y));
+}
+template <int P>
+__device__ __forceinline__ float total(const float2 (&x)[P]) {
+  float2 t = x[0], u = x[1];
+#pragma unroll
+  for (int i = 2; i + 1 < P; i += 2) t = add2(t, x[i]), u = add2(u, x[i + 1]);
+  t = add2(t, u);
+  return t.x + t.y;
 }
 
 // Order of floats as unsigned numbers: -0 and 0 are one, every NaN is the largest.
@@ -326,24 +370,34 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A part of a warp (or all of it): `size` lanes, a power of two.
+// A part of a warp (or all of it): `size` lanes, a power of two; S: that, where
+// it is known at compile time (else 0).
+template <int S>
 struct WarpTeam {
   int lane, size;
+  __device__ __forceinline__ WarpTeam(int lane_, int size_) : lane(lane_), size(S ? S : size_) {}
   // The largest of the team's.
   __device__ __forceinline__ float top(float m) {
-    if (size == 32) return warp_max(m);
+    if (S == 32 || (S == 0 && size == 32)) return warp_max(m);
 #pragma unroll
-    for (int o = 8; o; o >>= 1)
-      if (size > o) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o; o >>= 1) {
+      if (S ? o >= S : o == 16) continue;
+      const float y = __shfl_xor_sync(0xffffffffu, m, o);
+      m = S || size > o ? max_nan(m, y) : m;
+    }
     return m;
   }
   template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-      if (size > o) {
+    for (int o = 16; o; o >>= 1) {
+      if (S && o >= S) continue;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], o);
+      for (int q = 0; q < Q; ++q) {
+        // selected rather than branched to: two instructions a step
+        const float y = __shfl_xor_sync(0xffffffffu, v[q], o);
+        v[q] = S || size > o ? v[q] + y : v[q];
       }
+    }
   }
 };
 
@@ -393,8 +447,8 @@ struct BlockTeam {
       if (q == 0) p[2 * kWarps + (threadIdx.x >> 5)] = top;
     }
   }
-  // The team's top and sums with it (0 for -inf); what takes a warp of top
-  // `mine` there.
+  // The team's top and sums with it; what takes a warp of top `mine` there.
+  // Exponents between tops are roundings apart from those of Base, no more.
   template <int Q> __device__ __forceinline__ float hear(float (&v)[Q], float& top, float mine, float k) {
     constexpr int G = 32 / Q;
     const int l = threadIdx.x & 31, q = l / G, c = l % G;
@@ -402,13 +456,19 @@ struct BlockTeam {
     turn ^= 1;
     const float there = c < all ? p[2 * kWarps + c] : -INFINITY;
     top = warp_max(there);
-    if (top == -INFINITY) top = 0.f;
-    float x = c < all ? p[q * kWarps + c] * ex2((there - top) * k) : 0.f;
+    const float low = top == -INFINITY ? 0.f : top;
+    float x = c < all ? p[q * kWarps + c] * between(there, low, k) : 0.f;
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
 #pragma unroll
     for (int i = 0; i < Q; ++i) v[i] = Q == 1 ? x : __shfl_sync(0xffffffffu, x, i * G);
-    return ex2((mine - top) * k);
+    return between(mine, low, k);
+  }
+  // 2^(base of a - base of b)
+  static __device__ __forceinline__ float between(float a, float b, float k) {
+    const Base p(a, k), q(b, k);
+    if (a == -INFINITY) return 0.f;
+    return ex2(fabsf(p.base) == INFINITY || fabsf(q.base) == INFINITY ? (a - b) * k : p.base - q.base);
   }
   template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
     static_assert(Q == 1 || Q == 2 || Q == 4, "a power of two");

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kWarpThreads) norm_warp_kernel(Args a, int siz
   const int lane = threadIdx.x & 31, per = 32 / size;
   const uint32_t warp = (blockIdx.x * kWarpThreads + threadIdx.x) >> 5;
   const uint32_t warps = gridDim.x * (kWarpThreads / 32);
-  norm_rows<T, W, V, NV>(a, smem, WarpTeam{lane & (size - 1), size}, warp * per + lane / size, warps * per,
+  norm_rows<T, W, V, NV>(a, smem, WarpTeam<0>(lane & (size - 1), size), warp * per + lane / size, warps * per,
                          warp * per);
 }
 
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kWarpThreads) norm_grad_warp_kernel(Args a, in
   const uint32_t warp = (blockIdx.x * kWarpThreads + threadIdx.x) >> 5;
   const uint32_t warps = gridDim.x * (kWarpThreads / 32);
   float2 dw[E / 2], db[E / 2];
-  grad_rows<T, W, V, NV>(a, smem, WarpTeam{lane & (size - 1), size}, warp * per + lane / size, warps * per,
+  grad_rows<T, W, V, NV>(a, smem, WarpTeam<0>(lane & (size - 1), size), warp * per + lane / size, warps * per,
                          warp * per, dw, db);
   if (!a.sums) return;
   // the warp's groups, then the warps in order
