@@ -171,27 +171,26 @@ struct Feed {
 #pragma unroll
     for (int a = 0; a < NA; ++a) from[a] += step;
   }
-  // Element `at` of the row (of this thread's team) that `next` gave last, in the
-  // words of whoever holds it, until the next call; between lanes it takes a
-  // __syncwarp.
-  __device__ __forceinline__ T* peer(int at) const {
+  // In shared memory until the next call: this thread's vector j of the row that
+  // `next` gave last, element `at` of that row whoever of the team holds it (which
+  // takes a __syncwarp between lanes), and all of this thread's vectors.
+  __device__ __forceinline__ char* word(int j) const {
     static_assert(kAsync, "in shared memory");
-    const int v = at / V, j = v / size;
     const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
-    return reinterpret_cast<T*>(slot + ((int64_t)(s * NA * NV + j) * blockDim.x + (v - j * size) - lane) * 16) + at % V;
+    return slot + (size_t)(s * NA * NV + j) * blockDim.x * 16;
   }
-  // This thread's part of that row, written and read again.
+  __device__ __forceinline__ Vec<T, V> vector(int j) const { return *reinterpret_cast<const Vec<T, V>*>(word(j)); }
+  __device__ __forceinline__ T* peer(int at) const {
+    const int v = at / V, j = v / size;
+    return reinterpret_cast<T*>(word(j) + (v - j * size - lane) * 16) + at % V;
+  }
   __device__ __forceinline__ void put(const Row<T, V, NV>& r) const {
-    const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      *reinterpret_cast<Vec<T, V>*>(slot + (size_t)(s * NA * NV + j) * blockDim.x * 16) = r.r[j];
+    for (int j = 0; j < NV; ++j) *reinterpret_cast<Vec<T, V>*>(word(j)) = r.r[j];
   }
   __device__ __forceinline__ void again(Row<T, V, NV>& r) const {
-    const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      r.r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)(s * NA * NV + j) * blockDim.x * 16);
+    for (int j = 0; j < NV; ++j) r.r[j] = vector(j);
   }
   // The next row and true; what was there before and false past the last one and
   // for a row that is not fetched.

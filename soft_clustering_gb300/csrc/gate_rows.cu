@@ -1,13 +1,6 @@
-// gate_rows.cu - a learned gate: the m largest logits of a row, their softmax,
-// the balance loss, and the gradient of the logits.
-//
-//   gmm_gate       ids, gamma, lse; counts, mass, share, loss
-//   gmm_gate_grad  dL = p (coef (share - <share, p>) - S) + v at ids
-//
-// A block takes a row at a time and passes over it once for each of the m
-// entries, for the sum and for the mass.  Column k of a row belongs to thread
-// k mod 256 of every block, so a block's sums over its rows need no atomics.
-#include "gate_internal.cuh"
+// gate_rows.cu - a learned gate: entry points, and what follows its kernels
+// (gate_rows.cuh).
+#include "gate_rows.cuh"
 
 namespace gmm {
 namespace {
@@ -15,126 +8,59 @@ namespace {
 using namespace gate;
 
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 304;
+constexpr int kFinishColumns = 32;
+constexpr int kFinishThreads = 1024;
 
-// A block's sums of the balance outputs: rows that count, then mass [K] and
-// counts [K]; the head holds the finish's partial losses and its ticket.
-struct Ws {
-  float* mass;      // blocks * K
-  int32_t* counts;  // blocks * K
-  int32_t* rows;    // blocks
-  double* part;     // finish blocks
-  uint32_t* ticket;
-};
-constexpr int kFinishColumns = 256;
-
-int blocks_for(int64_t N) { return (int)(N < 1 ? 1 : N < kMaxBlocks ? N : kMaxBlocks); }
-
-size_t ws_layout(int64_t N, int K, void* base, Ws* w) {
-  const int b = blocks_for(N), f = (K + kFinishColumns - 1) / kFinishColumns;
+size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
+  const int64_t b = N < 1 ? 1 : N < kGateGrid ? N : kGateGrid;
   size_t o = 0;
   auto take = [&](size_t n) { const size_t at = o; o += align_up(n); return (char*)base + at; };
-  Ws t;
+  GateWs t;
   t.ticket = (uint32_t*)take(4);
-  t.part = (double*)take(sizeof(double) * f);
+  t.part = (double*)take(sizeof(double) * ((K + kFinishColumns - 1) / kFinishColumns));
   t.rows = (int32_t*)take(sizeof(int32_t) * b);
+  t.kept = (int32_t*)take(sizeof(int32_t) * b);
   t.mass = (float*)take(sizeof(float) * (size_t)b * K);
   t.counts = (int32_t*)take(sizeof(int32_t) * (size_t)b * K);
+  t.scale = (float2*)take(sizeof(float2) * (size_t)(K > 16 * kGateBlockThreads ? N : 0));
   if (w) *w = t;
   return o;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-gate_kernel(const T* __restrict__ L, int64_t N, int K, int m, int normalised,
-            const uint8_t* __restrict__ live, int32_t* __restrict__ ids, float* __restrict__ gamma,
-            float* __restrict__ lse, Ws ws, int balance) {
-  __shared__ uint64_t part64[32];
-  __shared__ float partf[32];
-  float* mass = ws.mass + (size_t)blockIdx.x * K;
-  int32_t* counts = ws.counts + (size_t)blockIdx.x * K;
-  int rows = 0;
-  if (balance) {
-    for (int k = threadIdx.x; k < K; k += kThreads) mass[k] = 0.f, counts[k] = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
-  }
-  for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
-    const T* x = L + n * K;
-    uint64_t key[kMaxTop];
-#pragma unroll
-    for (int t = 0; t < kMaxTop; ++t) key[t] = 0;
-    const bool on = !live || live[n];
-    if (on) {
-      uint64_t below = ~0ull;
-#pragma unroll
-      for (int t = 0; t < kMaxTop; ++t) {
-        if (t >= m) break;
-        uint64_t best = 0;
-        for (int k = threadIdx.x; k < K; k += kThreads) {
-          const uint64_t v = (uint64_t)ordered(to_f(x[k])) << 32 | (0xfffffffeu - (uint32_t)k);  // never ~0
-          if (v < below && v > best) best = v;
-        }
-        key[t] = below = block_reduce(best, (uint64_t)0, MaxOp(), part64);
-      }
-    }
-    const float top = unordered((uint32_t)(key[0] >> 32));
-    const bool some = (uint32_t)(key[0] >> 32) > kOrderedNegInf;
-    float sum = 0.f;
-    if (some)
-      for (int k = threadIdx.x; k < K; k += kThreads) sum += expf(to_f(x[k]) - top);
-    sum = block_reduce(sum, 0.f, SumOp(), partf);
-    float g[kMaxTop], kept = 0.f;
-    int id[kMaxTop];
-#pragma unroll
-    for (int t = 0; t < kMaxTop; ++t) {
-      const uint32_t u = (uint32_t)(key[t] >> 32);
-      id[t] = u > kOrderedNegInf ? (int)(0xfffffffeu - (uint32_t)key[t]) : -1;
-      g[t] = id[t] >= 0 ? expf(unordered(u) - top) : 0.f;
-      kept += g[t];
-    }
-    if (threadIdx.x == 0) {
-      const float per = normalised ? kept : sum;
-#pragma unroll
-      for (int t = 0; t < kMaxTop; ++t)
-        if (t < m) {
-          ids[n * m + t] = id[t];
-          // a NaN or infinity in the row shows in the normalised shares too
-          gamma[n * m + t] = id[t] >= 0 ? (isnan(sum) ? sum : g[t] / per) : 0.f;
-          if (balance && id[t] >= 0) ++counts[id[t]];
-        }
-      if (lse) lse[n] = some ? top + logf(sum) : -INFINITY;
-    }
-    if (balance && some) {
-      ++rows;
-      for (int k = threadIdx.x; k < K; k += kThreads) mass[k] += expf(to_f(x[k]) - top) / sum;
-    }
-  }
-  if (balance && threadIdx.x == 0) ws.rows[blockIdx.x] = rows;
-}
-
-// Columns of all blocks in order, in 64 bits; the last block to end adds up the loss.
-__global__ void __launch_bounds__(kFinishColumns)
-gate_finish_kernel(Ws ws, int blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
+// The blocks' sums in order, 32 columns a block, in 64 bits; the last block to
+// end adds up the loss.
+__global__ void __launch_bounds__(kFinishThreads)
+gate_finish_kernel(GateWs ws, int blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
                    float* __restrict__ share, float* __restrict__ loss) {
-  __shared__ double part[32];
+  constexpr int R = kFinishThreads / kFinishColumns;
+  __shared__ double part[32], sums[R][kFinishColumns + 1];
   __shared__ long long parti[32];
+  __shared__ int numbers[R][kFinishColumns + 1];
   __shared__ bool last;
   long long rows = 0, all = 0;
-  for (int b = threadIdx.x; b < blocks; b += kFinishColumns) rows += ws.rows[b];
+  for (int b = threadIdx.x; b < blocks; b += kFinishThreads) rows += ws.rows[b], all += ws.kept[b];
   rows = block_reduce(rows, 0ll, SumOp(), parti);
-  for (int64_t i = threadIdx.x; i < (int64_t)blocks * K; i += kFinishColumns) all += ws.counts[i];
   all = block_reduce(all, 0ll, SumOp(), parti);
-  const int k = blockIdx.x * kFinishColumns + threadIdx.x;
-  double term = 0.0;
-  if (k < K) {
-    double s = 0.0;
-    long long c = 0;
-    for (int b = 0; b < blocks; ++b) {
+  const int c = threadIdx.x % kFinishColumns, r = threadIdx.x / kFinishColumns;
+  const int k = blockIdx.x * kFinishColumns + c;
+  double s = 0.0;
+  int n = 0;
+  if (k < K)
+    for (int b = r; b < blocks; b += R) {
       s += ws.mass[(size_t)b * K + k];
-      c += ws.counts[(size_t)b * K + k];
+      n += ws.counts[(size_t)b * K + k];
     }
-    const double f = rows > 0 && all > 0 ? (double)K * c / ((double)all * rows) : 0.0;
-    counts[k] = c;
+  sums[r][c] = s;
+  numbers[r][c] = n;
+  __syncthreads();
+  double term = 0.0;
+  if (r == 0 && k < K) {
+    long long count = 0;
+    s = 0.0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) s += sums[i][c], count += numbers[i][c];
+    const double f = rows > 0 && all > 0 ? (double)K * count / ((double)all * rows) : 0.0;
+    counts[k] = count;
     mass[k] = (float)s;
     share[k] = (float)f;
     term = f * s;
@@ -148,8 +74,8 @@ gate_finish_kernel(Ws ws, int blocks, int K, int64_t* __restrict__ counts, float
   __syncthreads();
   if (!last) return;
   __threadfence();
-  double s = 0.0;
-  for (int b = threadIdx.x; b < gridDim.x; b += kFinishColumns) s += __ldcg(ws.part + b);
+  s = 0.0;
+  for (int b = threadIdx.x; b < gridDim.x; b += kFinishThreads) s += __ldcg(ws.part + b);
   s = block_reduce(s, 0.0, SumOp(), part);
   if (threadIdx.x == 0) *loss = (float)s;
 }
@@ -255,26 +181,26 @@ gmm_status gmm_gate(const void* L, gmm_dtype xdtype, int64_t N, int K, int m, in
   if ((uintptr_t)L % dtype_size(xdtype) || !aligned(4, ids, gamma, lse, mass, share, loss) ||
       !aligned(8, counts))
     return GMM_ERR_INVALID_ARG;
-  Ws w{};
+  GateWs w{};
   if (outs) {
     if (!ws || !aligned(256, (char*)ws)) return GMM_ERR_INVALID_ARG;
     if (ws_bytes < ws_layout(N, K, ws, &w)) return GMM_ERR_WORKSPACE;
   }
   if (N == 0 && !outs) return GMM_OK;
   cudaStream_t s = (cudaStream_t)stream;
-  const int b = blocks_for(N);
+  const GateArgs a{L, live, ids, gamma, lse, N, K, m, flags & GMM_GATE_NORMALISED, outs != 0, w};
+  int64_t blocks;
   {
     ProfScope p("gate_kernel", s);
-#define CALL(T) gate_kernel<T><<<b, kThreads, 0, s>>>((const T*)L, N, K, m, flags, live, ids, gamma, lse, w, outs != 0)
-    if (xdtype == GMM_F32) CALL(float);
-    else if (xdtype == GMM_F16) CALL(__half);
-    else CALL(__nv_bfloat16);
-#undef CALL
+    blocks = xdtype == GMM_F32   ? launch_gate_f32(a, s)
+             : xdtype == GMM_F16 ? launch_gate_f16(a, s)
+                                 : launch_gate_bf16(a, s);
   }
+  if (!blocks) return GMM_ERR_CUDA;
   if (outs) {
     ProfScope p("gate_finish_kernel", s);
-    gate_finish_kernel<<<(K + kFinishColumns - 1) / kFinishColumns, kFinishColumns, 0, s>>>(
-        w, b, K, counts, mass, share, loss);
+    gate_finish_kernel<<<(K + kFinishColumns - 1) / kFinishColumns, kFinishThreads, 0, s>>>(
+        w, (int)blocks, K, counts, mass, share, loss);
   }
   return launched();
 }

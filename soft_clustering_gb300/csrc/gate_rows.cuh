@@ -1,0 +1,627 @@
+// gate_rows.cuh - a learned gate's answer: the m largest logits of a row, their
+// shares of its softmax, and the balance loss's sums.
+//
+//   ids, gamma, lse; mass_k = sum_n p[n,k], counts_k
+//
+// One pass over the logits: a row stays in registers from its load on.  Rows of
+// up to 1024 logits belong to lanes of a warp (8 at least, so that each of the
+// m entries has one; a row of up to 8 logits has one lane to itself), of up to
+// 16384 (fp32: 8192) to a block, 32 (16) logits a thread; longer ones are streamed by a block, and
+// their mass is summed by columns in a second reading.  Rows that do not start
+// on 16 bytes are read by single elements, up to 16 a thread.
+//
+// The m largest are found one at a time.  A lane keeps the largest of each of
+// its vectors and the place of the first of those; a round takes the team's best
+// (by value, then the lower column), and only the lane that had it looks on in
+// the vector that it came from, which waits in shared memory.  With sorting keys
+// for all elements instead a round of all lanes would read every one again.
+//
+// A lane has the same columns of every row, so it sums their mass in registers;
+// a block's sums are joined in order, by the finish over the blocks in 64 bits.
+#pragma once
+
+#include "gate_internal.cuh"
+
+namespace gmm {
+namespace gate {
+
+constexpr int kGateWarpThreads = 256;
+constexpr int kGateBlockThreads = 512;
+constexpr int kGateGrid = 4 * kSms;     // blocks, at most
+constexpr int kGateStreamGrid = 2 * kSms;
+
+// A block's sums of the balance outputs, and of rows that are streamed what
+// their second reading takes.
+struct GateWs {
+  float* mass;       // blocks * K
+  int32_t* counts;   // blocks * K
+  int32_t* rows;     // blocks: rows that count
+  int32_t* kept;     // blocks: entries
+  double* part;      // of the finish's blocks
+  uint32_t* ticket;
+  float2* scale;     // N: base (or top), 1 / sum
+};
+
+struct GateArgs {
+  const void* L;
+  const uint8_t* live;
+  int32_t* ids;
+  float *gamma, *lse;
+  int64_t N;
+  int K, m, normalised, balance;
+  GateWs ws;
+};
+
+// Returns the blocks launched, 0 on failure.
+int64_t launch_gate_f32(const GateArgs& a, cudaStream_t s);
+int64_t launch_gate_f16(const GateArgs& a, cudaStream_t s);
+int64_t launch_gate_bf16(const GateArgs& a, cudaStream_t s);
+
+namespace rows_impl {
+
+constexpr uint32_t kNone = 0u;  // below every number's order
+
+// A number's order; a logit that is not there (-inf) has none.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t o = ordered(x);
+  return o > kOrderedNegInf ? o : kNone;
+}
+
+template <int V> __device__ __forceinline__ float vector_max(const Vec<float, V>& x) {
+  float m = x.v[0];
+#pragma unroll
+  for (int e = 1; e < V; ++e) m = max_nan(m, x.v[e]);
+  return m;
+}
+template <int V> __device__ __forceinline__ float vector_max(const Vec<__half, V>& x) {
+  __half2 m = __halves2half2(x.v[0], x.v[1]);
+#pragma unroll
+  for (int e = 2; e < V; e += 2) m = __hmax2_nan(m, __halves2half2(x.v[e], x.v[e + 1]));
+  return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+}
+template <int V> __device__ __forceinline__ float vector_max(const Vec<__nv_bfloat16, V>& x) {
+  __nv_bfloat162 m = __halves2bfloat162(x.v[0], x.v[1]);
+#pragma unroll
+  for (int e = 2; e < V; e += 2) m = __hmax2_nan(m, __halves2bfloat162(x.v[e], x.v[e + 1]));
+  return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
+// The place of the first element equal to the vector's largest, `m` (a NaN: of
+// the first NaN; there is none where m is a number).
+template <typename T, int V> __device__ __forceinline__ int first_of(const Vec<T, V>& x, float m) {
+  int at = V - 1;
+#pragma unroll
+  for (int e = V - 2; e >= 0; --e) {
+    const float f = to_f(x.v[e]);
+    if (f == m || f != f) at = e;
+  }
+  return at;
+}
+
+// A lane's best element not yet taken: its order and column.
+template <typename T, int V, int NV, typename F>
+struct Best {
+  static constexpr bool kWideRows = V > 1;
+  uint32_t order, col;
+  uint32_t o[kWideRows ? NV : V * NV];  // of each vector's (element's) largest
+  int j;                                // where the best is
+
+  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, bool on) {
+#pragma unroll
+    for (int i = 0; i < (kWideRows ? NV : V * NV); ++i) {
+      if constexpr (kWideRows) o[i] = order_of(vector_max(r.r[i]));
+      else o[i] = order_of(to_f(r.at(i)));
+      if (!on) o[i] = kNone;
+    }
+    pick(feed);
+  }
+  __device__ __forceinline__ void pick(const F& feed) {
+    order = o[0], j = 0;
+#pragma unroll
+    for (int i = 1; i < (kWideRows ? NV : V * NV); ++i)
+      if (o[i] > order) order = o[i], j = i;
+    col = (uint32_t)((j * feed.size + feed.lane) * V);
+    if constexpr (kWideRows) {
+      if (order != kNone) col += first_of(feed.vector(j), unordered(order));
+    }
+  }
+  // Takes the best away.
+  __device__ __forceinline__ void pop(const F& feed) {
+    uint32_t left = kNone;
+    if constexpr (kWideRows) {
+      T* p = reinterpret_cast<T*>(feed.word(j));
+      p[col % V] = from_f<T>(-INFINITY);
+      left = order_of(vector_max(feed.vector(j)));
+    }
+#pragma unroll
+    for (int i = 0; i < (kWideRows ? NV : V * NV); ++i)
+      if (i == j) o[i] = left;
+    pick(feed);
+  }
+};
+
+// The team's best: the largest order, of equal ones the lowest column.  Where
+// both fit one word (a 16-bit type's order as a float has 19 bits, columns 13)
+// they are compared as one.
+template <typename T, int S>
+__device__ __forceinline__ void team_best(uint32_t& order, uint32_t& col) {
+  if (S == 1) return;
+  if (S == 32) {
+    const uint32_t o = __reduce_max_sync(0xffffffffu, order);
+    col = __reduce_min_sync(0xffffffffu, order == o ? col : 0xffffffffu);
+    order = o;
+  } else if (sizeof(T) == 2) {
+    uint32_t key = (order & 0xffffe000u) | (8191u - col);
+#pragma unroll
+    for (int s = S / 2; s; s >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, s));
+    // the low bits of a number's order: ones of a negative, none of a positive
+    order = (key & 0xffffe000u) | (key >> 31 ? 0u : 0x1fffu);
+    if (order <= 0x1fffu) order = kNone;
+    col = 8191u - (key & 8191u);
+  } else {
+    uint32_t o = order;
+#pragma unroll
+    for (int s = S / 2; s; s >>= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, s));
+    uint32_t c = order == o ? col : 0xffffffffu;
+#pragma unroll
+    for (int s = S / 2; s; s >>= 1) c = min(c, __shfl_xor_sync(0xffffffffu, c, s));
+    order = o, col = c;
+  }
+}
+
+// log of a row's sum of exponentials, taken with `base`.
+__device__ __forceinline__ float log_sum(const Base& b, float k, float sum) {
+  const float left = fabsf(b.base) == INFINITY ? 0.f : fmaf(b.top, k, -b.base);
+  return b.top + kLn2 * (lg2(sum) - left);
+}
+
+// Adds a block's sums to the workspace: `rows` and `kept` of its threads.
+__device__ __forceinline__ void store_counts(const GateArgs& a, int rows, int kept) {
+  __shared__ int part[32];
+  rows = block_reduce(rows, 0, SumOp(), part);
+  kept = block_reduce(kept, 0, SumOp(), part);
+  if (threadIdx.x == 0) {
+    a.ws.rows[blockIdx.x] = rows;
+    a.ws.kept[blockIdx.x] = kept;
+    if (blockIdx.x == 0) *a.ws.ticket = 0;
+  }
+}
+
+template <typename T, int V, int NV, int S, bool BALANCE>
+__global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  constexpr int P = V * NV / 2, per = 32 / S;
+  using F = Feed<T, V, NV, 1, LiveRows>;
+  const int l = threadIdx.x & 31, K = a.K, nv = K / V, m = a.m;
+  const int64_t warp = ((int64_t)blockIdx.x * kGateWarpThreads + threadIdx.x) >> 5;
+  const int64_t stride = (int64_t)gridDim.x * (kGateWarpThreads / 32) * per;
+  WarpTeam<S> team(l & (S - 1), S);
+  const T none = from_f<T>(-INFINITY);
+  float* cols = reinterpret_cast<float*>(smem + F::bytes(kGateWarpThreads));  // K, at the end
+  int32_t* counts = reinterpret_cast<int32_t*>(cols + K);
+  if (BALANCE) {
+    for (int k = threadIdx.x; k < K; k += kGateWarpThreads) counts[k] = 0;
+    __syncthreads();
+  }
+  int64_t n = warp * per + l / S;
+  F feed;
+  feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, S, nv, none, LiveRows{a.live});
+  float2 mass[BALANCE ? P : 1];
+#pragma unroll
+  for (int i = 0; i < (BALANCE ? P : 1); ++i) mass[i] = both(0.f);
+  int rows = 0, kept = 0;
+  for (int64_t end = warp * per; end < a.N; n += stride, end += stride) {
+    Row<T, V, NV> row[1];
+    const bool on = feed.next(row);
+    if (!on) row[0].fill(none);
+    Best<T, V, NV, F> best;
+    best.start(row[0], feed, on);
+    // lane t takes the t-th; one lane alone writes them as they come
+    uint32_t mine = kNone, id = 0, first = kNone;
+    float other[S == 1 ? kMaxTop : 1];
+#pragma unroll
+    for (int t = 0; t < kMaxTop; ++t) {
+      if (t >= m) break;
+      uint32_t o = best.order, c = best.col;
+      team_best<T, S>(o, c);
+      if (t == 0) first = o;
+      if (S == 1) {
+        other[t % (S == 1 ? kMaxTop : 1)] = o == kNone ? -INFINITY : unordered(o);
+        if (n < a.N) a.ids[n * m + t] = o == kNone ? -1 : (int)c;
+        if (BALANCE && o != kNone) {
+          atomicAdd(counts + c, 1);
+          ++kept;
+        }
+      } else if (team.lane == t) {
+        mine = o, id = c;
+      }
+      if (t + 1 < m && o != kNone && c == best.col) best.pop(feed);  // columns are one lane's
+    }
+    const bool some = first != kNone;
+    const Base base(some ? unordered(first) : -INFINITY, kLog2E);
+    float2 x[P];
+    row[0].get(x);
+    exponentials(x, base, kLog2E);
+    float s[1] = {total(x)};
+    team.sum(s);
+    const float rsum = some ? rcp(s[0]) : 0.f;
+    if (BALANCE) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) mass[i] = fma2(x[i], both(rsum), mass[i]);
+    }
+    if (S == 1) {
+      float all = 0.f;
+#pragma unroll
+      for (int t = 0; t < kMaxTop; ++t)
+        if (t < m) {
+          float& e = other[t % (S == 1 ? kMaxTop : 1)];
+          e = e == -INFINITY ? 0.f : ex2(base(e, kLog2E));
+          all += e;
+        }
+      const float r = !some ? 0.f : a.normalised ? rcp(s[0] == s[0] ? all : s[0]) : rsum;
+#pragma unroll
+      for (int t = 0; t < kMaxTop; ++t)
+        if (t < m && n < a.N) a.gamma[n * m + t] = other[t % (S == 1 ? kMaxTop : 1)] * r;
+    } else {
+      const float e = mine == kNone ? 0.f : ex2(base(unordered(mine), kLog2E));
+      float r = rsum;
+      if (a.normalised) {
+        float all[1] = {e};
+        team.sum(all);
+        r = some ? rcp(s[0] == s[0] ? all[0] : s[0]) : 0.f;
+      }
+      if (team.lane < m && n < a.N) {
+        a.ids[n * m + team.lane] = mine == kNone ? -1 : (int)id;
+        a.gamma[n * m + team.lane] = mine == kNone ? 0.f : e * r;
+        if (BALANCE && mine != kNone) {
+          atomicAdd(counts + id, 1);
+          ++kept;
+        }
+      }
+    }
+    if (team.lane == 0 && n < a.N) {
+      if (a.lse) a.lse[n] = some ? log_sum(base, kLog2E, s[0]) : -INFINITY;
+      rows += some;
+    }
+  }
+  if (!BALANCE) return;
+  // the warp's groups, then the warps in order
+#pragma unroll
+  for (int i = 0; i < (BALANCE ? P : 1); ++i)
+#pragma unroll
+    for (int o = 16; o >= S; o >>= 1) {
+      mass[i].x += __shfl_xor_sync(0xffffffffu, mass[i].x, o);
+      mass[i].y += __shfl_xor_sync(0xffffffffu, mass[i].y, o);
+    }
+  for (int turn = 0; turn < kGateWarpThreads / 32; ++turn) {
+    if ((int)(threadIdx.x >> 5) == turn && l < S) {
+#pragma unroll
+      for (int i = 0; i < V * NV; ++i) {
+        const int c = column<V>(i, l, S);
+        const float2 f = mass[BALANCE ? i / 2 : 0];
+        if (c < K) cols[c] = (turn ? cols[c] : 0.f) + (i & 1 ? f.y : f.x);
+      }
+    }
+    __syncthreads();
+  }
+  for (int k = threadIdx.x; k < K; k += kGateWarpThreads) {
+    a.ws.mass[(size_t)blockIdx.x * K + k] = cols[k];
+    a.ws.counts[(size_t)blockIdx.x * K + k] = counts[k];
+  }
+  store_counts(a, rows, kept);
+}
+
+// One warp joins the block's lists: lane i has words i, i + 32, ... of `all` * 8.
+// Lane t ends with the t-th, as its order and column.
+__device__ __forceinline__ void join_lists(const uint64_t* keys, int all, int m, uint32_t& mine, uint32_t& id) {
+  const int l = threadIdx.x & 31;
+  uint64_t k[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k[i] = l + 32 * i < all * kMaxTop && (l & 7) < m ? keys[l + 32 * i] : 0;
+  mine = kNone, id = 0;
+  for (int t = 0; t < m; ++t) {
+    uint64_t b = k[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) b = k[i] > b ? k[i] : b;
+    const uint32_t o = __reduce_max_sync(0xffffffffu, (uint32_t)(b >> 32));
+    const uint32_t c = __reduce_max_sync(0xffffffffu, (uint32_t)(b >> 32) == o ? (uint32_t)b : 0u);
+    const uint64_t won = (uint64_t)o << 32 | c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k[i] == won) k[i] = 0;
+    if (l == t) mine = o, id = ~c;
+  }
+}
+
+// A row's outputs from its list, by one warp.
+__device__ __forceinline__ int store_row(const GateArgs& a, int64_t n, uint32_t mine, uint32_t id, bool some,
+                                         const Base& base, float sum) {
+  const int l = threadIdx.x & 31;
+  const float e = mine == kNone ? 0.f : ex2(base(unordered(mine), kLog2E));
+  float r = some ? rcp(sum) : 0.f;
+  if (a.normalised) {
+    const float all = warp_reduce(e, SumOp());
+    r = some ? rcp(sum == sum ? all : sum) : 0.f;
+  }
+  if (l < a.m) {
+    a.ids[n * a.m + l] = mine == kNone ? -1 : (int)id;
+    a.gamma[n * a.m + l] = mine == kNone ? 0.f : e * r;
+  }
+  if (l == 0 && a.lse) a.lse[n] = some ? log_sum(base, kLog2E, sum) : -INFINITY;
+  return l < a.m && mine != kNone;
+}
+
+template <typename T, int V, int NV, bool BALANCE>
+__global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float part[BlockTeam<false>::kWords];
+  __shared__ uint64_t lists[2][16 * kMaxTop];
+  constexpr int P = V * NV / 2;
+  using F = Feed<T, V, NV, 1, LiveRows>;
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5, K = a.K, nv = K / V, m = a.m;
+  BlockTeam<false> team(part, blockDim.x);
+  const T none = from_f<T>(-INFINITY);
+  int32_t* counts = reinterpret_cast<int32_t*>(smem + F::bytes(blockDim.x));
+  if (BALANCE) {
+    for (int k = threadIdx.x; k < K; k += blockDim.x) counts[k] = 0;
+    __syncthreads();
+  }
+  F feed;
+  feed.start(smem, {(const T*)a.L}, blockIdx.x, gridDim.x, a.N, K, team.lane, team.size, nv, none, LiveRows{a.live});
+  float2 mass[BALANCE ? P : 1];
+#pragma unroll
+  for (int i = 0; i < (BALANCE ? P : 1); ++i) mass[i] = both(0.f);
+  int rows = 0, kept = 0, duty = 0;
+  uint32_t turn = 0;
+  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1, duty = duty + 1 == team.all ? 0 : duty + 1) {
+    Row<T, V, NV> row[1];
+    const bool on = feed.next(row);
+    if (!on) row[0].fill(none);
+    Best<T, V, NV, F> best;
+    best.start(row[0], feed, on);
+    uint32_t first = kNone, o = kNone, c = 0;
+    for (int t = 0; t < m; ++t) {
+      o = best.order, c = best.col;
+      team_best<T, 32>(o, c);
+      if (t == 0) first = o;
+      if (l == t) lists[turn][w * kMaxTop + t] = o == kNone ? 0 : (uint64_t)o << 32 | (uint32_t)~c;
+      if (t + 1 < m && o != kNone && c == best.col) best.pop(feed);  // columns are one lane's
+    }
+    const float mine = first == kNone ? -INFINITY : unordered(first);
+    float2 x[P];
+    row[0].get(x);
+    exponentials(x, Base(mine, kLog2E), kLog2E);
+    float s[1] = {total(x)}, top;
+    team.tell(s, mine);
+    __syncthreads();
+    const float own = team.hear(s, top, mine, kLog2E);
+    const bool some = top != -INFINITY;
+    if (BALANCE) {
+      const float2 f = both(some ? own * rcp(s[0]) : 0.f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) mass[i] = fma2(x[i], f, mass[i]);
+    }
+    if (w == duty) {
+      uint32_t order, id;
+      join_lists(lists[turn], team.all, m, order, id);
+      const int is = store_row(a, n, order, id, some, Base(top, kLog2E), s[0]);
+      if (BALANCE && is) atomicAdd(counts + id, 1);
+      kept += is;
+      rows += some && l == 0;
+    }
+  }
+  if (!BALANCE) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < V * NV; ++i) {
+    const int c = column<V>(i, team.lane, team.size);
+    const float2 f = mass[BALANCE ? i / 2 : 0];
+    if (c < K) a.ws.mass[(size_t)blockIdx.x * K + c] = i & 1 ? f.y : f.x;
+  }
+  for (int k = threadIdx.x; k < K; k += blockDim.x) a.ws.counts[(size_t)blockIdx.x * K + k] = counts[k];
+  store_counts(a, rows, kept);
+}
+
+// Rows that no block holds.  A thread's list of the m largest so far is kept
+// sorted; few logits of a long row pass its last one.
+template <typename T>
+__global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateArgs a) {
+  __shared__ float part[BlockTeam<false>::kWords];
+  __shared__ uint64_t lists[2][16 * kMaxTop];
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5, K = a.K, m = a.m;
+  BlockTeam<false> team(part, kGateBlockThreads);
+  int32_t* counts = a.balance ? a.ws.counts + (size_t)blockIdx.x * K : nullptr;
+  if (a.balance) {
+    for (int k = threadIdx.x; k < K; k += kGateBlockThreads) counts[k] = 0;
+    __syncthreads();
+  }
+  int rows = 0, kept = 0;
+  uint32_t turn = 0;
+  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
+    const T* L = (const T*)a.L + n * K;
+    const bool on = !a.live || a.live[n];
+    uint64_t list[kMaxTop];
+#pragma unroll
+    for (int t = 0; t < kMaxTop; ++t) list[t] = 0;
+    float top = -INFINITY, sum = 0.f;
+    auto take = [&](float x, int c) {
+      const uint32_t o = order_of(x);
+      uint64_t key = (uint64_t)o << 32 | (uint32_t)~c;
+      uint64_t last = 0;
+#pragma unroll
+      for (int t = 0; t < kMaxTop; ++t)
+        if (t == m - 1) last = list[t];
+      if (o != kNone && key > last) {
+#pragma unroll
+        for (int t = 0; t < kMaxTop; ++t)
+          if (t < m && key > list[t]) {
+            const uint64_t was = list[t];
+            list[t] = key;
+            key = was;
+          }
+      }
+    };
+    if (on) {
+      constexpr int V = kWide<T>, U = 4;
+      const int h0 = (int)((16 - ((uintptr_t)L & 15)) & 15) / (int)sizeof(T), head = h0 < K ? h0 : K;
+      const int nv = (K - head) / V, tail = head + nv * V;
+      const int t = threadIdx.x;
+      const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;
+      if (edge >= 0) {
+        const float x = to_f(L[edge]);
+        take(x, edge);
+        top = x;
+        if (x != -INFINITY) sum = ex2((x - x) * kLog2E);
+      }
+      for (int v0 = t; v0 < nv; v0 += U * kGateBlockThreads) {
+        Row<T, V, U> x;
+        x.fill(from_f<T>(-INFINITY));
+        x.read(L + head + (int64_t)(v0 - t) * V, t, kGateBlockThreads, nv - (v0 - t));
+        const float high = lane_max(x), to = max_nan(top, high);
+        if (to != top) {
+          sum *= BlockTeam<false>::between(top, to, kLog2E);
+          top = to;
+        }
+        uint64_t last = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxTop; ++i)
+          if (i == m - 1) last = list[i];
+        if (order_of(high) >= (uint32_t)(last >> 32) && order_of(high) != kNone) {
+#pragma unroll 1
+          for (int u = 0; u < U; ++u) {
+            Vec<T, V> y = x.r[0];
+#pragma unroll
+            for (int i = 1; i < U; ++i)
+              if (i == u) y = x.r[i];
+#pragma unroll
+            for (int e = 0; e < V; ++e) take(to_f(y.v[e]), head + (v0 + u * kGateBlockThreads) * V + e);
+          }
+        }
+        float2 f[U * V / 2];
+        x.get(f);
+        exponentials(f, Base(top, kLog2E), kLog2E);
+        sum += total(f);
+      }
+    }
+    // the warp's list, one round each
+    for (int t = 0; t < m; ++t) {
+      const uint32_t o = __reduce_max_sync(0xffffffffu, (uint32_t)(list[0] >> 32));
+      const uint32_t c = __reduce_max_sync(0xffffffffu, (uint32_t)(list[0] >> 32) == o ? (uint32_t)list[0] : 0u);
+      const uint64_t won = (uint64_t)o << 32 | c;
+      if (l == 0) lists[turn][w * kMaxTop + t] = o == kNone ? 0 : won;
+      if (list[0] == won) {
+#pragma unroll
+        for (int i = 0; i + 1 < kMaxTop; ++i) list[i] = list[i + 1];
+        list[kMaxTop - 1] = 0;
+      }
+    }
+    const float mine = warp_max(top);
+    float s[1] = {sum * BlockTeam<false>::between(top, mine == -INFINITY ? 0.f : mine, kLog2E)};
+    team.tell(s, mine);
+    __syncthreads();
+    team.hear(s, top, mine, kLog2E);
+    const bool some = top != -INFINITY;
+    if (w == 0) {
+      uint32_t order, id;
+      join_lists(lists[turn], team.all, m, order, id);
+      const Base base(top, kLog2E);
+      const int is = store_row(a, n, order, id, some, base, s[0]);
+      if (a.balance) {
+        if (is) atomicAdd(counts + id, 1);
+        if (l == 0) a.ws.scale[n] = make_float2(some ? top : 0.f, some ? rcp(s[0]) : 0.f);
+      }
+      kept += is;
+      rows += some && l == 0;
+    }
+  }
+  if (a.balance) store_counts(a, rows, kept);
+}
+
+// The mass of streamed rows, a thread a column, blockIdx.y a stretch of rows.
+constexpr int kMassThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kMassThreads) gate_mass_kernel(GateArgs a, int64_t stretch) {
+  const int k = blockIdx.x * kMassThreads + threadIdx.x;
+  if (k >= a.K) return;
+  const int64_t begin = blockIdx.y * stretch, end = begin + stretch < a.N ? begin + stretch : a.N;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int64_t n = begin; n < end; ++n) {
+    const float2 c = a.ws.scale[n];
+    if (a.live && !a.live[n]) continue;
+    const float x = to_f(((const T*)a.L)[n * a.K + k]);
+    sum += c.y == 0.f ? 0.f : ex2(Base(c.x, kLog2E)(x, kLog2E)) * c.y;
+  }
+  a.ws.mass[(size_t)blockIdx.y * a.K + k] = sum;
+}
+
+template <typename T, int V, int E, int S>
+int64_t launch_lanes(const GateArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done[2];
+  constexpr int NV = E / V;
+  using F = Feed<T, V, NV, 1, LiveRows>;
+  const size_t feed = F::bytes(kGateWarpThreads);
+  const int64_t rows = kGateWarpThreads / S, need = (a.N + rows - 1) / rows;
+  const int64_t grid = need < 1 ? 1 : need < kGateGrid ? need : kGateGrid;
+  if (a.balance) {
+    if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, true>, feed + 8 * E * S, done[1])) return 0;
+    gate_warp_kernel<T, V, NV, S, true><<<(unsigned)grid, kGateWarpThreads, feed + 8 * a.K, s>>>(a);
+  } else {
+    if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, false>, feed, done[0])) return 0;
+    gate_warp_kernel<T, V, NV, S, false><<<(unsigned)grid, kGateWarpThreads, feed, s>>>(a);
+  }
+  return grid;
+}
+
+template <typename T, int V, int E>
+int64_t launch_block(const GateArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done[2];
+  constexpr int NV = E / V;
+  using F = Feed<T, V, NV, 1, LiveRows>;
+  const int threads = ((a.K + E - 1) / E + 31) / 32 * 32;
+  const int resident = 640 / threads < 1 ? 1 : 640 / threads < 4 ? 640 / threads : 4;
+  const int64_t most = (int64_t)resident * kSms, grid = a.N < 1 ? 1 : a.N < most ? a.N : most;
+  const size_t feed = F::bytes(threads);
+  if (a.balance) {
+    if (!allow_smem((const void*)gate_block_kernel<T, V, NV, true>, F::bytes(kGateBlockThreads) + 4 * E * kGateBlockThreads, done[1])) return 0;
+    gate_block_kernel<T, V, NV, true><<<(unsigned)grid, threads, feed + 4 * (size_t)a.K, s>>>(a);
+  } else {
+    if (!allow_smem((const void*)gate_block_kernel<T, V, NV, false>, F::bytes(kGateBlockThreads), done[0])) return 0;
+    gate_block_kernel<T, V, NV, false><<<(unsigned)grid, threads, feed, s>>>(a);
+  }
+  return grid;
+}
+
+template <typename T>
+int64_t launch_gate(const GateArgs& a, cudaStream_t s) {
+  constexpr int V = kWide<T>;
+  const int K = a.K;
+  if (wide<T>(K, (const char*)a.L)) {
+    if (K <= 8) return launch_lanes<T, V, 8, 1>(a, s);
+    if (K <= 64) return launch_lanes<T, V, 8, 8>(a, s);
+    if (K <= 128) return launch_lanes<T, V, 16, 8>(a, s);
+    if (K <= 256) return launch_lanes<T, V, 32, 8>(a, s);
+    if (K <= 512) return launch_lanes<T, V, 32, 16>(a, s);
+    if (K <= 1024) return launch_lanes<T, V, 32, 32>(a, s);
+    constexpr int E = sizeof(T) == 2 ? 32 : 16;  // rows ahead and counts fit in shared memory
+    if (K <= E * kGateBlockThreads) return launch_block<T, V, E>(a, s);
+  } else {
+    if (K <= 64) return launch_lanes<T, 1, 8, 8>(a, s);
+    if (K <= 128) return launch_lanes<T, 1, 8, 16>(a, s);
+    if (K <= 256) return launch_lanes<T, 1, 8, 32>(a, s);
+    if (K <= 512) return launch_lanes<T, 1, 16, 32>(a, s);
+    if (K <= 16 * kGateBlockThreads) return launch_block<T, 1, 16>(a, s);
+  }
+  const int64_t grid = a.N < 1 ? 1 : a.N < kGateStreamGrid ? a.N : kGateStreamGrid;
+  gate_stream_kernel<T><<<(unsigned)grid, kGateBlockThreads, 0, s>>>(a);
+  if (a.balance) {
+    const int64_t stretch = (a.N + grid - 1) / grid;
+    const dim3 g((K + kMassThreads - 1) / kMassThreads, (unsigned)grid);
+    gate_mass_kernel<T><<<g, kMassThreads, 0, s>>>(a, stretch);
+  }
+  return grid;
+}
+
+}  // namespace rows_impl
+}  // namespace gate
+}  // namespace gmm

@@ -1,0 +1,8 @@
+// gate_rows_f32.cu - the learned gate's kernels (gate_rows.cuh) for this type.
+#include "gate_rows.cuh"
+
+namespace gmm {
+namespace gate {
+int64_t launch_gate_f32(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<float>(a, s); }
+}  // namespace gate
+}  // namespace gmm
