@@ -19,6 +19,7 @@ using namespace gate;
 
 constexpr int kWarpThreads = 256;
 constexpr int kBlockThreads = 512;
+constexpr int kStreamThreads = 512;
 constexpr int kMaxGrid = 8 * kSms;
 constexpr int kStudent = 1 << 18;
 
@@ -395,81 +396,6 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
   store_total(a, losses);
 }
 
-// Rows that no block holds, at any address.  The 16-byte vectors between a row's
-// first and last boundary go through shared memory as a Feed's do, kDepth copies
-// a thread ahead, and without a break from the first reading of a row to the
-// second (out of L2) and on to the next row; the elements before and behind,
-// fewer than a vector, belong to one thread each.
-constexpr int kStreamThreads = 512;
-constexpr int kStreamVectors = 4;  // a copy
-constexpr int kDepth = 3;
-
-template <typename T>
-struct Stream {
-  static constexpr int V = kWide<T>, U = kStreamVectors;
-  const T* L;
-  int64_t n, N, stride, row_step;
-  int K, passes;
-  // the copy to be asked for next
-  const T* body;
-  int nv, at, pass;
-  uint32_t slot_in, slot_out;
-  char* slot;
-  int threads;
-
-  // The row's vectors begin `head` elements in; nv of them.
-  static __device__ __forceinline__ int head_of(const T* p, int K) {
-    const int h = (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T);
-    return h < K ? h : K;
-  }
-  __device__ __forceinline__ void row() {
-    const int h = head_of(L, K);
-    body = L + h;
-    nv = (K - h) / V;
-  }
-  __device__ __forceinline__ void start(char* smem, const T* L_, int64_t n_, int64_t stride_, int64_t N_, int K_, int passes_,
-                                        int threads_) {
-    L = L_ + n_ * K_, n = n_, N = N_, stride = stride_, row_step = stride_ * K_, K = K_, passes = passes_;
-    threads = threads_;
-    at = (int)threadIdx.x, pass = 0, slot_in = slot_out = 0;
-    slot = smem + threadIdx.x * 16;
-    row();
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) ask();
-  }
-  __device__ __forceinline__ void ask() {
-    if (n < N) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (at + u * threads < nv)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(
-                           slot + (size_t)(slot_in * U + u) * threads * 16)),
-                       "l"(body + (int64_t)(at + u * threads) * V)
-                       : "memory");
-      at += U * threads;
-      if (at - (int)threadIdx.x >= nv) {
-        at = (int)threadIdx.x;
-        if (++pass == passes) {
-          pass = 0;
-          n += stride;
-          L += row_step;
-          if (n < N) row();
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    slot_in = slot_in == kDepth - 1 ? 0 : slot_in + 1;
-  }
-  __device__ __forceinline__ void next(Row<T, V, U>& x) {
-    ask();
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      x.r[u] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)(slot_out * U + u) * threads * 16);
-    slot_out = slot_out == kDepth - 1 ? 0 : slot_out + 1;
-  }
-};
-
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(Args a) {
   extern __shared__ __align__(16) char smem[];
@@ -687,7 +613,7 @@ int64_t launch_typed(const Args& a, cudaStream_t s) {
   const bool vectors = wide<T>(a.K, (const char*)a.L, (const char*)a.dL);
   if (a.K > (vectors ? 32 : 16) * kBlockThreads) {
     static std::atomic<uint64_t> done;
-    const size_t smem = (size_t)kDepth * kStreamVectors * kStreamThreads * 16;
+    const size_t smem = Stream<T>::bytes(kStreamThreads);
     if (!allow_smem((const void*)distill_stream_kernel<T>, smem, done)) return 0;
     const int64_t grid = a.N < 1 ? 1 : a.N < 2 * kSms ? a.N : 2 * kSms;
     distill_stream_kernel<T><<<(unsigned)grid, kStreamThreads + 32, smem, s>>>(a);

@@ -1,0 +1,8 @@
+// gate_grad_f16.cu - the gradient kernels (gate_grad.cuh) for this type.
+#include "gate_grad.cuh"
+
+namespace gmm {
+namespace gate {
+bool launch_grad_f16(const GradArgs& a, cudaStream_t s) { return grad_impl::launch_grad<__half>(a, s); }
+}  // namespace gate
+}  // namespace gmm

@@ -377,10 +377,10 @@ struct WarpTeam {
   __device__ __forceinline__ WarpTeam(int lane_, int size_) : lane(lane_), size(S ? S : size_) {}
   // The largest of the team's.
   __device__ __forceinline__ float top(float m) {
-    if (S == 32 || (S == 0 && size == 32)) return warp_max(m);
+    if constexpr (S == 32) return warp_max(m);
+    if (S == 0 && size == 32) return warp_max(m);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      if (S ? o >= S : o == 16) continue;
+    for (int o = S ? S / 2 : 8; o; o >>= 1) {
       const float y = __shfl_xor_sync(0xffffffffu, m, o);
       m = S || size > o ? max_nan(m, y) : m;
     }
@@ -514,6 +514,81 @@ struct BlockTeam {
     for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
 #pragma unroll
     for (int k = 0; k < Q; ++k) v[k] = Q == 1 ? x : __shfl_sync(0xffffffffu, x, k * G);
+  }
+};
+
+// Rows that no block holds, at any address.  The 16-byte vectors between a row's
+// first and last boundary go through shared memory as a Feed's do, kDepth copies
+// a thread ahead, and without a break from the first reading of a row to the
+// second (out of L2) and on to the next row; the elements before and behind,
+// fewer than a vector, belong to one thread each.
+constexpr int kStreamVectors = 4;  // a copy
+constexpr int kDepth = 3;
+
+template <typename T>
+struct Stream {
+  static constexpr int V = kWide<T>, U = kStreamVectors;
+  static constexpr size_t bytes(int threads) { return (size_t)kDepth * U * threads * 16; }
+  const T* L;
+  int64_t n, N, stride, row_step;
+  int K, passes;
+  // the copy to be asked for next
+  const T* body;
+  int nv, at, pass;
+  uint32_t slot_in, slot_out;
+  char* slot;
+  int threads;
+
+  // The row's vectors begin `head` elements in; nv of them.
+  static __device__ __forceinline__ int head_of(const T* p, int K) {
+    const int h = (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T);
+    return h < K ? h : K;
+  }
+  __device__ __forceinline__ void row() {
+    const int h = head_of(L, K);
+    body = L + h;
+    nv = (K - h) / V;
+  }
+  __device__ __forceinline__ void start(char* smem, const T* L_, int64_t n_, int64_t stride_, int64_t N_, int K_, int passes_,
+                                        int threads_) {
+    L = L_ + n_ * K_, n = n_, N = N_, stride = stride_, row_step = stride_ * K_, K = K_, passes = passes_;
+    threads = threads_;
+    at = (int)threadIdx.x, pass = 0, slot_in = slot_out = 0;
+    slot = smem + threadIdx.x * 16;
+    row();
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) ask();
+  }
+  __device__ __forceinline__ void ask() {
+    if (n < N) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (at + u * threads < nv)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(
+                           slot + (size_t)(slot_in * U + u) * threads * 16)),
+                       "l"(body + (int64_t)(at + u * threads) * V)
+                       : "memory");
+      at += U * threads;
+      if (at - (int)threadIdx.x >= nv) {
+        at = (int)threadIdx.x;
+        if (++pass == passes) {
+          pass = 0;
+          n += stride;
+          L += row_step;
+          if (n < N) row();
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    slot_in = slot_in == kDepth - 1 ? 0 : slot_in + 1;
+  }
+  __device__ __forceinline__ void next(Row<T, V, U>& x) {
+    ask();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      x.r[u] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)(slot_out * U + u) * threads * 16);
+    slot_out = slot_out == kDepth - 1 ? 0 : slot_out + 1;
   }
 };
 

@@ -1,5 +1,6 @@
 // gate_rows.cu - a learned gate: entry points, and what follows its kernels
-// (gate_rows.cuh).
+// (gate_rows.cuh, gate_grad.cuh).
+#include "gate_grad.cuh"
 #include "gate_rows.cuh"
 
 namespace gmm {
@@ -7,7 +8,6 @@ namespace {
 
 using namespace gate;
 
-constexpr int kThreads = 256;
 constexpr int kFinishColumns = 32;
 constexpr int kFinishThreads = 1024;
 
@@ -80,80 +80,6 @@ gate_finish_kernel(GateWs ws, int blocks, int K, int64_t* __restrict__ counts, f
   if (threadIdx.x == 0) *loss = (float)s;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-gate_grad_kernel(const T* __restrict__ L, int64_t N, int K, int m, int normalised,
-                 const uint8_t* __restrict__ live, const int32_t* __restrict__ ids,
-                 const float* __restrict__ gamma, const float* __restrict__ dgamma,
-                 const float* __restrict__ share, float coef, T* __restrict__ dL) {
-  __shared__ float partf[32];
-  for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
-    const T* x = L + n * K;
-    T* d = dL + n * K;
-    const bool on = !live || live[n];
-    float top = -INFINITY;
-    if (on)
-      for (int k = threadIdx.x; k < K; k += kThreads) {
-        const float v = to_f(x[k]);
-        top = v > top || isnan(v) ? v : top;
-      }
-    // NaN is the largest
-    top = unordered(block_reduce(ordered(top), 0u, MaxOp(), (uint32_t*)partf));
-    if (!on || top == -INFINITY) {
-      for (int k = threadIdx.x; k < K; k += kThreads) d[k] = from_f<T>(0.f);
-      continue;
-    }
-    float v[kMaxTop], S = 0.f;
-    int id[kMaxTop];
-#pragma unroll
-    for (int t = 0; t < kMaxTop; ++t) {
-      id[t] = -1, v[t] = 0.f;
-      if (dgamma && t < m) {
-        id[t] = ids[n * m + t];
-        if (id[t] >= K) id[t] = -1;
-        if (id[t] >= 0) v[t] = gamma[n * m + t] * dgamma[n * m + t];
-      }
-      S += v[t];
-    }
-    if (normalised) {
-#pragma unroll
-      for (int t = 0; t < kMaxTop; ++t)
-        if (id[t] >= 0) v[t] -= gamma[n * m + t] * S;
-      S = 0.f;
-    }
-    float sum = 0.f, dot = 0.f;
-    for (int k = threadIdx.x; k < K; k += kThreads) {
-      const float e = expf(to_f(x[k]) - top);
-      sum += e;
-      if (share) dot += e * share[k];
-    }
-    sum = block_reduce(sum, 0.f, SumOp(), partf);
-    dot = block_reduce(dot, 0.f, SumOp(), partf) / sum;
-    auto base = [&](int k) {
-      const float p = expf(to_f(x[k]) - top) / sum;
-      return p * ((share ? coef * (share[k] - dot) : 0.f) - S);
-    };
-    for (int k = threadIdx.x; k < K; k += kThreads) d[k] = from_f<T>(base(k));
-    __syncthreads();
-    if (threadIdx.x < m) {
-      // the entries of a component together, by the first of them
-      int k = -1;
-      float w = 0.f;
-      bool first = true;
-#pragma unroll
-      for (int t = 0; t < kMaxTop; ++t)
-        if (t == (int)threadIdx.x) k = id[t];
-#pragma unroll
-      for (int t = 0; t < kMaxTop; ++t)
-        if (id[t] == k) {
-          if (t < (int)threadIdx.x) first = false;
-          w += v[t];
-        }
-      if (k >= 0 && first) d[k] = from_f<T>(base(k) + w);
-    }
-  }
-}
-
 }  // namespace
 }  // namespace gmm
 
@@ -216,13 +142,11 @@ gmm_status gmm_gate_grad(const void* L, gmm_dtype xdtype, int64_t N, int K, int 
     return GMM_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   ProfScope p("gate_grad_kernel", s);
-  const int b = (int)(N < 8 * 152 ? N : 8 * 152);
-#define CALL(T) gate_grad_kernel<T><<<b, kThreads, 0, s>>>((const T*)L, N, K, m, flags, live, ids, gamma, dgamma, share, (float)coef, (T*)dL)
-  if (xdtype == GMM_F32) CALL(float);
-  else if (xdtype == GMM_F16) CALL(__half);
-  else CALL(__nv_bfloat16);
-#undef CALL
-  return launched();
+  const GradArgs a{L, live, ids, gamma, dgamma, share, dL, N, K, m, flags & GMM_GATE_NORMALISED, (float)coef};
+  const bool ok = xdtype == GMM_F32   ? launch_grad_f32(a, s)
+                  : xdtype == GMM_F16 ? launch_grad_f16(a, s)
+                                      : launch_grad_bf16(a, s);
+  return ok ? launched() : GMM_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -145,12 +145,12 @@ struct Best {
 // they are compared as one.
 template <typename T, int S>
 __device__ __forceinline__ void team_best(uint32_t& order, uint32_t& col) {
-  if (S == 1) return;
-  if (S == 32) {
+  if constexpr (S == 1) return;
+  if constexpr (S == 32) {
     const uint32_t o = __reduce_max_sync(0xffffffffu, order);
     col = __reduce_min_sync(0xffffffffu, order == o ? col : 0xffffffffu);
     order = o;
-  } else if (sizeof(T) == 2) {
+  } else if constexpr (sizeof(T) == 2) {
     uint32_t key = (order & 0xffffe000u) | (8191u - col);
 #pragma unroll
     for (int s = S / 2; s; s >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, s));
