@@ -88,7 +88,7 @@ template <int V> __device__ __forceinline__ float vector_max(const Vec<__nv_bflo
 
 // The place of the first element equal to the vector's largest, `m` (a NaN: of
 // the first NaN; there is none where m is a number).
-template <typename T, int V> __device__ __forceinline__ int first_of(const Vec<T, V>& x, float m) {
+template <typename T, int V> __device__ __forceinline__ int first_of_any(const Vec<T, V>& x, float m) {
   int at = V - 1;
 #pragma unroll
   for (int e = V - 2; e >= 0; --e) {
@@ -97,46 +97,83 @@ template <typename T, int V> __device__ __forceinline__ int first_of(const Vec<T
   }
   return at;
 }
+template <int V> __device__ __forceinline__ int first_of(const Vec<float, V>& x, float m) { return first_of_any(x, m); }
+// Pairs compared at once: a bit for each element, those of the high halves above.
+__device__ __forceinline__ int first_bit(uint32_t bits) { return __ffs((int)((bits | bits >> 16) & 0xffffu)) - 1; }
+template <int V> __device__ __forceinline__ int first_of(const Vec<__half, V>& x, float m) {
+  if (m != m) return first_of_any(x, m);
+  const __half2 t = __float2half2_rn(m);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    bits |= __heq2_mask(__halves2half2(x.v[e], x.v[e + 1]), t) & (1u << e | 1u << (16 + e + 1));
+  return first_bit(bits);
+}
+template <int V> __device__ __forceinline__ int first_of(const Vec<__nv_bfloat16, V>& x, float m) {
+  if (m != m) return first_of_any(x, m);
+  const __nv_bfloat162 t = __float2bfloat162_rn(m);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    bits |= __heq2_mask(__halves2bfloat162(x.v[e], x.v[e + 1]), t) & (1u << e | 1u << (16 + e + 1));
+  return first_bit(bits);
+}
 
-// A lane's best element not yet taken: its order and column.
+// A lane's best element not yet taken: its order and column.  The second best is
+// found beforehand, by all lanes at once: a lane that is taken from looks on by
+// itself, while the others wait, from its third on.
 template <typename T, int V, int NV, typename F>
 struct Best {
   static constexpr bool kWideRows = V > 1;
-  uint32_t order, col;
-  uint32_t o[kWideRows ? NV : V * NV];  // of each vector's (element's) largest
-  int j;                                // where the best is
+  static constexpr int N = kWideRows ? NV : V * NV;
+  uint32_t order, col, order2, col2;
+  uint32_t o[N];  // of each vector's (element's) largest left
+  int j;          // where the last one picked is
+  bool second;    // order2 and col2 are the next
 
-  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, bool on) {
+  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, bool on, bool more) {
 #pragma unroll
-    for (int i = 0; i < (kWideRows ? NV : V * NV); ++i) {
+    for (int i = 0; i < N; ++i) {
       if constexpr (kWideRows) o[i] = order_of(vector_max(r.r[i]));
       else o[i] = order_of(to_f(r.at(i)));
       if (!on) o[i] = kNone;
     }
-    pick(feed);
+    pick(feed, order, col);
+    second = false;
+    if (more) {
+      drop(feed, col);
+      pick(feed, order2, col2);
+      second = true;
+    }
   }
-  __device__ __forceinline__ void pick(const F& feed) {
+  __device__ __forceinline__ void pick(const F& feed, uint32_t& order, uint32_t& col) {
     order = o[0], j = 0;
 #pragma unroll
-    for (int i = 1; i < (kWideRows ? NV : V * NV); ++i)
+    for (int i = 1; i < N; ++i)
       if (o[i] > order) order = o[i], j = i;
     col = (uint32_t)((j * feed.size + feed.lane) * V);
     if constexpr (kWideRows) {
       if (order != kNone) col += first_of(feed.vector(j), unordered(order));
     }
   }
-  // Takes the best away.
-  __device__ __forceinline__ void pop(const F& feed) {
+  // Takes the one last picked away.
+  __device__ __forceinline__ void drop(const F& feed, uint32_t col) {
     uint32_t left = kNone;
     if constexpr (kWideRows) {
-      T* p = reinterpret_cast<T*>(feed.word(j));
-      p[col % V] = from_f<T>(-INFINITY);
+      reinterpret_cast<T*>(feed.word(j))[col % V] = from_f<T>(-INFINITY);
       left = order_of(vector_max(feed.vector(j)));
     }
 #pragma unroll
-    for (int i = 0; i < (kWideRows ? NV : V * NV); ++i)
+    for (int i = 0; i < N; ++i)
       if (i == j) o[i] = left;
-    pick(feed);
+  }
+  __device__ __forceinline__ void pop(const F& feed) {
+    if (second) {
+      order = order2, col = col2, second = false;
+    } else {
+      drop(feed, col);
+      pick(feed, order, col);
+    }
   }
 };
 
@@ -210,12 +247,13 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
 #pragma unroll
   for (int i = 0; i < (BALANCE ? P : 1); ++i) mass[i] = both(0.f);
   int rows = 0, kept = 0;
-  for (int64_t end = warp * per; end < a.N; n += stride, end += stride) {
+  int64_t at = n * m;
+  for (int64_t end = warp * per; end < a.N; n += stride, end += stride, at += stride * m) {
     Row<T, V, NV> row[1];
     const bool on = feed.next(row);
     if (!on) row[0].fill(none);
     Best<T, V, NV, F> best;
-    best.start(row[0], feed, on);
+    best.start(row[0], feed, on, m > 1);
     // lane t takes the t-th; one lane alone writes them as they come
     uint32_t mine = kNone, id = 0, first = kNone;
     float other[S == 1 ? kMaxTop : 1];
@@ -227,7 +265,7 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
       if (t == 0) first = o;
       if (S == 1) {
         other[t % (S == 1 ? kMaxTop : 1)] = o == kNone ? -INFINITY : unordered(o);
-        if (n < a.N) a.ids[n * m + t] = o == kNone ? -1 : (int)c;
+        if (n < a.N) a.ids[at + t] = o == kNone ? -1 : (int)c;
         if (BALANCE && o != kNone) {
           atomicAdd(counts + c, 1);
           ++kept;
@@ -261,7 +299,7 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
       const float r = !some ? 0.f : a.normalised ? rcp(s[0] == s[0] ? all : s[0]) : rsum;
 #pragma unroll
       for (int t = 0; t < kMaxTop; ++t)
-        if (t < m && n < a.N) a.gamma[n * m + t] = other[t % (S == 1 ? kMaxTop : 1)] * r;
+        if (t < m && n < a.N) a.gamma[at + t] = other[t % (S == 1 ? kMaxTop : 1)] * r;
     } else {
       const float e = mine == kNone ? 0.f : ex2(base(unordered(mine), kLog2E));
       float r = rsum;
@@ -271,8 +309,8 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
         r = some ? rcp(s[0] == s[0] ? all[0] : s[0]) : 0.f;
       }
       if (team.lane < m && n < a.N) {
-        a.ids[n * m + team.lane] = mine == kNone ? -1 : (int)id;
-        a.gamma[n * m + team.lane] = mine == kNone ? 0.f : e * r;
+        a.ids[at + team.lane] = mine == kNone ? -1 : (int)id;
+        a.gamma[at + team.lane] = mine == kNone ? 0.f : e * r;
         if (BALANCE && mine != kNone) {
           atomicAdd(counts + id, 1);
           ++kept;
@@ -378,7 +416,7 @@ __global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs 
     const bool on = feed.next(row);
     if (!on) row[0].fill(none);
     Best<T, V, NV, F> best;
-    best.start(row[0], feed, on);
+    best.start(row[0], feed, on, m > 1);
     uint32_t first = kNone, o = kNone, c = 0;
     for (int t = 0; t < m; ++t) {
       o = best.order, c = best.col;
