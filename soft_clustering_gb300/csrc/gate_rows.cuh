@@ -119,48 +119,93 @@ template <int V> __device__ __forceinline__ int first_of(const Vec<__nv_bfloat16
   return first_bit(bits);
 }
 
-// A lane's best element not yet taken: its order and column.  The second best is
-// found beforehand, by all lanes at once: a lane that is taken from looks on by
-// itself, while the others wait, from its third on.
-template <typename T, int V, int NV, typename F>
+// A candidate of a warp's team: a number's order and its place among the team's
+// up to 1024 (in the columns' order).  Larger is better: by value, then the lower
+// place.  In one word for 16-bit types, whose orders as floats have 19 bits.
+template <typename T> struct Key {
+  uint32_t k;
+  static __device__ __forceinline__ Key none() { return {0}; }
+  static __device__ __forceinline__ Key make(uint32_t order, uint32_t place) {
+    return {(order & 0xffffe000u) | (8191u - place)};
+  }
+  __device__ __forceinline__ bool is() const { return k != 0; }
+  __device__ __forceinline__ bool same(const Key& o) const { return k == o.k; }
+  // the low bits of an order: ones of a negative number, none of a positive one
+  __device__ __forceinline__ uint32_t order() const { return (k & 0xffffe000u) | (k >> 31 ? 0u : 0x1fffu); }
+  __device__ __forceinline__ uint32_t place() const { return 8191u - (k & 8191u); }
+  template <int S> __device__ __forceinline__ Key best() const {
+    if constexpr (S == 32) return {__reduce_max_sync(0xffffffffu, k)};
+    uint32_t b = k;
+#pragma unroll
+    for (int s = S / 2; s; s >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, s));
+    return {b};
+  }
+};
+template <> struct Key<float> {
+  uint32_t o, c;
+  static __device__ __forceinline__ Key none() { return {kNone, 0}; }
+  static __device__ __forceinline__ Key make(uint32_t order, uint32_t place) { return {order, ~place}; }
+  __device__ __forceinline__ bool is() const { return o != kNone; }
+  __device__ __forceinline__ bool same(const Key& k) const { return o == k.o && c == k.c; }
+  __device__ __forceinline__ uint32_t order() const { return o; }
+  __device__ __forceinline__ uint32_t place() const { return ~c; }
+  template <int S> __device__ __forceinline__ Key best() const {
+    Key b;
+    if constexpr (S == 32) {
+      b.o = __reduce_max_sync(0xffffffffu, o);
+      b.c = __reduce_max_sync(0xffffffffu, o == b.o ? c : 0u);
+    } else {
+      b.o = o;
+#pragma unroll
+      for (int s = S / 2; s; s >>= 1) b.o = max(b.o, __shfl_xor_sync(0xffffffffu, b.o, s));
+      b.c = o == b.o ? c : 0u;
+#pragma unroll
+      for (int s = S / 2; s; s >>= 1) b.c = max(b.c, __shfl_xor_sync(0xffffffffu, b.c, s));
+    }
+    return b;
+  }
+};
+
+// A lane's best element not yet taken.  The second best is found beforehand, by
+// all lanes at once: a lane that is taken from looks on by itself, while the
+// others wait, from its third on.
+template <typename T, int V, int NV, int S, typename F>
 struct Best {
   static constexpr bool kWideRows = V > 1;
   static constexpr int N = kWideRows ? NV : V * NV;
-  uint32_t order, col, order2, col2;
+  Key<T> key, next;
   uint32_t o[N];  // of each vector's (element's) largest left
-  int j;          // where the last one picked is
-  bool second;    // order2 and col2 are the next
+  int j, e;       // where the last one picked is
+  bool second;    // `next` is the next
 
-  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, bool on, bool more) {
+  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, bool more) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if constexpr (kWideRows) o[i] = order_of(vector_max(r.r[i]));
       else o[i] = order_of(to_f(r.at(i)));
-      if (!on) o[i] = kNone;
     }
-    pick(feed, order, col);
-    second = false;
+    key = pick(feed);
+    second = more;
     if (more) {
-      drop(feed, col);
-      pick(feed, order2, col2);
-      second = true;
+      drop(feed);
+      next = pick(feed);
     }
   }
-  __device__ __forceinline__ void pick(const F& feed, uint32_t& order, uint32_t& col) {
-    order = o[0], j = 0;
+  __device__ __forceinline__ Key<T> pick(const F& feed) {
+    uint32_t order = o[0];
+    j = 0, e = 0;
 #pragma unroll
     for (int i = 1; i < N; ++i)
       if (o[i] > order) order = o[i], j = i;
-    col = (uint32_t)((j * feed.size + feed.lane) * V);
-    if constexpr (kWideRows) {
-      if (order != kNone) col += first_of(feed.vector(j), unordered(order));
-    }
+    if (order == kNone) return Key<T>::none();
+    if constexpr (kWideRows) e = first_of(feed.vector(j), unordered(order));
+    return Key<T>::make(order, (uint32_t)((j * S + (feed.lane & (S - 1))) * V + e));
   }
   // Takes the one last picked away.
-  __device__ __forceinline__ void drop(const F& feed, uint32_t col) {
+  __device__ __forceinline__ void drop(const F& feed) {
     uint32_t left = kNone;
     if constexpr (kWideRows) {
-      reinterpret_cast<T*>(feed.word(j))[col % V] = from_f<T>(-INFINITY);
+      reinterpret_cast<T*>(feed.word(j))[e] = from_f<T>(-INFINITY);
       left = order_of(vector_max(feed.vector(j)));
     }
 #pragma unroll
@@ -169,42 +214,14 @@ struct Best {
   }
   __device__ __forceinline__ void pop(const F& feed) {
     if (second) {
-      order = order2, col = col2, second = false;
+      key = next;
+      second = false;
     } else {
-      drop(feed, col);
-      pick(feed, order, col);
+      drop(feed);
+      key = pick(feed);
     }
   }
 };
-
-// The team's best: the largest order, of equal ones the lowest column.  Where
-// both fit one word (a 16-bit type's order as a float has 19 bits, columns 13)
-// they are compared as one.
-template <typename T, int S>
-__device__ __forceinline__ void team_best(uint32_t& order, uint32_t& col) {
-  if constexpr (S == 1) return;
-  if constexpr (S == 32) {
-    const uint32_t o = __reduce_max_sync(0xffffffffu, order);
-    col = __reduce_min_sync(0xffffffffu, order == o ? col : 0xffffffffu);
-    order = o;
-  } else if constexpr (sizeof(T) == 2) {
-    uint32_t key = (order & 0xffffe000u) | (8191u - col);
-#pragma unroll
-    for (int s = S / 2; s; s >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, s));
-    // the low bits of a number's order: ones of a negative, none of a positive
-    order = (key & 0xffffe000u) | (key >> 31 ? 0u : 0x1fffu);
-    if (order <= 0x1fffu) order = kNone;
-    col = 8191u - (key & 8191u);
-  } else {
-    uint32_t o = order;
-#pragma unroll
-    for (int s = S / 2; s; s >>= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, s));
-    uint32_t c = order == o ? col : 0xffffffffu;
-#pragma unroll
-    for (int s = S / 2; s; s >>= 1) c = min(c, __shfl_xor_sync(0xffffffffu, c, s));
-    order = o, col = c;
-  }
-}
 
 // log of a row's sum of exponentials, taken with `base`.
 __device__ __forceinline__ float log_sum(const Base& b, float k, float sum) {
@@ -250,33 +267,37 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
   int64_t at = n * m;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, at += stride * m) {
     Row<T, V, NV> row[1];
-    const bool on = feed.next(row);
-    if (!on) row[0].fill(none);
-    Best<T, V, NV, F> best;
-    best.start(row[0], feed, on, m > 1);
+    if (!feed.next(row)) row[0].fill(none);
+    Best<T, V, NV, S, F> best;
+    best.start(row[0], feed, m > 1);
     // lane t takes the t-th; one lane alone writes them as they come
-    uint32_t mine = kNone, id = 0, first = kNone;
+    Key<T> mine = Key<T>::none(), first = Key<T>::none();
     float other[S == 1 ? kMaxTop : 1];
+    if constexpr (S == 1) {
 #pragma unroll
-    for (int t = 0; t < kMaxTop; ++t) {
-      if (t >= m) break;
-      uint32_t o = best.order, c = best.col;
-      team_best<T, S>(o, c);
-      if (t == 0) first = o;
-      if (S == 1) {
-        other[t % (S == 1 ? kMaxTop : 1)] = o == kNone ? -INFINITY : unordered(o);
-        if (n < a.N) a.ids[at + t] = o == kNone ? -1 : (int)c;
-        if (BALANCE && o != kNone) {
-          atomicAdd(counts + c, 1);
+      for (int t = 0; t < kMaxTop; ++t) {
+        if (t >= m) break;
+        const Key<T> k = best.key;
+        if (t == 0) first = k;
+        other[t] = k.is() ? unordered(k.order()) : -INFINITY;
+        if (n < a.N) a.ids[at + t] = k.is() ? (int)k.place() : -1;
+        if (BALANCE && k.is()) {
+          atomicAdd(counts + k.place(), 1);
           ++kept;
         }
-      } else if (team.lane == t) {
-        mine = o, id = c;
+        if (t + 1 < m && k.is()) best.pop(feed);
       }
-      if (t + 1 < m && o != kNone && c == best.col) best.pop(feed);  // columns are one lane's
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < m; ++t) {
+        const Key<T> k = best.key.template best<S>();
+        if (t == 0) first = k;
+        if (team.lane == t) mine = k;
+        if (t + 1 < m && k.is() && k.same(best.key)) best.pop(feed);  // places are one lane's
+      }
     }
-    const bool some = first != kNone;
-    const Base base(some ? unordered(first) : -INFINITY, kLog2E);
+    const bool some = first.is();
+    const Base base(some ? unordered(first.order()) : -INFINITY, kLog2E);
     float2 x[P];
     row[0].get(x);
     exponentials(x, base, kLog2E);
@@ -292,16 +313,16 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
 #pragma unroll
       for (int t = 0; t < kMaxTop; ++t)
         if (t < m) {
-          float& e = other[t % (S == 1 ? kMaxTop : 1)];
+          float& e = other[S == 1 ? t : 0];
           e = e == -INFINITY ? 0.f : ex2(base(e, kLog2E));
           all += e;
         }
       const float r = !some ? 0.f : a.normalised ? rcp(s[0] == s[0] ? all : s[0]) : rsum;
 #pragma unroll
       for (int t = 0; t < kMaxTop; ++t)
-        if (t < m && n < a.N) a.gamma[at + t] = other[t % (S == 1 ? kMaxTop : 1)] * r;
+        if (t < m && n < a.N) a.gamma[at + t] = other[S == 1 ? t : 0] * r;
     } else {
-      const float e = mine == kNone ? 0.f : ex2(base(unordered(mine), kLog2E));
+      const float e = mine.is() ? ex2(base(unordered(mine.order()), kLog2E)) : 0.f;
       float r = rsum;
       if (a.normalised) {
         float all[1] = {e};
@@ -309,10 +330,10 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
         r = some ? rcp(s[0] == s[0] ? all[0] : s[0]) : 0.f;
       }
       if (team.lane < m && n < a.N) {
-        a.ids[at + team.lane] = mine == kNone ? -1 : (int)id;
-        a.gamma[at + team.lane] = mine == kNone ? 0.f : e * r;
-        if (BALANCE && mine != kNone) {
-          atomicAdd(counts + id, 1);
+        a.ids[at + team.lane] = mine.is() ? (int)mine.place() : -1;
+        a.gamma[at + team.lane] = mine.is() ? e * r : 0.f;
+        if (BALANCE && mine.is()) {
+          atomicAdd(counts + mine.place(), 1);
           ++kept;
         }
       }
@@ -413,19 +434,22 @@ __global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs 
   uint32_t turn = 0;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1, duty = duty + 1 == team.all ? 0 : duty + 1) {
     Row<T, V, NV> row[1];
-    const bool on = feed.next(row);
-    if (!on) row[0].fill(none);
-    Best<T, V, NV, F> best;
-    best.start(row[0], feed, on, m > 1);
-    uint32_t first = kNone, o = kNone, c = 0;
+    if (!feed.next(row)) row[0].fill(none);
+    Best<T, V, NV, 32, F> best;
+    best.start(row[0], feed, m > 1);
+    Key<T> first = Key<T>::none(), tth = Key<T>::none();
+#pragma unroll 1
     for (int t = 0; t < m; ++t) {
-      o = best.order, c = best.col;
-      team_best<T, 32>(o, c);
-      if (t == 0) first = o;
-      if (l == t) lists[turn][w * kMaxTop + t] = o == kNone ? 0 : (uint64_t)o << 32 | (uint32_t)~c;
-      if (t + 1 < m && o != kNone && c == best.col) best.pop(feed);  // columns are one lane's
+      const Key<T> k = best.key.template best<32>();
+      if (t == 0) first = k;
+      if (l == t) tth = k;
+      if (t + 1 < m && k.is() && k.same(best.key)) best.pop(feed);
     }
-    const float mine = first == kNone ? -INFINITY : unordered(first);
+    if (l < m) {
+      const int v = (int)tth.place() / V, c = ((v / 32) * team.size + w * 32 + v % 32) * V + (int)tth.place() % V;
+      lists[turn][w * kMaxTop + l] = tth.is() ? (uint64_t)tth.order() << 32 | (uint32_t)~c : 0;
+    }
+    const float mine = first.is() ? unordered(first.order()) : -INFINITY;
     float2 x[P];
     row[0].get(x);
     exponentials(x, Base(mine, kLog2E), kLog2E);
