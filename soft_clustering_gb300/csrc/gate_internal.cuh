@@ -26,20 +26,26 @@ inline bool wide(int64_t width, const P*... p) {
   return width % kWide<T> == 0 && aligned(16, (const char*)p...);
 }
 
-// Two elements of a row in fp32, and back.
-__device__ __forceinline__ float2 to_f2(float a, float b) { return make_float2(a, b); }
-__device__ __forceinline__ float2 to_f2(__half a, __half b) { return __half22float2(__halves2half2(a, b)); }
-__device__ __forceinline__ float2 to_f2(__nv_bfloat16 a, __nv_bfloat16 b) {
-  return __bfloat1622float2(__halves2bfloat162(a, b));
-}
-__device__ __forceinline__ void from_f2(float2 f, float& a, float& b) { a = f.x, b = f.y; }
-__device__ __forceinline__ void from_f2(float2 f, __half& a, __half& b) {
-  const __half2 h = __float22half2_rn(f);
-  a = __low2half(h), b = __high2half(h);
-}
-__device__ __forceinline__ void from_f2(float2 f, __nv_bfloat16& a, __nv_bfloat16& b) {
-  const __nv_bfloat162 h = __float22bfloat162_rn(f);
-  a = __low2bfloat16(h), b = __high2bfloat16(h);
+// Two neighbouring elements as one word, in fp32, and back.
+template <typename T> struct PairOf { using type = float2; };
+template <> struct PairOf<__half> { using type = __half2; };
+template <> struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <typename T> using Pair = typename PairOf<T>::type;
+
+__device__ __forceinline__ float2 pair_of(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ __half2 pair_of(__half a, __half b) { return __halves2half2(a, b); }
+__device__ __forceinline__ __nv_bfloat162 pair_of(__nv_bfloat16 a, __nv_bfloat16 b) { return __halves2bfloat162(a, b); }
+__device__ __forceinline__ float2 to_f2(float2 a) { return a; }
+__device__ __forceinline__ float2 to_f2(__half2 a) { return __half22float2(a); }
+__device__ __forceinline__ float2 to_f2(__nv_bfloat162 a) { return __bfloat1622float2(a); }
+template <typename T> __device__ __forceinline__ Pair<T> from_f2(float2 f);
+template <> __device__ __forceinline__ float2 from_f2<float>(float2 f) { return f; }
+template <> __device__ __forceinline__ __half2 from_f2<__half>(float2 f) { return __float22half2_rn(f); }
+template <> __device__ __forceinline__ __nv_bfloat162 from_f2<__nv_bfloat16>(float2 f) { return __float22bfloat162_rn(f); }
+// Elements e and e + 1 of a vector (e even).
+template <typename T, int V> __device__ __forceinline__ Pair<T> pair_at(const Vec<T, V>& x, int e) {
+  static_assert(V % 2 == 0, "pairs");
+  return *reinterpret_cast<const Pair<T>*>(&x.v[e]);
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
@@ -71,13 +77,21 @@ struct Row {
   }
   __device__ __forceinline__ T& at(int i) { return r[i / V].v[i % V]; }
   __device__ __forceinline__ const T& at(int i) const { return r[i / V].v[i % V]; }
+  __device__ __forceinline__ Pair<T> pair(int i) const {  // elements 2 i and 2 i + 1
+    if constexpr (V == 1) return pair_of(at(2 * i), at(2 * i + 1));
+    else return pair_at(r[2 * i / V], 2 * i % V);
+  }
   __device__ __forceinline__ void get(float2 (&f)[E / 2]) const {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) f[i] = to_f2(at(2 * i), at(2 * i + 1));
+    for (int i = 0; i < E / 2; ++i) f[i] = to_f2(pair(i));
   }
   __device__ __forceinline__ void set(const float2 (&f)[E / 2]) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) from_f2(f[i], at(2 * i), at(2 * i + 1));
+    for (int i = 0; i < E / 2; ++i) {
+      const Pair<T> p = from_f2<T>(f[i]);
+      if constexpr (V == 1) at(2 * i) = reinterpret_cast<const T*>(&p)[0], at(2 * i + 1) = reinterpret_cast<const T*>(&p)[1];
+      else *reinterpret_cast<Pair<T>*>(&r[2 * i / V].v[2 * i % V]) = p;
+    }
   }
 };
 
@@ -276,16 +290,16 @@ __device__ __forceinline__ float lane_max(const Row<float, V, NV>& r) {
 }
 template <int V, int NV>
 __device__ __forceinline__ float lane_max(const Row<__half, V, NV>& r) {
-  __half2 m = __halves2half2(r.at(0), r.at(1));
+  __half2 m = r.pair(0);
 #pragma unroll
-  for (int i = 2; i < V * NV; i += 2) m = __hmax2_nan(m, __halves2half2(r.at(i), r.at(i + 1)));
+  for (int i = 1; i < V * NV / 2; ++i) m = __hmax2_nan(m, r.pair(i));
   return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
 }
 template <int V, int NV>
 __device__ __forceinline__ float lane_max(const Row<__nv_bfloat16, V, NV>& r) {
-  __nv_bfloat162 m = __halves2bfloat162(r.at(0), r.at(1));
+  __nv_bfloat162 m = r.pair(0);
 #pragma unroll
-  for (int i = 2; i < V * NV; i += 2) m = __hmax2_nan(m, __halves2bfloat162(r.at(i), r.at(i + 1)));
+  for (int i = 1; i < V * NV / 2; ++i) m = __hmax2_nan(m, r.pair(i));
   return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
 }
 // x -> 2^(x k - base) with base = top k rounded: its rounding is a factor that

@@ -27,57 +27,75 @@ size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
   return o;
 }
 
-// The blocks' sums in order, 32 columns a block, in 64 bits; the last block to
-// end adds up the loss.
+// The blocks' sums in a fixed order, 32 columns a block, in 64 bits: a warp reads
+// 32 columns of every 32nd block, then each column has a warp of its own.  The
+// last block to end adds up the loss.
 __global__ void __launch_bounds__(kFinishThreads)
 gate_finish_kernel(GateWs ws, int blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
                    float* __restrict__ share, float* __restrict__ loss) {
-  constexpr int R = kFinishThreads / kFinishColumns;
-  __shared__ double part[32], sums[R][kFinishColumns + 1];
-  __shared__ long long parti[32];
-  __shared__ int numbers[R][kFinishColumns + 1];
+  static_assert(kFinishThreads == 32 * kFinishColumns, "a warp a column");
+  __shared__ double sums[32][kFinishColumns + 1], terms[32];
+  __shared__ int numbers[32][kFinishColumns + 1], heads[2][32];
   __shared__ bool last;
-  long long rows = 0, all = 0;
-  for (int b = threadIdx.x; b < blocks; b += kFinishThreads) rows += ws.rows[b], all += ws.kept[b];
-  rows = block_reduce(rows, 0ll, SumOp(), parti);
-  all = block_reduce(all, 0ll, SumOp(), parti);
-  const int c = threadIdx.x % kFinishColumns, r = threadIdx.x / kFinishColumns;
-  const int k = blockIdx.x * kFinishColumns + c;
-  double s = 0.0;
-  int n = 0;
-  if (k < K)
-    for (int b = r; b < blocks; b += R) {
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int k = blockIdx.x * kFinishColumns + l;
+  double s = 0.0, s2 = 0.0;
+  int n = 0, rows = 0, all = 0;
+  if (threadIdx.x < blocks) rows = ws.rows[threadIdx.x], all = ws.kept[threadIdx.x];
+  if (k < K) {
+    int b = w;
+#pragma unroll 4
+    for (; b + 32 < blocks; b += 64) {
+      s += ws.mass[(size_t)b * K + k];
+      s2 += ws.mass[(size_t)(b + 32) * K + k];
+      n += ws.counts[(size_t)b * K + k] + ws.counts[(size_t)(b + 32) * K + k];
+    }
+    if (b < blocks) {
       s += ws.mass[(size_t)b * K + k];
       n += ws.counts[(size_t)b * K + k];
     }
-  sums[r][c] = s;
-  numbers[r][c] = n;
-  __syncthreads();
-  double term = 0.0;
-  if (r == 0 && k < K) {
-    long long count = 0;
-    s = 0.0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) s += sums[i][c], count += numbers[i][c];
-    const double f = rows > 0 && all > 0 ? (double)K * count / ((double)all * rows) : 0.0;
-    counts[k] = count;
-    mass[k] = (float)s;
-    share[k] = (float)f;
-    term = f * s;
   }
-  term = block_reduce(term, 0.0, SumOp(), part);
-  if (threadIdx.x == 0) {
-    ws.part[blockIdx.x] = term;
+  sums[w][l] = s + s2;
+  numbers[w][l] = n;
+  rows = __reduce_add_sync(0xffffffffu, rows);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (l == 0) heads[0][w] = rows, heads[1][w] = all;
+  __syncthreads();
+  rows = __reduce_add_sync(0xffffffffu, heads[0][l]);
+  all = __reduce_add_sync(0xffffffffu, heads[1][l]);
+  s = warp_reduce(sums[l][w], SumOp());
+  n = __reduce_add_sync(0xffffffffu, numbers[l][w]);
+  const int c = blockIdx.x * kFinishColumns + w;
+  if (l == 0) {
+    double f = 0.0;
+    if (c < K) {
+      f = rows > 0 && all > 0 ? (double)K * n / ((double)all * rows) : 0.0;
+      counts[c] = n;
+      mass[c] = (float)s;
+      share[c] = (float)f;
+      f *= s;
+    }
+    terms[w] = f;
+  }
+  __syncthreads();
+  if (w != 0) return;
+  s = warp_reduce(terms[l], SumOp());
+  if (gridDim.x == 1) {
+    if (l == 0) *loss = (float)s;
+    return;
+  }
+  if (l == 0) {
+    ws.part[blockIdx.x] = s;
     __threadfence();
     last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
   }
-  __syncthreads();
+  __syncwarp();
   if (!last) return;
   __threadfence();
   s = 0.0;
-  for (int b = threadIdx.x; b < gridDim.x; b += kFinishThreads) s += __ldcg(ws.part + b);
-  s = block_reduce(s, 0.0, SumOp(), part);
-  if (threadIdx.x == 0) *loss = (float)s;
+  for (int b = l; b < gridDim.x; b += 32) s += __ldcg(ws.part + b);
+  s = warp_reduce(s, SumOp());
+  if (l == 0) *loss = (float)s;
 }
 
 }  // namespace

@@ -74,15 +74,15 @@ template <int V> __device__ __forceinline__ float vector_max(const Vec<float, V>
   return m;
 }
 template <int V> __device__ __forceinline__ float vector_max(const Vec<__half, V>& x) {
-  __half2 m = __halves2half2(x.v[0], x.v[1]);
+  __half2 m = pair_at(x, 0);
 #pragma unroll
-  for (int e = 2; e < V; e += 2) m = __hmax2_nan(m, __halves2half2(x.v[e], x.v[e + 1]));
+  for (int e = 2; e < V; e += 2) m = __hmax2_nan(m, pair_at(x, e));
   return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
 }
 template <int V> __device__ __forceinline__ float vector_max(const Vec<__nv_bfloat16, V>& x) {
-  __nv_bfloat162 m = __halves2bfloat162(x.v[0], x.v[1]);
+  __nv_bfloat162 m = pair_at(x, 0);
 #pragma unroll
-  for (int e = 2; e < V; e += 2) m = __hmax2_nan(m, __halves2bfloat162(x.v[e], x.v[e + 1]));
+  for (int e = 2; e < V; e += 2) m = __hmax2_nan(m, pair_at(x, e));
   return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
 }
 
@@ -106,7 +106,7 @@ template <int V> __device__ __forceinline__ int first_of(const Vec<__half, V>& x
   uint32_t bits = 0;
 #pragma unroll
   for (int e = 0; e < V; e += 2)
-    bits |= __heq2_mask(__halves2half2(x.v[e], x.v[e + 1]), t) & (1u << e | 1u << (16 + e + 1));
+    bits |= __heq2_mask(pair_at(x, e), t) & (1u << e | 1u << (16 + e + 1));
   return first_bit(bits);
 }
 template <int V> __device__ __forceinline__ int first_of(const Vec<__nv_bfloat16, V>& x, float m) {
@@ -115,7 +115,7 @@ template <int V> __device__ __forceinline__ int first_of(const Vec<__nv_bfloat16
   uint32_t bits = 0;
 #pragma unroll
   for (int e = 0; e < V; e += 2)
-    bits |= __heq2_mask(__halves2bfloat162(x.v[e], x.v[e + 1]), t) & (1u << e | 1u << (16 + e + 1));
+    bits |= __heq2_mask(pair_at(x, e), t) & (1u << e | 1u << (16 + e + 1));
   return first_bit(bits);
 }
 
@@ -212,13 +212,15 @@ struct Best {
     for (int i = 0; i < N; ++i)
       if (i == j) o[i] = left;
   }
-  __device__ __forceinline__ void pop(const F& feed) {
-    if (second) {
-      key = next;
-      second = false;
-    } else {
-      drop(feed);
-      key = pick(feed);
+  // Takes the best away from the lane that `won` (all of the warp call it).
+  __device__ __forceinline__ void pop(const F& feed, bool won) {
+    const bool look = won && !second;
+    if (won) key = next, second = false;
+    if (__any_sync(0xffffffffu, look)) {
+      if (look) {
+        drop(feed);
+        key = pick(feed);
+      }
     }
   }
 };
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
           atomicAdd(counts + k.place(), 1);
           ++kept;
         }
-        if (t + 1 < m && k.is()) best.pop(feed);
+        if (t + 1 < m) best.pop(feed, k.is());
       }
     } else {
 #pragma unroll 1
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
         const Key<T> k = best.key.template best<S>();
         if (t == 0) first = k;
         if (team.lane == t) mine = k;
-        if (t + 1 < m && k.is() && k.same(best.key)) best.pop(feed);  // places are one lane's
+        if (t + 1 < m) best.pop(feed, k.is() && k.same(best.key));  // places are one lane's
       }
     }
     const bool some = first.is();
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs 
       const Key<T> k = best.key.template best<32>();
       if (t == 0) first = k;
       if (l == t) tth = k;
-      if (t + 1 < m && k.is() && k.same(best.key)) best.pop(feed);
+      if (t + 1 < m) best.pop(feed, k.is() && k.same(best.key));
     }
     if (l < m) {
       const int v = (int)tth.place() / V, c = ((v / 32) * team.size + w * 32 + v % 32) * V + (int)tth.place() % V;
