@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
   const T* L = (const T*)a.L + n * K;
   T* d = (T*)a.dL + n * K;
   float wn = a.weights && n < a.N ? a.weights[n] : 1.f;
-  double losses = 0.0;
+  Sum2 losses;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
     Row<T, V, NV> row[1];
     const bool on = feed.next(row);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
     if (team.lane == 0 && n < a.N) {
       const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
       a.rows[n] = r;
-      losses += r;
+      losses.add(r);
     }
     if (!a.dL) continue;
     const float c = a.scale * w * a.T, rsum = rsum_of(s[0]);
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
       e.template store<T>([&](int i) { return d + i; });
     }
   }
-  store_total(a, losses);
+  store_total(a, losses.value());
 }
 
 // The last warp has the entries, and no part of the row: what it waits for and
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
   const float k = kLog2E * a.inv;
   const T none = from_f<T>(-INFINITY);
   uint32_t turn = 0;
-  double losses = 0.0;
+  Sum2 losses;
   const int64_t step = (int64_t)gridDim.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   if ((int)threadIdx.x >= team.size) {
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
       if (warp.lane == 0) {
         const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
         a.rows[n] = r;
-        losses += r;
+        losses.add(r);
       }
       if (a.dL) {
         e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]),
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
     }
     __syncthreads();
   }
-  store_total(a, losses);
+  store_total(a, losses.value());
 }
 
 template <typename T>
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
   const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   uint32_t turn = 0;
-  double losses = 0.0;
+  Sum2 losses;
   if ((int)threadIdx.x >= kStreamThreads) {
     const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
     Entries<MT> ahead, late;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
       if (warp.lane == 0) {
         const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
         a.rows[n] = r;
-        losses += r;
+        losses.add(r);
       }
       if (a.dL) {
         e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]),
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
     }
     __syncthreads();
   }
-  store_total(a, losses);
+  store_total(a, losses.value());
 }
 
 // The blocks' sums in order, in 64 bits.

@@ -34,28 +34,23 @@ __global__ void __launch_bounds__(kFinishThreads)
 gate_finish_kernel(GateWs ws, int blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
                    float* __restrict__ share, float* __restrict__ loss) {
   static_assert(kFinishThreads == 32 * kFinishColumns, "a warp a column");
-  __shared__ double sums[32][kFinishColumns + 1], terms[32];
+  __shared__ Sum2 sums[32][kFinishColumns + 1];
+  __shared__ double terms[32];
   __shared__ int numbers[32][kFinishColumns + 1], heads[2][32];
   __shared__ bool last;
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int k = blockIdx.x * kFinishColumns + l;
-  double s = 0.0, s2 = 0.0;
+  Sum2 sum;
   int n = 0, rows = 0, all = 0;
   if (threadIdx.x < blocks) rows = ws.rows[threadIdx.x], all = ws.kept[threadIdx.x];
   if (k < K) {
-    int b = w;
 #pragma unroll 4
-    for (; b + 32 < blocks; b += 64) {
-      s += ws.mass[(size_t)b * K + k];
-      s2 += ws.mass[(size_t)(b + 32) * K + k];
-      n += ws.counts[(size_t)b * K + k] + ws.counts[(size_t)(b + 32) * K + k];
-    }
-    if (b < blocks) {
-      s += ws.mass[(size_t)b * K + k];
+    for (int b = w; b < blocks; b += 32) {
+      sum.add(ws.mass[(size_t)b * K + k]);
       n += ws.counts[(size_t)b * K + k];
     }
   }
-  sums[w][l] = s + s2;
+  sums[w][l] = sum;
   numbers[w][l] = n;
   rows = __reduce_add_sync(0xffffffffu, rows);
   all = __reduce_add_sync(0xffffffffu, all);
@@ -63,7 +58,7 @@ gate_finish_kernel(GateWs ws, int blocks, int K, int64_t* __restrict__ counts, f
   __syncthreads();
   rows = __reduce_add_sync(0xffffffffu, heads[0][l]);
   all = __reduce_add_sync(0xffffffffu, heads[1][l]);
-  s = warp_reduce(sums[l][w], SumOp());
+  double s = warp_reduce(sums[l][w].value(), SumOp());
   n = __reduce_add_sync(0xffffffffu, numbers[l][w]);
   const int c = blockIdx.x * kFinishColumns + w;
   if (l == 0) {

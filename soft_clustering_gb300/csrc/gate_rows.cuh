@@ -626,7 +626,8 @@ int64_t launch_lanes(const GateArgs& a, cudaStream_t s) {
   using F = Feed<T, V, NV, 1, LiveRows>;
   const size_t feed = F::bytes(kGateWarpThreads);
   const int64_t rows = kGateWarpThreads / S, need = (a.N + rows - 1) / rows;
-  const int64_t grid = need < 1 ? 1 : need < kGateGrid ? need : kGateGrid;
+  const int64_t most = a.balance ? kGateGrid : 2 * kGateGrid;  // short blocks where none keeps sums
+  const int64_t grid = need < 1 ? 1 : need < most ? need : most;
   if (a.balance) {
     if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, true>, feed + 8 * E * S, done[1])) return 0;
     gate_warp_kernel<T, V, NV, S, true><<<(unsigned)grid, kGateWarpThreads, feed + 8 * a.K, s>>>(a);

@@ -248,26 +248,27 @@ __global__ void __launch_bounds__(kBlockThreads) norm_grad_block_kernel(Args a, 
   if (CLUSTER) cluster_barrier();  // nothing is on its way to a block that has ended
 }
 
-// The blocks' sums in order, 32 columns a block, in 64 bits.
+// The blocks' sums in a fixed order, 32 columns a block: a warp reads 32 columns
+// of every 32nd block, then each column has a warp of its own.
 template <typename W>
 __global__ void __launch_bounds__(kFinishThreads)
 norm_finish_kernel(const float* __restrict__ sums, int blocks, int D, W* __restrict__ dweight,
                    W* __restrict__ dbias) {
-  constexpr int R = kFinishThreads / kFinishColumns;
-  __shared__ double part[R][kFinishColumns + 1];
-  const int c = threadIdx.x % kFinishColumns, r = threadIdx.x / kFinishColumns;
-  const int i = blockIdx.x * kFinishColumns + c;
-  double s = 0.0;
+  static_assert(kFinishThreads == 32 * kFinishColumns, "a warp a column");
+  __shared__ Sum2 part[32][kFinishColumns + 1];
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int i = blockIdx.x * kFinishColumns + l;
+  Sum2 s;
   if (i < 2 * D)
-    for (int b = r; b < blocks; b += R) s += sums[(size_t)b * 2 * D + i];
-  part[r][c] = s;
+#pragma unroll 4
+    for (int b = w; b < blocks; b += 32) s.add(sums[(size_t)b * 2 * D + i]);
+  part[w][l] = s;
   __syncthreads();
-  if (r == 0 && i < 2 * D) {
-    s = 0.0;
-#pragma unroll
-    for (int k = 0; k < R; ++k) s += part[k][c];
-    if (i < D) dweight[i] = from_f<W>((float)s);
-    else dbias[i - D] = from_f<W>((float)s);
+  const float all = warp_reduce(part[l][w].s, SumOp()) + warp_reduce(part[l][w].left, SumOp());
+  const int c = blockIdx.x * kFinishColumns + w;
+  if (l == 0 && c < 2 * D) {
+    if (c < D) dweight[c] = from_f<W>(all);
+    else dbias[c - D] = from_f<W>(all);
   }
 }
 
