@@ -214,20 +214,25 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
   int64_t n = warp * per + l / size;
   F feed;
   feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, size, nv, none, WeightedRows{a.weights});
-  Entries<MT> ahead;
-  ahead.fetch(a, n, team.lane, size);
+  // ids and values come two rows ahead (eight a lane: one)
+  constexpr int D = MT == 1 ? 2 : 1;
+  Entries<MT> ahead[D];
+#pragma unroll
+  for (int i = 0; i < D; ++i) ahead[i].fetch(a, n + i * stride, team.lane, size);
   const T* L = (const T*)a.L + n * K;
   T* d = (T*)a.dL + n * K;
-  float wn = a.weights && n < a.N ? a.weights[n] : 1.f;
+  float wn = a.weights && n < a.N ? a.weights[n] : 1.f, wnn = a.weights && n + stride < a.N ? a.weights[n + stride] : 1.f;
   Sum2 losses;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
     Row<T, V, NV> row[1];
     const bool on = feed.next(row);
-    Entries<MT> e = ahead;
+    Entries<MT> e = ahead[0];
     e.check(a, on);
-    ahead.fetch(a, n + stride, team.lane, size);
+    ahead[0] = ahead[D - 1];
+    ahead[D - 1].fetch(a, n + D * stride, team.lane, size);
     const float w = wn;
-    if (a.weights && n + stride < a.N) wn = a.weights[n + stride];
+    wn = wnn;
+    if (a.weights && n + 2 * stride < a.N) wnn = a.weights[n + 2 * stride];
     bool twice;
     if constexpr (F::kAsync) {
       __syncwarp();
@@ -297,9 +302,62 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
   store_total(a, losses.value());
 }
 
-// The last warp has the entries, and no part of the row: what it waits for and
-// works out goes beside the others' work.  It puts a row's elements right after
-// the next row's barrier, before which the others have stored the row.
+// The entries' warp of a block, the last one, which has no part of the row: what
+// it waits for and works out goes beside the others' work.  Entries come two rows
+// and the student's logits at them one row ahead.  It puts a row's elements right
+// after the next row's barrier, before which the others have stored the row.
+template <typename T, int MT>
+__device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<false>& team, int* some_s) {
+  const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
+  const int64_t stride = gridDim.x, step = stride * a.K;
+  const T* L = (const T*)a.L + (int64_t)blockIdx.x * a.K;
+  T* d = (T*)a.dL + (int64_t)blockIdx.x * a.K;
+  const float k = kLog2E * a.inv;
+  auto weight = [&](int64_t n) { return n >= a.N ? 0.f : a.weights ? a.weights[n] : 1.f; };
+  Entries<MT> next, ahead, late;
+  float w = weight(blockIdx.x), w_next = weight(blockIdx.x + stride);
+  ahead.fetch(a, blockIdx.x, warp.lane, 32);
+  next = ahead;
+  next.check(a, w != 0.f);
+  next.gather([&](int i) { return L + i; });
+  ahead.fetch(a, blockIdx.x + stride, warp.lane, 32);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) late.id[i] = -1;
+  Sum2 losses;
+  uint32_t turn = 0;
+  for (int64_t n = blockIdx.x; n < a.N; n += stride, L += step, d += step, turn ^= 1) {
+    Entries<MT> e = next;
+    e.gather_old(a, d);
+    float logsum, top, s[1];
+    const bool some = e.normalise(warp, logsum);
+    if (warp.lane == 0) some_s[turn] = some;
+    next = ahead;
+    next.check(a, w_next != 0.f);
+    next.gather([&](int i) { return L + step + i; });
+    ahead.fetch(a, n + 2 * stride, warp.lane, 32);
+    const float w_after = weight(n + 2 * stride);
+    __syncthreads();
+    if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
+    team.hear(s, top, 0.f, k);
+    const Base base(top, k);
+    const float divergence = e.divergence(warp, base, k);
+    if (warp.lane == 0) {
+      const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
+      a.rows[n] = r;
+      losses.add(r);
+    }
+    if (a.dL) {
+      e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]), e.twice(warp));
+      late = e;
+    }
+    w = w_next;
+    w_next = w_after;
+  }
+  __syncthreads();
+  if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
+  return losses;
+}
+
 template <typename T, int V, int NV, int MT>
 __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args a) {
   extern __shared__ __align__(16) char smem[];
@@ -315,42 +373,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
   const int64_t step = (int64_t)gridDim.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   if ((int)threadIdx.x >= team.size) {
-    const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
-    const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
-    Entries<MT> ahead, late;  // of the next row and of the last one
-    ahead.fetch(a, blockIdx.x, warp.lane, 32);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) late.id[i] = -1;
-    float wn = !a.weights || blockIdx.x >= a.N ? 1.f : a.weights[blockIdx.x];
-    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
-      const float w = wn;
-      Entries<MT> e = ahead;
-      e.check(a, w != 0.f);
-      e.gather([&](int i) { return L + i; });
-      e.gather_old(a, d);
-      ahead.fetch(a, n + gridDim.x, warp.lane, 32);
-      if (a.weights && n + gridDim.x < a.N) wn = a.weights[n + gridDim.x];
-      float logsum, top, s[1];
-      const bool some = e.normalise(warp, logsum);
-      if (warp.lane == 0) some_s[turn] = some;
-      __syncthreads();
-      if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
-      team.hear(s, top, 0.f, k);
-      const Base base(top, k);
-      const float divergence = e.divergence(warp, base, k);
-      if (warp.lane == 0) {
-        const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
-        a.rows[n] = r;
-        losses.add(r);
-      }
-      if (a.dL) {
-        e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]),
-                   e.twice(warp));
-        late = e;
-      }
-    }
-    __syncthreads();
-    if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
+    losses = entries_warp<T, MT>(a, team, some_s);
   } else {
     Feed<T, V, NV, 1, WeightedRows> feed;
     feed.start(smem, {(const T*)a.L}, blockIdx.x, gridDim.x, a.N, K, team.lane, team.size, nv, none,
@@ -412,39 +435,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
   uint32_t turn = 0;
   Sum2 losses;
   if ((int)threadIdx.x >= kStreamThreads) {
-    const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
-    Entries<MT> ahead, late;
-    ahead.fetch(a, blockIdx.x, warp.lane, 32);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) late.id[i] = -1;
-    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
-      const float w = a.weights ? a.weights[n] : 1.f;
-      Entries<MT> e = ahead;
-      e.check(a, w != 0.f);
-      e.gather([&](int i) { return L + i; });
-      e.gather_old(a, d);
-      ahead.fetch(a, n + gridDim.x, warp.lane, 32);
-      float logsum, top, s[1];
-      const bool some = e.normalise(warp, logsum);
-      if (warp.lane == 0) some_s[turn] = some;
-      __syncthreads();
-      if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
-      team.hear(s, top, 0.f, k);
-      const Base base(top, k);
-      const float divergence = e.divergence(warp, base, k);
-      if (warp.lane == 0) {
-        const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
-        a.rows[n] = r;
-        losses.add(r);
-      }
-      if (a.dL) {
-        e.gradient(warp, a.m, a.scale * w * a.T, base, k, rsum_of(s[0]),
-                   e.twice(warp));
-        late = e;
-      }
-    }
-    __syncthreads();
-    if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
+    losses = entries_warp<T, MT>(a, team, some_s);
   } else {
     const int t = threadIdx.x;
     Stream<T> feed;

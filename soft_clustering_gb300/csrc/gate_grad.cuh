@@ -168,16 +168,20 @@ __global__ void __launch_bounds__(kWarpThreads) grad_warp_kernel(GradArgs a) {
   if constexpr (SHARE) load_columns<V, NV>(c, a.share, team.lane, S, nv, 0.f);
   F feed;
   feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, S, nv, none, LiveRows{a.live});
-  Entries<MT> ahead;
-  ahead.fetch(a, n, team.lane, S);
+  // ids and shares come two rows ahead (eight a lane: one)
+  constexpr int D = MT == 1 ? 2 : 1;
+  Entries<MT> ahead[D];
+#pragma unroll
+  for (int i = 0; i < D; ++i) ahead[i].fetch(a, n + i * stride, team.lane, S);
   const T* L = (const T*)a.L + n * K;
   T* d = (T*)a.dL + n * K;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
     Row<T, V, NV> row[1];
     const bool on = feed.next(row);
-    Entries<MT> e = ahead;
+    Entries<MT> e = ahead[0];
     const float sum_v = e.check(a, team, on);
-    ahead.fetch(a, n + stride, team.lane, S);
+    ahead[0] = ahead[D - 1];
+    ahead[D - 1].fetch(a, n + D * stride, team.lane, S);
     if constexpr (F::kAsync) {
       __syncwarp();
       e.gather([&](int i) { return feed.peer(i); });

@@ -128,8 +128,8 @@ struct Feed {
   char* slot;         // this thread's, [stage][array][vector][thread] of 16 bytes
   uint32_t stage;
   Rows rows;
-  int64_t row, stride;  // the next one to be fetched (of masked rows alone)
-  bool on;              // and whether it is
+  int64_t row, stride;  // two behind the next one to be fetched (of masked rows alone)
+  bool on, later;       // whether the next one is, and the one after it: known two rows ahead
   uint32_t were;        // whether the last ones were, a bit each
   Row<T, V, NV> ahead[kAsync ? 1 : NA];
 
@@ -140,7 +140,11 @@ struct Feed {
     lane = lane_, size = size_, nv = nv_, stage = 0, step = stride_ * width;
     rows = rows_, row = row_, stride = stride_, were = 0;
     left = row < N ? (int)((N - row + stride - 1) / stride) : 0;
-    on = left > 0 && rows(row);
+    if (Rows::kMasked) {
+      on = left > 0 && rows(row);
+      later = left > 1 && rows(row + stride);
+      row += 2 * stride;
+    }
 #pragma unroll
     for (int a = 0; a < NA; ++a) from[a] = array[a] + row_ * width + (int64_t)lane * V;
 #pragma unroll
@@ -179,8 +183,9 @@ struct Feed {
     if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
     --left;
     if (Rows::kMasked) {
+      on = later;
+      later = left > 1 && rows(row);
       row += stride;
-      on = left > 0 && rows(row);
     }
 #pragma unroll
     for (int a = 0; a < NA; ++a) from[a] += step;
@@ -353,7 +358,8 @@ struct Sum2 {
     left += (s - (t - z)) + (v - z);
     s = t;
   }
-  __device__ __forceinline__ double value() const { return (double)s + left; }
+  // an infinite sum leaves NaN, which is not its value
+  __device__ __forceinline__ double value() const { return isfinite(s) ? (double)s + left : (double)s; }
 };
 
 struct MaxOp {

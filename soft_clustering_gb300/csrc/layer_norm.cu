@@ -264,7 +264,8 @@ norm_finish_kernel(const float* __restrict__ sums, int blocks, int D, W* __restr
     for (int b = w; b < blocks; b += 32) s.add(sums[(size_t)b * 2 * D + i]);
   part[w][l] = s;
   __syncthreads();
-  const float all = warp_reduce(part[l][w].s, SumOp()) + warp_reduce(part[l][w].left, SumOp());
+  const float sum = warp_reduce(part[l][w].s, SumOp()), left = warp_reduce(part[l][w].left, SumOp());
+  const float all = isfinite(sum) ? sum + left : sum;
   const int c = blockIdx.x * kFinishColumns + w;
   if (l == 0 && c < 2 * D) {
     if (c < D) dweight[c] = from_f<W>(all);
