@@ -8,11 +8,13 @@ namespace {
 
 using namespace gate;
 
-constexpr int kFinishColumns = 32;
+constexpr int kFinishColumns = 8;
 constexpr int kFinishThreads = 1024;
+constexpr int kFinishRows = kFinishThreads / kFinishColumns;
 
 size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
-  const int64_t b = N < 1 ? 1 : N < kGateGrid ? N : kGateGrid;
+  const int most = gate_blocks(K);
+  const int64_t b = N < 1 ? 1 : N < most ? N : most;
   size_t o = 0;
   auto take = [&](size_t n) { const size_t at = o; o += align_up(n); return (char*)base + at; };
   GateWs t;
@@ -27,54 +29,59 @@ size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
   return o;
 }
 
-// The blocks' sums in a fixed order, 32 columns a block, in 64 bits: a warp reads
-// 32 columns of every 32nd block, then each column has a warp of its own.  The
-// last block to end adds up the loss.
+// The blocks' sums in a fixed order, 8 columns a block (a sector): 128 threads a
+// column over the blocks, then a warp for each.  The last block to end adds up
+// the loss.
 __global__ void __launch_bounds__(kFinishThreads)
-gate_finish_kernel(GateWs ws, int blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
+gate_finish_kernel(GateWs ws, GateBlocks blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
                    float* __restrict__ share, float* __restrict__ loss) {
-  static_assert(kFinishThreads == 32 * kFinishColumns, "a warp a column");
-  __shared__ Sum2 sums[32][kFinishColumns + 1];
+  __shared__ Sum2 sums[kFinishRows][kFinishColumns + 1];
   __shared__ double terms[32];
-  __shared__ int numbers[32][kFinishColumns + 1], heads[2][32];
+  __shared__ int numbers[kFinishRows][kFinishColumns + 1], heads[2][32];
   __shared__ bool last;
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int k = blockIdx.x * kFinishColumns + l;
+  const int column = threadIdx.x % kFinishColumns, row = threadIdx.x / kFinishColumns;
+  const int k = blockIdx.x * kFinishColumns + column;
   Sum2 sum;
   int n = 0, rows = 0, all = 0;
-  if (threadIdx.x < blocks) rows = ws.rows[threadIdx.x], all = ws.kept[threadIdx.x];
+  for (int b = threadIdx.x; b < blocks.heads; b += kFinishThreads) rows += ws.rows[b], all += ws.kept[b];
   if (k < K) {
 #pragma unroll 4
-    for (int b = w; b < blocks; b += 32) {
-      sum.add(ws.mass[(size_t)b * K + k]);
-      n += ws.counts[(size_t)b * K + k];
-    }
+    for (int b = row; b < blocks.mass; b += kFinishRows) sum.add(ws.mass[(size_t)b * K + k]);
+#pragma unroll 4
+    for (int b = row; b < blocks.counts; b += kFinishRows) n += ws.counts[(size_t)b * K + k];
   }
-  sums[w][l] = sum;
-  numbers[w][l] = n;
+  sums[row][column] = sum;
+  numbers[row][column] = n;
   rows = __reduce_add_sync(0xffffffffu, rows);
   all = __reduce_add_sync(0xffffffffu, all);
   if (l == 0) heads[0][w] = rows, heads[1][w] = all;
   __syncthreads();
-  rows = __reduce_add_sync(0xffffffffu, heads[0][l]);
-  all = __reduce_add_sync(0xffffffffu, heads[1][l]);
-  double s = warp_reduce(sums[l][w].value(), SumOp());
-  n = __reduce_add_sync(0xffffffffu, numbers[l][w]);
-  const int c = blockIdx.x * kFinishColumns + w;
-  if (l == 0) {
-    double f = 0.0;
-    if (c < K) {
-      f = rows > 0 && all > 0 ? (double)K * n / ((double)all * rows) : 0.0;
-      counts[c] = n;
-      mass[c] = (float)s;
-      share[c] = (float)f;
-      f *= s;
+  if (w < kFinishColumns) {
+    rows = __reduce_add_sync(0xffffffffu, heads[0][l]);
+    all = __reduce_add_sync(0xffffffffu, heads[1][l]);
+    double s = 0.0;
+    n = 0;
+#pragma unroll
+    for (int i = l; i < kFinishRows; i += 32) s += sums[i][w].value(), n += numbers[i][w];
+    s = warp_reduce(s, SumOp());
+    n = __reduce_add_sync(0xffffffffu, n);
+    const int c = blockIdx.x * kFinishColumns + w;
+    if (l == 0) {
+      double f = 0.0;
+      if (c < K) {
+        f = rows > 0 && all > 0 ? (double)K * n / ((double)all * rows) : 0.0;
+        counts[c] = n;
+        mass[c] = (float)s;
+        share[c] = (float)f;
+        f *= s;
+      }
+      terms[w] = f;
     }
-    terms[w] = f;
   }
   __syncthreads();
   if (w != 0) return;
-  s = warp_reduce(terms[l], SumOp());
+  double s = warp_reduce(l < kFinishColumns ? terms[l] : 0.0, SumOp());
   if (gridDim.x == 1) {
     if (l == 0) *loss = (float)s;
     return;
@@ -128,18 +135,18 @@ gmm_status gmm_gate(const void* L, gmm_dtype xdtype, int64_t N, int K, int m, in
   if (N == 0 && !outs) return GMM_OK;
   cudaStream_t s = (cudaStream_t)stream;
   const GateArgs a{L, live, ids, gamma, lse, N, K, m, flags & GMM_GATE_NORMALISED, outs != 0, w};
-  int64_t blocks;
+  GateBlocks blocks;
   {
     ProfScope p("gate_kernel", s);
     blocks = xdtype == GMM_F32   ? launch_gate_f32(a, s)
              : xdtype == GMM_F16 ? launch_gate_f16(a, s)
                                  : launch_gate_bf16(a, s);
   }
-  if (!blocks) return GMM_ERR_CUDA;
+  if (!blocks.heads) return GMM_ERR_CUDA;
   if (outs) {
     ProfScope p("gate_finish_kernel", s);
     gate_finish_kernel<<<(K + kFinishColumns - 1) / kFinishColumns, kFinishThreads, 0, s>>>(
-        w, (int)blocks, K, counts, mass, share, loss);
+        w, blocks, K, counts, mass, share, loss);
   }
   return launched();
 }

@@ -27,14 +27,21 @@ namespace gate {
 
 constexpr int kGateWarpThreads = 256;
 constexpr int kGateBlockThreads = 512;
-constexpr int kGateGrid = 4 * kSms;     // blocks, at most
 constexpr int kGateStreamGrid = 2 * kSms;
+constexpr int kGateMassBlocks = 16;  // stretches of rows that are streamed
+// Blocks that keep sums, at most: as many as fit a multiprocessor.
+inline int gate_blocks(int K) { return (K <= 512 ? 4 : K <= 1100 ? 8 : K <= 4096 ? 4 : K <= 8192 ? 2 : 1) * kSms; }
+
+// How many blocks left rows and entries, mass, and counts; none: a failure.
+struct GateBlocks {
+  int heads, mass, counts;
+};
 
 // A block's sums of the balance outputs, and of rows that are streamed what
 // their second reading takes.
 struct GateWs {
   float* mass;       // blocks * K
-  int32_t* counts;   // blocks * K
+  int32_t* counts;   // blocks * K (of streamed rows: K)
   int32_t* rows;     // blocks: rows that count
   int32_t* kept;     // blocks: entries
   double* part;      // of the finish's blocks
@@ -52,10 +59,9 @@ struct GateArgs {
   GateWs ws;
 };
 
-// Returns the blocks launched, 0 on failure.
-int64_t launch_gate_f32(const GateArgs& a, cudaStream_t s);
-int64_t launch_gate_f16(const GateArgs& a, cudaStream_t s);
-int64_t launch_gate_bf16(const GateArgs& a, cudaStream_t s);
+GateBlocks launch_gate_f32(const GateArgs& a, cudaStream_t s);
+GateBlocks launch_gate_f16(const GateArgs& a, cudaStream_t s);
+GateBlocks launch_gate_bf16(const GateArgs& a, cudaStream_t s);
 
 namespace rows_impl {
 
@@ -494,11 +500,7 @@ __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateA
   __shared__ uint64_t lists[2][16 * kMaxTop];
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5, K = a.K, m = a.m;
   BlockTeam<false> team(part, kGateBlockThreads);
-  int32_t* counts = a.balance ? a.ws.counts + (size_t)blockIdx.x * K : nullptr;
-  if (a.balance) {
-    for (int k = threadIdx.x; k < K; k += kGateBlockThreads) counts[k] = 0;
-    __syncthreads();
-  }
+  int32_t* counts = a.ws.counts;  // one for all blocks; sums of whole numbers have no order
   int rows = 0, kept = 0;
   uint32_t turn = 0;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
@@ -620,45 +622,44 @@ __global__ void __launch_bounds__(kMassThreads) gate_mass_kernel(GateArgs a, int
 }
 
 template <typename T, int V, int E, int S>
-int64_t launch_lanes(const GateArgs& a, cudaStream_t s) {
+GateBlocks launch_lanes(const GateArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done[2];
   constexpr int NV = E / V;
   using F = Feed<T, V, NV, 1, LiveRows>;
   const size_t feed = F::bytes(kGateWarpThreads);
   const int64_t rows = kGateWarpThreads / S, need = (a.N + rows - 1) / rows;
-  const int64_t most = a.balance ? kGateGrid : 2 * kGateGrid;  // short blocks where none keeps sums
+  const int64_t most = a.balance ? gate_blocks(E * S) : 8 * kSms;  // short blocks where none keeps sums
   const int64_t grid = need < 1 ? 1 : need < most ? need : most;
   if (a.balance) {
-    if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, true>, feed + 8 * E * S, done[1])) return 0;
+    if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, true>, feed + 8 * E * S, done[1])) return {};
     gate_warp_kernel<T, V, NV, S, true><<<(unsigned)grid, kGateWarpThreads, feed + 8 * a.K, s>>>(a);
   } else {
-    if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, false>, feed, done[0])) return 0;
+    if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, false>, feed, done[0])) return {};
     gate_warp_kernel<T, V, NV, S, false><<<(unsigned)grid, kGateWarpThreads, feed, s>>>(a);
   }
-  return grid;
+  return {(int)grid, (int)grid, (int)grid};
 }
 
 template <typename T, int V, int E>
-int64_t launch_block(const GateArgs& a, cudaStream_t s) {
+GateBlocks launch_block(const GateArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done[2];
   constexpr int NV = E / V;
   using F = Feed<T, V, NV, 1, LiveRows>;
   const int threads = ((a.K + E - 1) / E + 31) / 32 * 32;
-  const int resident = 640 / threads < 1 ? 1 : 640 / threads < 4 ? 640 / threads : 4;
-  const int64_t most = (int64_t)resident * kSms, grid = a.N < 1 ? 1 : a.N < most ? a.N : most;
+  const int64_t most = gate_blocks(a.K), grid = a.N < 1 ? 1 : a.N < most ? a.N : most;
   const size_t feed = F::bytes(threads);
   if (a.balance) {
-    if (!allow_smem((const void*)gate_block_kernel<T, V, NV, true>, F::bytes(kGateBlockThreads) + 4 * E * kGateBlockThreads, done[1])) return 0;
+    if (!allow_smem((const void*)gate_block_kernel<T, V, NV, true>, F::bytes(kGateBlockThreads) + 4 * E * kGateBlockThreads, done[1])) return {};
     gate_block_kernel<T, V, NV, true><<<(unsigned)grid, threads, feed + 4 * (size_t)a.K, s>>>(a);
   } else {
-    if (!allow_smem((const void*)gate_block_kernel<T, V, NV, false>, F::bytes(kGateBlockThreads), done[0])) return 0;
+    if (!allow_smem((const void*)gate_block_kernel<T, V, NV, false>, F::bytes(kGateBlockThreads), done[0])) return {};
     gate_block_kernel<T, V, NV, false><<<(unsigned)grid, threads, feed, s>>>(a);
   }
-  return grid;
+  return {(int)grid, (int)grid, (int)grid};
 }
 
 template <typename T>
-int64_t launch_gate(const GateArgs& a, cudaStream_t s) {
+GateBlocks launch_gate(const GateArgs& a, cudaStream_t s) {
   constexpr int V = kWide<T>;
   const int K = a.K;
   if (wide<T>(K, (const char*)a.L)) {
@@ -678,13 +679,14 @@ int64_t launch_gate(const GateArgs& a, cudaStream_t s) {
     if (K <= 16 * kGateBlockThreads) return launch_block<T, 1, 16>(a, s);
   }
   const int64_t grid = a.N < 1 ? 1 : a.N < kGateStreamGrid ? a.N : kGateStreamGrid;
+  if (a.balance && cudaMemsetAsync(a.ws.counts, 0, sizeof(int32_t) * (size_t)K, s) != cudaSuccess) return {};
   gate_stream_kernel<T><<<(unsigned)grid, kGateBlockThreads, 0, s>>>(a);
+  const int64_t blocks = grid < kGateMassBlocks ? grid : kGateMassBlocks;
   if (a.balance) {
-    const int64_t stretch = (a.N + grid - 1) / grid;
-    const dim3 g((K + kMassThreads - 1) / kMassThreads, (unsigned)grid);
-    gate_mass_kernel<T><<<g, kMassThreads, 0, s>>>(a, stretch);
+    const dim3 g((K + kMassThreads - 1) / kMassThreads, (unsigned)blocks);
+    gate_mass_kernel<T><<<g, kMassThreads, 0, s>>>(a, (a.N + blocks - 1) / blocks);
   }
-  return grid;
+  return {(int)grid, (int)blocks, 1};
 }
 
 }  // namespace rows_impl

@@ -3,6 +3,6 @@
 
 namespace gmm {
 namespace gate {
-int64_t launch_gate_bf16(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<__nv_bfloat16>(a, s); }
+GateBlocks launch_gate_bf16(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<__nv_bfloat16>(a, s); }
 }  // namespace gate
 }  // namespace gmm

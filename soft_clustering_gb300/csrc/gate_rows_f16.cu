@@ -3,6 +3,6 @@
 
 namespace gmm {
 namespace gate {
-int64_t launch_gate_f16(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<__half>(a, s); }
+GateBlocks launch_gate_f16(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<__half>(a, s); }
 }  // namespace gate
 }  // namespace gmm

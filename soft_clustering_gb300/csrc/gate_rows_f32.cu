@@ -3,6 +3,6 @@
 
 namespace gmm {
 namespace gate {
-int64_t launch_gate_f32(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<float>(a, s); }
+GateBlocks launch_gate_f32(const GateArgs& a, cudaStream_t s) { return rows_impl::launch_gate<float>(a, s); }
 }  // namespace gate
 }  // namespace gmm
