@@ -95,11 +95,11 @@ struct Row {
   }
 };
 
-// A lane's own vectors of the rows ahead, of NA arrays of one shape.  Wide ones
-// wait in shared memory, put there by asynchronous copies kStages - 1 rows before
-// they are used: the bytes in flight that HBM needs, without registers for them.
-// A lane reads what it copied itself, so there is nothing to synchronise.  Single
-// elements (rows that do not start on 16 bytes) wait in registers, one row ahead.
+// A lane's own vectors of the rows ahead, of NA arrays of one shape.  They wait in
+// shared memory, put there by asynchronous copies kStages - 1 rows before they are
+// used: the bytes in flight that HBM needs, without registers for them.  A lane
+// reads what it copied itself, so there is nothing to synchronise.  Single 16-bit
+// elements, for which there is no such copy, wait in registers, one row ahead.
 // Which rows are fetched at all.
 struct EveryRow {
   static constexpr bool kMasked = false;
@@ -118,10 +118,11 @@ struct WeightedRows {  // weights, or NULL
 
 template <typename T, int V, int NV, int NA, typename Rows = EveryRow>
 struct Feed {
-  static constexpr bool kAsync = sizeof(T) * V == 16;
+  static constexpr int kBytes = sizeof(T) * V;  // of a vector
+  static constexpr bool kAsync = kBytes >= 4;
   // 512 threads' rows fit a multiprocessor's shared memory
-  static constexpr int kStages = NA * NV >= 8 ? 3 : 4;
-  static constexpr size_t bytes(int threads) { return kAsync ? (size_t)kStages * NA * NV * threads * 16 : 0; }
+  static constexpr int kStages = NA * NV * kBytes >= 128 ? 3 : 4;
+  static constexpr size_t bytes(int threads) { return kAsync ? (size_t)kStages * NA * NV * threads * kBytes : 0; }
   const T* from[NA];  // the next row to be fetched, at this lane's first vector
   int64_t step;       // elements from a row to the next
   int left, size, lane, nv;
@@ -150,12 +151,12 @@ struct Feed {
 #pragma unroll
     for (int a = 0; a < (kAsync ? 1 : NA); ++a) ahead[a].fill(none);
     if constexpr (kAsync) {
-      slot = smem + threadIdx.x * 16;
+      slot = smem + threadIdx.x * kBytes;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (j * size + lane >= nv)
           for (int s = 0; s < kStages * NA; ++s)
-            *reinterpret_cast<Vec<T, V>*>(slot + (size_t)(s * NV + j) * blockDim.x * 16) = ahead[0].r[j];
+            *reinterpret_cast<Vec<T, V>*>(slot + (size_t)(s * NV + j) * blockDim.x * kBytes) = ahead[0].r[j];
 #pragma unroll
       for (int s = 0; s < kStages - 1; ++s) fetch(s);
     } else {
@@ -171,11 +172,15 @@ struct Feed {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (j * size + lane < nv) {
-            if constexpr (kAsync)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(
-                               slot + (size_t)((into * NA + a) * NV + j) * blockDim.x * 16)),
-                           "l"(from[a] + j * size * V)
-                           : "memory");
+            if constexpr (kAsync) {
+              const uint32_t to = (uint32_t)__cvta_generic_to_shared(
+                  slot + (size_t)((into * NA + a) * NV + j) * blockDim.x * kBytes);
+              if constexpr (kBytes == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from[a] + j * size * V) : "memory");
+              else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from[a] + j * size * V), "n"(kBytes)
+                             : "memory");
+            }
             else
               ahead[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(from[a] + j * size * V);
           }
@@ -196,12 +201,12 @@ struct Feed {
   __device__ __forceinline__ char* word(int j) const {
     static_assert(kAsync, "in shared memory");
     const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
-    return slot + (size_t)(s * NA * NV + j) * blockDim.x * 16;
+    return slot + (size_t)(s * NA * NV + j) * blockDim.x * kBytes;
   }
   __device__ __forceinline__ Vec<T, V> vector(int j) const { return *reinterpret_cast<const Vec<T, V>*>(word(j)); }
   __device__ __forceinline__ T* peer(int at) const {
     const int v = at / V, j = v / size;
-    return reinterpret_cast<T*>(word(j) + (v - j * size - lane) * 16) + at % V;
+    return reinterpret_cast<T*>(word(j) + (v - j * size - lane) * kBytes) + at % V;
   }
   __device__ __forceinline__ void put(const Row<T, V, NV>& r) const {
 #pragma unroll
@@ -221,7 +226,7 @@ struct Feed {
       for (int a = 0; a < NA; ++a)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-          out[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)((stage * NA + a) * NV + j) * blockDim.x * 16);
+          out[a].r[j] = *reinterpret_cast<const Vec<T, V>*>(slot + (size_t)((stage * NA + a) * NV + j) * blockDim.x * kBytes);
       stage = stage == kStages - 1 ? 0 : stage + 1;
     } else {
 #pragma unroll

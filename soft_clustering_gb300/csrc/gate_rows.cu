@@ -8,9 +8,8 @@ namespace {
 
 using namespace gate;
 
-constexpr int kFinishColumns = 8;
 constexpr int kFinishThreads = 1024;
-constexpr int kFinishRows = kFinishThreads / kFinishColumns;
+inline int finish_columns(int blocks, int K) { return blocks > 64 || K < 4096 ? 8 : 64; }
 
 size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
   const int most = gate_blocks(K);
@@ -19,7 +18,7 @@ size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
   auto take = [&](size_t n) { const size_t at = o; o += align_up(n); return (char*)base + at; };
   GateWs t;
   t.ticket = (uint32_t*)take(4);
-  t.part = (double*)take(sizeof(double) * ((K + kFinishColumns - 1) / kFinishColumns));
+  t.part = (double*)take(sizeof(double) * ((K + 7) / 8));
   t.rows = (int32_t*)take(sizeof(int32_t) * b);
   t.kept = (int32_t*)take(sizeof(int32_t) * b);
   t.mass = (float*)take(sizeof(float) * (size_t)b * K);
@@ -29,14 +28,16 @@ size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
   return o;
 }
 
-// The blocks' sums in a fixed order, 8 columns a block (a sector): 128 threads a
-// column over the blocks, then a warp for each.  The last block to end adds up
-// the loss.
+// The blocks' sums in a fixed order, 8 columns a block (a sector), of few blocks
+// 64: the threads of a column over the blocks, then a warp for each.  The last
+// block to end adds up the loss.
+template <int kFinishColumns>
 __global__ void __launch_bounds__(kFinishThreads)
 gate_finish_kernel(GateWs ws, GateBlocks blocks, int K, int64_t* __restrict__ counts, float* __restrict__ mass,
                    float* __restrict__ share, float* __restrict__ loss) {
+  constexpr int kFinishRows = kFinishThreads / kFinishColumns;
   __shared__ Sum2 sums[kFinishRows][kFinishColumns + 1];
-  __shared__ double terms[32];
+  __shared__ double terms[64];
   __shared__ int numbers[kFinishRows][kFinishColumns + 1], heads[2][32];
   __shared__ bool last;
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -57,16 +58,16 @@ gate_finish_kernel(GateWs ws, GateBlocks blocks, int K, int64_t* __restrict__ co
   all = __reduce_add_sync(0xffffffffu, all);
   if (l == 0) heads[0][w] = rows, heads[1][w] = all;
   __syncthreads();
-  if (w < kFinishColumns) {
+  for (int v = w; v < kFinishColumns; v += 32) {
     rows = __reduce_add_sync(0xffffffffu, heads[0][l]);
     all = __reduce_add_sync(0xffffffffu, heads[1][l]);
     double s = 0.0;
     n = 0;
 #pragma unroll
-    for (int i = l; i < kFinishRows; i += 32) s += sums[i][w].value(), n += numbers[i][w];
+    for (int i = l; i < kFinishRows; i += 32) s += sums[i][v].value(), n += numbers[i][v];
     s = warp_reduce(s, SumOp());
     n = __reduce_add_sync(0xffffffffu, n);
-    const int c = blockIdx.x * kFinishColumns + w;
+    const int c = blockIdx.x * kFinishColumns + v;
     if (l == 0) {
       double f = 0.0;
       if (c < K) {
@@ -76,12 +77,12 @@ gate_finish_kernel(GateWs ws, GateBlocks blocks, int K, int64_t* __restrict__ co
         share[c] = (float)f;
         f *= s;
       }
-      terms[w] = f;
+      terms[v] = f;
     }
   }
   __syncthreads();
   if (w != 0) return;
-  double s = warp_reduce(l < kFinishColumns ? terms[l] : 0.0, SumOp());
+  double s = warp_reduce((l < kFinishColumns ? terms[l] : 0.0) + (l + 32 < kFinishColumns ? terms[l + 32] : 0.0), SumOp());
   if (gridDim.x == 1) {
     if (l == 0) *loss = (float)s;
     return;
@@ -145,8 +146,11 @@ gmm_status gmm_gate(const void* L, gmm_dtype xdtype, int64_t N, int K, int m, in
   if (!blocks.heads) return GMM_ERR_CUDA;
   if (outs) {
     ProfScope p("gate_finish_kernel", s);
-    gate_finish_kernel<<<(K + kFinishColumns - 1) / kFinishColumns, kFinishThreads, 0, s>>>(
-        w, blocks, K, counts, mass, share, loss);
+    const int columns = finish_columns(blocks.mass, K), g = (K + columns - 1) / columns;
+    if (columns == 8)
+      gate_finish_kernel<8><<<g, kFinishThreads, 0, s>>>(w, blocks, K, counts, mass, share, loss);
+    else
+      gate_finish_kernel<64><<<g, kFinishThreads, 0, s>>>(w, blocks, K, counts, mass, share, loss);
   }
   return launched();
 }

@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs 
   store_counts(a, rows, kept);
 }
 
-// Rows that no block holds.  A thread's list of the m largest so far is kept
-// sorted; few logits of a long row pass its last one.
+// Rows that no block holds.  A warp keeps the m largest so far, lane t the t-th;
+// a batch is looked through only where its largest logits pass the last of them.
 template <typename T>
 __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateArgs a) {
   __shared__ float part[BlockTeam<false>::kWords];
@@ -506,25 +506,24 @@ __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateA
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
     const T* L = (const T*)a.L + n * K;
     const bool on = !a.live || a.live[n];
-    uint64_t list[kMaxTop];
-#pragma unroll
-    for (int t = 0; t < kMaxTop; ++t) list[t] = 0;
+    uint64_t list = 0, last = 0;  // lane t's, and the m-th
     float top = -INFINITY, sum = 0.f;
-    auto take = [&](float x, int c) {
-      const uint32_t o = order_of(x);
-      uint64_t key = (uint64_t)o << 32 | (uint32_t)~c;
-      uint64_t last = 0;
-#pragma unroll
-      for (int t = 0; t < kMaxTop; ++t)
-        if (t == m - 1) last = list[t];
-      if (o != kNone && key > last) {
-#pragma unroll
-        for (int t = 0; t < kMaxTop; ++t)
-          if (t < m && key > list[t]) {
-            const uint64_t was = list[t];
-            list[t] = key;
-            key = was;
-          }
+    // Takes what passes into the warp's list: `best(bound)` is a lane's largest
+    // key up to `bound`.
+    auto take = [&](auto best) {
+      uint64_t bound = ~0ull;
+      while (true) {
+        const uint64_t b = best(bound);
+        const uint32_t o = __reduce_max_sync(0xffffffffu, (uint32_t)(b >> 32));
+        const uint32_t c = __reduce_max_sync(0xffffffffu, (uint32_t)(b >> 32) == o ? (uint32_t)b : 0u);
+        const uint64_t won = (uint64_t)o << 32 | c;
+        if (o == kNone || won <= last) break;
+        const int at = __popc(__ballot_sync(0xffffffffu, l < m && list > won));
+        const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+        list = l == at ? won : l > at ? up : list;
+        if (l >= m) list = 0;
+        last = __shfl_sync(0xffffffffu, list, m - 1);
+        bound = won - 1;
       }
     };
     if (on) {
@@ -533,13 +532,16 @@ __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateA
       const int nv = (K - head) / V, tail = head + nv * V;
       const int t = threadIdx.x;
       const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;
-      if (edge >= 0) {
-        const float x = to_f(L[edge]);
-        take(x, edge);
-        top = x;
-        if (x != -INFINITY) sum = ex2((x - x) * kLog2E);
-      }
-      for (int v0 = t; v0 < nv; v0 += U * kGateBlockThreads) {
+      const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
+      take([&](uint64_t bound) {
+        const uint64_t key = (uint64_t)order_of(xe) << 32 | (uint32_t)~edge;
+        return key <= bound && order_of(xe) != kNone ? key : 0ull;
+      });
+      top = xe;
+      if (xe != -INFINITY) sum = ex2((xe - xe) * kLog2E);
+      const int turns = (nv + U * kGateBlockThreads - 1) / (U * kGateBlockThreads);
+      for (int i = 0; i < turns; ++i) {
+        const int v0 = i * U * kGateBlockThreads + t;
         Row<T, V, U> x;
         x.fill(from_f<T>(-INFINITY));
         x.read(L + head + (int64_t)(v0 - t) * V, t, kGateBlockThreads, nv - (v0 - t));
@@ -548,39 +550,26 @@ __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateA
           sum *= BlockTeam<false>::between(top, to, kLog2E);
           top = to;
         }
-        uint64_t last = 0;
+        if (__any_sync(0xffffffffu, order_of(high) != kNone && order_of(high) >= (uint32_t)(last >> 32)))
+          take([&](uint64_t bound) {
+            uint64_t best = 0;
 #pragma unroll
-        for (int i = 0; i < kMaxTop; ++i)
-          if (i == m - 1) last = list[i];
-        if (order_of(high) >= (uint32_t)(last >> 32) && order_of(high) != kNone) {
-#pragma unroll 1
-          for (int u = 0; u < U; ++u) {
-            Vec<T, V> y = x.r[0];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 1; i < U; ++i)
-              if (i == u) y = x.r[i];
-#pragma unroll
-            for (int e = 0; e < V; ++e) take(to_f(y.v[e]), head + (v0 + u * kGateBlockThreads) * V + e);
-          }
-        }
+              for (int e = 0; e < V; ++e) {
+                const uint32_t o = order_of(to_f(x.r[u].v[e]));
+                const uint64_t key = (uint64_t)o << 32 | (uint32_t)~(head + (v0 + u * kGateBlockThreads) * V + e);
+                if (o != kNone && key <= bound && key > best) best = key;
+              }
+            return best;
+          });
         float2 f[U * V / 2];
         x.get(f);
         exponentials(f, Base(top, kLog2E), kLog2E);
         sum += total(f);
       }
     }
-    // the warp's list, one round each
-    for (int t = 0; t < m; ++t) {
-      const uint32_t o = __reduce_max_sync(0xffffffffu, (uint32_t)(list[0] >> 32));
-      const uint32_t c = __reduce_max_sync(0xffffffffu, (uint32_t)(list[0] >> 32) == o ? (uint32_t)list[0] : 0u);
-      const uint64_t won = (uint64_t)o << 32 | c;
-      if (l == 0) lists[turn][w * kMaxTop + t] = o == kNone ? 0 : won;
-      if (list[0] == won) {
-#pragma unroll
-        for (int i = 0; i + 1 < kMaxTop; ++i) list[i] = list[i + 1];
-        list[kMaxTop - 1] = 0;
-      }
-    }
+    if (l < m) lists[turn][w * kMaxTop + l] = list;
     const float mine = warp_max(top);
     float s[1] = {sum * BlockTeam<false>::between(top, mine == -INFINITY ? 0.f : mine, kLog2E)};
     team.tell(s, mine);
