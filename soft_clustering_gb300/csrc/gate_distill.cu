@@ -214,25 +214,20 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
   int64_t n = warp * per + l / size;
   F feed;
   feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, size, nv, none, WeightedRows{a.weights});
-  // ids and values come two rows ahead (eight a lane: one)
-  constexpr int D = MT == 1 ? 2 : 1;
-  Entries<MT> ahead[D];
-#pragma unroll
-  for (int i = 0; i < D; ++i) ahead[i].fetch(a, n + i * stride, team.lane, size);
+  Entries<MT> ahead;
+  ahead.fetch(a, n, team.lane, size);
   const T* L = (const T*)a.L + n * K;
   T* d = (T*)a.dL + n * K;
-  float wn = a.weights && n < a.N ? a.weights[n] : 1.f, wnn = a.weights && n + stride < a.N ? a.weights[n + stride] : 1.f;
+  float wn = a.weights && n < a.N ? a.weights[n] : 1.f;
   Sum2 losses;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
     Row<T, V, NV> row[1];
     const bool on = feed.next(row);
-    Entries<MT> e = ahead[0];
+    Entries<MT> e = ahead;
     e.check(a, on);
-    ahead[0] = ahead[D - 1];
-    ahead[D - 1].fetch(a, n + D * stride, team.lane, size);
+    ahead.fetch(a, n + stride, team.lane, size);
     const float w = wn;
-    wn = wnn;
-    if (a.weights && n + 2 * stride < a.N) wnn = a.weights[n + 2 * stride];
+    if (a.weights && n + stride < a.N) wn = a.weights[n + stride];
     bool twice;
     if constexpr (F::kAsync) {
       __syncwarp();
@@ -558,8 +553,9 @@ template <typename T, int V, int E, int MT, int S>
 bool launch_warp(const Args& a, int size, int64_t grid, cudaStream_t s) {
   static std::atomic<uint64_t> done;
   using F = Feed<T, V, E / V, 1, WeightedRows>;
-  if (!allow_smem((const void*)distill_warp_kernel<T, V, E / V, MT, S>, F::bytes(kWarpThreads), done)) return false;
-  distill_warp_kernel<T, V, E / V, MT, S><<<(unsigned)grid, kWarpThreads, F::bytes(kWarpThreads), s>>>(a, size);
+  const size_t smem = F::bytes(kWarpThreads);
+  if (!allow_smem((const void*)distill_warp_kernel<T, V, E / V, MT, S>, smem, done)) return false;
+  distill_warp_kernel<T, V, E / V, MT, S><<<(unsigned)grid, kWarpThreads, smem, s>>>(a, size);
   return true;
 }
 // With as many lanes as hold the row, but for entries: at most eight a lane.

@@ -166,22 +166,34 @@ __global__ void __launch_bounds__(kWarpThreads) grad_warp_kernel(GradArgs a) {
   int64_t n = warp * per + l / S;
   float2 c[SHARE ? P : 1];
   if constexpr (SHARE) load_columns<V, NV>(c, a.share, team.lane, S, nv, 0.f);
+  // the entries come with the row (eight a lane, or beside rows that wait in
+  // registers: a row ahead)
+  constexpr bool kWords = MT == 1 && F::kAsync;
+  Words<3, F::kStages> words;
+  words.start(smem + F::bytes(kWarpThreads), team.lane, a.m, stride);
+  words.array(0, kWords && a.dgamma ? a.ids : nullptr, n, team.lane, a.m);
+  words.array(1, kWords && a.dgamma ? a.gamma : nullptr, n, team.lane, a.m);
+  words.array(2, kWords ? a.dgamma : nullptr, n, team.lane, a.m);
   F feed;
-  feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, S, nv, none, LiveRows{a.live});
-  // ids and shares come two rows ahead (eight a lane: one)
-  constexpr int D = MT == 1 ? 2 : 1;
-  Entries<MT> ahead[D];
-#pragma unroll
-  for (int i = 0; i < D; ++i) ahead[i].fetch(a, n + i * stride, team.lane, S);
+  feed.start(smem, {(const T*)a.L}, n, stride, a.N, K, team.lane, S, nv, none, LiveRows{a.live}, words);
+  Entries<MT> ahead;
+  if (!kWords) ahead.fetch(a, n, team.lane, S);
   const T* L = (const T*)a.L + n * K;
   T* d = (T*)a.dL + n * K;
   for (int64_t end = warp * per; end < a.N; n += stride, end += stride, L += stride * K, d += stride * K) {
     Row<T, V, NV> row[1];
-    const bool on = feed.next(row);
-    Entries<MT> e = ahead[0];
+    const bool on = feed.next(row, words);
+    Entries<MT> e;
+    if constexpr (kWords) {
+      const bool is = a.dgamma && words.mine;
+      e.id[0] = is ? words.template word<int>(feed.taken(), 0) : -1;
+      e.g[0] = is ? words.template word<float>(feed.taken(), 1) : 0.f;
+      e.v[0] = is ? words.template word<float>(feed.taken(), 2) : 0.f;
+    } else {
+      e = ahead;
+      ahead.fetch(a, n + stride, team.lane, S);
+    }
     const float sum_v = e.check(a, team, on);
-    ahead[0] = ahead[D - 1];
-    ahead[D - 1].fetch(a, n + D * stride, team.lane, S);
     if constexpr (F::kAsync) {
       __syncwarp();
       e.gather([&](int i) { return feed.peer(i); });
@@ -445,7 +457,8 @@ template <typename T, int V, int E, int MT, int S>
 bool launch_lanes(const GradArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done[2];
   constexpr int NV = E / V;
-  const size_t smem = Feed<T, V, NV, 1, LiveRows>::bytes(kWarpThreads);
+  using F = Feed<T, V, NV, 1, LiveRows>;
+  const size_t smem = F::bytes(kWarpThreads) + Words<3, F::kStages>::bytes(kWarpThreads);
   const int64_t rows = kWarpThreads / S, need = (a.N + rows - 1) / rows;
   const int64_t grid = need < 4 * kSms ? need : 4 * kSms;
   if (a.share) {

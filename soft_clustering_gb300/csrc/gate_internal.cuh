@@ -116,6 +116,46 @@ struct WeightedRows {  // weights, or NULL
   __device__ __forceinline__ bool operator()(int64_t n) const { return !weights || weights[n] != 0.f; }
 };
 
+// Nothing beside the rows.
+struct NoWords {
+  __device__ __forceinline__ void fetch(uint32_t, bool) {}
+};
+// NW words of 4 bytes a lane that come with each row: entry `lane` of the m that
+// a row has in each array.
+template <int NW, int STAGES>
+struct Words {
+  static constexpr size_t bytes(int threads) { return (size_t)STAGES * NW * threads * 4; }
+  const char* from[NW];  // NULL: none; this lane's of the next row
+  int64_t step;
+  char* slot;
+  bool mine;  // whether this lane has an entry
+  __device__ __forceinline__ void start(char* smem, int lane, int m, int64_t stride) {
+    slot = smem + threadIdx.x * 4;
+    mine = lane < m;
+    step = stride * m * 4;
+  }
+  template <typename T>
+  __device__ __forceinline__ void array(int w, const T* p, int64_t row, int lane, int m) {
+    static_assert(sizeof(T) == 4, "words");
+    from[w] = p ? reinterpret_cast<const char*>(p + row * m + lane) : nullptr;
+  }
+  __device__ __forceinline__ void fetch(uint32_t into, bool there) {
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      if (from[w]) {
+        if (there && mine)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(
+                           slot + (size_t)(into * NW + w) * blockDim.x * 4)),
+                       "l"(from[w])
+                       : "memory");
+        from[w] += step;
+      }
+  }
+  template <typename T> __device__ __forceinline__ T word(uint32_t stage, int w) const {
+    return *reinterpret_cast<const T*>(slot + (size_t)(stage * NW + w) * blockDim.x * 4);
+  }
+};
+
 template <typename T, int V, int NV, int NA, typename Rows = EveryRow>
 struct Feed {
   static constexpr int kBytes = sizeof(T) * V;  // of a vector
@@ -138,6 +178,12 @@ struct Feed {
   // vectors of a row, those that a lane has past them are `none`.
   __device__ __forceinline__ void start(char* smem, const T* const (&array)[NA], int64_t row_, int64_t stride_, int64_t N,
                                         int64_t width, int lane_, int size_, int nv_, T none, Rows rows_ = Rows()) {
+    NoWords no;
+    start(smem, array, row_, stride_, N, width, lane_, size_, nv_, none, rows_, no);
+  }
+  template <typename W>
+  __device__ __forceinline__ void start(char* smem, const T* const (&array)[NA], int64_t row_, int64_t stride_, int64_t N,
+                                        int64_t width, int lane_, int size_, int nv_, T none, Rows rows_, W& words) {
     lane = lane_, size = size_, nv = nv_, stage = 0, step = stride_ * width;
     rows = rows_, row = row_, stride = stride_, were = 0;
     left = row < N ? (int)((N - row + stride - 1) / stride) : 0;
@@ -158,12 +204,14 @@ struct Feed {
           for (int s = 0; s < kStages * NA; ++s)
             *reinterpret_cast<Vec<T, V>*>(slot + (size_t)(s * NV + j) * blockDim.x * kBytes) = ahead[0].r[j];
 #pragma unroll
-      for (int s = 0; s < kStages - 1; ++s) fetch(s);
+      for (int s = 0; s < kStages - 1; ++s) fetch(s, words);
     } else {
-      fetch(0);
+      fetch(0, words);
     }
   }
-  __device__ __forceinline__ void fetch(uint32_t into) {
+  template <typename W>
+  __device__ __forceinline__ void fetch(uint32_t into, W& words) {
+    words.fetch(into, left > 0);
     const bool there = Rows::kMasked ? on : left > 0;
     were = were << 1 | (uint32_t)there;
     if (there) {
@@ -198,9 +246,10 @@ struct Feed {
   // In shared memory until the next call: this thread's vector j of the row that
   // `next` gave last, element `at` of that row whoever of the team holds it (which
   // takes a __syncwarp between lanes), and all of this thread's vectors.
+  __device__ __forceinline__ uint32_t taken() const { return stage == 0 ? kStages - 1 : stage - 1; }
   __device__ __forceinline__ char* word(int j) const {
     static_assert(kAsync, "in shared memory");
-    const uint32_t s = stage == 0 ? kStages - 1 : stage - 1;
+    const uint32_t s = taken();
     return slot + (size_t)(s * NA * NV + j) * blockDim.x * kBytes;
   }
   __device__ __forceinline__ Vec<T, V> vector(int j) const { return *reinterpret_cast<const Vec<T, V>*>(word(j)); }
@@ -219,8 +268,13 @@ struct Feed {
   // The next row and true; what was there before and false past the last one and
   // for a row that is not fetched.
   __device__ __forceinline__ bool next(Row<T, V, NV> (&out)[NA]) {
+    NoWords no;
+    return next(out, no);
+  }
+  template <typename W>
+  __device__ __forceinline__ bool next(Row<T, V, NV> (&out)[NA], W& words) {
     if constexpr (kAsync) {
-      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      fetch(stage == 0 ? kStages - 1 : stage - 1, words);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 #pragma unroll
       for (int a = 0; a < NA; ++a)
@@ -231,7 +285,7 @@ struct Feed {
     } else {
 #pragma unroll
       for (int a = 0; a < NA; ++a) out[a] = ahead[a];
-      fetch(0);
+      fetch(0, words);
     }
     return were >> (kAsync ? kStages - 1 : 1) & 1u;
   }

@@ -172,29 +172,34 @@ template <> struct Key<float> {
   }
 };
 
-// A lane's best element not yet taken.  The second best is found beforehand, by
-// all lanes at once: a lane that is taken from looks on by itself, while the
-// others wait, from its third on.
+// A lane's best element not yet taken.  The second best (of more than four
+// entries the third too) is found beforehand, by all lanes at once: a lane that
+// is taken from more often looks on by itself, while the others wait.
 template <typename T, int V, int NV, int S, typename F>
 struct Best {
   static constexpr bool kWideRows = V > 1;
   static constexpr int N = kWideRows ? NV : V * NV;
-  Key<T> key, next;
+  Key<T> key, next, third;
   uint32_t o[N];  // of each vector's (element's) largest left
   int j, e;       // where the last one picked is
-  bool second;    // `next` is the next
+  int known;      // how many of `next` and `third` are left
 
-  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, bool more) {
+  __device__ __forceinline__ void start(const Row<T, V, NV>& r, const F& feed, int m) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if constexpr (kWideRows) o[i] = order_of(vector_max(r.r[i]));
       else o[i] = order_of(to_f(r.at(i)));
     }
     key = pick(feed);
-    second = more;
-    if (more) {
+    known = m > 4 ? 2 : m > 1;
+    next = third = Key<T>::none();
+    if (m > 1) {
       drop(feed);
       next = pick(feed);
+    }
+    if (m > 4) {
+      drop(feed);
+      third = pick(feed);
     }
   }
   __device__ __forceinline__ Key<T> pick(const F& feed) {
@@ -220,12 +225,13 @@ struct Best {
   }
   // Takes the best away from the lane that `won` (all of the warp call it).
   __device__ __forceinline__ void pop(const F& feed, bool won) {
-    const bool look = won && !second;
-    if (won) key = next, second = false;
+    const bool look = won && known == 0;
+    if (won) key = next, next = third, --known;
     if (__any_sync(0xffffffffu, look)) {
       if (look) {
         drop(feed);
         key = pick(feed);
+        known = 0;
       }
     }
   }
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
     Row<T, V, NV> row[1];
     if (!feed.next(row)) row[0].fill(none);
     Best<T, V, NV, S, F> best;
-    best.start(row[0], feed, m > 1);
+    best.start(row[0], feed, m);
     // lane t takes the t-th; one lane alone writes them as they come
     Key<T> mine = Key<T>::none(), first = Key<T>::none();
     float other[S == 1 ? kMaxTop : 1];
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs 
     Row<T, V, NV> row[1];
     if (!feed.next(row)) row[0].fill(none);
     Best<T, V, NV, 32, F> best;
-    best.start(row[0], feed, m > 1);
+    best.start(row[0], feed, m);
     Key<T> first = Key<T>::none(), tth = Key<T>::none();
 #pragma unroll 1
     for (int t = 0; t < m; ++t) {
