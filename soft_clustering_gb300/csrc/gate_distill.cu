@@ -301,37 +301,44 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
 // it waits for and works out goes beside the others' work.  Entries come two rows
 // and the student's logits at them one row ahead.  It puts a row's elements right
 // after the next row's barrier, before which the others have stored the row.
-template <typename T, int MT>
-__device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<false>& team, int* some_s) {
+// `first` and `stride`: the rows of the block (the cluster, whose first block has
+// them).
+template <typename T, int MT, bool CLUSTER>
+__device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<CLUSTER>& team, float* some_s, int64_t first_row,
+                                             int64_t stride) {
   const WarpTeam<32> warp((int)threadIdx.x & 31, 32);
-  const int64_t stride = gridDim.x, step = stride * a.K;
-  const T* L = (const T*)a.L + (int64_t)blockIdx.x * a.K;
-  T* d = (T*)a.dL + (int64_t)blockIdx.x * a.K;
+  const int64_t step = stride * a.K;
+  const T* L = (const T*)a.L + first_row * a.K;
+  T* d = (T*)a.dL + first_row * a.K;
   const float k = kLog2E * a.inv;
   auto weight = [&](int64_t n) { return n >= a.N ? 0.f : a.weights ? a.weights[n] : 1.f; };
   Entries<MT> next, ahead, late;
-  float w = weight(blockIdx.x), w_next = weight(blockIdx.x + stride);
-  ahead.fetch(a, blockIdx.x, warp.lane, 32);
+  float w = weight(first_row), w_next = weight(first_row + stride);
+  ahead.fetch(a, first_row, warp.lane, 32);
   next = ahead;
   next.check(a, w != 0.f);
   next.gather([&](int i) { return L + i; });
-  ahead.fetch(a, blockIdx.x + stride, warp.lane, 32);
+  ahead.fetch(a, first_row + stride, warp.lane, 32);
 #pragma unroll
   for (int i = 0; i < MT; ++i) late.id[i] = -1;
   Sum2 losses;
   uint32_t turn = 0;
-  for (int64_t n = blockIdx.x; n < a.N; n += stride, L += step, d += step, turn ^= 1) {
+  for (int64_t n = first_row; n < a.N; n += stride, L += step, d += step, turn ^= 1) {
     Entries<MT> e = next;
     e.gather_old(a, d);
     float logsum, top, s[1];
     const bool some = e.normalise(warp, logsum);
-    if (warp.lane == 0) some_s[turn] = some;
+    if (CLUSTER) {
+      if (warp.lane < (int)cluster_blocks()) team.to_block(some_s + turn, warp.lane, some ? 1.f : 0.f);
+    } else if (warp.lane == 0) {
+      some_s[turn] = some ? 1.f : 0.f;
+    }
     next = ahead;
     next.check(a, w_next != 0.f);
     next.gather([&](int i) { return L + step + i; });
     ahead.fetch(a, n + 2 * stride, warp.lane, 32);
     const float w_after = weight(n + 2 * stride);
-    __syncthreads();
+    team.barrier();
     if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
     team.hear(s, top, 0.f, k);
     const Base base(top, k);
@@ -348,7 +355,7 @@ __device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<false>& te
     w = w_next;
     w_next = w_after;
   }
-  __syncthreads();
+  team.barrier();
   if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
   return losses;
 }
@@ -357,7 +364,7 @@ template <typename T, int V, int NV, int MT>
 __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float part[BlockTeam<false>::kWords];
-  __shared__ int some_s[2];
+  __shared__ float some_s[2];
   constexpr int P = V * NV / 2;
   const int K = a.K, nv = K / V;
   BlockTeam<false> team(part, blockDim.x - 32);
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
   const int64_t step = (int64_t)gridDim.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   if ((int)threadIdx.x >= team.size) {
-    losses = entries_warp<T, MT>(a, team, some_s);
+    losses = entries_warp<T, MT, false>(a, team, some_s, blockIdx.x, gridDim.x);
   } else {
     Feed<T, V, NV, 1, WeightedRows> feed;
     feed.start(smem, {(const T*)a.L}, blockIdx.x, gridDim.x, a.N, K, team.lane, team.size, nv, none,
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
         team.turn ^= 1;
         continue;
       }
-      const bool some = on && some_s[turn];
+      const bool some = on && some_s[turn] != 0.f;
       const float own = team.hear(s, top, mine, k);
       if (a.add && !some) continue;
       const float2 f = both(a.scale * w * a.T * own * rsum_of(s[0]));
@@ -414,31 +421,39 @@ __global__ void __launch_bounds__(kBlockThreads + 32) distill_block_kernel(Args 
   store_total(a, losses.value());
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(Args a) {
+// A row to a block, or few rows to clusters of `blocks` each.
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(Args a, int blocks) {
   extern __shared__ __align__(16) char smem[];
-  __shared__ float part[BlockTeam<false>::kWords];
-  __shared__ int some_s[2];
+  __shared__ float part[BlockTeam<CLUSTER>::kWords];
+  __shared__ float some_s[2];
   constexpr int V = kWide<T>, U = kStreamVectors, P = U * V / 2, MT = 2;
   const int K = a.K;
-  BlockTeam<false> team(part, kStreamThreads);
+  BlockTeam<CLUSTER> team(part, kStreamThreads);
   const float k = kLog2E * a.inv;
   const T none = from_f<T>(-INFINITY);
-  const int64_t step = (int64_t)gridDim.x * K;
-  const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
-  T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
+  const int64_t first = CLUSTER ? blockIdx.x / blocks : blockIdx.x, stride = CLUSTER ? gridDim.x / blocks : gridDim.x;
+  const int64_t step = stride * K;
+  const T* L = (const T*)a.L + first * K;
+  T* d = (T*)a.dL + first * K;
+  if (CLUSTER) cluster_barrier();  // every block of the cluster runs
   uint32_t turn = 0;
   Sum2 losses;
   if ((int)threadIdx.x >= kStreamThreads) {
-    losses = entries_warp<T, MT>(a, team, some_s);
+    if (!CLUSTER || cluster_rank() == 0) {
+      losses = entries_warp<T, MT, CLUSTER>(a, team, some_s, first, stride);
+    } else {
+      for (int64_t n = first; n < a.N; n += stride) team.barrier();
+      team.barrier();
+    }
   } else {
-    const int t = threadIdx.x;
+    const int t = team.lane, size = CLUSTER ? team.size : kStreamThreads;
     Stream<T> feed;
-    feed.start(smem, (const T*)a.L, blockIdx.x, gridDim.x, a.N, K, a.dL ? 2 : 1, kStreamThreads);
-    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
+    feed.start(smem, (const T*)a.L, first, stride, a.N, K, a.dL ? 2 : 1, t, size, kStreamThreads);
+    for (int64_t n = first; n < a.N; n += stride, L += step, d += step, turn ^= 1) {
       const float w = a.weights ? a.weights[n] : 1.f;
       const int head = Stream<T>::head_of(L, K), nv = (K - head) / V, tail = head + nv * V;
-      const int turns = (nv + U * kStreamThreads - 1) / (U * kStreamThreads);
+      const int turns = (nv + U * size - 1) / (U * size);
       // the elements outside the vectors, one a thread
       const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;
       const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
@@ -448,10 +463,10 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
         Row<T, V, U> x;
         feed.next(x);
         if (i == turns - 1) {
-          const int v0 = i * U * kStreamThreads + t;
+          const int v0 = i * U * size + t;
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            if (v0 + u * kStreamThreads >= nv)
+            if (v0 + u * size >= nv)
 #pragma unroll
               for (int e = 0; e < V; ++e) x.r[u].v[e] = none;
         }
@@ -470,12 +485,12 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
       const float mine = warp_max(top);
       float s[1] = {(sum.x + sum.y) * BlockTeam<false>::between(top, mine == -INFINITY ? 0.f : mine, k)};
       team.tell(s, mine);
-      __syncthreads();
+      team.barrier();
       if (!a.dL) {
         team.turn ^= 1;
         continue;
       }
-      const bool some = w != 0.f && some_s[turn];
+      const bool some = w != 0.f && some_s[turn] != 0.f;
       team.hear(s, top, mine, k);
       const Base base(top, k);
       const float c = some ? a.scale * w * a.T * rsum_of(s[0]) : 0.f;
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
         d[edge] = from_f<T>(y);
       }
       T* out = d + head + (int64_t)t * V;
-      for (int i = 0; i < turns; ++i, out += U * kStreamThreads * V) {
+      for (int i = 0; i < turns; ++i, out += U * size * V) {
         Row<T, V, U> x;
         feed.next(x);
         if (a.add && !some) continue;
@@ -499,11 +514,11 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
           o.fill(none);
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            if (i * U * kStreamThreads + t + u * kStreamThreads < nv) {
-              if (same) o.r[u] = *reinterpret_cast<const Vec<T, V>*>(out + u * kStreamThreads * V);
+            if (i * U * size + t + u * size < nv) {
+              if (same) o.r[u] = *reinterpret_cast<const Vec<T, V>*>(out + u * size * V);
               else
 #pragma unroll
-                for (int e = 0; e < V; ++e) o.r[u].v[e] = out[u * kStreamThreads * V + e];
+                for (int e = 0; e < V; ++e) o.r[u].v[e] = out[u * size * V + e];
             }
           float2 z[P];
           o.get(z);
@@ -517,15 +532,15 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1) distill_stream_kernel(
         if (!some) x.fill(from_f<T>(0.f));
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (i * U * kStreamThreads + t + u * kStreamThreads < nv) {
-            if (same) *reinterpret_cast<Vec<T, V>*>(out + u * kStreamThreads * V) = x.r[u];
+          if (i * U * size + t + u * size < nv) {
+            if (same) *reinterpret_cast<Vec<T, V>*>(out + u * size * V) = x.r[u];
             else
 #pragma unroll
-              for (int e = 0; e < V; ++e) out[u * kStreamThreads * V + e] = x.r[u].v[e];
+              for (int e = 0; e < V; ++e) out[u * size * V + e] = x.r[u].v[e];
           }
       }
     }
-    __syncthreads();
+    team.barrier();
   }
   store_total(a, losses.value());
 }
@@ -599,11 +614,21 @@ template <typename T>
 int64_t launch_typed(const Args& a, cudaStream_t s) {
   const bool vectors = wide<T>(a.K, (const char*)a.L, (const char*)a.dL);
   if (a.K > (vectors ? 32 : 16) * kBlockThreads) {
-    static std::atomic<uint64_t> done;
+    static std::atomic<uint64_t> done[2];
     const size_t smem = Stream<T>::bytes(kStreamThreads);
-    if (!allow_smem((const void*)distill_stream_kernel<T>, smem, done)) return 0;
-    const int64_t grid = a.N < 1 ? 1 : a.N < 2 * kSms ? a.N : 2 * kSms;
-    distill_stream_kernel<T><<<(unsigned)grid, kStreamThreads + 32, smem, s>>>(a);
+    // few rows: as many blocks each as leave none without, a clusters' barrier
+    // being some microseconds of a row's time
+    int blocks = 1;
+    while (blocks < 8 && a.N * blocks * 2 <= kSms) blocks *= 2;
+    if (blocks > 1) {
+      if (!allow_smem((const void*)distill_stream_kernel<T, true>, smem, done[1])) return 0;
+      const int64_t grid = (a.N < 1 ? 1 : a.N) * blocks;
+      launch_clusters(distill_stream_kernel<T, true>, (unsigned)grid, kStreamThreads + 32, smem, blocks, s, a, blocks);
+      return grid;
+    }
+    if (!allow_smem((const void*)distill_stream_kernel<T, false>, smem, done[0])) return 0;
+    const int64_t grid = a.N < 2 * kSms ? a.N : 2 * kSms;
+    distill_stream_kernel<T, false><<<(unsigned)grid, kStreamThreads + 32, smem, s>>>(a, 1);
     return grid;
   }
   return vectors ? launch<T, kWide<T>>(a, s) : launch<T, 1>(a, s);

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32, 1) grad_stream_kernel(Grad
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   const LiveRows live{a.live};
   Stream<T> feed;
-  feed.start(smem, (const T*)a.L, blockIdx.x, gridDim.x, a.N, K, 2, kBlockThreads);
+  feed.start(smem, (const T*)a.L, blockIdx.x, gridDim.x, a.N, K, 2, t, kBlockThreads, kBlockThreads);
   uint32_t turn = 0;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
     const bool on = live(n);

@@ -508,7 +508,7 @@ struct BlockTeam {
   // `threads` of each block, from the first on; the others may listen.
   __device__ __forceinline__ BlockTeam(float* p, int threads) : part(p), turn(0) {
     if (CLUSTER) {
-      lane = (int)(cluster_rank() * blockDim.x + threadIdx.x);
+      lane = (int)cluster_rank() * threads + (int)threadIdx.x;
       size = (int)cluster_blocks() * threads;
     } else {
       lane = (int)threadIdx.x;
@@ -520,7 +520,7 @@ struct BlockTeam {
   // As WarpTeam's, where `top` was the warp's: what a warp tells, and what every
   // warp, of the team or not, makes of it after the block's barrier.
   template <int Q> __device__ __forceinline__ void tell(const float (&v)[Q], float top) {
-    static_assert(!CLUSTER && (Q == 1 || Q == 2), "one or two sums, and the maxima");
+    static_assert(Q == 1 || Q == 2, "one or two sums, and the maxima");
     constexpr int G = 32 / Q;
     const int l = threadIdx.x & 31, q = l / G, c = l % G;
     float x = v[0];
@@ -532,10 +532,28 @@ struct BlockTeam {
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     float* p = part + 4 * kWarps * turn;
-    if (c == 0) {
+    if (CLUSTER) {
+      if (c < (int)cluster_blocks()) {
+        to_block(p + q * kWarps + (lane >> 5), c, x);
+        if (q == 0) to_block(p + 2 * kWarps + (lane >> 5), c, top);
+      }
+    } else if (c == 0) {
       p[q * kWarps + (threadIdx.x >> 5)] = x;
       if (q == 0) p[2 * kWarps + (threadIdx.x >> 5)] = top;
     }
+  }
+  // Between what is told and heard.
+  static __device__ __forceinline__ void barrier() {
+    if (CLUSTER) cluster_barrier();
+    else __syncthreads();
+  }
+  // x at `p` of the cluster's block c.
+  static __device__ __forceinline__ void to_block(void* p, int c, float x) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(there)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(c));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(x) : "memory");
   }
   // The team's top and sums with it; what takes a warp of top `mine` there.
   // Exponents between tops are roundings apart from those of Base, no more.
@@ -544,10 +562,16 @@ struct BlockTeam {
     const int l = threadIdx.x & 31, q = l / G, c = l % G;
     const float* p = part + 4 * kWarps * turn;
     turn ^= 1;
-    const float there = c < all ? p[2 * kWarps + c] : -INFINITY;
+    float there = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kWarps; i += G)
+      if (c + i < all) there = max_nan(there, p[2 * kWarps + c + i]);
     top = warp_max(there);
     const float low = top == -INFINITY ? 0.f : top;
-    float x = c < all ? p[q * kWarps + c] * between(there, low, k) : 0.f;
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; i += G)
+      if (c + i < all) x += p[q * kWarps + c + i] * between(p[2 * kWarps + c + i], low, k);
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
 #pragma unroll
@@ -585,13 +609,7 @@ struct BlockTeam {
     float* p = part + 4 * kWarps * turn + q * kWarps;
     turn ^= 1;
     if (CLUSTER) {
-      if (c < (int)cluster_blocks()) {
-        uint32_t there;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(there)
-                     : "r"((uint32_t)__cvta_generic_to_shared(p + (lane >> 5))), "r"(c));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(x) : "memory");
-      }
+      if (c < (int)cluster_blocks()) to_block(p + (lane >> 5), c, x);
       cluster_barrier();
     } else {
       if (c == 0) p[threadIdx.x >> 5] = x;
@@ -628,7 +646,7 @@ struct Stream {
   int nv, at, pass;
   uint32_t slot_in, slot_out;
   char* slot;
-  int threads;
+  int lane, size, threads;  // of those that share a row; of a block
 
   // The row's vectors begin `head` elements in; nv of them.
   static __device__ __forceinline__ int head_of(const T* p, int K) {
@@ -641,10 +659,10 @@ struct Stream {
     nv = (K - h) / V;
   }
   __device__ __forceinline__ void start(char* smem, const T* L_, int64_t n_, int64_t stride_, int64_t N_, int K_, int passes_,
-                                        int threads_) {
+                                        int lane_, int size_, int threads_) {
     L = L_ + n_ * K_, n = n_, N = N_, stride = stride_, row_step = stride_ * K_, K = K_, passes = passes_;
-    threads = threads_;
-    at = (int)threadIdx.x, pass = 0, slot_in = slot_out = 0;
+    lane = lane_, size = size_, threads = threads_;
+    at = lane, pass = 0, slot_in = slot_out = 0;
     slot = smem + threadIdx.x * 16;
     row();
 #pragma unroll
@@ -654,14 +672,14 @@ struct Stream {
     if (n < N) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (at + u * threads < nv)
+        if (at + u * size < nv)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(
                            slot + (size_t)(slot_in * U + u) * threads * 16)),
-                       "l"(body + (int64_t)(at + u * threads) * V)
+                       "l"(body + (int64_t)(at + u * size) * V)
                        : "memory");
-      at += U * threads;
-      if (at - (int)threadIdx.x >= nv) {
-        at = (int)threadIdx.x;
+      at += U * size;
+      if (at - lane >= nv) {
+        at = lane;
         if (++pass == passes) {
           pass = 0;
           n += stride;
