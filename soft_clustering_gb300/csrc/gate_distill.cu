@@ -183,6 +183,7 @@ struct Entries {
 // Sums of the threads' row losses, in the order of the threads.
 __device__ __forceinline__ void store_total(const Args& a, double total) {
   __shared__ double part[32];
+  let_next_start();
   total = block_reduce(total, 0.0, SumOp(), part);
   if (threadIdx.x == 0) a.part[blockIdx.x] = total;
 }
@@ -550,6 +551,7 @@ __global__ void __launch_bounds__(kWarpThreads)
 distill_finish_kernel(const double* __restrict__ part, int blocks, double scale,
                       float* __restrict__ loss) {
   __shared__ double partd[32];
+  wait_for_last();
   double s = 0.0;
   for (int b = threadIdx.x; b < blocks; b += kWarpThreads) s += part[b];
   s = block_reduce(s, 0.0, SumOp(), partd);
@@ -670,7 +672,7 @@ gmm_status gmm_distill(const void* L, gmm_dtype xdtype, int64_t N, int K, int m,
   }
   if (!blocks) return GMM_ERR_CUDA;
   ProfScope p("distill_finish_kernel", s);
-  distill_finish_kernel<<<1, kWarpThreads, 0, s>>>((const double*)ws, (int)blocks, scale, loss);
+  launch_behind(distill_finish_kernel, 1, kWarpThreads, s, (const double*)ws, (int)blocks, scale, loss);
   return launched();
 }
 

@@ -701,6 +701,24 @@ struct Stream {
   }
 };
 
+// The kernel that joins the blocks' sums is launched while they still run: they
+// say when it may be (at their end), it waits for all they have written.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+inline void launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = threads;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // Launches `kernel` as clusters of `cluster` blocks (1: without any).
 template <typename... P, typename... A>
 inline void launch_clusters(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,

@@ -45,6 +45,7 @@ gate_finish_kernel(GateWs ws, GateBlocks blocks, int K, int64_t* __restrict__ co
   const int k = blockIdx.x * kFinishColumns + column;
   Sum2 sum;
   int n = 0, rows = 0, all = 0;
+  wait_for_last();
   for (int b = threadIdx.x; b < blocks.heads; b += kFinishThreads) rows += ws.rows[b], all += ws.kept[b];
   if (k < K) {
 #pragma unroll 4
@@ -148,9 +149,9 @@ gmm_status gmm_gate(const void* L, gmm_dtype xdtype, int64_t N, int K, int m, in
     ProfScope p("gate_finish_kernel", s);
     const int columns = finish_columns(blocks.mass, K), g = (K + columns - 1) / columns;
     if (columns == 8)
-      gate_finish_kernel<8><<<g, kFinishThreads, 0, s>>>(w, blocks, K, counts, mass, share, loss);
+      launch_behind(gate_finish_kernel<8>, g, kFinishThreads, s, w, blocks, K, counts, mass, share, loss);
     else
-      gate_finish_kernel<64><<<g, kFinishThreads, 0, s>>>(w, blocks, K, counts, mass, share, loss);
+      launch_behind(gate_finish_kernel<64>, g, kFinishThreads, s, w, blocks, K, counts, mass, share, loss);
   }
   return launched();
 }

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kGateWarpThreads) gate_warp_kernel(GateArgs a)
     }
   }
   if (!BALANCE) return;
+  let_next_start();
   // the warp's groups, then the warps in order
 #pragma unroll
   for (int i = 0; i < (BALANCE ? P : 1); ++i)
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kGateBlockThreads) gate_block_kernel(GateArgs 
     }
   }
   if (!BALANCE) return;
+  let_next_start();
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < V * NV; ++i) {

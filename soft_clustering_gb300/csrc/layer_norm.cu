@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kWarpThreads) norm_grad_warp_kernel(Args a, in
   grad_rows<T, W, V, NV>(a, smem, WarpTeam<0>(lane & (size - 1), size), warp * per + lane / size, warps * per,
                          warp * per, dw, db);
   if (!a.sums) return;
+  let_next_start();
   // the warp's groups, then the warps in order
 #pragma unroll
   for (int i = 0; i < E / 2; ++i)
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kBlockThreads) norm_grad_block_kernel(Args a, 
   if (CLUSTER) cluster_barrier();  // every block of the cluster runs
   grad_rows<T, W, V, NV>(a, smem, team, at, gridDim.x / blocks, at, dw, db);
   if (a.sums) {
+    let_next_start();
     float* out = a.sums + (size_t)at * 2 * a.D;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -259,6 +261,7 @@ norm_finish_kernel(const float* __restrict__ sums, int blocks, int D, W* __restr
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * kFinishColumns + l;
   Sum2 s;
+  wait_for_last();
   if (i < 2 * D)
 #pragma unroll 4
     for (int b = w; b < blocks; b += 32) s.add(sums[(size_t)b * 2 * D + i]);
@@ -433,7 +436,7 @@ gmm_status gmm_layer_norm_grad(const void* dY, const void* X, gmm_dtype xdtype, 
   if (dweight) {
     ProfScope p("norm_finish_kernel", s);
     const unsigned g = (unsigned)((2 * (int64_t)D + kFinishColumns - 1) / kFinishColumns);
-#define CALL(T, W) norm_finish_kernel<W><<<g, kFinishThreads, 0, s>>>((const float*)ws, (int)blocks, D, (W*)dweight, (W*)dbias)
+#define CALL(T, W) launch_behind(norm_finish_kernel<W>, g, kFinishThreads, s, (const float*)ws, (int)blocks, D, (W*)dweight, (W*)dbias)
     BY_TYPES(CALL)
 #undef CALL
   }
