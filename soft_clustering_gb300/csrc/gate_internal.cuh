@@ -631,12 +631,10 @@ struct BlockTeam {
 // a thread ahead, and without a break from the first reading of a row to the
 // second (out of L2) and on to the next row; the elements before and behind,
 // fewer than a vector, belong to one thread each.
-constexpr int kStreamVectors = 4;  // a copy
-constexpr int kDepth = 3;
-
-template <typename T>
+// U: vectors of a copy
+template <typename T, int U_ = 4>
 struct Stream {
-  static constexpr int V = kWide<T>, U = kStreamVectors;
+  static constexpr int V = kWide<T>, U = U_, kDepth = U >= 4 ? 3 : 4;
   static constexpr size_t bytes(int threads) { return (size_t)kDepth * U * threads * 16; }
   const T* L;
   int64_t n, N, stride, row_step;

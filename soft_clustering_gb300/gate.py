@@ -6,9 +6,10 @@ gradient of the logits, with the balance loss that keeps all components in use;
 ``Distiller`` compares logits with a teacher's top entries, the mixture's ids
 and gamma among them, and gives that loss's gradient.  Everything runs on the
 current torch stream (or ``stream``) in the library's kernels; tensors are
-dense, on one device, and have to stay valid until that work is done.  Objects
-own their outputs and workspaces: calls that overlap (two streams, two graphs
-replayed at once) need an object each.  No arithmetic happens here.
+dense, on one device, and they and these objects have to be kept until that work
+is done.  Objects own their outputs and workspaces: calls that overlap (two
+streams, two graphs replayed at once) need an object each.  No arithmetic happens
+here.
 """
 from __future__ import annotations
 

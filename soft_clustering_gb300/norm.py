@@ -2,9 +2,10 @@
 
 ``LayerNorm`` holds sizes and a workspace, not weights: those are the caller's
 (``adamw.AdamW`` trains them).  Everything runs on the current torch stream (or
-``stream``) in the library's kernels; tensors are dense, on one device, and have
-to stay valid until that work is done.  An object owns its workspace: backward
-passes that overlap need an object each.  No arithmetic happens here.
+``stream``) in the library's kernels; tensors are dense, on one device, and they
+and these objects have to be kept until that work is done.  An object owns its
+workspace: backward passes that overlap need an object each.  No arithmetic
+happens here.
 """
 from __future__ import annotations
 
