@@ -95,11 +95,6 @@ struct Row {
   }
 };
 
-// A lane's own vectors of the rows ahead, of NA arrays of one shape.  They wait in
-// shared memory, put there by asynchronous copies kStages - 1 rows before they are
-// used: the bytes in flight that HBM needs, without registers for them.  A lane
-// reads what it copied itself, so there is nothing to synchronise.  Single 16-bit
-// elements, for which there is no such copy, wait in registers, one row ahead.
 // Which rows are fetched at all.
 struct EveryRow {
   static constexpr bool kMasked = false;
@@ -156,6 +151,11 @@ struct Words {
   }
 };
 
+// A lane's own vectors of the rows ahead, of NA arrays of one shape.  They wait in
+// shared memory, put there by asynchronous copies kStages - 1 rows before they are
+// used: the bytes in flight that HBM needs, without registers for them.  A lane
+// reads what it copied itself, so there is nothing to synchronise.  Single 16-bit
+// elements, for which there is no such copy, wait in registers, one row ahead.
 template <typename T, int V, int NV, int NA, typename Rows = EveryRow>
 struct Feed {
   static constexpr int kBytes = sizeof(T) * V;  // of a vector
@@ -166,7 +166,7 @@ struct Feed {
   const T* from[NA];  // the next row to be fetched, at this lane's first vector
   int64_t step;       // elements from a row to the next
   int left, size, lane, nv;
-  char* slot;         // this thread's, [stage][array][vector][thread] of 16 bytes
+  char* slot;         // this thread's, [stage][array][vector][thread]
   uint32_t stage;
   Rows rows;
   int64_t row, stride;  // two behind the next one to be fetched (of masked rows alone)

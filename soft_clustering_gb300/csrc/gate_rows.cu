@@ -19,8 +19,9 @@ size_t ws_layout(int64_t N, int K, void* base, GateWs* w) {
   GateWs t;
   t.ticket = (uint32_t*)take(4);
   t.part = (double*)take(sizeof(double) * ((K + 7) / 8));
-  t.rows = (int32_t*)take(sizeof(int32_t) * b);
-  t.kept = (int32_t*)take(sizeof(int32_t) * b);
+  const int64_t heads = b > kGateStreamGrid ? b : kGateStreamGrid;  // streamed rows have more blocks than sums
+  t.rows = (int32_t*)take(sizeof(int32_t) * heads);
+  t.kept = (int32_t*)take(sizeof(int32_t) * heads);
   t.mass = (float*)take(sizeof(float) * (size_t)b * K);
   t.counts = (int32_t*)take(sizeof(int32_t) * (size_t)b * K);
   t.scale = (float2*)take(sizeof(float2) * (size_t)(K > 16 * kGateBlockThreads ? N : 0));

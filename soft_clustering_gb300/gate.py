@@ -24,6 +24,11 @@ MAX_TEACHER = 64
 MAX_STUDENT = 1 << 18
 
 
+def _like(t, stream):
+    """A new tensor as dense `t`, for work on `stream` (None: the current one)."""
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _type(dtype):
     if dtype not in TORCH_XDTYPE:
         raise ValueError("type %s is not supported" % dtype)
@@ -96,7 +101,7 @@ class Gate:
         if dgamma is not None:
             _need(dgamma, "dgamma", self._small, torch.float32, self.device)
         if out is None:
-            out = _empty(self._shape, self.dtype, self.device, stream)
+            out = _like(logits, stream)
         else:
             _need(out, "out", self._shape, self.dtype, self.device)
         _here(self.device)
@@ -158,7 +163,8 @@ class Distiller:
         if out is None:
             if add:
                 raise ValueError("add without out")
-            out = _empty(self._shape, self.dtype, self.device, stream)
+            _need(logits, "logits", self._shape, self.dtype, self.device)
+            out = _like(logits, stream)
         else:
             _need(out, "out", self._shape, self.dtype, self.device)
         self._call(logits, ids, values, weights, out, GMM_DISTILL_ADD if add else 0, stream)

@@ -13,7 +13,7 @@ import torch
 
 from . import gmm_layer_norm, gmm_layer_norm_grad, gmm_layer_norm_ws_bytes
 from .experts import _device, _empty, _here, _need, _rows_of
-from .gate import _type
+from .gate import _like, _type
 
 
 class LayerNorm:
@@ -54,7 +54,7 @@ class LayerNorm:
         self._param(bias, "bias")
         _here(self.device)
         if out is None:
-            out = _empty((N, self.D), self.dtype, self.device, stream)
+            out = _like(X, stream)
         else:
             self._rows(out, "out", N)
         gmm_layer_norm(X, self.xdtype, N, self.D, self.eps, weight, bias, self.wdtype, out,
@@ -69,7 +69,7 @@ class LayerNorm:
         self._param(weight, "weight")
         _here(self.device)
         if out is None:
-            out = _empty((N, self.D), self.dtype, self.device, stream)
+            out = _like(X, stream)
         else:
             self._rows(out, "out", N)
         dw = db = None

@@ -389,6 +389,26 @@ def test_gate(cuda, N, K, m, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,K", [("f32", 9000), ("bf16", 9001), ("f16", 16385), ("bf16", 16392), ("f16", 2048),
+                                     ("f32", 1025), ("bf16", 520), ("f16", 24)])
+def test_balance_of_many_rows(cuda, K, dtype):
+    """More rows than blocks keep sums for, in every form: rows, entries and mass of all of them."""
+    from soft_clustering_gb300.gate import Gate
+    N, m = 1300 if K < 5000 else 330, 2
+    L = _logits(np.random.default_rng(K), N, K, dtype, plain=True)
+    g = Gate(N, K, m, L.dtype)
+    ids, _ = g.forward(L, balance=True)
+    rid, _, rl, p, a = gate_ref(_f64(L), m)
+    assert np.array_equal(ids.cpu().numpy(), rid)
+    rc, rm, share, loss = balance_ref(rid, p, N)
+    assert np.array_equal(g.counts.cpu().numpy(), rc)
+    bm = (p * (_E(a) + _S(p, a) + 4 * U)).sum(0) + (N / 100 + 64) * U * rm + N * 2.0 ** -120
+    _near(g.mass, rm, bm, "mass")
+    _near(g.share, share, 2 * U * share, "share")
+    _near(g.loss, np.array([loss]), (share * (bm + 4 * U * rm)).sum() + 2 * U * loss, "loss")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("K", [5, 64, 200, 1024, 3001, 20000])
 def test_gate_of_rows_that_are_not_finite(cuda, K, dtype):
