@@ -20,7 +20,7 @@ using namespace gate;
 constexpr int kWarpThreads = 256;
 constexpr int kBlockThreads = 512;
 constexpr int kStreamThreads = 512;
-constexpr int kMaxGrid = 8 * kSms;
+constexpr int kMaxGrid = 32 * kSms;  // blocks that a device can hold
 constexpr int kStudent = 1 << 18;
 
 struct Args {
@@ -560,29 +560,33 @@ distill_finish_kernel(const double* __restrict__ part, int blocks, double scale,
 }
 
 template <typename T, int V, int NV, int MT>
-bool launch_block(const Args& a, int threads, int64_t grid, cudaStream_t s) {
+int64_t launch_block(const Args& a, int threads, cudaStream_t s) {
   static std::atomic<uint64_t> done;
+  static ResidentCache cache;
   using F = Feed<T, V, NV, 1, WeightedRows>;
-  if (!allow_smem((const void*)distill_block_kernel<T, V, NV, MT>, F::bytes(kBlockThreads + 32), done)) return false;
+  if (!allow_smem((const void*)distill_block_kernel<T, V, NV, MT>, F::bytes(kBlockThreads + 32), done)) return 0;
+  const int64_t most = resident(distill_block_kernel<T, V, NV, MT>, threads, F::bytes(threads), cache);
+  const int64_t grid = a.N < 1 ? 1 : a.N < most ? a.N : most;
   distill_block_kernel<T, V, NV, MT><<<(unsigned)grid, threads, F::bytes(threads), s>>>(a);
-  return true;
+  return grid;
 }
 template <typename T, int V, int E, int MT, int S>
-bool launch_warp(const Args& a, int size, int64_t grid, cudaStream_t s) {
+int64_t launch_warp(const Args& a, int size, cudaStream_t s) {
   static std::atomic<uint64_t> done;
+  static ResidentCache cache;
   using F = Feed<T, V, E / V, 1, WeightedRows>;
   const size_t smem = F::bytes(kWarpThreads);
-  if (!allow_smem((const void*)distill_warp_kernel<T, V, E / V, MT, S>, smem, done)) return false;
+  if (!allow_smem((const void*)distill_warp_kernel<T, V, E / V, MT, S>, smem, done)) return 0;
+  const int64_t rows = kWarpThreads / size, need = (a.N + rows - 1) / rows;
+  const int64_t most = resident(distill_warp_kernel<T, V, E / V, MT, S>, kWarpThreads, smem, cache);
+  const int64_t grid = need < 1 ? 1 : need < most ? need : most;
   distill_warp_kernel<T, V, E / V, MT, S><<<(unsigned)grid, kWarpThreads, smem, s>>>(a, size);
-  return true;
+  return grid;
 }
 // With as many lanes as hold the row, but for entries: at most eight a lane.
 template <typename T, int V, int E, int S>
 int64_t launch_lanes(const Args& a, int size, cudaStream_t s) {
-  const int64_t rows = kWarpThreads / size, need = (a.N + rows - 1) / rows;
-  const int64_t grid = need < 1 ? 1 : need < 4 * kSms ? need : 4 * kSms;
-  const bool ok = a.m <= size ? launch_warp<T, V, E, 1, S>(a, size, grid, s) : launch_warp<T, V, E, 8, S>(a, size, grid, s);
-  return ok ? grid : 0;
+  return a.m <= size ? launch_warp<T, V, E, 1, S>(a, size, s) : launch_warp<T, V, E, 8, S>(a, size, s);
 }
 
 // Returns the blocks launched; 0: none.
@@ -606,11 +610,7 @@ int64_t launch(const Args& a, cudaStream_t s) {
   }
   constexpr int E = V > 1 ? 32 : 16;
   const int threads = ((K + E - 1) / E + 31) / 32 * 32 + 32;
-  const int resident = 1024 / threads < 8 ? 1024 / threads : 8;
-  const int64_t grid = a.N < 1 ? 1 : a.N < (int64_t)resident * kSms ? a.N : (int64_t)resident * kSms;
-  const bool ok = m <= 32 ? launch_block<T, V, E / V, 1>(a, threads, grid, s)
-                          : launch_block<T, V, E / V, 2>(a, threads, grid, s);
-  return ok ? grid : 0;
+  return m <= 32 ? launch_block<T, V, E / V, 1>(a, threads, s) : launch_block<T, V, E / V, 2>(a, threads, s);
 }
 
 template <typename T, bool CLUSTER, int U>

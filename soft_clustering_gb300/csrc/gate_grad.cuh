@@ -456,16 +456,21 @@ __global__ void __launch_bounds__(kWarpThreads) grad_entries_kernel(GradArgs a, 
 template <typename T, int V, int E, int MT, int S>
 bool launch_lanes(const GradArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done[2];
+  static ResidentCache cache[2];
   constexpr int NV = E / V;
   using F = Feed<T, V, NV, 1, LiveRows>;
   const size_t smem = F::bytes(kWarpThreads) + Words<3, F::kStages>::bytes(kWarpThreads);
   const int64_t rows = kWarpThreads / S, need = (a.N + rows - 1) / rows;
-  const int64_t grid = need < 4 * kSms ? need : 4 * kSms;
+  int64_t grid;
   if (a.share) {
     if (!allow_smem((const void*)grad_warp_kernel<T, V, NV, MT, S, true>, smem, done[1])) return false;
+    grid = resident(grad_warp_kernel<T, V, NV, MT, S, true>, kWarpThreads, smem, cache[1]);
+    if (grid > need) grid = need;
     grad_warp_kernel<T, V, NV, MT, S, true><<<(unsigned)grid, kWarpThreads, smem, s>>>(a);
   } else {
     if (!allow_smem((const void*)grad_warp_kernel<T, V, NV, MT, S, false>, smem, done[0])) return false;
+    grid = resident(grad_warp_kernel<T, V, NV, MT, S, false>, kWarpThreads, smem, cache[0]);
+    if (grid > need) grid = need;
     grad_warp_kernel<T, V, NV, MT, S, false><<<(unsigned)grid, kWarpThreads, smem, s>>>(a);
   }
   return true;
@@ -474,17 +479,21 @@ bool launch_lanes(const GradArgs& a, cudaStream_t s) {
 template <typename T, int V, int E>
 bool launch_block(const GradArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done[2];
+  static ResidentCache cache[2];
   constexpr int NV = E / V;
   using F = Feed<T, V, NV, 1, LiveRows>;
   const int threads = ((a.K + E - 1) / E + 31) / 32 * 32 + 32;
-  const int resident = 1024 / threads < 8 ? 1024 / threads : 8;
-  const int64_t grid = a.N < (int64_t)resident * kSms ? a.N : (int64_t)resident * kSms;
+  int64_t grid;
   const size_t smem = F::bytes(threads), most = F::bytes(kBlockThreads + 32);
   if (a.share) {
     if (!allow_smem((const void*)grad_block_kernel<T, V, NV, true>, most, done[1])) return false;
+    grid = resident(grad_block_kernel<T, V, NV, true>, threads, smem, cache[1]);
+    if (grid > a.N) grid = a.N;
     grad_block_kernel<T, V, NV, true><<<(unsigned)grid, threads, smem, s>>>(a);
   } else {
     if (!allow_smem((const void*)grad_block_kernel<T, V, NV, false>, most, done[0])) return false;
+    grid = resident(grad_block_kernel<T, V, NV, false>, threads, smem, cache[0]);
+    if (grid > a.N) grid = a.N;
     grad_block_kernel<T, V, NV, false><<<(unsigned)grid, threads, smem, s>>>(a);
   }
   return true;

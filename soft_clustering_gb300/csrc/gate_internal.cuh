@@ -699,6 +699,23 @@ struct Stream {
   }
 };
 
+// Blocks of `kernel` that the device holds at once, so that a grid of persistent
+// blocks is one wave: `cache` (static, one for each kernel) keeps the answer for
+// each number of warps (the devices of a process are alike).
+struct ResidentCache {
+  std::atomic<int> per_sm[33];
+};
+template <typename K>
+inline int64_t resident(K kernel, int threads, size_t smem, ResidentCache& cache) {
+  std::atomic<int>& c = cache.per_sm[threads / 32];
+  int n = c.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, (const void*)kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+    c.store(n, std::memory_order_relaxed);
+  }
+  return (int64_t)n * kSms;
+}
+
 // The kernel that joins the blocks' sums is launched while they still run: they
 // say when it may be (at their end), it waits for all they have written.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -625,13 +625,18 @@ GateBlocks launch_lanes(const GateArgs& a, cudaStream_t s) {
   using F = Feed<T, V, NV, 1, LiveRows>;
   const size_t feed = F::bytes(kGateWarpThreads);
   const int64_t rows = kGateWarpThreads / S, need = (a.N + rows - 1) / rows;
-  const int64_t most = a.balance ? gate_blocks(E * S) : 8 * kSms;  // short blocks where none keeps sums
-  const int64_t grid = need < 1 ? 1 : need < most ? need : most;
+  static ResidentCache cache[2];
+  int64_t grid = need < 1 ? 1 : need;
+  auto at_most = [&](int64_t n) { grid = grid < n ? grid : n; };
   if (a.balance) {
     if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, true>, feed + 8 * E * S, done[1])) return {};
+    const size_t smem = feed + 8 * E * S;
+    at_most(gate_blocks(a.K));
+    at_most(resident(gate_warp_kernel<T, V, NV, S, true>, kGateWarpThreads, smem, cache[1]));
     gate_warp_kernel<T, V, NV, S, true><<<(unsigned)grid, kGateWarpThreads, feed + 8 * a.K, s>>>(a);
   } else {
     if (!allow_smem((const void*)gate_warp_kernel<T, V, NV, S, false>, feed, done[0])) return {};
+    at_most(resident(gate_warp_kernel<T, V, NV, S, false>, kGateWarpThreads, feed, cache[0]));
     gate_warp_kernel<T, V, NV, S, false><<<(unsigned)grid, kGateWarpThreads, feed, s>>>(a);
   }
   return {(int)grid, (int)grid, (int)grid};
@@ -643,13 +648,18 @@ GateBlocks launch_block(const GateArgs& a, cudaStream_t s) {
   constexpr int NV = E / V;
   using F = Feed<T, V, NV, 1, LiveRows>;
   const int threads = ((a.K + E - 1) / E + 31) / 32 * 32;
-  const int64_t most = gate_blocks(a.K), grid = a.N < 1 ? 1 : a.N < most ? a.N : most;
+  static ResidentCache cache[2];
+  int64_t grid = a.N < 1 ? 1 : a.N;
+  auto at_most = [&](int64_t n) { grid = grid < n ? grid : n; };
   const size_t feed = F::bytes(threads);
   if (a.balance) {
     if (!allow_smem((const void*)gate_block_kernel<T, V, NV, true>, F::bytes(kGateBlockThreads) + 4 * E * kGateBlockThreads, done[1])) return {};
+    at_most(gate_blocks(a.K));
+    at_most(resident(gate_block_kernel<T, V, NV, true>, threads, feed + 4 * (size_t)E * threads, cache[1]));
     gate_block_kernel<T, V, NV, true><<<(unsigned)grid, threads, feed + 4 * (size_t)a.K, s>>>(a);
   } else {
     if (!allow_smem((const void*)gate_block_kernel<T, V, NV, false>, F::bytes(kGateBlockThreads), done[0])) return {};
+    at_most(resident(gate_block_kernel<T, V, NV, false>, threads, feed, cache[0]));
     gate_block_kernel<T, V, NV, false><<<(unsigned)grid, threads, feed, s>>>(a);
   }
   return {(int)grid, (int)grid, (int)grid};

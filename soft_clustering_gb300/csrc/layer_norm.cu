@@ -320,8 +320,9 @@ Plan plan(int64_t N, int D, int V) {
 }
 
 template <typename T, typename W, int V, int NV, bool GRAD>
-bool launch_rows(const Args& a, const Plan& p, cudaStream_t s) {
+bool launch_rows(const Args& a, Plan& p, cudaStream_t s) {
   static std::atomic<uint64_t> done[3];
+  static ResidentCache cache[3];
   const size_t smem = Feed<T, V, NV, GRAD ? 2 : 1>::bytes(p.threads);
   const int form = p.size ? 0 : p.blocks == 1 ? 1 : 2;
   void (*kernel)(Args, int);
@@ -341,27 +342,25 @@ bool launch_rows(const Args& a, const Plan& p, cudaStream_t s) {
   if (smem > 48 * 1024 - 8192 &&
       !allow_smem((const void*)kernel, Feed<T, V, NV, GRAD ? 2 : 1>::bytes(kBlockThreads), done[form]))
     return false;
+  const int64_t most = resident(kernel, p.threads, smem, cache[form]) / p.blocks;
+  if (p.grid > most) p.grid = most;
   if (form == 2) launch_clusters(kernel, (unsigned)p.grid * p.blocks, p.threads, smem, p.blocks, s, a, p.blocks);
   else kernel<<<(unsigned)p.grid, p.threads, smem, s>>>(a, form ? 1 : p.size);
   return true;
 }
 
 template <typename T, typename W, int V, bool GRAD>
-bool launch(const Args& a, const Plan& p, cudaStream_t s) {
+bool launch(const Args& a, Plan& p, cudaStream_t s) {
   return p.per == 8 ? launch_rows<T, W, V, 8 / V, GRAD>(a, p, s) : launch_rows<T, W, V, 16 / V, GRAD>(a, p, s);
 }
 
 template <typename T, typename W, bool GRAD>
 bool launch_typed(const Args& a, cudaStream_t s, int64_t& blocks) {
-  if (wide<T>(a.D, (const char*)a.X, (const char*)a.dY, (const char*)a.Y)) {
-    const Plan p = plan(a.N, a.D, kWide<T>);
-    blocks = p.grid;
-    return launch<T, W, kWide<T>, GRAD>(a, p, s);
-  } else {
-    const Plan p = plan(a.N, a.D, 1);
-    blocks = p.grid;
-    return launch<T, W, 1, GRAD>(a, p, s);
-  }
+  const bool vectors = wide<T>(a.D, (const char*)a.X, (const char*)a.dY, (const char*)a.Y);
+  Plan p = plan(a.N, a.D, vectors ? kWide<T> : 1);
+  const bool ok = vectors ? launch<T, W, kWide<T>, GRAD>(a, p, s) : launch<T, W, 1, GRAD>(a, p, s);
+  blocks = p.grid;
+  return ok;
 }
 
 }  // namespace
