@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, U == 2 ? 2 : 1) distill_s
       const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;
       const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
       float top = xe;
-      float2 sum = make_float2(xe == -INFINITY ? 0.f : ex2((xe - xe) * k), 0.f);
+      float2 sum = make_float2(xe == -INFINITY ? 0.f : ex2(Base(xe, k)(xe, k)), 0.f);
       for (int i = 0; i < turns; ++i) {
         Row<T, V, U> x;
         feed.next(x);

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kBlockThreads + 32, 1) grad_stream_kernel(Grad
     const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;  // an element outside the vectors
     const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
     const float ce = SHARE && edge >= 0 ? a.share[edge] : 0.f;
-    float top = xe, sum = xe == -INFINITY ? 0.f : ex2((xe - xe) * kLog2E), dot = sum * ce;
+    float top = xe, sum = xe == -INFINITY ? 0.f : ex2(Base(xe, kLog2E)(xe, kLog2E)), dot = sum * ce;
     for (int i = 0; i < turns; ++i) {
       Row<T, V, U> x;
       feed.next(x);

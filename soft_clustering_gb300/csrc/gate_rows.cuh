@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateA
         return key <= bound && order_of(xe) != kNone ? key : 0ull;
       });
       top = xe;
-      if (xe != -INFINITY) sum = ex2((xe - xe) * kLog2E);
+      if (xe != -INFINITY) sum = ex2(Base(xe, kLog2E)(xe, kLog2E));
       const int turns = (nv + U * kGateBlockThreads - 1) / (U * kGateBlockThreads);
       for (int i = 0; i < turns; ++i) {
         const int v0 = i * U * kGateBlockThreads + t;
