@@ -368,18 +368,22 @@ __device__ __forceinline__ float lane_max(const Row<__nv_bfloat16, V, NV>& r) {
 }
 // x -> 2^(x k - base) with base = top k rounded: its rounding is a factor that
 // all of a row have in common, so shares do not see it, and a logarithm of their
-// sum takes base itself.  A top so large, or so low, that base is not finite is
-// taken off first.
+// sum takes base itself.  That factor is a number near 1 (2^-2^-5 to 2^2^-5) while
+// |base| is below 2^20; from there on (masks of -1e9, small temperatures, bases
+// that are infinite) the top is taken off first, which costs one more instruction.
 struct Base {
   float top, base;
   __device__ __forceinline__ Base(float t, float k) : top(t == -INFINITY ? 0.f : t), base(top * k) {}
+  __device__ __forceinline__ bool near() const { return fabsf(base) < 1048576.f; }  // not if NaN
   __device__ __forceinline__ float operator()(float x, float k) const {
-    return fabsf(base) == INFINITY ? (x - top) * k : fmaf(x, k, -base);
+    return near() ? fmaf(x, k, -base) : (x - top) * k;
   }
+  // log2 of what the exponentials are too large by
+  __device__ __forceinline__ float over(float k) const { return near() ? fmaf(top, k, -base) : 0.f; }
 };
 template <int P>
 __device__ __forceinline__ void exponentials(float2 (&x)[P], const Base& b, float k) {
-  if (fabsf(b.base) == INFINITY) {
+  if (!b.near()) {
 #pragma unroll
     for (int i = 0; i < P; ++i) x[i] = mul2(sub2(x[i], both(b.top)), both(k));
   } else {
@@ -578,11 +582,13 @@ struct BlockTeam {
     for (int i = 0; i < Q; ++i) v[i] = Q == 1 ? x : __shfl_sync(0xffffffffu, x, i * G);
     return between(mine, low, k);
   }
-  // 2^(base of a - base of b)
+  // What takes exponentials of Base(a) to those of Base(b); where one of the two
+  // takes its top off and the other does not, from the one's base to the other's.
   static __device__ __forceinline__ float between(float a, float b, float k) {
     const Base p(a, k), q(b, k);
     if (a == -INFINITY) return 0.f;
-    return ex2(fabsf(p.base) == INFINITY || fabsf(q.base) == INFINITY ? (a - b) * k : p.base - q.base);
+    if (q.near()) return ex2(p.near() ? p.base - q.base : fmaf(a, k, -q.base));
+    return ex2(p.near() ? -fmaf(b, k, -p.base) : (a - b) * k);
   }
   template <int Q> __device__ __forceinline__ void sum(float (&v)[Q]) {
     static_assert(Q == 1 || Q == 2 || Q == 4, "a power of two");

@@ -244,8 +244,7 @@ struct Best {
 
 // log of a row's sum of exponentials, taken with `base`.
 __device__ __forceinline__ float log_sum(const Base& b, float k, float sum) {
-  const float left = fabsf(b.base) == INFINITY ? 0.f : fmaf(b.top, k, -b.base);
-  return b.top + kLn2 * (lg2(sum) - left);
+  return b.top + kLn2 * (lg2(sum) - b.over(k));
 }
 
 // Adds a block's sums to the workspace: `rows` and `kept` of its threads.
