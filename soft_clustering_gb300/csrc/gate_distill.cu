@@ -44,7 +44,7 @@ struct Args {
 template <int MT>
 struct Entries {
   int id[MT];     // -1: none
-  float b[MT];    // log2 q, but for a constant
+  float b[MT];    // the value, of a gamma its log; then log2 q, but for a constant
   float x[MT];    // the student's logit
   float old[MT];  // what the gradient is added to
   float q[MT];
@@ -66,7 +66,7 @@ struct Entries {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (!on || (uint32_t)id[i] >= (uint32_t)a.K) id[i] = -1;
-      b[i] = (a.gammas ? lg2(b[i]) : b[i] * kLog2E) * a.inv;
+      if (a.gammas) b[i] = kLn2 * lg2(b[i]);
       if (id[i] < 0) b[i] = -INFINITY;
       if (b[i] == -INFINITY) id[i] = -1;
       x[i] = old[i] = 0.f;
@@ -87,9 +87,11 @@ struct Entries {
         if (id[i] >= 0) old[i] = to_f(dL[id[i]]);
     }
   }
-  // q, and whether there is an entry.
+  // q, and whether there is an entry.  The largest is taken off the values as they
+  // are: a product's rounding goes by its size, and the lowest number times log2 e
+  // is no number.
   template <typename Team>
-  __device__ __forceinline__ bool normalise(Team team, float& logsum) {
+  __device__ __forceinline__ bool normalise(Team team, float k, float& logsum) {
     float top = b[0];
 #pragma unroll
     for (int i = 1; i < MT; ++i) top = max_nan(top, b[i]);
@@ -98,7 +100,7 @@ struct Entries {
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      b[i] -= some ? top : 0.f;
+      b[i] = (b[i] - (some ? top : 0.f)) * k;
       q[i] = ex2(b[i]);
       s[0] += q[i];
     }
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
     float s[1] = {total(x)};
     team.sum(s);
     float logsum;
-    const bool some = e.normalise(team, logsum) && on;
+    const bool some = e.normalise(team, k, logsum) && on;
     const float divergence = e.divergence(team, base, k);
     if (team.lane == 0 && n < a.N) {
       const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
@@ -332,7 +334,7 @@ __device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<CLUSTER>& 
     Entries<MT> e = next;
     e.gather_old(a, d);
     float logsum, top, s[1];
-    const bool some = e.normalise(warp, logsum);
+    const bool some = e.normalise(warp, k, logsum);
     if (CLUSTER) {
       if (warp.lane < (int)cluster_blocks()) team.to_block(some_s + turn, warp.lane, some ? 1.f : 0.f);
     } else if (warp.lane == 0) {
