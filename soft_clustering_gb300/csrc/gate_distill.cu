@@ -39,6 +39,13 @@ struct Args {
   float T, inv, scale;
 };
 
+// log of a teacher's share.  One below 2^-126, which lg2 takes for 0, is as good as
+// any other: a temperature, or a row of nothing larger, makes it count.
+__device__ __forceinline__ float log_of(float g) {
+  const bool tiny = g < 1.17549435e-38f;
+  return kLn2 * (lg2(tiny ? g * 0x1p64f : g) - (tiny ? 64.f : 0.f));
+}
+
 // A teacher's entries of one row, MT a lane of the `size` (a power of two) that
 // share them, entry i * size + lane in place i.
 template <int MT>
@@ -66,7 +73,7 @@ struct Entries {
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if (!on || (uint32_t)id[i] >= (uint32_t)a.K) id[i] = -1;
-      if (a.gammas) b[i] = kLn2 * lg2(b[i]);
+      if (a.gammas) b[i] = log_of(b[i]);
       if (id[i] < 0) b[i] = -INFINITY;
       if (b[i] == -INFINITY) id[i] = -1;
       x[i] = old[i] = 0.f;

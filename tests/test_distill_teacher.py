@@ -92,3 +92,26 @@ def test_teacher_far_from_zero(cuda, N, K, m, dtype):
     relq = lambda u, spread: 4 * U * spread + 2.0 ** -20 + 300 * U  # noqa: E731
     for T, shifted in ((1.0, False), (0.5, True), (3.0, False)):
         _check(L, ids, vals, "logits", T, dtype, relq, shifted)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K,m", FORMS)
+def test_small_gammas(cuda, N, K, m):
+    """Shares below 2^-126 are shares: large where the temperature is, and where all
+    of a row are as small.
+
+    The log of a share s is within 2^-21 |log s|: so its power within 2^-20 of the
+    exponents, at most 104 / T."""
+    rng = np.random.default_rng(K + m)
+    L = _logits(rng, N, K, "f32", plain=True)
+    ids = _apart(rng, N, K, m)
+    with np.errstate(under="ignore"):
+        vals = (10.0 ** rng.uniform(-44, 0, (N, m))).astype(np.float32)
+    vals[1] = np.float32(1e-40) * (1 + np.arange(m) % 3)
+    vals[2] = np.float32(1.4e-45)
+    vals[3] = 0.0
+    vals[4, 0] = 0.0
+    for T, shifted in ((1.0, False), (50.0, True), (1000.0, False)):
+        _check(L, ids, vals, "gamma", T, "f32",
+               lambda u, spread: 2.0 ** -20 * np.where(np.isfinite(u), np.abs(u), 0.0).max(1, keepdims=True)
+               + 4 * U * spread + 2.0 ** -20 + 300 * U, shifted)
