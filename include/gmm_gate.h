@@ -108,7 +108,8 @@ gmm_status gmm_gate_grad(const void* L, gmm_dtype xdtype, int64_t N, int K, int 
  *          of -inf, a gamma of 0) is none.
  * weights: N float or NULL (1).  A row of weight 0, or without an entry, is
  *          left out: its row_n and dL are 0 and its logits are not read.
- * A row whose logits are all -inf has row_n = inf and p = 0.
+ * A row whose logits are all -inf has row_n = inf and p = 0.  A large T leaves
+ * row_n the difference of logarithms in 32 bits, T^2 times their rounding.
  * rows:    N float (written).
  * loss:    1 float (written).
  * dL:      N*K of L's type (written), or NULL: no gradient.  With

@@ -51,7 +51,7 @@ __device__ __forceinline__ float log_of(float g) {
 template <int MT>
 struct Entries {
   int id[MT];     // -1: none
-  float b[MT];    // the value, of a gamma its log; then log2 q, but for a constant
+  float b[MT];    // the value, of a gamma its log: T log q, but for a constant
   float x[MT];    // the student's logit
   float old[MT];  // what the gradient is added to
   float q[MT];
@@ -107,8 +107,8 @@ struct Entries {
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      b[i] = (b[i] - (some ? top : 0.f)) * k;
-      q[i] = ex2(b[i]);
+      b[i] -= some ? top : 0.f;
+      q[i] = ex2(b[i] * k);
       s[0] += q[i];
     }
     team.sum(s);
@@ -118,13 +118,14 @@ struct Entries {
     for (int i = 0; i < MT; ++i) q[i] *= r;
     return some;
   }
-  // sum_t q_t (b_t - (x_t k - base))
+  // sum_t q_t (b_t - (x_t - top)): in the logits' own units, which hold what a
+  // temperature or log2 e times it does not
   template <typename Team>
-  __device__ __forceinline__ float divergence(Team team, const Base& base, float k) {
+  __device__ __forceinline__ float divergence(Team team, const Base& base) {
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      if (id[i] >= 0 && q[i] != 0.f) s[0] += q[i] * (b[i] - base(x[i], k));
+      if (id[i] >= 0 && q[i] != 0.f) s[0] += q[i] * (b[i] - (x[i] - base.top));
     team.sum(s);
     return s[0];
   }
@@ -201,10 +202,12 @@ __device__ __forceinline__ void store_total(const Args& a, double total) {
   if (threadIdx.x == 0) a.part[blockIdx.x] = total;
 }
 
-__device__ __forceinline__ float row_loss(const Args& a, float w, float divergence, float logsum, float sum) {
+__device__ __forceinline__ float row_loss(const Args& a, float w, float divergence, float logsum, float sum,
+                                          const Base& base, float k) {
   // a row with no student at all is infinitely far
   if (sum == 0.f) return w * INFINITY;
-  return w * a.T * a.T * kLn2 * (divergence - logsum + lg2(sum));
+  // T twice and not T^2, which may be past fp32 where the row's loss is not
+  return w * a.T * (divergence + a.T * kLn2 * (lg2(sum) - base.over(k) - logsum));
 }
 
 // 1 / the sum; no student: p = 0
@@ -261,9 +264,9 @@ __global__ void __launch_bounds__(kWarpThreads) distill_warp_kernel(Args a, int 
     team.sum(s);
     float logsum;
     const bool some = e.normalise(team, k, logsum) && on;
-    const float divergence = e.divergence(team, base, k);
+    const float divergence = e.divergence(team, base);
     if (team.lane == 0 && n < a.N) {
-      const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
+      const float r = some ? row_loss(a, w, divergence, logsum, s[0], base, k) : 0.f;
       a.rows[n] = r;
       losses.add(r);
     }
@@ -356,9 +359,9 @@ __device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<CLUSTER>& 
     if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
     team.hear(s, top, 0.f, k);
     const Base base(top, k);
-    const float divergence = e.divergence(warp, base, k);
+    const float divergence = e.divergence(warp, base);
     if (warp.lane == 0) {
-      const float r = some ? row_loss(a, w, divergence, logsum, s[0]) : 0.f;
+      const float r = some ? row_loss(a, w, divergence, logsum, s[0], base, k) : 0.f;
       a.rows[n] = r;
       losses.add(r);
     }

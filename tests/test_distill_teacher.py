@@ -115,3 +115,30 @@ def test_small_gammas(cuda, N, K, m):
         _check(L, ids, vals, "gamma", T, "f32",
                lambda u, spread: 2.0 ** -20 * np.where(np.isfinite(u), np.abs(u), 0.0).max(1, keepdims=True)
                + 4 * U * spread + 2.0 ** -20 + 300 * U, shifted)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K,m", FORMS)
+def test_small_temperatures(cuda, N, K, m):
+    """T^2 is below 2^-126 where T times the logits is not."""
+    rng = np.random.default_rng(K + m)
+    L = _logits(rng, N, K, "f32", plain=True)
+    ids = _apart(rng, N, K, m)
+    vals = (rng.standard_normal((N, m))).astype(np.float32)
+    for T in (1e-12, 2.0 ** -80, 1e-30):
+        _check(L, ids, vals, "logits", T, "f32", lambda u, spread: 4 * U * spread + 2.0 ** -20 + 300 * U, scale=1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K,m", FORMS)
+def test_a_masked_student_at_the_teachers_entry(cuda, N, K, m):
+    """The lowest number is far away, not infinitely far, whatever the temperature."""
+    rng = np.random.default_rng(K + m)
+    L = _logits(rng, N, K, "f32", plain=True)
+    ids = _apart(rng, N, K, m)
+    low = float(np.finfo(np.float32).min)
+    import torch
+    L[torch.arange(N, device="cuda"), torch.from_numpy(ids[:, 0].astype(np.int64)).cuda()] = low
+    vals = np.full((N, m), 1.0, dtype=np.float32)
+    for T in (1.0, 0.5, 0.01):
+        _check(L, ids, vals, "gamma", T, "f32", lambda u, spread: 2.0 ** -20 + 300 * U, scale=2.0 ** -10)
