@@ -117,7 +117,7 @@ gmm_status gmm_gate_grad(const void* L, gmm_dtype xdtype, int64_t N, int K, int 
  *          (gmm_gate_grad's), in 32 bits, rounded once.
  * ws:      gmm_distill_ws_bytes() bytes, 256-byte aligned, of one call at a
  *          time.
- * T > 0 and finite, 1 <= K <= 2^18, 1 <= m <= 64, N*m <= 2^31 - 1.
+ * T > 0, T and log2 e / T finite in fp32, 1 <= K <= 2^18, 1 <= m <= 64, N*m <= 2^31 - 1.
  */
 size_t gmm_distill_ws_bytes(void);
 gmm_status gmm_distill(const void* L, gmm_dtype xdtype, int64_t N, int K, int m, int kind, int flags,

@@ -675,7 +675,7 @@ gmm_status gmm_distill(const void* L, gmm_dtype xdtype, int64_t N, int K, int m,
   if (!dtype_ok(xdtype) || N < 0 || K < 1 || K > kStudent || m < 1 || m > gate::kMaxTeacher ||
       N > INT32_MAX / m || (kind != GMM_TEACHER_LOGITS && kind != GMM_TEACHER_GAMMA) ||
       (flags & ~GMM_DISTILL_ADD) || !((float)temperature > 0.f) ||
-      !((float)temperature < INFINITY) || !loss || !ws)
+      !((float)temperature < INFINITY) || !((float)(1.0 / temperature) * kLog2E < INFINITY) || !loss || !ws)
     return GMM_ERR_INVALID_ARG;
   if (N > 0 && (!L || !ids || !values || !rows)) return GMM_ERR_INVALID_ARG;
   if (((uintptr_t)L | (uintptr_t)dL) % dtype_size(xdtype) ||

@@ -9,6 +9,7 @@ relq = 4 u spread + 2^-20 + 300 u.
 import numpy as np
 import pytest
 
+import soft_clustering_gb300 as G
 from test_gate import SUB, U, UT, _E, _S, _f64, _logits, _misaligned, _near, distill_ref, softmax_ref
 
 # lanes of a warp with an entry each and with eight, all of it, a block, streamed, shared by blocks
@@ -142,3 +143,12 @@ def test_a_masked_student_at_the_teachers_entry(cuda, N, K, m):
     vals = np.full((N, m), 1.0, dtype=np.float32)
     for T in (1.0, 0.5, 0.01):
         _check(L, ids, vals, "gamma", T, "f32", lambda u, spread: 2.0 ** -20 + 300 * U, scale=2.0 ** -10)
+
+
+def test_temperatures_whose_inverse_is_no_number_are_refused():
+    from soft_clustering_gb300 import build
+    build.build()
+    P = 4096
+    for T in (1e-45, 1e-39, 3e-39, 4e38, 1e300):
+        assert G.lib().gmm_distill(P, 1, 10, 64, 2, 0, 0, T, 1.0, P, P, P, P, P, P, P, 1 << 40,
+                                   None) == G.GMM_ERR_INVALID_ARG, T
