@@ -106,8 +106,9 @@ gmm_status gmm_gate_grad(const void* L, gmm_dtype xdtype, int64_t N, int K, int 
  *          GMM_TEACHER_GAMMA: q in proportion to values^(1/T), values >= 0
  *          (gmm_assign_topm's ids and gamma).  An entry of share 0 (a logit
  *          of -inf, a gamma of 0) is none.
- * weights: N float or NULL (1).  A row of weight 0, or without an entry, is
- *          left out: its row_n and dL are 0 and its logits are not read.
+ * weights: N float or NULL (1).  A row of weight 0, whose logits are not read,
+ *          or without an entry is left out: its row_n and dL are 0 (added: dL is
+ *          as it was).
  * A row whose logits are all -inf has row_n = inf and p = 0.  A large T leaves
  * row_n the difference of logarithms in 32 bits, T^2 times their rounding.
  * rows:    N float (written).

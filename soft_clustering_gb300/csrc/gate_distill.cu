@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, U == 2 ? 2 : 1) distill_s
   extern __shared__ __align__(16) char smem[];
   __shared__ float part[BlockTeam<CLUSTER>::kWords];
   __shared__ float some_s[2];
+  using F = Stream<T, WeightedRows, U>;
   constexpr int V = kWide<T>, P = U * V / 2, MT = 2;
   const int K = a.K;
   BlockTeam<CLUSTER> team(part, kStreamThreads);
@@ -466,18 +467,20 @@ __global__ void __launch_bounds__(kStreamThreads + 32, U == 2 ? 2 : 1) distill_s
     }
   } else {
     const int t = team.lane, size = CLUSTER ? team.size : kStreamThreads;
-    Stream<T, U> feed;
-    feed.start(smem, (const T*)a.L, first, stride, a.N, K, a.dL ? 2 : 1, t, size, kStreamThreads);
+    F feed;
+    feed.start(smem, (const T*)a.L, first, stride, a.N, K, a.dL ? 2 : 1, t, size, kStreamThreads,
+               WeightedRows{a.weights});
     for (int64_t n = first; n < a.N; n += stride, L += step, d += step, turn ^= 1) {
       const float w = a.weights ? a.weights[n] : 1.f;
-      const int head = Stream<T>::head_of(L, K), nv = (K - head) / V, tail = head + nv * V;
+      const bool on = w != 0.f;
+      const int head = F::head_of(L, K), nv = (K - head) / V, tail = head + nv * V;
       const int turns = (nv + U * size - 1) / (U * size);
       // the elements outside the vectors, one a thread
       const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;
-      const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
+      const float xe = on && edge >= 0 ? to_f(L[edge]) : -INFINITY;
       float top = xe;
       float2 sum = make_float2(xe == -INFINITY ? 0.f : ex2(Base(xe, k)(xe, k)), 0.f);
-      for (int i = 0; i < turns; ++i) {
+      for (int i = 0; on && i < turns; ++i) {
         Row<T, V, U> x;
         feed.next(x);
         if (i == turns - 1) {
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, U == 2 ? 2 : 1) distill_s
         team.turn ^= 1;
         continue;
       }
-      const bool some = w != 0.f && some_s[turn] != 0.f;
+      const bool some = on && some_s[turn] != 0.f;
       team.hear(s, top, mine, k);
       const Base base(top, k);
       const float c = some ? a.scale * w * a.T * rsum_of(s[0]) : 0.f;
@@ -522,7 +525,8 @@ __global__ void __launch_bounds__(kStreamThreads + 32, U == 2 ? 2 : 1) distill_s
       T* out = d + head + (int64_t)t * V;
       for (int i = 0; i < turns; ++i, out += U * size * V) {
         Row<T, V, U> x;
-        feed.next(x);
+        if (on) feed.next(x);
+        else x.fill(from_f<T>(0.f));
         if (a.add && !some) continue;
         float2 y[P];
         x.get(y);
@@ -632,7 +636,7 @@ int64_t launch(const Args& a, cudaStream_t s) {
 template <typename T, bool CLUSTER, int U>
 int64_t launch_stream(const Args& a, int64_t grid, int blocks, cudaStream_t s) {
   static std::atomic<uint64_t> done;
-  const size_t smem = Stream<T, U>::bytes(kStreamThreads);
+  const size_t smem = Stream<T, WeightedRows, U>::bytes(kStreamThreads);
   if (!allow_smem((const void*)distill_stream_kernel<T, CLUSTER, U>, smem, done)) return 0;
   if (CLUSTER)
     launch_clusters(distill_stream_kernel<T, CLUSTER, U>, (unsigned)grid, kStreamThreads + 32, smem, blocks, s, a, blocks);

@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kBlockThreads + 32, 1) grad_stream_kernel(Grad
   extern __shared__ __align__(16) char smem[];
   __shared__ float part[BlockTeam<false>::kWords];
   __shared__ float sum_v[2];
-  constexpr int V = kWide<T>, U = Stream<T>::U, P = U * V / 2;
+  using F = Stream<T, LiveRows>;
+  constexpr int V = kWide<T>, U = F::U, P = U * V / 2;
   const int K = a.K, t = threadIdx.x;
   BlockTeam<false> team(part, kBlockThreads);
   if (t >= kBlockThreads) {
@@ -340,18 +341,18 @@ __global__ void __launch_bounds__(kBlockThreads + 32, 1) grad_stream_kernel(Grad
   const T* L = (const T*)a.L + (int64_t)blockIdx.x * K;
   T* d = (T*)a.dL + (int64_t)blockIdx.x * K;
   const LiveRows live{a.live};
-  Stream<T> feed;
-  feed.start(smem, (const T*)a.L, blockIdx.x, gridDim.x, a.N, K, 2, t, kBlockThreads, kBlockThreads);
+  F feed;
+  feed.start(smem, (const T*)a.L, blockIdx.x, gridDim.x, a.N, K, 2, t, kBlockThreads, kBlockThreads, live);
   uint32_t turn = 0;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, L += step, d += step, turn ^= 1) {
     const bool on = live(n);
-    const int head = Stream<T>::head_of(L, K), nv = (K - head) / V, tail = head + nv * V;
+    const int head = F::head_of(L, K), nv = (K - head) / V, tail = head + nv * V;
     const int turns = (nv + U * kBlockThreads - 1) / (U * kBlockThreads);
     const int edge = t < head ? t : t - head < K - tail ? tail + t - head : -1;  // an element outside the vectors
-    const float xe = edge >= 0 ? to_f(L[edge]) : -INFINITY;
+    const float xe = on && edge >= 0 ? to_f(L[edge]) : -INFINITY;
     const float ce = SHARE && edge >= 0 ? a.share[edge] : 0.f;
     float top = xe, sum = xe == -INFINITY ? 0.f : ex2(Base(xe, kLog2E)(xe, kLog2E)), dot = sum * ce;
-    for (int i = 0; i < turns; ++i) {
+    for (int i = 0; on && i < turns; ++i) {
       Row<T, V, U> x;
       feed.next(x);
       const int v0 = i * U * kBlockThreads + t;
@@ -395,16 +396,19 @@ __global__ void __launch_bounds__(kBlockThreads + 32, 1) grad_stream_kernel(Grad
     T* out = d + head + (int64_t)t * V;
     for (int i = 0; i < turns; ++i, out += U * kBlockThreads * V) {
       Row<T, V, U> x;
-      feed.next(x);
       const int v0 = i * U * kBlockThreads + t;
-      float2 y[P], c[SHARE ? P : 1];
-      x.get(y);
-      exponentials(y, base, kLog2E);
-      if constexpr (SHARE)
-        load_columns<V, U>(c, a.share + head + (int64_t)(v0 - t) * V, t, kBlockThreads, nv - (v0 - t), 0.f);
-      apply<SHARE>(y, c, scale, shift);
-      x.set(y);
-      if (!on) x.fill(from_f<T>(0.f));
+      if (on) {
+        feed.next(x);
+        float2 y[P], c[SHARE ? P : 1];
+        x.get(y);
+        exponentials(y, base, kLog2E);
+        if constexpr (SHARE)
+          load_columns<V, U>(c, a.share + head + (int64_t)(v0 - t) * V, t, kBlockThreads, nv - (v0 - t), 0.f);
+        apply<SHARE>(y, c, scale, shift);
+        x.set(y);
+      } else {
+        x.fill(from_f<T>(0.f));
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + u * kBlockThreads < nv) {
@@ -530,7 +534,7 @@ bool launch_grad(const GradArgs& a, cudaStream_t s) {
     if (K <= 16 * kBlockThreads) return launch_block<T, 1, 16>(a, s);
   }
   static std::atomic<uint64_t> done[2];
-  const size_t smem = Stream<T>::bytes(kBlockThreads);
+  const size_t smem = Stream<T, LiveRows>::bytes(kBlockThreads);
   const int64_t grid = a.N < 2 * kSms ? a.N : 2 * kSms;
   if (a.share) {
     if (!allow_smem((const void*)grad_stream_kernel<T, true>, smem, done[1])) return false;

@@ -636,15 +636,17 @@ struct BlockTeam {
 // first and last boundary go through shared memory as a Feed's do, kDepth copies
 // a thread ahead, and without a break from the first reading of a row to the
 // second (out of L2) and on to the next row; the elements before and behind,
-// fewer than a vector, belong to one thread each.
+// fewer than a vector, belong to one thread each.  Rows that do not count are
+// passed over: who reads does not ask for theirs.
 // U: vectors of a copy
-template <typename T, int U_ = 4>
+template <typename T, typename Rows, int U_ = 4>
 struct Stream {
   static constexpr int V = kWide<T>, U = U_, kDepth = U >= 4 ? 3 : 4;
   static constexpr size_t bytes(int threads) { return (size_t)kDepth * U * threads * 16; }
   const T* L;
   int64_t n, N, stride, row_step;
   int K, passes;
+  Rows rows;
   // the copy to be asked for next
   const T* body;
   int nv, at, pass;
@@ -652,20 +654,22 @@ struct Stream {
   char* slot;
   int lane, size, threads;  // of those that share a row; of a block
 
-  // The row's vectors begin `head` elements in; nv of them.
+  // Elements of a row before its first vector.
   static __device__ __forceinline__ int head_of(const T* p, int K) {
     const int h = (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T);
     return h < K ? h : K;
   }
+  // To the next row that counts.
   __device__ __forceinline__ void row() {
+    for (; n < N && !rows(n); n += stride) L += row_step;
     const int h = head_of(L, K);
     body = L + h;
     nv = (K - h) / V;
   }
   __device__ __forceinline__ void start(char* smem, const T* L_, int64_t n_, int64_t stride_, int64_t N_, int K_, int passes_,
-                                        int lane_, int size_, int threads_) {
+                                        int lane_, int size_, int threads_, Rows rows_) {
     L = L_ + n_ * K_, n = n_, N = N_, stride = stride_, row_step = stride_ * K_, K = K_, passes = passes_;
-    lane = lane_, size = size_, threads = threads_;
+    lane = lane_, size = size_, threads = threads_, rows = rows_;
     at = lane, pass = 0, slot_in = slot_out = 0;
     slot = smem + threadIdx.x * 16;
     row();
@@ -688,7 +692,7 @@ struct Stream {
           pass = 0;
           n += stride;
           L += row_step;
-          if (n < N) row();
+          row();
         }
       }
     }
