@@ -342,7 +342,6 @@ __device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<CLUSTER>& 
   uint32_t turn = 0;
   for (int64_t n = first_row; n < a.N; n += stride, L += step, d += step, turn ^= 1) {
     Entries<MT> e = next;
-    e.gather_old(a, d);
     float logsum, top, s[1];
     const bool some = e.normalise(warp, k, logsum);
     if (CLUSTER) {
@@ -355,6 +354,7 @@ __device__ __forceinline__ Sum2 entries_warp(const Args& a, BlockTeam<CLUSTER>& 
     next.gather([&](int i) { return L + step + i; });
     ahead.fetch(a, n + 2 * stride, warp.lane, 32);
     const float w_after = weight(n + 2 * stride);
+    e.gather_old(a, d);
     team.barrier();
     if (a.dL) late.template store<T>([&](int i) { return d - step + i; });
     team.hear(s, top, 0.f, k);
