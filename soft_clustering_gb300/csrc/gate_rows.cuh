@@ -604,22 +604,23 @@ __global__ void __launch_bounds__(kGateBlockThreads, 1) gate_stream_kernel(GateA
   if (a.balance) store_counts(a, rows, kept);
 }
 
-// The mass of streamed rows, a thread a column, blockIdx.y a stretch of rows.
+// The mass of streamed rows, a thread a column, blockIdx.y a stretch of rows: N / 16
+// additions one after another, so with what their roundings leave.
 constexpr int kMassThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kMassThreads) gate_mass_kernel(GateArgs a, int64_t stretch) {
   const int k = blockIdx.x * kMassThreads + threadIdx.x;
   if (k >= a.K) return;
   const int64_t begin = blockIdx.y * stretch, end = begin + stretch < a.N ? begin + stretch : a.N;
-  float sum = 0.f;
+  Sum2 sum;
 #pragma unroll 8
   for (int64_t n = begin; n < end; ++n) {
     const float2 c = a.ws.scale[n];
     if (a.live && !a.live[n]) continue;
     const float x = to_f(((const T*)a.L)[n * a.K + k]);
-    sum += c.y == 0.f ? 0.f : ex2(Base(c.x, kLog2E)(x, kLog2E)) * c.y;
+    sum.add(c.y == 0.f ? 0.f : ex2(Base(c.x, kLog2E)(x, kLog2E)) * c.y);
   }
-  a.ws.mass[(size_t)blockIdx.y * a.K + k] = sum;
+  a.ws.mass[(size_t)blockIdx.y * a.K + k] = (float)sum.value();
 }
 
 template <typename T, int V, int E, int S>

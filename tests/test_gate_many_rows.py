@@ -1,8 +1,14 @@
-"""Rows that are streamed by a block, with padding anywhere."""
+"""Rows that are streamed by a block, many of them and with padding anywhere.
+
+A share 1 / K of equal logits is within two units of 2^-24 (exp2(0) = 1 and whole
+sums below 2^24 are exact, the reciprocal is within one unit in the last place),
+its N-fold sum within one more for each rounding to 32 bits that is left: that of
+a stretch of rows, and the result's.
+"""
 import numpy as np
 import pytest
 
-from test_gate import U, _logits
+from test_gate import U, _f64, _logits
 
 
 @pytest.fixture(scope="module")
@@ -13,6 +19,23 @@ def cuda():
     from soft_clustering_gb300 import build
     build.build()
     return torch.device("cuda", 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,K", [("f16", 8201), ("bf16", 16392), ("f32", 8196), ("f32", 8201)])
+def test_mass_of_many_rows(cuda, dtype, K):
+    import torch
+    from soft_clustering_gb300.gate import Gate
+    N = 40000
+    t = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    L = torch.zeros(N, K, dtype=t, device="cuda")
+    live = torch.arange(N, device="cuda") % 5 != 4
+    g = Gate(N, K, 2, t)
+    g.forward(L, live=live, balance=True)
+    rows = int(live.sum())
+    assert (np.abs(_f64(g.mass) / (rows / K) - 1) <= 6 * U).all()
+    assert abs(float(g.loss) - 1) <= 8 * U  # even mass, and the entries' shares sum to K / rows
+    assert g.counts.tolist()[:3] == [rows, rows, 0]
 
 
 @pytest.mark.gpu
