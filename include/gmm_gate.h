@@ -131,6 +131,8 @@ gmm_status gmm_distill(const void* L, gmm_dtype xdtype, int64_t N, int K, int m,
  *   h[n] = (X[n] - mean) / sqrt(var + eps),  Y[n] = weight h[n] + bias
  * with mean and var = mean of squares about it over the row (Ba, Kiros and
  * Hinton 2016); var is taken about the mean, not as a difference of squares.
+ * Sums are fp32: the elements' and the squared deviations' over a row have to be
+ * below 2^128 (deviations up to 2^64 / sqrt(D), 10^17 at D = 32768).
  * X: N*D; weight, bias: D of wdtype (xdtype or GMM_F32), or NULL (1, 0); Y: N*D
  * of xdtype (written).  eps >= 0; 1 <= D <= 32768; N <= 2^31 - 1.
  *

@@ -11,9 +11,11 @@
 // first; the lane that holds a teacher's entry puts that element right.  All
 // exponents are of base 2.
 //
-// Bound by issue slots: with the gradient 1000003 rows of 256 f16 and 4 entries
-// 212 us (149 at the copy rate; 16 logits a lane: 488), 8191 of 50257 bf16 and 32
-// entries 355 us (243); the loss alone of 65536 of 4096 bf16 120 us (79).
+// 1000003 rows of 256 f16 and 4 entries take 212 us with the gradient (149 at the
+// copy rate; 16 logits a lane: 488): 125 registers leave 16 warps a multiprocessor,
+// which wait on latency (issue slots at 51 %, HBM at 59 %).  8191 of 50257 bf16 and
+// 32 entries, 355 us (243), are near their issue slots (74 %), 300 us with half the
+// rows padding; the loss alone of 65536 of 4096 bf16 takes 123 us (79).
 #include "gate_internal.cuh"
 
 namespace gmm {

@@ -10,12 +10,15 @@
 // put right where the row waits in shared memory (warps), or by a warp of their
 // own after the next row's barrier (blocks).
 //
-// Bound by HBM where rows are long (65536 of 4096 bf16: 175 us, 6.1 TB/s), by HBM
-// and issue slots with the balance loss (262144 of 1024 bf16, a tenth of them
-// padding: 203 us, 5.1 TB/s).
+// Bound by HBM where rows are long (65536 of 4096 bf16: 173 us, 6.2 TB/s).  With
+// the balance loss (262144 of 1024 bf16, a tenth of them padding: 202 us, 5.1 TB/s)
+// 120 registers leave 16 warps a multiprocessor, HBM at 61 % and the issue slots at
+// 58 %.  Streamed, 2048 of 65536 bf16: 117 us, with the balance loss 300 (79), with
+// half the rows padding 230.
 //
 // A normalised gate without the balance loss has a gradient at its entries alone:
-// zeros are written and the logits not read.
+// zeros are written and the logits not read (65536 of 4096 bf16: 86 us, 6.2 TB/s;
+// 1000003 of 256 f16: 115, 4.9 TB/s).
 #pragma once
 
 #include "gate_internal.cuh"

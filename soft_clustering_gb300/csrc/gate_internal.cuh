@@ -320,7 +320,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 1 / x for x of 1 to 2^20 (or NaN) to an ulp, and log2 x to 2^-21.
+// 1 / x for x of 0.97 to 2^20 (or NaN) to an ulp, and log2 x to 2^-21.
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -425,9 +425,6 @@ struct Sum2 {
   __device__ __forceinline__ double value() const { return isfinite(s) ? (double)s + left : (double)s; }
 };
 
-struct MaxOp {
-  template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
-};
 struct SumOp {
   template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
 };

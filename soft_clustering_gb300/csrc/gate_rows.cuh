@@ -11,18 +11,24 @@
 // on 16 bytes are read by single elements, up to 16 a thread.
 //
 // The m largest are found one at a time.  A lane keeps the largest of each of
-// its vectors and the place of the first of those; a round takes the team's best
-// (by value, then the lower column), and only the lane that had it looks on in
-// the vector that it came from, which waits in shared memory.  With sorting keys
-// for all elements instead a round of all lanes would read every one again.
+// its vectors; its best and second best (of more than four entries its third too)
+// are found beforehand, by all lanes at once.  A round takes the team's best (by
+// value, then the lower column), and the lane that had it goes on to its next:
+// only one that is taken from more often looks on, in the vector that its last
+// came from, which waits in shared memory.  With sorting keys for all elements
+// instead a round of all lanes would read every one again.
 //
 // A lane has the same columns of every row, so it sums their mass in registers;
 // a block's sums are joined in order, by the finish over the blocks with what
 // their roundings left.
 //
-// Bound by issue slots: 1000003 rows of 256 f16, m = 4, with the balance loss take
-// 216 us (of which the finish 13), 166 instructions a warp for a row, where reading
-// them takes 81; 65536 of 1024 fp32, m = 4, 59 us (40).
+// Bound by latency: 1000003 rows of 256 f16, m = 4, with the balance loss take 216
+// us (of which the finish 13), where reading them takes 81: 166 instructions a warp
+// for a row use 66 % of the issue slots, HBM is at 33 %, and 120 registers leave 15
+// warps a multiprocessor.  65536 of 1024 fp32, m = 4: 71 us (40), of 4096 bf16 294
+// (79).  Of streamed rows 2048 of 65536 bf16 take 607 us (319 without the balance
+// loss; 40): 1.4 warp instructions a logit with 16 warps, and the mass is read by
+// single elements.
 #pragma once
 
 #include "gate_internal.cuh"
@@ -34,7 +40,9 @@ constexpr int kGateWarpThreads = 256;
 constexpr int kGateBlockThreads = 512;
 constexpr int kGateStreamGrid = 2 * kSms;
 constexpr int kGateMassBlocks = 16;  // stretches of rows that are streamed
-// Blocks that keep sums, at most: as many as fit a multiprocessor.
+// Blocks that keep sums, at most: grids are as many as the device holds at once or
+// these, and the workspace has room for these, which it has to know without asking
+// the device.  8 bytes a column each: 20 MB at 8192 columns, 80 MB at 65536.
 inline int gate_blocks(int K) { return (K <= 512 ? 4 : K <= 1100 ? 8 : K <= 4096 ? 4 : K <= 8192 ? 2 : 1) * kSms; }
 
 // How many blocks left rows and entries, mass, and counts; none: a failure.

@@ -41,7 +41,8 @@ class Gate:
     After ``forward``: ids [N, m] int32 and gamma [N, m] float32, what
     ``LocalExperts.forward`` takes; lse [N]; with ``balance`` also counts [K]
     int64, mass [K], share [K] and loss [1]: device tensors that the next
-    ``forward`` overwrites.  normalised: the m shares of a row sum to one.
+    ``forward`` overwrites (those of the balance loss the next that has it, until
+    which they stay).  normalised: the m shares of a row sum to one.
     """
 
     def __init__(self, N, K, m, dtype, normalised=False, device="cuda"):
