@@ -23,8 +23,8 @@
  * returned before anything is queued; arrays dense, row-major, aligned to
  * their element type (GMM_ERR_INVALID_ARG if not), outputs apart from inputs
  * and from one another.  Logits and rows are of a gmm_dtype; sums are held in
- * 32 bits or more and rounded once.  Results are bitwise reproducible.  N may
- * be 0.
+ * 32 bits or more and rounded once; a share below 2^-126 may be 0.  Results are
+ * bitwise reproducible.  N may be 0.
  */
 #ifndef GMM_GATE_H
 #define GMM_GATE_H
@@ -109,7 +109,8 @@ gmm_status gmm_gate_grad(const void* L, gmm_dtype xdtype, int64_t N, int K, int 
  * weights: N float or NULL (1).  A row of weight 0, whose logits are not read,
  *          or without an entry is left out: its row_n and dL are 0 (added: dL is
  *          as it was).
- * A row whose logits are all -inf has row_n = inf and p = 0.  A large T leaves
+ * A row whose logits are all -inf has row_n = inf and p = 0; one that has -inf, or
+ * a number 2^128 below its largest, at an entry has row_n = inf.  A large T leaves
  * row_n the difference of logarithms in 32 bits, T^2 times their rounding.
  * rows:    N float (written).
  * loss:    1 float (written).
